@@ -428,6 +428,199 @@ ssd_status_t ssd_scan_bwd(const void *x, const float *dt_raw, const float *dt_bi
                           float *ddt_bias, float *dA_log, float *dB, float *dC, float *dD,
                           float *d_init, const ssd_dims_t *dims, void *stream);
 
+/* ---- the attention layers of hybrid state-space models ---------------------
+ *
+ * Hybrid stacks put a few attention layers between the scan layers.  The
+ * operators below are such a layer's own: the step plan of a paged key-value
+ * cache, the norm and rotary position of its queries and keys (forward, into
+ * the cache when serving, and backward), and the attention that reads the
+ * cache.  They have no counterpart in the cited pages; their formulas are in
+ * the comments here.
+ *
+ * The paged cache.  Keys and values are kept in pages of page_size tokens.
+ * Request r's token at position p lies in page block_table[r][p / page_size]
+ * at offset p % page_size; its slot number is page * page_size + offset.
+ * k_cache and v_cache are [npages, page_size, nkv, headdim] in dtype, addressed
+ * by the strides given (elements) for page, token and head, headdim
+ * contiguous: token-major and head-major pages and caches that share one
+ * buffer are all covered.  Strides are multiples of 16 bytes.
+ *
+ * Arrays are DEVICE pointers of the current device, caller-owned.  Data
+ * pointers are 16-byte aligned; positions, slots and the start array have
+ * their type's alignment.  Calls enqueue on `stream` only, never synchronise,
+ * may be captured into a CUDA graph, and return an ssd_status_t; nothing is
+ * enqueued on an argument error.
+ */
+
+typedef struct ssd_plan_dims {
+    int64_t nreq;        /* requests: 0 .. SSD_PLAN_MAX_REQUESTS */
+    int64_t max_tokens;  /* rows of positions, token_req and slots: 0 .. 2^31 - 1 */
+    int64_t ring_size;   /* entries of free_ring: 1 .. 2^31 - 1 */
+    int32_t page_size;   /* tokens per page, >= 1; page_size * max_pages <= 2^31 - 1 */
+    int32_t max_pages;   /* columns of block_table (contiguous), >= 1 */
+    uint32_t flags;      /* must be 0 */
+    uint32_t reserved;   /* must be 0 */
+} ssd_plan_dims_t;
+
+#define SSD_PLAN_MAX_REQUESTS 8192
+
+/*
+ * ssd_paged_plan -- block tables, positions and slots of one serving step.
+ *
+ * Request r holds lens[r] cached tokens (in ceil(lens[r] / page_size) pages of
+ * its block_table row) and brings new_lens[r] tokens: 0 none, < 0 the request
+ * is finished and gives its pages back.  Free pages are the ring entries
+ * free_ring[i mod ring_size], ring_pos[0] <= i < ring_pos[1].
+ * In request order: a request that brings tokens is granted all of them if
+ * lens + new_lens fits its table row and the tokens and the new pages of it
+ * and of all requests before it (that fit their rows) are at most max_tokens
+ * and the free pages; else it is granted none and keeps its state.  So the
+ * first request that finds no room and every later one wait.  Granted
+ * requests take their pages from the ring's head, in request order, into
+ * their block_table rows; finished ones put theirs at its tail, in request
+ * order, to be handed out from the next call on.
+ *   lens_out [nreq]   lens + granted; 0 for a finished request
+ *   granted  [nreq]   new_lens or 0
+ *   start    [nreq+1] exclusive prefix sum of granted: request r's tokens are
+ *                     rows start[r] .. start[r+1] - 1 of the step
+ *   positions, token_req, slots [max_tokens]  per row, -1 beyond start[nreq]
+ *   ring_pos_out [2]  the ring's head and tail afterwards
+ *   counts   [4]      tokens granted, pages taken, pages given back, requests
+ *                     refused
+ * lens_out may be lens and ring_pos_out may be ring_pos (in place); nothing
+ * else may overlap.  block_table rows change only in the entries of new
+ * pages.  A negative len counts as 0; a ring with fewer than 0 or more than
+ * ring_size free entries counts as one with 0 or ring_size.  Pointers are
+ * 16-byte aligned; the arrays of max_tokens entries may be NULL when it is 0.
+ */
+ssd_status_t ssd_paged_plan(const int32_t *lens, const int32_t *new_lens, int32_t *block_table,
+                            int32_t *free_ring, const int64_t *ring_pos, int32_t *lens_out,
+                            int32_t *granted, int32_t *start, int32_t *positions,
+                            int32_t *token_req, int64_t *slots, int64_t *ring_pos_out,
+                            int32_t *counts, const ssd_plan_dims_t *dims, void *stream);
+
+/* In ssd_qk_dims_t.flags: rotated pairs are the adjacent elements (2i, 2i+1);
+ * without it they are (i, i + rotary_dim / 2). */
+#define SSD_ROPE_INTERLEAVED 1u
+
+typedef struct ssd_qk_dims {
+    int64_t ntokens;     /* >= 0 */
+    int64_t max_pos;     /* rows of cos and sin, >= 0 */
+    int64_t npages;      /* pages of the cache (0 without one) */
+    int32_t nheads_q;    /* >= 1 */
+    int32_t nheads_k;    /* >= 1; also the heads of v */
+    int32_t headdim;     /* D: a multiple of 8, 8 .. 256 */
+    int32_t rotary_dim;  /* R: a multiple of 16, 0 .. D; the elements from R on are not rotated */
+    int32_t page_size;   /* >= 1 with a cache */
+    int32_t dtype;       /* ssd_dtype_t of q, k, v, their outputs and gradients, and the cache */
+    uint32_t flags;      /* 0 or SSD_ROPE_INTERLEAVED */
+    float eps;           /* >= 0 */
+    /* strides in elements, {token, head}, D contiguous; multiples of 16 bytes */
+    int64_t q_stride[2], k_stride[2], v_stride[2];
+    int64_t qo_stride[2], ko_stride[2];   /* q_out, k_out; in the backward dq_out, dk_out */
+    int64_t dq_stride[2], dk_stride[2];   /* backward only */
+    /* strides in elements, {page, token, head} */
+    int64_t kc_stride[3], vc_stride[3];
+} ssd_qk_dims_t;
+
+/*
+ * ssd_qk_norm_rope_fwd -- per token and head, RMSNorm of the queries and keys
+ * over the head's D elements, then the rotary position:
+ *   n = x / sqrt(mean(x^2) + eps) * weight
+ *   (a, b) -> (a cos - b sin, b cos + a sin) for each rotated pair of n
+ * with cos and sin [max_pos, R/2] fp32 taken at the token's position; computed
+ * in fp32 and rounded once.  Inputs q [ntokens, Hq, D], k [ntokens, Hk, D],
+ * q_weight and k_weight [D] fp32 (NULL: ones), positions [ntokens].  Outputs
+ * q_out, k_out (k_out may be NULL when there is a cache).
+ * With k_cache (then v, v_cache and slots are required too): token t's keys
+ * and its v [ntokens, Hk, D], unchanged, are also written to slot slots[t] of
+ * the caches; a slot outside 0 .. npages * page_size - 1 is not written.
+ * A token whose position is outside 0 .. max_pos - 1 is padding: its q_out and
+ * k_out are zero and nothing of it goes to the cache.
+ * q_out may be q, and k_out k, with equal strides (in place); outputs overlap
+ * no other input.  Two tokens of a call must not have the same slot.
+ */
+ssd_status_t ssd_qk_norm_rope_fwd(const void *q, const void *k, const void *v,
+                                  const float *q_weight, const float *k_weight,
+                                  const float *cos, const float *sin, const int32_t *positions,
+                                  void *q_out, void *k_out, void *k_cache, void *v_cache,
+                                  const int64_t *slots, const ssd_qk_dims_t *dims, void *stream);
+
+/*
+ * ssd_qk_norm_rope_bwd -- the gradients of ssd_qk_norm_rope_fwd with respect
+ * to q, k and the weights, given dq_out = dL/dq_out and dk_out = dL/dk_out.
+ * With g the inversely rotated gradient, r = 1 / sqrt(mean(x^2) + eps):
+ *   dweight = sum over tokens and heads of g x r   (fp32, a fixed order)
+ *   dx = r (g weight - x r mean(g weight x r))
+ * dq, dk in dtype; dq_weight, dk_weight [D] fp32 (NULL: not written).  Padding
+ * tokens have zero dq, dk and no part in the weights' gradients.  Outputs
+ * overlap no input, except that dq may be dq_out and dk dk_out with equal
+ * strides.  `workspace`: NULL (scratch comes stream-ordered from the library
+ * pool), or a 16-byte aligned buffer of workspace_bytes >= the size that
+ * ssd_qk_norm_rope_bwd_workspace_size gives (else SSD_ERR_SCRATCH_LIMIT),
+ * which calls that may overlap must not share; its contents do not matter.
+ */
+ssd_status_t ssd_qk_norm_rope_bwd(const void *q, const void *k, const float *q_weight,
+                                  const float *k_weight, const float *cos, const float *sin,
+                                  const int32_t *positions, const void *dq_out,
+                                  const void *dk_out, void *dq, void *dk, float *dq_weight,
+                                  float *dk_weight, void *workspace, uint64_t workspace_bytes,
+                                  const ssd_qk_dims_t *dims, void *stream);
+ssd_status_t ssd_qk_norm_rope_bwd_workspace_size(const ssd_qk_dims_t *dims, uint64_t *bytes);
+
+#define SSD_ATTN_MAX_REQUESTS 16384
+
+typedef struct ssd_attn_dims {
+    int64_t nrows;       /* query rows (tokens), >= 0 */
+    int64_t nreq;        /* requests: rows of block_table, >= 0 */
+    int64_t npages;      /* pages of the cache, >= 0 */
+    int32_t nheads;      /* query heads, >= 1 */
+    int32_t nkv;         /* key-value heads, >= 1, nheads % nkv == 0; query head h reads head h / (nheads / nkv) */
+    int32_t headdim;     /* D: a multiple of 8, 8 .. 256 */
+    int32_t page_size;   /* >= 1; page_size * max_pages <= 2^31 - 1 */
+    int32_t max_pages;   /* columns of block_table, >= 1 */
+    int32_t window;      /* 0: none; else a row sees its last `window` positions only */
+    int32_t dtype;       /* ssd_dtype_t of q, the caches and out */
+    uint32_t flags;      /* must be 0 */
+    float scale;         /* factor of q . k */
+    uint32_t reserved;   /* must be 0 */
+    /* strides in elements, D contiguous; multiples of 16 bytes (table_stride: any) */
+    int64_t q_stride[2], o_stride[2];     /* row, head */
+    int64_t kc_stride[3], vc_stride[3];   /* page, token, head */
+    int64_t table_stride;                 /* request */
+} ssd_attn_dims_t;
+
+/*
+ * ssd_paged_attn_fwd -- attention of new tokens over a paged cache.
+ *
+ * Row i is the token at position positions[i] of its request and sees the
+ * cached positions t with max(0, positions[i] - window + 1) <= t <=
+ * positions[i] (all from 0 without a window):
+ *   s_t = scale q . k_t,  out = sum_t softmax(s)_t v_t,  lse = log sum_t e^{s_t}
+ * start NULL: row i is request i's one row (nrows == nreq).  Else start
+ * [nreq+1], ascending, as ssd_paged_plan writes it: request r has the rows
+ * start[r] .. start[r+1] - 1, their positions ascending; rows from
+ * start[nreq] on are padding.  nreq <= SSD_ATTN_MAX_REQUESTS then.
+ * A row that sees nothing (position -1, padding) has out 0 and lse -inf.
+ * Positions past max_pages * page_size, and pages whose table entry is outside
+ * 0 .. npages - 1, are not seen; table entries past a request's positions are not
+ * read into the result, and neither are cache contents that a row does not
+ * see, whatever they hold (infinities and NaN included).
+ * q, out [nrows, nheads, D]; lse [nrows, nheads] fp32 (NULL: not written);
+ * block_table [nreq, max_pages].  Sums, maxima and the accumulated output are
+ * fp32.  The work is split over the cache's length into equal shares and
+ * joined in a fixed order: equal calls on one device give equal bits.
+ * out may be q with equal strides; outputs overlap no other input.
+ * `workspace` as for ssd_qk_norm_rope_bwd, with
+ * ssd_paged_attn_workspace_size's bytes.
+ */
+ssd_status_t ssd_paged_attn_fwd(const void *q, const void *k_cache, const void *v_cache,
+                                const int32_t *block_table, const int32_t *positions,
+                                const int32_t *start, void *out, float *lse, void *workspace,
+                                uint64_t workspace_bytes, const ssd_attn_dims_t *dims,
+                                void *stream);
+ssd_status_t ssd_paged_attn_workspace_size(const ssd_attn_dims_t *dims, uint64_t *bytes);
+
 /* Which path SSD_PATH_AUTO resolves to for these dims on the current device
  * (SSD_PATH_SEQUENTIAL, SSD_PATH_CHUNKED or SSD_PATH_DECODE), or
  * -(ssd_status_t) if the dims are

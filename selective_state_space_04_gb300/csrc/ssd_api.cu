@@ -346,6 +346,160 @@ void *noalloc_scratch(int dev)
     return addr[dev];
 }
 
+// ---- strided operands of the attention-layer entry points ----------------
+
+// [n0, n1, D] with strides in bytes, D contiguous
+struct Strided {
+    const void *p;
+    int64_t n0, n1, s0, s1, width;   // counts, byte strides, bytes of one [D] row
+    int64_t extent() const { return n0 > 0 && n1 > 0 ? (n0 - 1) * s0 + (n1 - 1) * s1 + width : 0; }
+};
+
+// whether two strided operands share bytes.  Views of one fused buffer (equal
+// row strides, each row's heads within the stride) are told apart exactly;
+// otherwise overlapping extents count as overlap.
+bool overlaps(const Strided &a, const Strided &b)
+{
+    if (!overlaps(a.p, a.extent(), b.p, b.extent()))
+        return false;
+    const int64_t wa = (a.n1 - 1) * a.s1 + a.width, wb = (b.n1 - 1) * b.s1 + b.width;
+    if (a.s0 != b.s0 || a.s0 <= 0 || wa > a.s0 || wb > a.s0)
+        return true;
+    int64_t delta = (int64_t)((uintptr_t)b.p - (uintptr_t)a.p) % a.s0;
+    if (delta < 0)
+        delta += a.s0;
+    return !(delta >= wa && delta + wb <= a.s0);
+}
+
+bool same_view(const Strided &a, const Strided &b)
+{
+    return a.p == b.p && a.n0 == b.n0 && a.n1 == b.n1 && a.s0 == b.s0 && a.s1 == b.s1;
+}
+
+// whether an output's [D] rows are all distinct memory
+bool distinct_rows(const Strided &a)
+{
+    if (!a.p || a.n0 <= 0)
+        return true;
+    const bool row_major = (a.n1 == 1 || a.s1 >= a.width) && (a.n0 == 1 || a.s0 >= (a.n1 - 1) * a.s1 + a.width);
+    const bool head_major = (a.n0 == 1 || a.s0 >= a.width) && (a.n1 == 1 || a.s1 >= (a.n0 - 1) * a.s0 + a.width);
+    return row_major || head_major;
+}
+
+bool aligned(const void *p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+
+// strides: >= 0, multiples of 16 bytes, and small enough that the extent fits
+bool strides_ok(const int64_t *s, int n, const int64_t *counts, int64_t es, ssd_status_t *why)
+{
+    int64_t total = 0;
+    for (int i = 0; i < n; ++i) {
+        int64_t t;
+        if (counts[i] <= 1)   // (the stride of a single row is not used)
+            continue;
+        if (s[i] < 0 || !mul_ok(s[i], es, &t) || !mul_ok(t, counts[i], &t) ||
+            (total += t) > (INT64_C(1) << 46)) {
+            *why = SSD_ERR_INVALID_DIMS;
+            return false;
+        }
+        if (s[i] * es % 16 != 0) {
+            *why = SSD_ERR_MISALIGNED;
+            return false;
+        }
+    }
+    return true;
+}
+
+ssd_status_t check_qk_dims(const ssd_qk_dims_t *d, bool cache, bool bwd)
+{
+    if (!d)
+        return SSD_ERR_NULL_PTR;
+    if (d->ntokens < 0 || d->ntokens >= (INT64_C(1) << 31) || d->max_pos < 0 || d->max_pos >= (INT64_C(1) << 31) ||
+        d->nheads_q < 1 || d->nheads_k < 1 || d->nheads_q > (1 << 20) || d->nheads_k > (1 << 20) || d->headdim < 1 ||
+        d->rotary_dim < 0 || d->rotary_dim > d->headdim || !(d->eps >= 0.f) || (d->flags & ~SSD_ROPE_INTERLEAVED) != 0)
+        return SSD_ERR_INVALID_DIMS;
+    if (d->dtype != SSD_DTYPE_F32 && d->dtype != SSD_DTYPE_BF16)
+        return SSD_ERR_UNSUPPORTED_DTYPE;
+    if (d->headdim % 8 != 0 || d->headdim > 256 || d->rotary_dim % 16 != 0)
+        return SSD_ERR_UNSUPPORTED;
+    const int64_t es = (int64_t)elem_size(d->dtype);
+    const int64_t nq[] = {d->ntokens, d->nheads_q}, nk[] = {d->ntokens, d->nheads_k};
+    ssd_status_t why = SSD_OK;
+    if (!strides_ok(d->q_stride, 2, nq, es, &why) || !strides_ok(d->k_stride, 2, nk, es, &why) ||
+        !strides_ok(d->qo_stride, 2, nq, es, &why) || !strides_ok(d->ko_stride, 2, nk, es, &why))
+        return why;
+    if (bwd && (!strides_ok(d->dq_stride, 2, nq, es, &why) || !strides_ok(d->dk_stride, 2, nk, es, &why)))
+        return why;
+    if (cache) {
+        if (d->page_size < 1 || d->npages < 0 || d->npages >= (INT64_C(1) << 31))
+            return SSD_ERR_INVALID_DIMS;
+        const int64_t nc[] = {d->npages, d->page_size, d->nheads_k};
+        if (!strides_ok(d->v_stride, 2, nk, es, &why) || !strides_ok(d->kc_stride, 3, nc, es, &why) ||
+            !strides_ok(d->vc_stride, 3, nc, es, &why))
+            return why;
+    }
+    return SSD_OK;
+}
+
+Strided view(const void *p, int64_t n0, int64_t n1, const int64_t *s, int64_t width, int64_t es)
+{
+    return {p, n0, n1, s[0] * es, s[1] * es, width};
+}
+
+// bytes that a paged cache spans
+int64_t cache_extent(int64_t npages, int64_t page, int64_t heads, const int64_t *s, int64_t D, int64_t es)
+{
+    return npages > 0 ? ((npages - 1) * s[0] + (page - 1) * s[1] + (heads - 1) * s[2] + D) * es : 0;
+}
+
+ssd_status_t check_attn_dims(const ssd_attn_dims_t *d)
+{
+    if (!d)
+        return SSD_ERR_NULL_PTR;
+    int64_t t;
+    if (d->flags != 0 || d->reserved != 0 || d->nrows < 0 || d->nrows >= (INT64_C(1) << 31) || d->nreq < 0 ||
+        d->nreq >= (INT64_C(1) << 31) || d->npages < 0 || d->npages >= (INT64_C(1) << 31) || d->nheads < 1 ||
+        d->nheads > (1 << 20) || d->nkv < 1 || d->nheads % d->nkv != 0 || d->headdim < 1 || d->page_size < 1 ||
+        d->max_pages < 1 || (int64_t)d->page_size * d->max_pages >= (INT64_C(1) << 31) || d->window < 0 ||
+        !(d->scale == d->scale) || d->table_stride < 0 || !mul_ok(d->nreq, d->table_stride, &t) ||
+        t > (INT64_C(1) << 44))
+        return SSD_ERR_INVALID_DIMS;
+    if (d->dtype != SSD_DTYPE_F32 && d->dtype != SSD_DTYPE_BF16)
+        return SSD_ERR_UNSUPPORTED_DTYPE;
+    if (d->headdim % 8 != 0 || d->headdim > 256)
+        return SSD_ERR_UNSUPPORTED;
+    const int64_t es = (int64_t)elem_size(d->dtype);
+    const int64_t nq[] = {d->nrows, d->nheads}, nc[] = {d->npages, d->page_size, d->nkv};
+    ssd_status_t why = SSD_OK;
+    if (!strides_ok(d->q_stride, 2, nq, es, &why) || !strides_ok(d->o_stride, 2, nq, es, &why) ||
+        !strides_ok(d->kc_stride, 3, nc, es, &why) || !strides_ok(d->vc_stride, 3, nc, es, &why))
+        return why;
+    return SSD_OK;
+}
+
+// Runs `launch` with the caller's workspace, or with one from the library pool.
+template <typename F>
+ssd_status_t with_workspace(void *workspace, uint64_t have, size_t need, cudaStream_t st, F launch)
+{
+    if (need == 0)
+        return launch(nullptr) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+    if (workspace) {
+        if (have < need)
+            return SSD_ERR_SCRATCH_LIMIT;
+        return launch(workspace) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+    }
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        return SSD_ERR_CUDA;
+    cudaMemPool_t pool = scratch_pool(dev);
+    void *ws = nullptr;
+    if (!pool || cudaMallocFromPoolAsync(&ws, need, pool, st) != cudaSuccess)
+        return SSD_ERR_CUDA;
+    ssd_status_t s = launch(ws) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+    if (cudaFreeAsync(ws, st) != cudaSuccess && s == SSD_OK)
+        s = SSD_ERR_CUDA;
+    return s;
+}
+
 }  // namespace
 
 void note_launches(int n) { g_launches.fetch_add((uint64_t)n, std::memory_order_relaxed); }
@@ -1216,6 +1370,287 @@ ssd_status_t ssd_scan_bwd(const void *x, const float *dt_raw, const float *dt_bi
     if (cudaFreeAsync(ws, st) != cudaSuccess && rs == SSD_OK)
         rs = SSD_ERR_CUDA;
     return rs;
+}
+
+ssd_status_t ssd_paged_plan(const int32_t *lens, const int32_t *new_lens, int32_t *block_table, int32_t *free_ring,
+                            const int64_t *ring_pos, int32_t *lens_out, int32_t *granted, int32_t *start,
+                            int32_t *positions, int32_t *token_req, int64_t *slots, int64_t *ring_pos_out,
+                            int32_t *counts, const ssd_plan_dims_t *dims, void *stream)
+{
+    SSD_NVTX_RANGE("ssd_paged_plan");
+    if (!dims)
+        return SSD_ERR_NULL_PTR;
+    const int64_t lim = INT64_C(1) << 31;
+    if (dims->flags != 0 || dims->reserved != 0 || dims->nreq < 0 || dims->max_tokens < 0 || dims->max_tokens >= lim ||
+        dims->ring_size < 1 || dims->ring_size >= lim || dims->page_size < 1 || dims->max_pages < 1 ||
+        (int64_t)dims->page_size * dims->max_pages >= lim)
+        return SSD_ERR_INVALID_DIMS;
+    if (dims->nreq > SSD_PLAN_MAX_REQUESTS)
+        return SSD_ERR_UNSUPPORTED;
+    const int64_t n = dims->nreq, T = dims->max_tokens;
+    if (!free_ring || !ring_pos || !start || !ring_pos_out || !counts ||
+        (n > 0 && (!lens || !new_lens || !block_table || !lens_out || !granted)) ||
+        (T > 0 && (!positions || !token_req || !slots)))
+        return SSD_ERR_NULL_PTR;
+    struct { const void *p; int64_t bytes; bool out; } a[] = {
+        {lens, n * 4, false}, {new_lens, n * 4, false}, {ring_pos, 16, false},
+        {block_table, n * dims->max_pages * 4, true}, {free_ring, dims->ring_size * 4, true}, {lens_out, n * 4, true},
+        {granted, n * 4, true}, {start, (n + 1) * 4, true}, {positions, T * 4, true}, {token_req, T * 4, true},
+        {slots, T * 8, true}, {ring_pos_out, 16, true}, {counts, 16, true}};
+    constexpr int na = sizeof(a) / sizeof(a[0]);
+    for (const auto &x : a)
+        if (!aligned16(x.p))
+            return SSD_ERR_MISALIGNED;
+    for (int i = 0; i < na; ++i)
+        for (int j = i + 1; j < na; ++j) {
+            const bool in_place = a[i].p == a[j].p && ((a[i].p == lens && a[j].p == lens_out && i == 0 && j == 5) ||
+                                                       (i == 2 && j == 11));
+            if ((a[i].out || a[j].out) && !in_place && overlaps(a[i].p, a[i].bytes, a[j].p, a[j].bytes))
+                return SSD_ERR_ALIASING;
+        }
+    PlanArgs pa;
+    pa.lens = lens;
+    pa.new_lens = new_lens;
+    pa.table = block_table;
+    pa.ring = free_ring;
+    pa.ring_pos = ring_pos;
+    pa.lens_out = lens_out;
+    pa.granted = granted;
+    pa.start = start;
+    pa.positions = positions;
+    pa.token_req = token_req;
+    pa.slots = slots;
+    pa.ring_pos_out = ring_pos_out;
+    pa.counts = counts;
+    pa.nreq = (int)n;
+    pa.max_tokens = (int)T;
+    pa.ring_size = (int)dims->ring_size;
+    pa.page_size = dims->page_size;
+    pa.max_pages = dims->max_pages;
+    return plan_launch(pa, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
+ssd_status_t ssd_qk_norm_rope_fwd(const void *q, const void *k, const void *v, const float *q_weight,
+                                  const float *k_weight, const float *cos, const float *sin, const int32_t *positions,
+                                  void *q_out, void *k_out, void *k_cache, void *v_cache, const int64_t *slots,
+                                  const ssd_qk_dims_t *dims, void *stream)
+{
+    SSD_NVTX_RANGE("ssd_qk_norm_rope_fwd");
+    const bool cache = k_cache || v_cache || slots;
+    const ssd_status_t s = check_qk_dims(dims, cache, false);
+    if (s != SSD_OK)
+        return s;
+    const int64_t T = dims->ntokens, D = dims->headdim, es = (int64_t)elem_size(dims->dtype);
+    if (T > 0 && (!q || !k || !positions || !q_out || (!k_out && !cache) ||
+                  (dims->rotary_dim > 0 && dims->max_pos > 0 && (!cos || !sin))))
+        return SSD_ERR_NULL_PTR;
+    if (cache && (!k_cache || !v_cache || (T > 0 && (!v || !slots))))
+        return SSD_ERR_NULL_PTR;
+    const void *ptrs[] = {q, k, v, q_weight, k_weight, cos, sin, q_out, k_out, k_cache, v_cache};
+    for (const void *p : ptrs)
+        if (!aligned16(p))
+            return SSD_ERR_MISALIGNED;
+    if (!aligned(positions, 4) || !aligned(slots, 8))
+        return SSD_ERR_MISALIGNED;
+    const int64_t Hq = dims->nheads_q, Hk = dims->nheads_k, w = D * es;
+    const int64_t tab = dims->max_pos * (dims->rotary_dim / 2) * 4;
+    const Strided vq = view(q, T, Hq, dims->q_stride, w, es), vk = view(k, T, Hk, dims->k_stride, w, es);
+    const Strided vv = view(cache ? v : nullptr, T, Hk, dims->v_stride, w, es);
+    const Strided oq = view(q_out, T, Hq, dims->qo_stride, w, es), ok = view(k_out, T, Hk, dims->ko_stride, w, es);
+    const Strided *ins[] = {&vq, &vk, &vv}, *outs[] = {&oq, &ok};
+    const struct { const void *p; int64_t bytes; } flat[] = {{q_weight, D * 4}, {k_weight, D * 4}, {cos, tab}, {sin, tab},
+                                                              {positions, T * 4}, {slots, cache ? T * 8 : 0}};
+    const int64_t kcb = cache ? cache_extent(dims->npages, dims->page_size, Hk, dims->kc_stride, D, es) : 0;
+    const int64_t vcb = cache ? cache_extent(dims->npages, dims->page_size, Hk, dims->vc_stride, D, es) : 0;
+    for (int o = 0; o < 2; ++o) {
+        for (int i = 0; i < 3; ++i)
+            if (overlaps(*outs[o], *ins[i]) && !(o == i && same_view(*outs[o], *ins[i])))
+                return SSD_ERR_ALIASING;
+        for (const auto &f : flat)
+            if (overlaps(outs[o]->p, outs[o]->extent(), f.p, f.bytes))
+                return SSD_ERR_ALIASING;
+        if (overlaps(outs[o]->p, outs[o]->extent(), k_cache, kcb) || overlaps(outs[o]->p, outs[o]->extent(), v_cache, vcb))
+            return SSD_ERR_ALIASING;
+    }
+    if (overlaps(oq, ok) || !distinct_rows(oq) || !distinct_rows(ok))
+        return SSD_ERR_ALIASING;
+    for (int i = 0; i < 3; ++i)
+        if (overlaps(ins[i]->p, ins[i]->extent(), k_cache, kcb) || overlaps(ins[i]->p, ins[i]->extent(), v_cache, vcb))
+            return SSD_ERR_ALIASING;
+    for (const auto &f : flat)
+        if (overlaps(f.p, f.bytes, k_cache, kcb) || overlaps(f.p, f.bytes, v_cache, vcb))
+            return SSD_ERR_ALIASING;
+    if (T == 0)
+        return SSD_OK;
+    QkArgs qa{};
+    qa.q = q;
+    qa.k = k;
+    qa.v = v;
+    qa.qw = q_weight;
+    qa.kw = k_weight;
+    qa.cos = cos;
+    qa.sin = sin;
+    qa.positions = positions;
+    qa.qo = q_out;
+    qa.ko = k_out;
+    qa.kc = k_cache;
+    qa.vc = v_cache;
+    qa.slots = slots;
+    qa.d = *dims;
+    return qk_fwd_launch(qa, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
+ssd_status_t ssd_qk_norm_rope_bwd_workspace_size(const ssd_qk_dims_t *dims, uint64_t *bytes)
+{
+    if (!bytes)
+        return SSD_ERR_NULL_PTR;
+    const ssd_status_t s = check_qk_dims(dims, false, true);
+    if (s != SSD_OK)
+        return s;
+    *bytes = qk_bwd_workspace_bytes(*dims);
+    return SSD_OK;
+}
+
+ssd_status_t ssd_qk_norm_rope_bwd(const void *q, const void *k, const float *q_weight, const float *k_weight,
+                                  const float *cos, const float *sin, const int32_t *positions, const void *dq_out,
+                                  const void *dk_out, void *dq, void *dk, float *dq_weight, float *dk_weight,
+                                  void *workspace, uint64_t workspace_bytes, const ssd_qk_dims_t *dims, void *stream)
+{
+    SSD_NVTX_RANGE("ssd_qk_norm_rope_bwd");
+    const ssd_status_t s = check_qk_dims(dims, false, true);
+    if (s != SSD_OK)
+        return s;
+    const int64_t T = dims->ntokens, D = dims->headdim, es = (int64_t)elem_size(dims->dtype);
+    if (T > 0 && (!q || !k || !positions || !dq_out || !dk_out || !dq || !dk ||
+                  (dims->rotary_dim > 0 && dims->max_pos > 0 && (!cos || !sin))))
+        return SSD_ERR_NULL_PTR;
+    const void *ptrs[] = {q, k, q_weight, k_weight, cos, sin, dq_out, dk_out, dq, dk, dq_weight, dk_weight, workspace};
+    for (const void *p : ptrs)
+        if (!aligned16(p))
+            return SSD_ERR_MISALIGNED;
+    if (!aligned(positions, 4))
+        return SSD_ERR_MISALIGNED;
+    const int64_t Hq = dims->nheads_q, Hk = dims->nheads_k, w = D * es;
+    const int64_t tab = dims->max_pos * (dims->rotary_dim / 2) * 4;
+    const Strided v[] = {view(q, T, Hq, dims->q_stride, w, es), view(k, T, Hk, dims->k_stride, w, es),
+                         view(dq_out, T, Hq, dims->qo_stride, w, es), view(dk_out, T, Hk, dims->ko_stride, w, es)};
+    const Strided o[] = {view(dq, T, Hq, dims->dq_stride, w, es), view(dk, T, Hk, dims->dk_stride, w, es)};
+    const int64_t wsb = workspace ? (int64_t)(workspace_bytes > (uint64_t)INT64_MAX ? INT64_MAX : workspace_bytes) : 0;
+    // every other array as a flat range, outputs last
+    const struct { const void *p; int64_t bytes; } flat[] = {{q_weight, D * 4}, {k_weight, D * 4}, {cos, tab}, {sin, tab},
+                                                              {positions, T * 4}, {dq_weight, D * 4}, {dk_weight, D * 4},
+                                                              {workspace, wsb}};
+    for (int i = 0; i < 2; ++i) {
+        for (int j = 0; j < 4; ++j)
+            if (overlaps(o[i], v[j]) && !(j == i + 2 && same_view(o[i], v[j])))
+                return SSD_ERR_ALIASING;
+        for (const auto &f : flat)
+            if (overlaps(o[i].p, o[i].extent(), f.p, f.bytes))
+                return SSD_ERR_ALIASING;
+    }
+    if (overlaps(o[0], o[1]) || !distinct_rows(o[0]) || !distinct_rows(o[1]))
+        return SSD_ERR_ALIASING;
+    for (int i = 5; i < 8; ++i) {
+        for (int j = 0; j < 4; ++j)
+            if (overlaps(v[j].p, v[j].extent(), flat[i].p, flat[i].bytes))
+                return SSD_ERR_ALIASING;
+        for (int j = 0; j < i; ++j)
+            if (overlaps(flat[j].p, flat[j].bytes, flat[i].p, flat[i].bytes))
+                return SSD_ERR_ALIASING;
+    }
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (T == 0) {   // no tokens: the weights' gradients are zero
+        if ((dq_weight && cudaMemsetAsync(dq_weight, 0, (size_t)D * 4, st) != cudaSuccess) ||
+            (dk_weight && cudaMemsetAsync(dk_weight, 0, (size_t)D * 4, st) != cudaSuccess))
+            return SSD_ERR_CUDA;
+        return SSD_OK;
+    }
+    QkArgs qa{};
+    qa.q = q;
+    qa.k = k;
+    qa.qw = q_weight;
+    qa.kw = k_weight;
+    qa.cos = cos;
+    qa.sin = sin;
+    qa.positions = positions;
+    qa.qo = const_cast<void *>(dq_out);
+    qa.ko = const_cast<void *>(dk_out);
+    qa.dq = dq;
+    qa.dk = dk;
+    qa.dqw = dq_weight;
+    qa.dkw = dk_weight;
+    qa.d = *dims;
+    const size_t need = dq_weight || dk_weight ? qk_bwd_workspace_bytes(*dims) : 0;
+    return with_workspace(workspace, workspace_bytes, need, st, [&](void *ws) { return qk_bwd_launch(qa, ws, st); });
+}
+
+ssd_status_t ssd_paged_attn_workspace_size(const ssd_attn_dims_t *dims, uint64_t *bytes)
+{
+    if (!bytes)
+        return SSD_ERR_NULL_PTR;
+    const ssd_status_t s = check_attn_dims(dims);
+    if (s != SSD_OK)
+        return s;
+    *bytes = dims->nrows > 0 ? attn_workspace_bytes(*dims) : 0;
+    return SSD_OK;
+}
+
+ssd_status_t ssd_paged_attn_fwd(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_table,
+                                const int32_t *positions, const int32_t *start, void *out, float *lse, void *workspace,
+                                uint64_t workspace_bytes, const ssd_attn_dims_t *dims, void *stream)
+{
+    SSD_NVTX_RANGE("ssd_paged_attn_fwd");
+    const ssd_status_t s = check_attn_dims(dims);
+    if (s != SSD_OK)
+        return s;
+    if (!start && dims->nrows != dims->nreq)
+        return SSD_ERR_INVALID_DIMS;
+    if (start && dims->nreq > SSD_ATTN_MAX_REQUESTS)
+        return SSD_ERR_UNSUPPORTED;
+    const int64_t R = dims->nrows, D = dims->headdim, es = (int64_t)elem_size(dims->dtype);
+    if (R > 0 && (!q || !positions || !out || (dims->nreq > 0 && !block_table) ||
+                  (dims->npages > 0 && (!k_cache || !v_cache))))
+        return SSD_ERR_NULL_PTR;
+    const void *ptrs[] = {q, k_cache, v_cache, out, lse, workspace};
+    for (const void *p : ptrs)
+        if (!aligned16(p))
+            return SSD_ERR_MISALIGNED;
+    if (!aligned(block_table, 4) || !aligned(positions, 4) || !aligned(start, 4))
+        return SSD_ERR_MISALIGNED;
+    const int64_t w = D * es;
+    const Strided vq = view(q, R, dims->nheads, dims->q_stride, w, es), vo = view(out, R, dims->nheads, dims->o_stride, w, es);
+    if ((overlaps(vo, vq) && !same_view(vo, vq)) || !distinct_rows(vo))
+        return SSD_ERR_ALIASING;
+    const int64_t wsb = workspace ? (int64_t)(workspace_bytes > (uint64_t)INT64_MAX ? INT64_MAX : workspace_bytes) : 0;
+    const struct { const void *p; int64_t bytes; } in[] = {
+        {k_cache, cache_extent(dims->npages, dims->page_size, dims->nkv, dims->kc_stride, D, es)},
+        {v_cache, cache_extent(dims->npages, dims->page_size, dims->nkv, dims->vc_stride, D, es)},
+        {block_table, dims->nreq > 0 ? ((dims->nreq - 1) * dims->table_stride + dims->max_pages) * 4 : 0},
+        {positions, R * 4}, {start, (dims->nreq + 1) * 4}, {q, vq.extent()}};
+    const struct { const void *p; int64_t bytes; } ob[] = {{out, vo.extent()}, {lse, R * dims->nheads * 4}, {workspace, wsb}};
+    for (int o = 0; o < 3; ++o) {
+        for (int i = 0; i < (o == 0 ? 5 : 6); ++i)
+            if (overlaps(ob[o].p, ob[o].bytes, in[i].p, in[i].bytes))
+                return SSD_ERR_ALIASING;
+        for (int o2 = o + 1; o2 < 3; ++o2)
+            if (overlaps(ob[o].p, ob[o].bytes, ob[o2].p, ob[o2].bytes))
+                return SSD_ERR_ALIASING;
+    }
+    if (R == 0)
+        return SSD_OK;
+    AttnArgs aa;
+    aa.q = q;
+    aa.kc = k_cache;
+    aa.vc = v_cache;
+    aa.table = block_table;
+    aa.positions = positions;
+    aa.start = start;
+    aa.out = out;
+    aa.lse = lse;
+    aa.d = *dims;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return with_workspace(workspace, workspace_bytes, attn_workspace_bytes(*dims), st,
+                          [&](void *ws) { return attn_launch(aa, ws, st); });
 }
 
 }  // extern "C"

@@ -212,6 +212,47 @@ int chunk_launches(const ScanArgs &a);
 int chunk_schedule(const ScanArgs &a);
 ssd_status_t chunk_read_device_error(cudaStream_t stream, uint32_t *code);
 
+// ---- the attention layers of hybrid stacks, after validation.  Device pointers.
+// ssd_paged_plan.cu: block tables, positions and slots of one step
+struct PlanArgs {
+    const int32_t *lens, *new_lens;
+    int32_t *table, *ring;                      // [nreq, max_pages], [ring_size]
+    const int64_t *ring_pos;                    // head, tail
+    int32_t *lens_out, *granted, *start, *positions, *token_req;
+    int64_t *slots, *ring_pos_out;
+    int32_t *counts;
+    int nreq, max_tokens, ring_size, page_size, max_pages;
+};
+cudaError_t plan_launch(const PlanArgs &a, cudaStream_t stream);
+
+// ssd_qk_rope.cu: per-head norm of queries and keys with the rotary position
+struct QkArgs {
+    const void *q, *k, *v;                      // [T,Hq,D], [T,Hk,D] x2 (v null without a cache)
+    const float *qw, *kw;                       // [D] or null
+    const float *cos, *sin;                     // [max_pos, R/2]
+    const int32_t *positions;
+    void *qo, *ko;                              // forward: outputs (ko may be null); backward: dq_out, dk_out
+    void *dq, *dk;                              // backward only
+    float *dqw, *dkw;                           // backward only; or null
+    void *kc, *vc;                              // caches or null
+    const int64_t *slots;
+    ssd_qk_dims_t d;
+};
+cudaError_t qk_fwd_launch(const QkArgs &a, cudaStream_t stream);
+size_t qk_bwd_workspace_bytes(const ssd_qk_dims_t &d);
+cudaError_t qk_bwd_launch(const QkArgs &a, void *workspace, cudaStream_t stream);
+
+// ssd_paged_attn.cu: attention of new tokens over the paged cache
+struct AttnArgs {
+    const void *q, *kc, *vc;
+    const int32_t *table, *positions, *start;   // start may be null
+    void *out;
+    float *lse;                                 // or null
+    ssd_attn_dims_t d;
+};
+size_t attn_workspace_bytes(const ssd_attn_dims_t &d);
+cudaError_t attn_launch(const AttnArgs &a, void *workspace, cudaStream_t stream);
+
 // launch accounting
 void note_launches(int n);
 

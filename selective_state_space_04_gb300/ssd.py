@@ -44,6 +44,36 @@ class SsdDims(ctypes.Structure):
                 ("flags", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
 
 
+class SsdPlanDims(ctypes.Structure):
+    _fields_ = [("nreq", ctypes.c_int64), ("max_tokens", ctypes.c_int64), ("ring_size", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("flags", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint32)]
+
+
+ROPE_INTERLEAVED = 1
+
+
+class SsdQkDims(ctypes.Structure):
+    _fields_ = [("ntokens", ctypes.c_int64), ("max_pos", ctypes.c_int64), ("npages", ctypes.c_int64),
+                ("nheads_q", ctypes.c_int32), ("nheads_k", ctypes.c_int32), ("headdim", ctypes.c_int32),
+                ("rotary_dim", ctypes.c_int32), ("page_size", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("flags", ctypes.c_uint32), ("eps", ctypes.c_float),
+                ("q_stride", ctypes.c_int64 * 2), ("k_stride", ctypes.c_int64 * 2), ("v_stride", ctypes.c_int64 * 2),
+                ("qo_stride", ctypes.c_int64 * 2), ("ko_stride", ctypes.c_int64 * 2),
+                ("dq_stride", ctypes.c_int64 * 2), ("dk_stride", ctypes.c_int64 * 2),
+                ("kc_stride", ctypes.c_int64 * 3), ("vc_stride", ctypes.c_int64 * 3)]
+
+
+class SsdAttnDims(ctypes.Structure):
+    _fields_ = [("nrows", ctypes.c_int64), ("nreq", ctypes.c_int64), ("npages", ctypes.c_int64),
+                ("nheads", ctypes.c_int32), ("nkv", ctypes.c_int32), ("headdim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("flags", ctypes.c_uint32), ("scale", ctypes.c_float),
+                ("reserved", ctypes.c_uint32),
+                ("q_stride", ctypes.c_int64 * 2), ("o_stride", ctypes.c_int64 * 2),
+                ("kc_stride", ctypes.c_int64 * 3), ("vc_stride", ctypes.c_int64 * 3), ("table_stride", ctypes.c_int64)]
+
+
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise ImportError(f"libssd is not built ({path} missing); run "
@@ -85,6 +115,18 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.ssd_scan_bwd.argtypes = [vp] * 18 + [ctypes.POINTER(SsdDims), vp]
     lib.ssd_complex_scan_fwd.restype = ctypes.c_int
     lib.ssd_complex_scan_fwd.argtypes = [vp] * 10 + [ctypes.POINTER(SsdDims), vp]
+    lib.ssd_paged_plan.restype = ctypes.c_int
+    lib.ssd_paged_plan.argtypes = [vp] * 13 + [ctypes.POINTER(SsdPlanDims), vp]
+    lib.ssd_qk_norm_rope_fwd.restype = ctypes.c_int
+    lib.ssd_qk_norm_rope_fwd.argtypes = [vp] * 13 + [ctypes.POINTER(SsdQkDims), vp]
+    lib.ssd_qk_norm_rope_bwd.restype = ctypes.c_int
+    lib.ssd_qk_norm_rope_bwd.argtypes = [vp] * 14 + [ctypes.c_uint64, ctypes.POINTER(SsdQkDims), vp]
+    lib.ssd_qk_norm_rope_bwd_workspace_size.restype = ctypes.c_int
+    lib.ssd_qk_norm_rope_bwd_workspace_size.argtypes = [ctypes.POINTER(SsdQkDims), ctypes.POINTER(ctypes.c_uint64)]
+    lib.ssd_paged_attn_fwd.restype = ctypes.c_int
+    lib.ssd_paged_attn_fwd.argtypes = [vp] * 9 + [ctypes.c_uint64, ctypes.POINTER(SsdAttnDims), vp]
+    lib.ssd_paged_attn_workspace_size.restype = ctypes.c_int
+    lib.ssd_paged_attn_workspace_size.argtypes = [ctypes.POINTER(SsdAttnDims), ctypes.POINTER(ctypes.c_uint64)]
     return lib
 
 
@@ -446,3 +488,242 @@ def ssd_scan_bwd(x, dt_raw, dt_bias, A_log, B, C, D, init_state, dy, d_final=Non
     _check(_lib.ssd_scan_bwd(*(_ptr(t) for _, t in named), ctypes.byref(d), ctypes.c_void_p(st.cuda_stream)),
            "ssd_scan_bwd")
     return out
+
+
+# ---- the attention layers of hybrid stacks: a step's plan, queries and keys, attention over the paged cache ----
+
+_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream_ptr(device, stream):
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def _vectors(device, named, dtype):
+    """Contiguous 1-d tensors of ``dtype`` on ``device`` (``named``: (name, tensor or None, length or None))."""
+    for name, t, n in named:
+        if t is None:
+            continue
+        if t.dtype != dtype or t.device != device or t.dim() != 1 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous 1-d {dtype} tensor on {device}")
+        if n is not None and t.shape[0] != n:
+            raise ValueError(f"{name} must have {n} elements, not {t.shape[0]}")
+
+
+def _rows(device, named, dtype):
+    """[n, heads, D] tensors of ``dtype`` with a contiguous last axis (``named``: (name, tensor or None, shape))."""
+    for name, t, shape in named:
+        if t is None:
+            continue
+        if t.dtype != dtype or t.device != device or t.shape != shape:
+            raise ValueError(f"{name} must be a {tuple(shape)} {dtype} tensor on {device}")
+        if t.stride(2) != 1 and shape[2] != 1:
+            raise ValueError(f"{name} must have a contiguous last axis")
+
+
+def _cache_args(device, dtype, k_cache, v_cache, heads, D):
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.shape[2] != heads or k_cache.shape[3] != D:
+        raise ValueError(f"k_cache and v_cache must be [npages, page_size, {heads}, {D}]")
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if t.dtype != dtype or t.device != device or t.stride(3) != 1:
+            raise ValueError(f"{name} must be a {dtype} tensor on {device} with a contiguous last axis")
+
+
+def _workspace(workspace):
+    if workspace is None:
+        return None, 0
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def paged_plan(lens, new_lens, block_table, free_ring, ring_pos, *, page_size, max_tokens, out=None, stream=None):
+    """Block tables, positions and slots of one serving step, on the GPU (``ssd_paged_plan``).
+
+    ``lens, new_lens [R]`` int32: tokens each request holds, and brings (negative: finished, its pages go back);
+    ``block_table [R, max_pages]`` int32 and ``free_ring [n]`` int32 are updated in place; ``ring_pos [2]`` int64 is
+    the ring's head and tail.  Returns a dict of ``lens, granted [R]``, ``start [R+1]``, ``positions, token_req,
+    slots [max_tokens]`` (-1 past ``start[R]``), ``ring_pos [2]`` and ``counts [4]`` (tokens granted, pages taken,
+    pages given back, requests refused); slots and ring_pos int64, the others int32.  ``out`` gives the tensors to
+    write, as such a dict; its ``lens`` and ``ring_pos`` may be the inputs (in place).
+    """
+    R, dev = lens.shape[0], lens.device
+    if not lens.is_cuda:
+        raise ValueError("lens must be a CUDA tensor")
+    if block_table.dtype != torch.int32 or block_table.device != dev or block_table.dim() != 2 or \
+            block_table.shape[0] != R or not block_table.is_contiguous():
+        raise ValueError(f"block_table must be a contiguous [{R}, max_pages] int32 tensor on {dev}")
+    if out is None:
+        i32 = dict(dtype=torch.int32, device=dev)
+        i64 = dict(dtype=torch.int64, device=dev)
+        out = dict(lens=torch.empty(R, **i32), granted=torch.empty(R, **i32), start=torch.empty(R + 1, **i32),
+                   positions=torch.empty(max_tokens, **i32), token_req=torch.empty(max_tokens, **i32),
+                   slots=torch.empty(max_tokens, **i64), ring_pos=torch.empty(2, **i64), counts=torch.empty(4, **i32))
+    o = out
+    _vectors(dev, (("lens", lens, R), ("new_lens", new_lens, R), ("free_ring", free_ring, None), ("out lens", o["lens"], R),
+                   ("granted", o["granted"], R), ("start", o["start"], R + 1), ("positions", o["positions"], max_tokens),
+                   ("token_req", o["token_req"], max_tokens), ("counts", o["counts"], 4)), torch.int32)
+    _vectors(dev, (("ring_pos", ring_pos, 2), ("out ring_pos", o["ring_pos"], 2), ("slots", o["slots"], max_tokens)),
+             torch.int64)
+    d = SsdPlanDims(R, max_tokens, free_ring.shape[0], page_size, block_table.shape[1], 0, 0)
+    _check(_lib.ssd_paged_plan(lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), free_ring.data_ptr(),
+                               ring_pos.data_ptr(), o["lens"].data_ptr(), o["granted"].data_ptr(), o["start"].data_ptr(),
+                               o["positions"].data_ptr(), o["token_req"].data_ptr(), o["slots"].data_ptr(),
+                               o["ring_pos"].data_ptr(), o["counts"].data_ptr(), d, _stream_ptr(dev, stream)),
+           "ssd_paged_plan")
+    return out
+
+
+def rope_table(max_pos, rotary_dim, base=10000.0, device="cuda"):
+    """``(cos, sin)``, each ``[max_pos, rotary_dim / 2]`` fp32, of the angles ``pos * base^(-2 i / rotary_dim)``,
+    computed in fp64."""
+    i = torch.arange(rotary_dim // 2, dtype=torch.float64)
+    ang = torch.arange(max_pos, dtype=torch.float64)[:, None] * base ** (-2.0 * i / max(rotary_dim, 1))[None, :]
+    return ang.cos().float().to(device), ang.sin().float().to(device)
+
+
+def _qk_dims(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved):
+    if q.dim() != 3 or not q.is_cuda:
+        raise ValueError("q must be a [tokens, heads, D] CUDA tensor")
+    T, Hq, D = q.shape
+    dev = q.device
+    if q.dtype not in _DTYPES:
+        raise SsdError(9, "q must be bf16 or fp32")
+    if k.dim() != 3:
+        raise ValueError("k must be a [tokens, heads, D] CUDA tensor")
+    Hk = k.shape[1]
+    _rows(dev, (("q", q, (T, Hq, D)), ("k", k, (T, Hk, D))), q.dtype)
+    _vectors(dev, (("q_weight", q_weight, D), ("k_weight", k_weight, D)), torch.float32)
+    _vectors(dev, (("positions", positions, T),), torch.int32)
+    for name, t in (("cos", cos), ("sin", sin)):
+        if t.dtype != torch.float32 or t.device != dev or t.dim() != 2 or t.shape != cos.shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous [max_pos, rotary_dim / 2] fp32 tensor on {dev}, as the other is")
+    d = SsdQkDims(T, cos.shape[0], 0, Hq, Hk, D, 2 * cos.shape[1], 0, _DTYPES[q.dtype],
+                  ROPE_INTERLEAVED if interleaved else 0, eps, q.stride()[:2], k.stride()[:2])
+    return d
+
+
+def qk_norm_rope_fwd(q, k, q_weight, k_weight, cos, sin, positions, *, eps=1e-6, interleaved=False, v=None, k_cache=None,
+                     v_cache=None, slots=None, q_out=None, k_out=None, return_k=True, stream=None):
+    """RMSNorm of every query and key head and the rotary position in one pass (``ssd_qk_norm_rope_fwd``).
+    Returns ``(q_out, k_out)``.
+
+    ``q [T,Hq,D]`` and ``k, v [T,Hk,D]`` in bf16 or fp32 with a contiguous last axis (views of a fused projection are
+    fine); ``q_weight, k_weight [D]`` fp32 or None; ``cos, sin [max_pos, R/2]`` fp32 (:func:`rope_table`);
+    ``positions [T]`` int32 (a token whose position is outside the table is padding).  Given ``v``, ``k_cache, v_cache
+    [npages, page_size, Hk, D]`` (any strides, contiguous last axis) and ``slots [T]`` int64, keys and values go into
+    the cache as well; ``return_k=False`` then leaves ``k_out`` out (None).  ``q_out`` may be ``q`` and ``k_out`` ``k``.
+    """
+    d = _qk_dims(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
+    dev = q.device
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    if k_out is None and return_k:
+        k_out = torch.empty(k.shape, dtype=q.dtype, device=dev)
+    _rows(dev, (("q_out", q_out, q.shape), ("k_out", k_out, k.shape), ("v", v, k.shape)), q.dtype)
+    d.qo_stride = q_out.stride()[:2]
+    if k_out is not None:
+        d.ko_stride = k_out.stride()[:2]
+    if k_cache is not None or v_cache is not None or slots is not None:
+        if k_cache is None or v_cache is None or slots is None or v is None:
+            raise ValueError("writing the cache takes v, k_cache, v_cache and slots")
+        _cache_args(dev, q.dtype, k_cache, v_cache, k.shape[1], q.shape[2])
+        _vectors(dev, (("slots", slots, q.shape[0]),), torch.int64)
+        d.npages, d.page_size = k_cache.shape[0], k_cache.shape[1]
+        d.v_stride, d.kc_stride, d.vc_stride = v.stride()[:2], k_cache.stride()[:3], v_cache.stride()[:3]
+    elif k_out is None:
+        raise ValueError("return_k=False takes a cache to write the keys to")
+    _check(_lib.ssd_qk_norm_rope_fwd(q.data_ptr(), k.data_ptr(), _addr(v), _addr(q_weight), _addr(k_weight), cos.data_ptr(),
+                                     sin.data_ptr(), positions.data_ptr(), q_out.data_ptr(), _addr(k_out), _addr(k_cache),
+                                     _addr(v_cache), _addr(slots), d, _stream_ptr(dev, stream)), "ssd_qk_norm_rope_fwd")
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_out, *, eps=1e-6, interleaved=False, dq=None,
+                     dk=None, workspace=None, stream=None):
+    """Gradients of :func:`qk_norm_rope_fwd` given those of its outputs.  Returns a dict: ``dq, dk`` in the inputs'
+    dtype, ``dq_weight, dk_weight [D]`` fp32.  ``dq`` and ``dk`` may be given (views of a fused gradient, or ``dq_out``
+    and ``dk_out`` themselves)."""
+    d = _qk_dims(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
+    dev, D = q.device, q.shape[2]
+    if dq is None:
+        dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    if dk is None:
+        dk = torch.empty(k.shape, dtype=q.dtype, device=dev)
+    _rows(dev, (("dq_out", dq_out, q.shape), ("dk_out", dk_out, k.shape), ("dq", dq, q.shape), ("dk", dk, k.shape)), q.dtype)
+    d.qo_stride, d.ko_stride = dq_out.stride()[:2], dk_out.stride()[:2]
+    d.dq_stride, d.dk_stride = dq.stride()[:2], dk.stride()[:2]
+    dw = torch.empty((2, (D + 3) // 4 * 4), dtype=torch.float32, device=dev)
+    dqw, dkw = dw[0, :D], dw[1, :D]
+    ws, nws = _workspace(workspace)
+    _check(_lib.ssd_qk_norm_rope_bwd(q.data_ptr(), k.data_ptr(), _addr(q_weight), _addr(k_weight), cos.data_ptr(),
+                                     sin.data_ptr(), positions.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(),
+                                     dq.data_ptr(), dk.data_ptr(), dqw.data_ptr(), dkw.data_ptr(), ws, nws, d,
+                                     _stream_ptr(dev, stream)), "ssd_qk_norm_rope_bwd")
+    return dict(dq=dq, dk=dk, dq_weight=dqw, dk_weight=dkw)
+
+
+def qk_norm_rope_bwd_workspace_size(ntokens, headdim) -> int:
+    """Bytes of scratch ``qk_norm_rope_bwd`` needs."""
+    d = SsdQkDims(ntokens, 0, 0, 1, 1, headdim, 0, 0, DTYPE_BF16, 0, 0.0)
+    n = ctypes.c_uint64(0)
+    _check(_lib.ssd_qk_norm_rope_bwd_workspace_size(ctypes.byref(d), ctypes.byref(n)), "ssd_qk_norm_rope_bwd_workspace_size")
+    return int(n.value)
+
+
+def _attn_dims(q, k_cache, v_cache, block_table, scale, window):
+    if q.dim() != 3 or not q.is_cuda:
+        raise ValueError("q must be a [rows, heads, D] CUDA tensor")
+    if q.dtype not in _DTYPES:
+        raise SsdError(9, "q must be bf16 or fp32")
+    n, H, D = q.shape
+    dev = q.device
+    _rows(dev, (("q", q, (n, H, D)),), q.dtype)
+    _cache_args(dev, q.dtype, k_cache, v_cache, k_cache.shape[2], D)
+    if block_table.dtype != torch.int32 or block_table.device != dev or block_table.dim() != 2 or \
+            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError(f"block_table must be a [requests, max_pages] int32 tensor on {dev} with contiguous rows")
+    return SsdAttnDims(n, block_table.shape[0], k_cache.shape[0], H, k_cache.shape[2], D, k_cache.shape[1],
+                       block_table.shape[1], window, _DTYPES[q.dtype], 0, D ** -0.5 if scale is None else scale, 0,
+                       q.stride()[:2], q.stride()[:2], k_cache.stride()[:3], v_cache.stride()[:3], block_table.stride(0))
+
+
+def paged_attn_fwd(q, k_cache, v_cache, block_table, positions, start=None, *, scale=None, window=0, out=None, lse=None,
+                   return_lse=True, workspace=None, stream=None):
+    """Attention of new tokens over a paged key-value cache (``ssd_paged_attn_fwd``).  Returns ``(out, lse)``.
+
+    ``q [rows,H,D]``; ``k_cache, v_cache [npages, page_size, Hkv, D]`` (any strides, contiguous last axis; H a multiple
+    of Hkv); ``block_table [R, max_pages]`` int32; ``positions [rows]`` int32: each row sees its request's cached
+    positions up to its own (the last ``window`` of them, if given).  Without ``start`` row i is request i's one new
+    token; with ``start [R+1]`` int32 request r has the rows ``start[r] .. start[r+1]-1``, as :func:`paged_plan` gives
+    them.  Rows that see nothing get 0 (lse -inf).  ``scale`` defaults to D^-1/2.  ``out [rows,H,D]`` is in q's dtype,
+    ``lse [rows,H]`` fp32.
+    """
+    d = _attn_dims(q, k_cache, v_cache, block_table, scale, window)
+    dev, n, H = q.device, q.shape[0], q.shape[1]
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    if lse is None and return_lse:
+        lse = torch.empty((n, H), dtype=torch.float32, device=dev)
+    _rows(dev, (("out", out, q.shape),), q.dtype)
+    if lse is not None and (lse.dtype != torch.float32 or lse.device != dev or lse.shape != (n, H) or not lse.is_contiguous()):
+        raise ValueError(f"lse must be a contiguous [{n}, {H}] fp32 tensor on {dev}")
+    _vectors(dev, (("positions", positions, n), ("start", start, block_table.shape[0] + 1)), torch.int32)
+    d.o_stride = out.stride()[:2]
+    ws, nws = _workspace(workspace)
+    _check(_lib.ssd_paged_attn_fwd(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                                   positions.data_ptr(), _addr(start), out.data_ptr(), _addr(lse), ws, nws, d,
+                                   _stream_ptr(dev, stream)), "ssd_paged_attn_fwd")
+    return out, lse
+
+
+def paged_attn_workspace_size(q, k_cache, v_cache, block_table) -> int:
+    """Bytes of scratch ``paged_attn_fwd`` needs for such tensors on the current device."""
+    d = _attn_dims(q, k_cache, v_cache, block_table, 1.0, 0)
+    n = ctypes.c_uint64(0)
+    _check(_lib.ssd_paged_attn_workspace_size(ctypes.byref(d), ctypes.byref(n)), "ssd_paged_attn_workspace_size")
+    return int(n.value)
