@@ -1,7 +1,31 @@
 // ssd_paged_attn.cu -- attention of new tokens over a paged key-value cache.
 //
-// One block per query row and head: its warps take the visible tokens in turn
-// with a running maximum and sum each, and are joined at the end.
+// A tile is up to MR query rows that read the same keys: the query heads of one
+// key-value head for one or several consecutive new tokens of a request.  The
+// tile's visible positions are cut into units of 16 tokens.  All units of all
+// tiles and key-value heads, laid end to end, are dealt to the CTAs in equal
+// contiguous shares, whatever the requests' lengths; one CTA per resident slot
+// stays for the whole launch.  Within its share a CTA's warps take units in
+// turn; each warp streams its own units through a ring of shared-memory slots
+// (asynchronous 16-byte copies, K and V halves alternating, zero-filled where a
+// token is not to be seen) and keeps its own running maximum, sum and output
+// rows in registers, so no barrier stands between loads and arithmetic.  Loads
+// run ahead across tile boundaries.  At the end of a tile's part in a share the
+// warps' results are joined in shared memory; a tile that lies in one share
+// is finished there, one that is cut leaves a partial result (maximum, sum,
+// unnormalised rows) for the second launch, which joins the parts in order of
+// their CTAs.
+//
+// The running form: with s2 = scale log2(e) q.k, m = max s2 so far,
+// p = 2^(s2 - m), l = sum p, o = sum p v; when m grows by d, l and o are
+// scaled by 2^-d.  out = o / l, lse = ln 2 (m + log2 l).
+//
+// bf16: both products run on mma.sync m16n8k16 (scores: 16 query rows x 8
+// tokens; output: 16 rows x 8 elements over 16 tokens).  A score tile's
+// accumulator registers are, as they stand, the second product's A operand.
+// The weights p enter it as two bf16 terms, so that they carry 16 bits: one
+// bf16 term would add an error as large as the output's own rounding.
+// fp32: fp32 FMA (see Simt below).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -14,117 +38,1174 @@
 namespace ssd {
 namespace {
 
+constexpr int kUnit = 16;        // tokens per unit
 constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr float kLn2 = 0.69314718055994531f;
+constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ void from_f32(float &o, float v) { o = v; }
-__device__ __forceinline__ void from_f32(__nv_bfloat16 &o, float v) { o = __float2bfloat16_rn(v); }
+// exact floor(n / d) for 0 <= n < 2^31: (n * mul) >> sh
+struct FastDiv {
+    uint32_t mul, sh;
+};
+
+struct AttnParams {
+    AttnArgs a;
+    FastDiv page;
+    float *part_o;      // [grid][2][MR][D] partial rows
+    float *part_ml;     // [grid][2][MR][2] their maxima (base 2) and sums
+    int4 *desc;         // [grid] the cut tile that starts in a CTA's share: first row, tokens | item << 8, last CTA; or x = -1
+    int group;          // query heads per key-value head
+    int gh;             // query heads of a tile (group, or a part of it when it is larger than MR)
+    int nhb;            // head blocks per key-value head
+    int tok;            // most new tokens of a tile
+    int items;          // nkv * nhb: tiles of the same rows
+    int seg;            // 16-byte segments per row of K or V
+    int stride;         // bytes from row to row of a ring slot (an odd number of segments)
+    int same_page;      // a unit never crosses a page
+};
+
+__device__ __forceinline__ int div_page(const FastDiv &f, int n) { return (int)(((uint64_t)(uint32_t)n * f.mul) >> f.sh); }
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+// 16 bytes, or zeros when !on (nothing is read then, but the address must be valid all the same)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool on)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// ---- the walk over tiles, items and units ---------------------------------
+
+// One tile of query rows: nq tokens from row `row` of request `req`; the tokens
+// they see lie in [first, end), in `units` units from unit `ub` on.
+struct Tile {
+    int req, j, row, nq, rows_left;   // j: tile of the request; rows_left: the request's rows after this tile
+    int first, end, ub, units;
+};
+
+__device__ __forceinline__ void tile_extent(const AttnParams &p, Tile &t)
+{
+    const int limit = p.a.d.max_pages * p.a.d.page_size;
+    const int p0 = p.a.positions[t.row], p1 = t.nq > 1 ? p.a.positions[t.row + t.nq - 1] : p0;
+    t.end = p1 < 0 ? 0 : min(p1, limit - 1) + 1;
+    t.first = p.a.d.window > 0 ? max(0, p0 - p.a.d.window + 1) : 0;
+    t.first = min(t.first, t.end);
+    t.ub = t.first / kUnit;
+    t.units = max(1, (t.end + kUnit - 1) / kUnit - t.ub);   // (a tile that sees nothing still writes its rows)
+}
+
+// rows [s, e) of request r, clamped to the rows there are
+__device__ __forceinline__ void request_rows(const AttnParams &p, int r, int &s, int &e)
+{
+    const int n = (int)p.a.d.nrows;
+    s = min(max(p.a.start[r], 0), n);
+    e = min(max(p.a.start[r + 1], s), n);
+}
+
+__device__ __forceinline__ void set_tile(const AttnParams &p, Tile &t, int req, int j)
+{
+    t.req = req;
+    t.j = j;
+    if (p.a.start) {
+        int s, e;
+        request_rows(p, req, s, e);
+        t.row = s + j * p.tok;
+        t.nq = min(p.tok, e - t.row);
+        t.rows_left = e - t.row - t.nq;
+    } else {
+        t.row = req;
+        t.nq = 1;
+        t.rows_left = 0;
+    }
+    tile_extent(p, t);
+}
+
+// the next tile (there is one)
+__device__ __forceinline__ void next_tile(const AttnParams &p, Tile &t)
+{
+    if (t.rows_left > 0) {
+        set_tile(p, t, t.req, t.j + 1);
+        return;
+    }
+    int r = t.req + 1;
+    if (p.a.start) {
+        int s, e;
+        while (r < (int)p.a.d.nreq - 1) {
+            request_rows(p, r, s, e);
+            if (e > s)
+                break;
+            ++r;
+        }
+    }
+    set_tile(p, t, r, 0);
+}
+
+// A place in the CTA's share: a tile, an item (key-value head and head block)
+// of it, and the linear number of the item's first unit.
+struct Cursor {
+    Tile t;
+    int item;
+    long long lin;
+};
+
+__device__ __forceinline__ void next_item(const AttnParams &p, Cursor &c)
+{
+    c.lin += c.t.units;
+    if (++c.item == p.items) {
+        c.item = 0;
+        next_tile(p, c.t);
+    }
+}
+
+// ---- block scan for the schedule ------------------------------------------
+
+__device__ __forceinline__ long long block_exclusive(long long v, long long *total, long long *tmp)
+{
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    long long inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o)
+            inc += u;
+    }
+    __syncthreads();
+    if (lane == 31)
+        tmp[w] = inc;
+    __syncthreads();
+    long long before = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        if (i < w)
+            before += tmp[i];
+        all += tmp[i];
+    }
+    *total = all;
+    return before + inc - v;
+}
+
+struct Found {
+    int req, j;
+    long long lin;   // the linear unit where the tile's first item begins
+};
+
+// Where the CTA's share begins.  Every CTA sums all tiles' units (a contiguous
+// run of tiles per thread); the thread whose run holds unit u0 finds the tile.
+// `counts` (shared memory, nreq + 1 ints) is used when there is a start array.
+__device__ void locate(const AttnParams &p, int *counts, long long *tmp, Found *found, long long &total, long long &per,
+                       long long &u0)
+{
+    const int tid = threadIdx.x, nreq = (int)p.a.d.nreq;
+    long long ntiles = p.a.d.nrows;
+    if (p.a.start) {
+        const int run = (nreq + kThreads - 1) / kThreads, r0 = min(tid * run, nreq), r1 = min(r0 + run, nreq);
+        long long n = 0, all;
+        for (int r = r0; r < r1; ++r) {
+            int s, e;
+            request_rows(p, r, s, e);
+            n += (e - s + p.tok - 1) / p.tok;
+        }
+        long long at = block_exclusive(n, &all, tmp);
+        for (int r = r0; r < r1; ++r) {
+            int s, e;
+            request_rows(p, r, s, e);
+            counts[r] = (int)at;
+            at += (e - s + p.tok - 1) / p.tok;
+        }
+        if (tid == 0)
+            counts[nreq] = (int)all;
+        ntiles = all;
+        __syncthreads();
+    }
+    const long long run = (ntiles + kThreads - 1) / kThreads, t0 = min((long long)tid * run, ntiles), t1 = min(t0 + run, ntiles);
+    // the run's first tile
+    Found f{0, 0, 0};
+    if (t0 < t1) {
+        if (p.a.start) {
+            int lo = 0, hi = nreq;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (counts[mid] <= t0)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+            f.req = lo;
+            f.j = (int)(t0 - counts[lo]);
+        } else
+            f.req = (int)t0;
+    }
+    long long n = 0;
+    Tile t;
+    for (long long i = t0; i < t1; ++i) {
+        if (i == t0)
+            set_tile(p, t, f.req, f.j);
+        else
+            next_tile(p, t);
+        n += t.units;
+    }
+    long long sum;
+    const long long before = block_exclusive(n, &sum, tmp) * p.items;
+    total = sum * p.items;
+    per = max((long long)kWarps, (total + gridDim.x - 1) / gridDim.x);
+    u0 = (long long)blockIdx.x * per;
+    if (t0 < t1 && u0 >= before && u0 < before + n * p.items) {
+        long long lin = before;
+        for (long long i = t0; i < t1; ++i) {
+            if (i == t0)
+                set_tile(p, t, f.req, f.j);
+            else
+                next_tile(p, t);
+            const long long here = (long long)t.units * p.items;
+            if (u0 < lin + here) {
+                found->req = t.req;
+                found->j = t.j;
+                found->lin = lin;
+                break;
+            }
+            lin += here;
+        }
+    }
+    __syncthreads();
+}
+
+// ---- the loader -------------------------------------------------------------
+
+// Streams a warp's units into its ring: one step per half (K then V).
+struct Loader {
+    Cursor c;
+    int u;                 // the unit within the item (-1: none left)
+    long long u1;          // end of the share
+    int page;              // table entry read ahead for this lane's token
+    long long koff, voff;  // byte offsets of this lane's token (same_page: of the unit's first token)
+    uint32_t mask;         // the unit's tokens that are to be read
+};
+
+// the loader's next unit: every kWarps-th of the share
+__device__ __forceinline__ void loader_skip(const AttnParams &p, Loader &l, int by)
+{
+    l.u += by;
+    while (true) {
+        if (l.c.lin + l.u >= l.u1) {
+            l.u = -1;
+            return;
+        }
+        if (l.u < l.c.t.units)
+            return;
+        l.u -= l.c.t.units;
+        next_item(p, l.c);
+    }
+}
+
+__device__ __forceinline__ void loader_fetch_page(const AttnParams &p, Loader &l, int lane)
+{
+    if (l.u < 0)
+        return;
+    const int tok = (l.c.t.ub + l.u) * kUnit + (p.same_page ? 0 : (lane & 15));
+    l.page = -1;
+    if (tok < l.c.t.end && tok >= 0)   // (same_page: the unit's first token is below end, its page holds them all)
+        l.page = __ldg(p.a.table + (long long)l.c.t.req * p.a.d.table_stride + div_page(p.page, tok));
+}
 
 template <typename T>
-__global__ void __launch_bounds__(kWarps * 32) ssd_paged_attn_simple_kernel(const __grid_constant__ AttnArgs a)
+__device__ __forceinline__ void loader_offsets(const AttnParams &p, Loader &l, int lane)
 {
-    __shared__ float sm[kWarps], sl[kWarps], so[kWarps][256];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, D = a.d.headdim;
-    const long long row = blockIdx.x;
-    const int h = blockIdx.y, kvh = h / (a.d.nheads / a.d.nkv);
-    long long req = row;
-    int pos = a.positions[row];
-    if (a.start) {   // the last request that starts at or before the row
-        int lo = -1, hi = (int)a.d.nreq;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (a.start[mid] <= row)
-                lo = mid;
-            else
-                hi = mid;
+    const int tok0 = (l.c.t.ub + l.u) * kUnit, tok = tok0 + (lane & 15);
+    const bool ok = tok >= l.c.t.first && tok < l.c.t.end && l.page >= 0 && l.page < (int)p.a.d.npages;
+    l.mask = __ballot_sync(0xffffffffu, ok) & 0xffffu;
+    const int at = p.same_page ? tok0 : tok;
+    const int off = at - div_page(p.page, at) * p.a.d.page_size;
+    const int kvh = l.c.item / p.nhb;
+    const long long pg = ok || (p.same_page && l.mask) ? l.page : 0;
+    l.koff = (pg * p.a.d.kc_stride[0] + off * p.a.d.kc_stride[1] + kvh * p.a.d.kc_stride[2]) * (long long)sizeof(T);
+    l.voff = (pg * p.a.d.vc_stride[0] + off * p.a.d.vc_stride[1] + kvh * p.a.d.vc_stride[2]) * (long long)sizeof(T);
+    if (!ok && !p.same_page)
+        l.koff = l.voff = 0;   // (not read)
+    if (p.same_page && !l.mask)
+        l.koff = l.voff = 0;
+}
+
+// copies one half (16 tokens of K or V) into a ring slot
+template <typename T, int DP>
+__device__ __forceinline__ void loader_copy(const AttnParams &p, const Loader &l, const void *base, long long off, long long tstride,
+                                            uint32_t slot, int lane)
+{
+    constexpr int kSegMax = DP * (int)sizeof(T) / 16;
+    const bool full = p.seg == kSegMax;   // the template's own size: constant shifts
+    const uint32_t inv = 65536u / (uint32_t)p.seg + 1;
+    const char *src = static_cast<const char *>(base);
+    const long long ts = tstride * (long long)sizeof(T);
+#pragma unroll
+    for (int i = 0; i < kSegMax / 2; ++i) {
+        const int idx = lane + 32 * i;
+        const int r = full ? idx / kSegMax : (int)((idx * inv) >> 16);
+        const int c = idx - r * p.seg;
+        const bool in = r < kUnit;
+        const bool on = in && ((l.mask >> r) & 1);
+        const long long o = p.same_page ? (on ? off + r * ts : 0) : __shfl_sync(0xffffffffu, off, r & 15);
+        if (in)
+            cp_async16(slot + r * p.stride + c * 16, on ? src + o + c * 16 : static_cast<const char *>(p.a.q), on);
+    }
+}
+
+// ---- the arithmetic: bf16 on mma.sync --------------------------------------
+
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// the rows a lane holds results of, and what each sees
+template <int NM, int DP>
+struct Mma {
+    using T = __nv_bfloat16;
+    static constexpr int MR = 16 * NM;
+    uint32_t q[NM][DP / 16][4];
+    float o[NM][DP / 8][4];
+    float s[NM][2][4];
+    float m[NM][2], l[NM][2];
+    int lo[NM][2], hi[NM][2];
+
+    __device__ __forceinline__ void begin(const AttnParams &p, const Tile &t, int item, int lane)
+    {
+        const int kvh = item / p.nhb, hb = item - kvh * p.nhb, D = p.a.d.headdim;
+        const int h0 = hb * p.gh, nh = min(p.gh, p.group - h0), rows = t.nq * nh;
+        const int limit = p.a.d.max_pages * p.a.d.page_size;
+#pragma unroll
+        for (int mt = 0; mt < NM; ++mt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int r = mt * 16 + x * 8 + (lane >> 2), rr = min(r, rows - 1), j = rr / nh, g = rr - j * nh;
+                const int pos = p.a.positions[t.row + j];
+                hi[mt][x] = pos < 0 ? 0 : min(pos, limit - 1) + 1;
+                lo[mt][x] = p.a.d.window > 0 ? max(0, pos - p.a.d.window + 1) : 0;
+                m[mt][x] = -INFINITY;
+                l[mt][x] = 0.f;
+                const T *src = static_cast<const T *>(p.a.q) + (long long)(t.row + j) * p.a.d.q_stride[0] +
+                               (long long)(kvh * p.group + h0 + g) * p.a.d.q_stride[1];
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const int c = 16 * k + 8 * y + 2 * (lane & 3);
+                        q[mt][k][x + 2 * y] = r < rows && c < D ? *reinterpret_cast<const uint32_t *>(src + c) : 0u;
+                    }
+            }
+#pragma unroll
+        for (int mt = 0; mt < NM; ++mt)
+#pragma unroll
+            for (int n = 0; n < DP / 8; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    o[mt][n][i] = 0.f;
+    }
+
+    // scores of a unit's tokens and their weights; mask: the tokens read;
+    // [all0, all1): tokens that every row sees
+    __device__ __forceinline__ void scores(const AttnParams &p, uint32_t slot, uint32_t mask, int tok0, int all0, int all1, int lane)
+    {
+        const int D = p.a.d.headdim;
+#pragma unroll
+        for (int mt = 0; mt < NM; ++mt)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    s[mt][n][i] = 0.f;
+        // lanes 0-7, 8-15: tokens 0-7, first and second 16 bytes; 16-23, 24-31: tokens 8-15
+        const uint32_t a = slot + ((lane & 7) + ((lane >> 4) << 3)) * p.stride + ((lane >> 3) & 1) * 16;
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) {
+            if (16 * k < D) {
+                uint32_t b[4];
+                ldsm4(a + k * 32, b);
+#pragma unroll
+                for (int mt = 0; mt < NM; ++mt) {
+                    mma16816(s[mt][0], q[mt][k], b[0], b[1]);
+                    mma16816(s[mt][1], q[mt][k], b[2], b[3]);
+                }
+            }
         }
-        req = lo;
-        if (lo < 0 || row >= a.start[a.d.nreq])
-            pos = -1;
-    }
-    const int limit = a.d.max_pages * a.d.page_size;
-    const int end = pos < 0 ? 0 : min(pos, limit - 1) + 1;
-    const int first = a.d.window > 0 ? max(0, pos - a.d.window + 1) : 0;
-    const T *q = static_cast<const T *>(a.q) + row * a.d.q_stride[0] + (long long)h * a.d.q_stride[1];
-    float qv[8], o[8], m = -INFINITY, l = 0.f;
+        const float f = p.a.d.scale * kLog2e;
+        const bool masked = mask != 0xffffu || tok0 < all0 || tok0 + kUnit > all1;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int d = lane + 32 * i;
-        qv[i] = d < D ? to_f32(q[d]) : 0.f;
-        o[i] = 0.f;
-    }
-    for (int t = first + w; t < end; t += kWarps) {
-        const int p = t / a.d.page_size, off = t - p * a.d.page_size;
-        const long long page = a.table[req * a.d.table_stride + p];
-        if (page < 0 || page >= a.d.npages)
-            continue;
-        const T *k = static_cast<const T *>(a.kc) + page * a.d.kc_stride[0] + off * a.d.kc_stride[1] + kvh * a.d.kc_stride[2];
-        const T *v = static_cast<const T *>(a.vc) + page * a.d.vc_stride[0] + off * a.d.vc_stride[1] + kvh * a.d.vc_stride[2];
-        float s = 0.f;
+        for (int mt = 0; mt < NM; ++mt)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int d = lane + 32 * i;
-            if (d < D)
-                s += qv[i] * to_f32(k[d]);
+            for (int x = 0; x < 2; ++x) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float &v = s[mt][n][2 * x + i];
+                        v *= f;
+                        if (masked) {
+                            const int tt = 8 * n + 2 * (lane & 3) + i, tok = tok0 + tt;
+                            if (!((mask >> tt) & 1) || tok < lo[mt][x] || tok >= hi[mt][x])
+                                v = -INFINITY;
+                        }
+                        top = fmaxf(top, v);
+                    }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const float mn = fmaxf(m[mt][x], top), base = mn == -INFINITY ? 0.f : mn;
+                const float keep = exp2_fast(m[mt][x] - base);
+                m[mt][x] = mn;
+                float sum = 0.f;
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float &v = s[mt][n][2 * x + i];
+                        v = exp2_fast(v - base);
+                        sum += v;
+                    }
+                l[mt][x] = l[mt][x] * keep + sum;
+                if (__any_sync(0xffffffffu, keep != 1.f)) {
+#pragma unroll
+                    for (int n = 0; n < DP / 8; ++n) {
+                        o[mt][n][2 * x] *= keep;
+                        o[mt][n][2 * x + 1] *= keep;
+                    }
+                }
+            }
+    }
+
+    // Tokens that some rows of the tile see and others do not are added row by
+    // row, to those that see them, and then left out of the product: there a
+    // weight 0 times an infinity or NaN of theirs would reach every row.
+    __device__ __forceinline__ void partial_tokens(const AttnParams &p, uint32_t slot, char *slot_ptr, uint32_t part, int tok0, int lane)
+    {
+        // (unrolled over the tokens: a running token number would index the
+        // score registers at run time and put them in local memory)
+#pragma unroll
+        for (int tt = 0; tt < kUnit; ++tt) {
+            if (!((part >> tt) & 1))
+                continue;
+            const uint32_t row = slot + tt * p.stride;
+            float wgt[NM][2];
+#pragma unroll
+            for (int mt = 0; mt < NM; ++mt)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    float &own = s[mt][tt >> 3][2 * x + (tt & 1)];
+                    const bool sees = tok0 + tt >= lo[mt][x] && tok0 + tt < hi[mt][x];
+                    wgt[mt][x] = __shfl_sync(0xffffffffu, own, (lane & ~3) | ((tt & 7) >> 1));
+                    if (!sees)
+                        wgt[mt][x] = -1.f;
+                    if ((lane & 3) == ((tt & 7) >> 1))
+                        own = 0.f;
+                }
+#pragma unroll
+            for (int n = 0; n < DP / 8; ++n) {
+                if (8 * n < p.a.d.headdim) {
+                    uint32_t v;
+                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(row + 16 * n + 4 * (lane & 3)) : "memory");
+#pragma unroll
+                    for (int mt = 0; mt < NM; ++mt)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+                            if (!(wgt[mt][x] < 0.f)) {
+                                o[mt][n][2 * x] += wgt[mt][x] * __uint_as_float(v << 16);
+                                o[mt][n][2 * x + 1] += wgt[mt][x] * __uint_as_float(v & 0xffff0000u);
+                            }
+                }
+            }
+            __syncwarp();
+            for (int c = lane; c < p.seg; c += 32)
+                *reinterpret_cast<uint4 *>(slot_ptr + tt * p.stride + c * 16) = make_uint4(0, 0, 0, 0);
         }
-#pragma unroll
-        for (int x = 16; x >= 1; x >>= 1)
-            s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= a.d.scale;
-        const float mn = fmaxf(m, s), base = mn == -INFINITY ? 0.f : mn;
-        const float keep = expf(m - base), e = expf(s - base);
-        l = l * keep + e;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int d = lane + 32 * i;
-            if (d < D)
-                o[i] = o[i] * keep + e * to_f32(v[d]);
+        __syncwarp();
+    }
+
+    __device__ __forceinline__ void values(const AttnParams &p, uint32_t slot, char *slot_ptr, uint32_t mask, int tok0, int all0,
+                                           int all1, int lane)
+    {
+        const int D = p.a.d.headdim;
+        if (tok0 < all0 || tok0 + kUnit > all1) {
+            // bit tt: every row sees token tok0 + tt
+            const int a0 = min(max(all0 - tok0, 0), kUnit), a1 = min(max(all1 - tok0, 0), kUnit);
+            const uint32_t all = a1 > a0 ? (0xffffu >> (16 - a1)) & (0xffffu << a0) : 0u;
+            const uint32_t part = mask & ~all;
+            if (part)
+                partial_tokens(p, slot, slot_ptr, part, tok0, lane);
         }
-        m = mn;
-    }
-    if (lane == 0) {
-        sm[w] = m;
-        sl[w] = l;
-    }
+        uint32_t hi4[NM][4], lo4[NM][4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        so[w][lane + 32 * i] = o[i];
+        for (int mt = 0; mt < NM; ++mt)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float a = s[mt][n][2 * x], b = s[mt][n][2 * x + 1];
+                    const uint32_t h = pack_bf16(a, b);
+                    hi4[mt][2 * n + x] = h;
+                    lo4[mt][2 * n + x] = pack_bf16(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xffff0000u));
+                }
+        // lanes 0-7, 8-15: tokens 0-7, 8-15 of the first 16 bytes; 16-31: of the second
+        const uint32_t a = slot + ((lane & 7) + (((lane >> 3) & 1) << 3)) * p.stride + (lane >> 4) * 16;
+#pragma unroll
+        for (int n = 0; n < DP / 16; ++n) {
+            if (16 * n < D) {
+                uint32_t b[4];
+                ldsm4t(a + n * 32, b);
+#pragma unroll
+                for (int mt = 0; mt < NM; ++mt) {
+                    mma16816(o[mt][2 * n], hi4[mt], b[0], b[1]);
+                    mma16816(o[mt][2 * n], lo4[mt], b[0], b[1]);
+                    mma16816(o[mt][2 * n + 1], hi4[mt], b[2], b[3]);
+                    mma16816(o[mt][2 * n + 1], lo4[mt], b[2], b[3]);
+                }
+            }
+        }
+    }
+
+    // the sums over the four lanes of a row, and the rows' maxima and sums to shared memory
+    __device__ __forceinline__ void end(float *ml, int lane)
+    {
+#pragma unroll
+        for (int mt = 0; mt < NM; ++mt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                l[mt][x] += __shfl_xor_sync(0xffffffffu, l[mt][x], 1);
+                l[mt][x] += __shfl_xor_sync(0xffffffffu, l[mt][x], 2);
+                if ((lane & 3) == 0) {
+                    const int r = mt * 16 + x * 8 + (lane >> 2);
+                    ml[2 * r] = m[mt][x];
+                    ml[2 * r + 1] = l[mt][x];
+                }
+            }
+    }
+    // rows scaled to the joint maximum `base[r]`, written to or added to buf [MR][ds]
+    template <bool ADD>
+    __device__ __forceinline__ void put(const AttnParams &p, const float *base, float *buf, int ds, int rows, int lane)
+    {
+#pragma unroll
+        for (int mt = 0; mt < NM; ++mt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int r = mt * 16 + x * 8 + (lane >> 2);
+                if (r < rows) {
+                    const float f = exp2_fast(m[mt][x] - base[r]);
+#pragma unroll
+                    for (int n = 0; n < DP / 8; ++n) {
+                        const int c = 8 * n + 2 * (lane & 3);
+                        if (8 * n < p.a.d.headdim) {
+                            float2 *at = reinterpret_cast<float2 *>(buf + r * ds + c);
+                            float2 v = make_float2(o[mt][n][2 * x] * f, o[mt][n][2 * x + 1] * f);
+                            if (ADD) {
+                                const float2 u = *at;
+                                v.x += u.x;
+                                v.y += u.y;
+                            }
+                            *at = v;
+                        }
+                    }
+                }
+            }
+    }
+};
+
+// ---- the arithmetic: fp32 ---------------------------------------------------
+
+// Scores: lane = token (16) and half of the head's elements (2), the query rows
+// read from shared memory (the same address for all tokens: a broadcast), one
+// shuffle to add the halves.  Output: lane = elements 4 lane .. (+ 128), the
+// weights read back from shared memory by token.
+template <int MRows, int DP>
+struct Simt {
+    using T = float;
+    static constexpr int MR = MRows;
+    static constexpr int NV = (DP + 127) / 128;   // float4 of the output per lane and row
+    float o[MR][NV][4];
+    float m[MR], l[MR];
+    int lo[MR], hi[MR];
+    float *qs, *ps;   // the CTA's query rows [MR][DP], this warp's weights [MR][16]
+
+    __device__ __forceinline__ void begin(const AttnParams &p, const Tile &t, int item, int lane)
+    {
+        const int kvh = item / p.nhb, hb = item - kvh * p.nhb, D = p.a.d.headdim;
+        const int h0 = hb * p.gh, nh = min(p.gh, p.group - h0), rows = t.nq * nh;
+        const int limit = p.a.d.max_pages * p.a.d.page_size;
+#pragma unroll
+        for (int r = 0; r < MR; ++r) {
+            const int rr = min(r, rows - 1), j = rr / nh, g = rr - j * nh;
+            const int pos = p.a.positions[t.row + j];
+            hi[r] = pos < 0 ? 0 : min(pos, limit - 1) + 1;
+            lo[r] = p.a.d.window > 0 ? max(0, pos - p.a.d.window + 1) : 0;
+            m[r] = -INFINITY;
+            l[r] = 0.f;
+            const float *src = static_cast<const float *>(p.a.q) + (long long)(t.row + j) * p.a.d.q_stride[0] +
+                               (long long)(kvh * p.group + h0 + g) * p.a.d.q_stride[1];
+            if (r % kWarps == (int)(threadIdx.x >> 5))
+                for (int c = 4 * lane; c < DP; c += 128)
+                    *reinterpret_cast<float4 *>(qs + r * DP + c) =
+                        r < rows && c < D ? *reinterpret_cast<const float4 *>(src + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int n = 0; n < NV; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    o[r][n][i] = 0.f;
+        }
+        __syncthreads();   // (each warp has loaded some of the rows)
+    }
+
+    __device__ __forceinline__ void scores(const AttnParams &p, const char *slot, uint32_t mask, int tok0, int all0, int all1, int lane)
+    {
+        const int tt = lane & 15, half = lane >> 4, D = p.a.d.headdim;
+        const float4 *k = reinterpret_cast<const float4 *>(slot + tt * p.stride);
+        float acc[MR];
+#pragma unroll
+        for (int r = 0; r < MR; ++r)
+            acc[r] = 0.f;
+        // the halves take float4s in turn: 2c + half
+        for (int c = half; c < D / 4; c += 2) {
+            const float4 kv = k[c];
+#pragma unroll
+            for (int r = 0; r < MR; ++r) {
+                const float4 qv = *reinterpret_cast<const float4 *>(qs + r * DP + 4 * c);
+                acc[r] += qv.x * kv.x;
+                acc[r] += qv.y * kv.y;
+                acc[r] += qv.z * kv.z;
+                acc[r] += qv.w * kv.w;
+            }
+        }
+        const float f = p.a.d.scale * kLog2e;
+        const bool masked = mask != 0xffffu || tok0 < all0 || tok0 + kUnit > all1;
+#pragma unroll
+        for (int r = 0; r < MR; ++r) {
+            float v = (acc[r] + __shfl_xor_sync(0xffffffffu, acc[r], 16)) * f;
+            if (masked && (!((mask >> tt) & 1) || tok0 + tt < lo[r] || tok0 + tt >= hi[r]))
+                v = -INFINITY;
+            float top = v;
+#pragma unroll
+            for (int x = 8; x >= 1; x >>= 1)
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+            const float mn = fmaxf(m[r], top), base = mn == -INFINITY ? 0.f : mn;
+            const float keep = exp2_fast(m[r] - base), e = exp2_fast(v - base);
+            m[r] = mn;
+            l[r] = l[r] * keep + (half == 0 ? e : 0.f);   // summed over the lanes at the end
+            if (half == 0)
+                ps[r * 16 + tt] = e;
+            if (keep != 1.f) {
+#pragma unroll
+                for (int n = 0; n < NV; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        o[r][n][i] *= keep;
+            }
+        }
+        __syncwarp();
+    }
+
+    __device__ __forceinline__ void values(const AttnParams &p, const char *slot, uint32_t mask, int tok0, int all0, int all1, int lane)
+    {
+        // tokens not read are zero in the slot; one that a row does not see is skipped for it
+        const bool ragged = tok0 < all0 || tok0 + kUnit > all1;
+#pragma unroll 4
+        for (int tt = 0; tt < kUnit; ++tt) {
+            float4 v[NV];
+#pragma unroll
+            for (int n = 0; n < NV; ++n) {
+                const int c = 4 * lane + 128 * n;
+                v[n] = c < p.a.d.headdim ? *reinterpret_cast<const float4 *>(slot + tt * p.stride + 4 * c)
+                                         : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int r = 0; r < MR; ++r) {
+                if (ragged && (tok0 + tt < lo[r] || tok0 + tt >= hi[r]))
+                    continue;
+                const float w = ps[r * 16 + tt];
+#pragma unroll
+                for (int n = 0; n < NV; ++n) {
+                    o[r][n][0] += w * v[n].x;
+                    o[r][n][1] += w * v[n].y;
+                    o[r][n][2] += w * v[n].z;
+                    o[r][n][3] += w * v[n].w;
+                }
+            }
+        }
+        __syncwarp();
+    }
+
+    __device__ __forceinline__ void end(float *ml, int lane)
+    {
+#pragma unroll
+        for (int r = 0; r < MR; ++r) {
+#pragma unroll
+            for (int x = 16; x >= 1; x >>= 1)
+                l[r] += __shfl_xor_sync(0xffffffffu, l[r], x);
+            if (lane == 0) {
+                ml[2 * r] = m[r];
+                ml[2 * r + 1] = l[r];
+            }
+        }
+    }
+    template <bool ADD>
+    __device__ __forceinline__ void put(const AttnParams &p, const float *base, float *buf, int ds, int rows, int lane)
+    {
+#pragma unroll
+        for (int r = 0; r < MR; ++r) {
+            if (r < rows) {
+                const float f = exp2_fast(m[r] - base[r]);
+#pragma unroll
+                for (int n = 0; n < NV; ++n) {
+                    const int c = 4 * lane + 128 * n;
+                    if (c < p.a.d.headdim) {
+                        float4 *at = reinterpret_cast<float4 *>(buf + r * ds + c);
+                        float4 v = make_float4(o[r][n][0] * f, o[r][n][1] * f, o[r][n][2] * f, o[r][n][3] * f);
+                        if (ADD) {
+                            const float4 u = *at;
+                            v.x += u.x;
+                            v.y += u.y;
+                            v.z += u.z;
+                            v.w += u.w;
+                        }
+                        *at = v;
+                    }
+                }
+            }
+        }
+    }
+};
+
+__device__ __forceinline__ void store4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 v)
+{
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+}
+
+// shared memory: the warps' rings, two join buffers, (fp32) the warps' query
+// rows and weights -- all of whole 16-byte segments -- then maxima, sums and
+// slot masks
+template <typename M, int DP, int NH>
+struct Layout {
+    static constexpr int kMask = kWarps * NH;
+    static __host__ __device__ int join_stride(int D) { return D + 8; }
+    static __host__ __device__ int ring_bytes(int stride) { return kWarps * NH * kUnit * stride; }
+    static __host__ __device__ int join_bytes(int D) { return 2 * M::MR * join_stride(D) * 4; }
+    static constexpr int kSmall = (kWarps * M::MR * 2 + M::MR * 2 + kMask) * 4;
+    static constexpr bool kSimt = sizeof(typename M::T) == 4;
+    static constexpr int kQuery = kSimt ? (M::MR * DP + kWarps * M::MR * 16) * 4 : 0;
+    static __host__ __device__ int total(int D, int stride) { return ring_bytes(stride) + join_bytes(D) + kSmall + kQuery; }
+};
+
+template <int R, int DP>
+__device__ __forceinline__ void bind(Simt<R, DP> &m, float *q, float *s) { m.qs = q; m.ps = s; }
+template <int NM, int DP>
+__device__ __forceinline__ void bind(Mma<NM, DP> &, float *, float *) {}
+
+template <int R, int DP>
+__device__ __forceinline__ void do_scores(Simt<R, DP> &m, const AttnParams &p, char *slot, uint32_t mask, int tok0, int a0, int a1, int lane)
+{
+    m.scores(p, slot, mask, tok0, a0, a1, lane);
+}
+template <int NM, int DP>
+__device__ __forceinline__ void do_scores(Mma<NM, DP> &m, const AttnParams &p, char *slot, uint32_t mask, int tok0, int a0, int a1, int lane)
+{
+    m.scores(p, smem_addr(slot), mask, tok0, a0, a1, lane);
+}
+template <int R, int DP>
+__device__ __forceinline__ void do_values(Simt<R, DP> &m, const AttnParams &p, char *slot, uint32_t mask, int tok0, int a0, int a1, int lane)
+{
+    m.values(p, slot, mask, tok0, a0, a1, lane);
+}
+template <int NM, int DP>
+__device__ __forceinline__ void do_values(Mma<NM, DP> &m, const AttnParams &p, char *slot, uint32_t mask, int tok0, int a0, int a1, int lane)
+{
+    m.values(p, smem_addr(slot), slot, mask, tok0, a0, a1, lane);
+}
+
+template <typename M, int DP, int NH>
+__global__ void __launch_bounds__(kThreads) ssd_paged_attn_kernel(const __grid_constant__ AttnParams p)
+{
+    using T = typename M::T;
+    using L = Layout<M, DP, NH>;
+    extern __shared__ __align__(16) char smem[];
+    __shared__ Found found;
+    __shared__ long long tmp[kWarps];
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, D = p.a.d.headdim;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    long long total, per, u0;
+    locate(p, reinterpret_cast<int *>(smem), tmp, &found, total, per, u0);
+    // padding rows see nothing
+    if (p.a.start) {
+        const long long r0 = min((long long)max(p.a.start[p.a.d.nreq], 0), (long long)p.a.d.nrows);
+        for (long long i = r0 * p.a.d.nheads + blockIdx.x; i < p.a.d.nrows * p.a.d.nheads; i += gridDim.x) {
+            const long long row = i / p.a.d.nheads, h = i - row * p.a.d.nheads;
+            T *out = static_cast<T *>(p.a.out) + row * p.a.d.o_stride[0] + h * p.a.d.o_stride[1];
+            for (int c = 4 * tid; c < D; c += 4 * kThreads)
+                store4(out + c, make_float4(0.f, 0.f, 0.f, 0.f));
+            if (p.a.lse && tid == 0)
+                p.a.lse[i] = -INFINITY;
+        }
+    }
+    if (tid == 0)
+        p.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (u0 >= total)
+        return;
+    const long long u1 = min(u0 + per, total);
+    char *ring = smem + (size_t)w * NH * kUnit * p.stride;
+    const int slot_bytes = kUnit * p.stride;
+    float *join = reinterpret_cast<float *>(smem + L::ring_bytes(p.stride));
+    float *qs = join + L::join_bytes(D) / 4;                 // (16-byte accesses up to here)
+    float *ml = join + (L::join_bytes(D) + L::kQuery) / 4;   // [kWarps][MR][2]
+    float *joint = ml + kWarps * M::MR * 2;                  // [MR] maxima, [MR] sums
+    uint32_t *masks = reinterpret_cast<uint32_t *>(joint + M::MR * 2) + w * NH;
+    const int ds = L::join_stride(D);
+    __syncthreads();   // (the schedule's use of the ring's memory is over)
+    // segments past the head's elements are read by the products: zero once
+    for (int i = tid; i < kWarps * NH * kUnit; i += kThreads)
+        for (int c = p.seg; c * 16 < p.stride; ++c)
+            *reinterpret_cast<uint4 *>(smem + (size_t)i * p.stride + c * 16) = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    float mm = -INFINITY, ll = 0.f;
-    for (int i = 0; i < kWarps; ++i)
-        mm = fmaxf(mm, sm[i]);
-    const float base = mm == -INFINITY ? 0.f : mm;
-    for (int i = 0; i < kWarps; ++i)
-        ll += sl[i] * expf(sm[i] - base);
-    const float inv = ll == 0.f ? 0.f : 1.f / ll;
-    T *out = static_cast<T *>(a.out) + row * a.d.o_stride[0] + (long long)h * a.d.o_stride[1];
-    for (int d = threadIdx.x; d < D; d += kWarps * 32) {
-        float v = 0.f;
-        for (int i = 0; i < kWarps; ++i)
-            v += so[i][d] * expf(sm[i] - base);
-        from_f32(out[d], v * inv);
+
+    Cursor cur;
+    set_tile(p, cur.t, found.req, found.j);
+    cur.item = (int)((u0 - found.lin) / cur.t.units);
+    cur.lin = found.lin + (long long)cur.item * cur.t.units;
+
+    Loader ld;
+    ld.c = cur;
+    ld.u1 = u1;
+    ld.u = (int)(u0 - cur.lin);
+    ld.page = -1;
+    loader_skip(p, ld, w);
+    loader_fetch_page(p, ld, lane);
+    int head = 0;        // ring slot of the next half to load
+    bool vhalf = false;  // the next half to load is V
+    auto load_half = [&]() {
+        if (ld.u >= 0) {
+            if (!vhalf) {
+                loader_offsets<T>(p, ld, lane);
+                if (lane == 0)
+                    masks[head] = ld.mask;
+                loader_copy<T, DP>(p, ld, p.a.kc, ld.koff, p.a.d.kc_stride[1], smem_addr(ring + head * slot_bytes), lane);
+            } else {
+                loader_copy<T, DP>(p, ld, p.a.vc, ld.voff, p.a.d.vc_stride[1], smem_addr(ring + head * slot_bytes), lane);
+                loader_skip(p, ld, kWarps);
+                loader_fetch_page(p, ld, lane);
+            }
+            vhalf = !vhalf;
+            head = head + 1 == NH ? 0 : head + 1;
+        }
+        cp_commit();
+    };
+#pragma unroll 1
+    for (int i = 0; i < NH - 1; ++i)
+        load_half();
+
+    M math;
+    bind(math, qs, qs + (size_t)M::MR * DP + w * M::MR * 16);
+    int tail = 0;
+    int u = (int)(u0 - cur.lin);   // first unit of the share in this item
+    while (true) {
+        const int ue = (int)min((long long)cur.t.units, u1 - cur.lin);   // the share's units of the item: [u, ue)
+        // tokens that every row of the tile sees: from the last row's first to the first row's last
+        int all0, all1;
+        {
+            const int limit = p.a.d.max_pages * p.a.d.page_size;
+            const int p0 = p.a.positions[cur.t.row], p1 = p.a.positions[cur.t.row + cur.t.nq - 1];
+            all1 = p0 < 0 ? 0 : min(p0, limit - 1) + 1;
+            all0 = p.a.d.window > 0 ? max(0, p1 - p.a.d.window + 1) : 0;
+        }
+        math.begin(p, cur.t, cur.item, lane);
+        const int kvh = cur.item / p.nhb, hb = cur.item - kvh * p.nhb;
+        const int h0 = kvh * p.group + hb * p.gh, nh = min(p.gh, p.group - hb * p.gh), rows = cur.t.nq * nh;
+        // this warp's units: those whose number in the share is w modulo the warps
+        const int skip = (w - (int)((cur.lin + u - u0) % kWarps) + kWarps) % kWarps;
+        for (int x = u + skip; x < ue; x += kWarps) {
+            const int tok0 = (cur.t.ub + x) * kUnit;
+            cp_wait<NH - 2>();
+            __syncwarp();
+            load_half();
+            const uint32_t mask = masks[tail];
+            do_scores(math, p, ring + tail * slot_bytes, mask, tok0, all0, all1, lane);
+            tail = tail + 1 == NH ? 0 : tail + 1;
+            cp_wait<NH - 2>();
+            __syncwarp();
+            load_half();
+            do_values(math, p, ring + tail * slot_bytes, mask, tok0, all0, all1, lane);
+            tail = tail + 1 == NH ? 0 : tail + 1;
+        }
+        // join the warps
+        math.end(ml + w * M::MR * 2, lane);
+        __syncthreads();
+        if (tid < M::MR) {
+            float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i)
+                mm = fmaxf(mm, ml[(i * M::MR + tid) * 2]);
+            const float base = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i)
+                ll += ml[(i * M::MR + tid) * 2 + 1] * exp2_fast(ml[(i * M::MR + tid) * 2] - base);
+            joint[tid] = base;
+            joint[M::MR + tid] = ll;
+        }
+        __syncthreads();
+        float *buf = join + (w & 1) * M::MR * ds;
+        if (w >= 2)
+            math.template put<false>(p, joint, buf, ds, rows, lane);
+        __syncthreads();
+        if (w < 2)
+            math.template put<true>(p, joint, buf, ds, rows, lane);
+        __syncthreads();
+        const bool whole = u == 0 && ue == cur.t.units;
+        const int slot = u > 0 ? 0 : 1;   // a tile begun in an earlier share, or in this one
+        const int n4 = D / 4;
+        for (int i = tid; i < rows * n4; i += kThreads) {
+            const int r = i / n4, c = 4 * (i - r * n4);
+            const float4 x = *reinterpret_cast<const float4 *>(join + r * ds + c);
+            const float4 y = *reinterpret_cast<const float4 *>(join + (M::MR + r) * ds + c);
+            float4 v = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+            if (whole) {
+                const float ll = joint[M::MR + r], inv = ll == 0.f ? 0.f : 1.f / ll;
+                const int j = r / nh, g = r - j * nh;
+                v.x *= inv; v.y *= inv; v.z *= inv; v.w *= inv;
+                store4(static_cast<T *>(p.a.out) + (long long)(cur.t.row + j) * p.a.d.o_stride[0] +
+                           (long long)(h0 + g) * p.a.d.o_stride[1] + c, v);
+                if (c == 0 && p.a.lse)
+                    p.a.lse[(long long)(cur.t.row + j) * p.a.d.nheads + h0 + g] =
+                        ll == 0.f ? -INFINITY : kLn2 * (joint[r] + log2f(ll));
+            } else {
+                const size_t at = ((size_t)blockIdx.x * 2 + slot) * M::MR + r;
+                *reinterpret_cast<float4 *>(p.part_o + at * D + c) = v;
+                if (c == 0) {
+                    p.part_ml[2 * at] = joint[r];
+                    p.part_ml[2 * at + 1] = joint[M::MR + r];
+                }
+            }
+        }
+        if (!whole && slot == 1 && tid == 0)   // the cut tile's first part: where the others are
+            p.desc[blockIdx.x] = make_int4(cur.t.row, cur.t.nq, cur.item, (int)((cur.lin + cur.t.units - 1) / per));
+        if (cur.lin + ue >= u1)
+            break;
+        __syncthreads();   // (the join buffers are free again)
+        u = 0;
+        next_item(p, cur);
     }
-    if (a.lse && threadIdx.x == 0)
-        a.lse[row * a.d.nheads + h] = ll == 0.f ? -INFINITY : base + logf(ll);
+    cp_wait<0>();
+}
+
+// Joins the parts of the tile that starts in share blockIdx.x and goes on in
+// the next ones, row blockIdx.y of it: warps take parts in turn, lanes the
+// elements.
+template <typename T, int MR>
+__global__ void __launch_bounds__(128) ssd_paged_attn_join_kernel(const __grid_constant__ AttnParams p)
+{
+    __shared__ float sm[4][2];
+    __shared__ float so[4][256];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 d = p.desc[blockIdx.x];
+    if (d.x < 0)
+        return;
+    const int row = d.x, nq = d.y, item = d.z, c0 = blockIdx.x, c1 = d.w, r = blockIdx.y, D = p.a.d.headdim;
+    const int kvh = item / p.nhb, hb = item - kvh * p.nhb, nh = min(p.gh, p.group - hb * p.gh);
+    if (r >= nq * nh)
+        return;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    // part i lies in share c0 + i: slot 1 of the first, slot 0 of the others
+    auto part = [&](int i) { return ((size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * MR + r; };
+    const int n = c1 - c0 + 1;
+    float mm = -INFINITY;
+    for (int i = threadIdx.x; i < n; i += 128)
+        mm = fmaxf(mm, p.part_ml[2 * part(i) + 1] == 0.f ? -INFINITY : p.part_ml[2 * part(i)]);
+#pragma unroll
+    for (int x = 16; x >= 1; x >>= 1)
+        mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x));
+    if (lane == 0)
+        sm[w][0] = mm;
+    __syncthreads();
+    mm = fmaxf(fmaxf(sm[0][0], sm[1][0]), fmaxf(sm[2][0], sm[3][0]));
+    const float base = mm == -INFINITY ? 0.f : mm;
+    float ll = 0.f, o[2][4] = {};
+#pragma unroll 4
+    for (int i = w; i < n; i += 4) {
+        const size_t at = part(i);
+        const float lp = p.part_ml[2 * at + 1], f = lp == 0.f ? 0.f : exp2_fast(p.part_ml[2 * at] - base);
+        ll += lp * f;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int c = 4 * lane + 128 * k;
+            if (c < D) {
+                const float4 v = *reinterpret_cast<const float4 *>(p.part_o + at * D + c);
+                o[k][0] += f * v.x;
+                o[k][1] += f * v.y;
+                o[k][2] += f * v.z;
+                o[k][3] += f * v.w;
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            so[w][4 * lane + 128 * k + e] = o[k][e];
+    if (lane == 0)
+        sm[w][1] = ll;
+    __syncthreads();
+    ll = (sm[0][1] + sm[1][1]) + (sm[2][1] + sm[3][1]);
+    const float inv = ll == 0.f ? 0.f : 1.f / ll;
+    const int j = r / nh, h = kvh * p.group + hb * p.gh + (r - j * nh);
+    for (int c = 4 * threadIdx.x; c < D; c += 512) {
+        float4 v;
+        float *e = &v.x;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            e[k] = ((so[0][c + k] + so[1][c + k]) + (so[2][c + k] + so[3][c + k])) * inv;
+        store4(static_cast<T *>(p.a.out) + (long long)(row + j) * p.a.d.o_stride[0] + (long long)h * p.a.d.o_stride[1] + c, v);
+    }
+    if (p.a.lse && threadIdx.x == 0)
+        p.a.lse[(long long)(row + j) * p.a.d.nheads + h] = ll == 0.f ? -INFINITY : kLn2 * (base + log2f(ll));
+}
+
+// ---- host: variant, sizes, launch -------------------------------------------
+
+// How many query rows of a key-value head one request brings, as far as the
+// sizes tell: the variant's rows per tile follow it.
+long long rows_wanted(const ssd_attn_dims_t &d)
+{
+    const long long group = d.nheads / d.nkv;
+    const long long tok = d.nreq > 0 ? (d.nrows + d.nreq - 1) / d.nreq : 1;
+    return group * std::max<long long>(tok, 1);
+}
+
+int tile_rows(const ssd_attn_dims_t &d)
+{
+    const long long want = rows_wanted(d);
+    if (d.dtype == SSD_DTYPE_BF16)
+        return want > 16 && d.headdim <= 128 ? 32 : 16;
+    if (d.headdim > 128)
+        return want <= 2 ? 2 : 8;
+    return want <= 1 ? 1 : want <= 2 ? 2 : want <= 4 ? 4 : 8;
+}
+
+constexpr int kMaxCtas = 1024;   // workspace is sized for at most this many CTAs
+
+int sm_count()
+{
+    static int n[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+        return 152;
+    if (!n[dev] && cudaDeviceGetAttribute(&n[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 152;
+    return n[dev];
+}
+
+template <typename M, int DP, int NH>
+cudaError_t launch(AttnParams &p, void *workspace, cudaStream_t stream)
+{
+    using T = typename M::T;
+    const int D = p.a.d.headdim;
+    const int smem = std::max(Layout<M, DP, NH>::total(D, p.stride), p.a.start ? (int)(p.a.d.nreq + 1) * 4 : 0);
+    auto kernel = ssd_paged_attn_kernel<M, DP, NH>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess)
+        return e;
+    int per_sm = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, smem);
+    if (e != cudaSuccess)
+        return e;
+    const int grid = std::min(kMaxCtas, sm_count() * std::max(1, std::min(per_sm, 4)));
+    p.part_o = static_cast<float *>(workspace);
+    p.part_ml = p.part_o + (size_t)grid * 2 * M::MR * D;
+    p.desc = reinterpret_cast<int4 *>(p.part_ml + (size_t)grid * 2 * M::MR * 2);
+    kernel<<<grid, kThreads, smem, stream>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess)
+        return e;
+    note_launches(1);
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, p.tok * p.gh);
+    cfg.blockDim = dim3(128);
+    cfg.stream = stream;
+    cfg.attrs = pdl;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, ssd_paged_attn_join_kernel<T, M::MR>, p);
+    if (e == cudaSuccess)
+        note_launches(1);
+    return e;
 }
 
 }  // namespace
 
-size_t attn_workspace_bytes(const ssd_attn_dims_t &) { return 0; }
+size_t attn_workspace_bytes(const ssd_attn_dims_t &d)
+{
+    const int grid = std::min(kMaxCtas, sm_count() * 4);
+    return (size_t)grid * (2 * tile_rows(d) * (d.headdim + 2) * sizeof(float) + sizeof(int4));
+}
 
-cudaError_t attn_launch(const AttnArgs &a, void *, cudaStream_t stream)
+cudaError_t attn_launch(const AttnArgs &a, void *workspace, cudaStream_t stream)
 {
     SSD_NVTX_RANGE("attn_launch");
-    const dim3 grid((unsigned)a.d.nrows, (unsigned)a.d.nheads);
-    if (a.d.dtype == SSD_DTYPE_BF16)
-        ssd_paged_attn_simple_kernel<__nv_bfloat16><<<grid, kWarps * 32, 0, stream>>>(a);
-    else
-        ssd_paged_attn_simple_kernel<float><<<grid, kWarps * 32, 0, stream>>>(a);
-    const cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess)
-        note_launches(1);
-    return e;
+    AttnParams p{};
+    p.a = a;
+    const int mr = tile_rows(a.d), D = a.d.headdim, es = a.d.dtype == SSD_DTYPE_BF16 ? 2 : 4;
+    p.group = a.d.nheads / a.d.nkv;
+    p.nhb = (p.group + mr - 1) / mr;
+    p.gh = (p.group + p.nhb - 1) / p.nhb;
+    p.tok = a.start ? std::max(1, mr / p.gh) : 1;
+    p.items = a.d.nkv * p.nhb;
+    p.seg = D * es / 16;
+    // rows of an odd number of 16-byte segments: eight rows' segments lie in different banks
+    const int seg = es == 2 ? (p.seg + 1) / 2 * 2 : p.seg;
+    p.stride = (seg | 1) * 16;
+    p.same_page = a.d.page_size % kUnit == 0;
+    p.page.sh = 31;
+    while ((1u << (p.page.sh - 31)) < (uint32_t)a.d.page_size)
+        ++p.page.sh;
+    p.page.mul = (uint32_t)((1ull << p.page.sh) / (uint32_t)a.d.page_size + 1);
+    if (a.d.dtype == SSD_DTYPE_BF16) {
+        if (D <= 64)
+            return mr == 32 ? launch<Mma<2, 64>, 64, 8>(p, workspace, stream) : launch<Mma<1, 64>, 64, 9>(p, workspace, stream);
+        if (D <= 128)
+            return mr == 32 ? launch<Mma<2, 128>, 128, 4>(p, workspace, stream) : launch<Mma<1, 128>, 128, 5>(p, workspace, stream);
+        return launch<Mma<1, 256>, 256, 5>(p, workspace, stream);
+    }
+    if (D <= 64)
+        return mr == 1 ? launch<Simt<1, 64>, 64, 5>(p, workspace, stream)
+             : mr == 2 ? launch<Simt<2, 64>, 64, 5>(p, workspace, stream)
+             : mr == 4 ? launch<Simt<4, 64>, 64, 5>(p, workspace, stream)
+                       : launch<Simt<8, 64>, 64, 5>(p, workspace, stream);
+    if (D <= 128)
+        return mr == 1 ? launch<Simt<1, 128>, 128, 3>(p, workspace, stream)
+             : mr == 2 ? launch<Simt<2, 128>, 128, 3>(p, workspace, stream)
+             : mr == 4 ? launch<Simt<4, 128>, 128, 3>(p, workspace, stream)
+                       : launch<Simt<8, 128>, 128, 2>(p, workspace, stream);
+    return mr == 2 ? launch<Simt<2, 256>, 256, 3>(p, workspace, stream)
+                   : launch<Simt<8, 256>, 256, 3>(p, workspace, stream);
 }
 
 }  // namespace ssd
