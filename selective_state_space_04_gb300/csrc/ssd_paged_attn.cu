@@ -2,7 +2,7 @@
 //
 // A tile is up to MR query rows that read the same keys: the query heads of one
 // key-value head for one or several consecutive new tokens of a request.  The
-// tile's visible positions are cut into units of 16 tokens.  All units of all
+// tile's visible positions are cut into units of 16 or 32 tokens.  All units of all
 // tiles and key-value heads, laid end to end, are dealt to the CTAs in equal
 // contiguous shares, whatever the requests' lengths; one CTA per resident slot
 // stays for the whole launch.  Within its share a CTA's warps take units in
@@ -38,7 +38,6 @@
 namespace ssd {
 namespace {
 
-constexpr int kUnit = 16;        // tokens per unit
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr float kLn2 = 0.69314718055994531f;
@@ -62,7 +61,9 @@ struct AttnParams {
     int items;          // nkv * nhb: tiles of the same rows
     int seg;            // 16-byte segments per row of K or V
     int stride;         // bytes from row to row of a ring slot (an odd number of segments)
-    int same_page;      // a unit never crosses a page
+    int same16;         // 16 tokens from a multiple of 16 on never cross a page
+    float f;            // |scale| log2(e), or 1 for scale 0
+    int sign;           // of scale
 };
 
 __device__ __forceinline__ int div_page(const FastDiv &f, int n) { return (int)(((uint64_t)(uint32_t)n * f.mul) >> f.sh); }
@@ -92,6 +93,7 @@ struct Tile {
     int first, end, ub, units;
 };
 
+template <int UT>
 __device__ __forceinline__ void tile_extent(const AttnParams &p, Tile &t)
 {
     const int limit = p.a.d.max_pages * p.a.d.page_size;
@@ -99,8 +101,8 @@ __device__ __forceinline__ void tile_extent(const AttnParams &p, Tile &t)
     t.end = p1 < 0 ? 0 : min(p1, limit - 1) + 1;
     t.first = p.a.d.window > 0 ? max(0, p0 - p.a.d.window + 1) : 0;
     t.first = min(t.first, t.end);
-    t.ub = t.first / kUnit;
-    t.units = max(1, (t.end + kUnit - 1) / kUnit - t.ub);   // (a tile that sees nothing still writes its rows)
+    t.ub = t.first / UT;
+    t.units = max(1, (t.end + UT - 1) / UT - t.ub);   // (a tile that sees nothing still writes its rows)
 }
 
 // rows [s, e) of request r, clamped to the rows there are
@@ -111,6 +113,7 @@ __device__ __forceinline__ void request_rows(const AttnParams &p, int r, int &s,
     e = min(max(p.a.start[r + 1], s), n);
 }
 
+template <int UT>
 __device__ __forceinline__ void set_tile(const AttnParams &p, Tile &t, int req, int j)
 {
     t.req = req;
@@ -126,14 +129,15 @@ __device__ __forceinline__ void set_tile(const AttnParams &p, Tile &t, int req, 
         t.nq = 1;
         t.rows_left = 0;
     }
-    tile_extent(p, t);
+    tile_extent<UT>(p, t);
 }
 
 // the next tile (there is one)
+template <int UT>
 __device__ __forceinline__ void next_tile(const AttnParams &p, Tile &t)
 {
     if (t.rows_left > 0) {
-        set_tile(p, t, t.req, t.j + 1);
+        set_tile<UT>(p, t, t.req, t.j + 1);
         return;
     }
     int r = t.req + 1;
@@ -146,7 +150,7 @@ __device__ __forceinline__ void next_tile(const AttnParams &p, Tile &t)
             ++r;
         }
     }
-    set_tile(p, t, r, 0);
+    set_tile<UT>(p, t, r, 0);
 }
 
 // A place in the CTA's share: a tile, an item (key-value head and head block)
@@ -157,12 +161,13 @@ struct Cursor {
     long long lin;
 };
 
+template <int UT>
 __device__ __forceinline__ void next_item(const AttnParams &p, Cursor &c)
 {
     c.lin += c.t.units;
     if (++c.item == p.items) {
         c.item = 0;
-        next_tile(p, c.t);
+        next_tile<UT>(p, c.t);
     }
 }
 
@@ -201,6 +206,7 @@ struct Found {
 // Where the CTA's share begins.  Every CTA sums all tiles' units (a contiguous
 // run of tiles per thread); the thread whose run holds unit u0 finds the tile.
 // `counts` (shared memory, nreq + 1 ints) is used when there is a start array.
+template <int UT>
 __device__ void locate(const AttnParams &p, int *counts, long long *tmp, Found *found, long long &total, long long &per,
                        long long &u0)
 {
@@ -248,9 +254,9 @@ __device__ void locate(const AttnParams &p, int *counts, long long *tmp, Found *
     Tile t;
     for (long long i = t0; i < t1; ++i) {
         if (i == t0)
-            set_tile(p, t, f.req, f.j);
+            set_tile<UT>(p, t, f.req, f.j);
         else
-            next_tile(p, t);
+            next_tile<UT>(p, t);
         n += t.units;
     }
     long long sum;
@@ -262,9 +268,9 @@ __device__ void locate(const AttnParams &p, int *counts, long long *tmp, Found *
         long long lin = before;
         for (long long i = t0; i < t1; ++i) {
             if (i == t0)
-                set_tile(p, t, f.req, f.j);
+                set_tile<UT>(p, t, f.req, f.j);
             else
-                next_tile(p, t);
+                next_tile<UT>(p, t);
             const long long here = (long long)t.units * p.items;
             if (u0 < lin + here) {
                 found->req = t.req;
@@ -280,82 +286,114 @@ __device__ void locate(const AttnParams &p, int *counts, long long *tmp, Found *
 
 // ---- the loader -------------------------------------------------------------
 
-// Streams a warp's units into its ring: one step per half (K then V).
+// Streams a warp's units into its ring, K halves and V halves in turn.
+template <typename T, int DP, bool EXACT, int UT>
 struct Loader {
+    static constexpr int kSegMax = DP * (int)sizeof(T) / 16;
+    static constexpr int kSub = UT / 16;
     Cursor c;
-    int u;                 // the unit within the item (-1: none left)
+    int u, u_end;          // the unit within the item (-1: none left); the share's units of the item
     long long u1;          // end of the share
-    int page;              // table entry read ahead for this lane's token
-    long long koff, voff;  // byte offsets of this lane's token (same_page: of the unit's first token)
+    int page;              // table entry read ahead (same16: of the lane's 16 tokens, else of the lane's token)
     uint32_t mask;         // the unit's tokens that are to be read
-};
+    // byte offsets in the caches; same16: of the first token of each 16, else [0] is the lane's token's
+    long long koff[kSub], voff[kSub];
 
-// the loader's next unit: every kWarps-th of the share
-__device__ __forceinline__ void loader_skip(const AttnParams &p, Loader &l, int by)
-{
-    l.u += by;
-    while (true) {
-        if (l.c.lin + l.u >= l.u1) {
-            l.u = -1;
-            return;
+    __device__ __forceinline__ void set_end() { u_end = (int)min((long long)c.t.units, u1 - c.lin); }
+    // the unit `by` further on in the share
+    __device__ __forceinline__ void skip(const AttnParams &p, int by)
+    {
+        u += by;
+        while (u >= u_end) {
+            if (c.lin + u >= u1) {
+                u = -1;
+                return;
+            }
+            u -= c.t.units;
+            next_item<UT>(p, c);
+            set_end();
         }
-        if (l.u < l.c.t.units)
-            return;
-        l.u -= l.c.t.units;
-        next_item(p, l.c);
     }
-}
-
-__device__ __forceinline__ void loader_fetch_page(const AttnParams &p, Loader &l, int lane)
-{
-    if (l.u < 0)
-        return;
-    const int tok = (l.c.t.ub + l.u) * kUnit + (p.same_page ? 0 : (lane & 15));
-    l.page = -1;
-    if (tok < l.c.t.end && tok >= 0)   // (same_page: the unit's first token is below end, its page holds them all)
-        l.page = __ldg(p.a.table + (long long)l.c.t.req * p.a.d.table_stride + div_page(p.page, tok));
-}
-
-template <typename T>
-__device__ __forceinline__ void loader_offsets(const AttnParams &p, Loader &l, int lane)
-{
-    const int tok0 = (l.c.t.ub + l.u) * kUnit, tok = tok0 + (lane & 15);
-    const bool ok = tok >= l.c.t.first && tok < l.c.t.end && l.page >= 0 && l.page < (int)p.a.d.npages;
-    l.mask = __ballot_sync(0xffffffffu, ok) & 0xffffu;
-    const int at = p.same_page ? tok0 : tok;
-    const int off = at - div_page(p.page, at) * p.a.d.page_size;
-    const int kvh = l.c.item / p.nhb;
-    const long long pg = ok || (p.same_page && l.mask) ? l.page : 0;
-    l.koff = (pg * p.a.d.kc_stride[0] + off * p.a.d.kc_stride[1] + kvh * p.a.d.kc_stride[2]) * (long long)sizeof(T);
-    l.voff = (pg * p.a.d.vc_stride[0] + off * p.a.d.vc_stride[1] + kvh * p.a.d.vc_stride[2]) * (long long)sizeof(T);
-    if (!ok && !p.same_page)
-        l.koff = l.voff = 0;   // (not read)
-    if (p.same_page && !l.mask)
-        l.koff = l.voff = 0;
-}
-
-// copies one half (16 tokens of K or V) into a ring slot
-template <typename T, int DP>
-__device__ __forceinline__ void loader_copy(const AttnParams &p, const Loader &l, const void *base, long long off, long long tstride,
-                                            uint32_t slot, int lane)
-{
-    constexpr int kSegMax = DP * (int)sizeof(T) / 16;
-    const bool full = p.seg == kSegMax;   // the template's own size: constant shifts
-    const uint32_t inv = 65536u / (uint32_t)p.seg + 1;
-    const char *src = static_cast<const char *>(base);
-    const long long ts = tstride * (long long)sizeof(T);
+    __device__ __forceinline__ void fetch_page(const AttnParams &p, int lane)
+    {
+        page = -1;
+        if (u >= 0) {
+            const int tok = (c.t.ub + u) * UT + (p.same16 ? (kSub > 1 ? lane & 16 : 0) : lane % UT);
+            if (tok < c.t.end)   // (same16: the page of 16 tokens is that of the first of them)
+                page = __ldg(p.a.table + (long long)c.t.req * p.a.d.table_stride + div_page(p.page, tok));
+        }
+    }
+    __device__ __forceinline__ void offsets(const AttnParams &p, int lane)
+    {
+        const int tok0 = (c.t.ub + u) * UT, tok = tok0 + lane % UT;
+        const bool there = (unsigned)page < (unsigned)p.a.d.npages;
+        mask = __ballot_sync(0xffffffffu, tok >= c.t.first && tok < c.t.end && there);
+        if (UT == 16)
+            mask &= 0xffffu;
+        const int kvh = p.nhb == 1 ? c.item : c.item / p.nhb;
+        if (p.same16) {
 #pragma unroll
-    for (int i = 0; i < kSegMax / 2; ++i) {
-        const int idx = lane + 32 * i;
-        const int r = full ? idx / kSegMax : (int)((idx * inv) >> 16);
-        const int c = idx - r * p.seg;
-        const bool in = r < kUnit;
-        const bool on = in && ((l.mask >> r) & 1);
-        const long long o = p.same_page ? (on ? off + r * ts : 0) : __shfl_sync(0xffffffffu, off, r & 15);
-        if (in)
-            cp_async16(slot + r * p.stride + c * 16, on ? src + o + c * 16 : static_cast<const char *>(p.a.q), on);
+            for (int b = 0; b < kSub; ++b) {
+                // (an entry out of range masks all 16 tokens: nothing is read at its offset)
+                const long long pg = max(kSub > 1 ? __shfl_sync(0xffffffffu, page, 16 * b) : page, 0);
+                const int at = tok0 + 16 * b, off = at - div_page(p.page, at) * p.a.d.page_size;
+                koff[b] = (pg * p.a.d.kc_stride[0] + off * p.a.d.kc_stride[1] + kvh * p.a.d.kc_stride[2]) * (long long)sizeof(T);
+                voff[b] = (pg * p.a.d.vc_stride[0] + off * p.a.d.vc_stride[1] + kvh * p.a.d.vc_stride[2]) * (long long)sizeof(T);
+            }
+        } else {
+            const long long pg = max(page, 0);
+            const int off = tok - div_page(p.page, tok) * p.a.d.page_size;
+            koff[0] = (pg * p.a.d.kc_stride[0] + off * p.a.d.kc_stride[1] + kvh * p.a.d.kc_stride[2]) * (long long)sizeof(T);
+            voff[0] = (pg * p.a.d.vc_stride[0] + off * p.a.d.vc_stride[1] + kvh * p.a.d.vc_stride[2]) * (long long)sizeof(T);
+        }
     }
-}
+    // copies one half (UT tokens of K or V) into a ring slot
+    __device__ __forceinline__ void copy(const AttnParams &p, const void *base, const long long (&off)[kSub], long long tstride,
+                                         uint32_t slot, int lane)
+    {
+        const char *src = static_cast<const char *>(base);
+        constexpr uint32_t kAll = UT == 16 ? 0xffffu : 0xffffffffu;
+        if (EXACT && p.same16) {
+            // a lane's segment is the same in each of its rows, which lie kRows apart
+            constexpr int kRows = 32 / kSegMax > 0 ? 32 / kSegMax : 1;   // rows per instruction
+            constexpr int kParts = kSegMax / 32 > 0 ? kSegMax / 32 : 1;  // instructions per row
+            constexpr int kStride = (kSegMax | 1) * 16;
+            const int r0 = lane / kSegMax, seg = lane % kSegMax;
+            const uint32_t dst = slot + r0 * kStride + seg * 16;
+            const long long ts = tstride * (long long)sizeof(T);
+#pragma unroll
+            for (int b = 0; b < kSub; ++b) {
+                const char *s = src + off[b] + r0 * ts + seg * 16;
+#pragma unroll
+                for (int i = 0; i < 16 / kRows; ++i) {
+#pragma unroll
+                    for (int x = 0; x < kParts; ++x) {
+                        const uint32_t d = dst + (16 * b + i * kRows) * kStride + x * 512;
+                        if (mask == kAll)
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(s + x * 512) : "memory");
+                        else {
+                            const bool on = (mask >> (16 * b + i * kRows + r0)) & 1;
+                            cp_async16(d, on ? s + x * 512 : static_cast<const char *>(p.a.q), on);
+                        }
+                    }
+                    s += kRows * ts;
+                }
+            }
+        } else {
+            const uint32_t inv = 65536u / (uint32_t)p.seg + 1;
+            const long long ts = tstride * (long long)sizeof(T);
+#pragma unroll 4
+            for (int i = 0; i < (UT * p.seg + 31) / 32; ++i) {
+                const int idx = lane + 32 * i, r = (int)((idx * inv) >> 16), s = idx - r * p.seg;
+                const bool in = r < UT, on = in && ((mask >> r) & 1);
+                const long long o = p.same16 ? (kSub > 1 && r >= 16 ? off[kSub - 1] : off[0]) + (r & 15) * ts
+                                             : __shfl_sync(0xffffffffu, off[0], r % UT);
+                if (in)
+                    cp_async16(slot + r * p.stride + s * 16, on ? src + o + s * 16 : static_cast<const char *>(p.a.q), on);
+            }
+        }
+    }
+};
 
 // ---- the arithmetic: bf16 on mma.sync --------------------------------------
 
@@ -381,22 +419,29 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// the rows a lane holds results of, and what each sees
-template <int NM, int DP>
+// NM: tiles of 16 query rows; DP: the head's elements, rounded up (EXACT: as
+// they are); NT: 16-token halves of a unit.  A lane holds results of rows
+// lane / 4 and lane / 4 + 8 of each tile.
+template <int NM, int DP, bool EX, int NT>
 struct Mma {
     using T = __nv_bfloat16;
-    static constexpr int MR = 16 * NM;
+    static constexpr int MR = 16 * NM, kDim = DP, kUnit = 16 * NT;
+    static constexpr bool kExact = EX;
     uint32_t q[NM][DP / 16][4];
     float o[NM][DP / 8][4];
-    float s[NM][2][4];
-    float m[NM][2], l[NM][2];
-    int lo[NM][2], hi[NM][2];
+    float s[NM][2 * NT][4];
+    float m[NM][2], l[NM][2];   // m: the running maximum of q.k (of -q.k for a negative scale)
+    int lo[NM][2], hi[NM][2];   // positions a row sees
+
+    __device__ __forceinline__ static int dim(const AttnParams &p) { return EX ? DP : p.a.d.headdim; }
+    __device__ __forceinline__ static int row_bytes(const AttnParams &p) { return EX ? ((DP / 8) | 1) * 16 : p.stride; }
 
     __device__ __forceinline__ void begin(const AttnParams &p, const Tile &t, int item, int lane)
     {
-        const int kvh = item / p.nhb, hb = item - kvh * p.nhb, D = p.a.d.headdim;
+        const int kvh = item / p.nhb, hb = item - kvh * p.nhb, D = dim(p);
         const int h0 = hb * p.gh, nh = min(p.gh, p.group - h0), rows = t.nq * nh;
         const int limit = p.a.d.max_pages * p.a.d.page_size;
+        const uint32_t keep = p.sign == 0 ? 0u : 0xffffffffu, flip = p.sign < 0 ? 0x80008000u : 0u;
 #pragma unroll
         for (int mt = 0; mt < NM; ++mt)
 #pragma unroll
@@ -414,7 +459,8 @@ struct Mma {
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
                         const int c = 16 * k + 8 * y + 2 * (lane & 3);
-                        q[mt][k][x + 2 * y] = r < rows && c < D ? *reinterpret_cast<const uint32_t *>(src + c) : 0u;
+                        const uint32_t v = r < rows && c < D ? *reinterpret_cast<const uint32_t *>(src + c) : 0u;
+                        q[mt][k][x + 2 * y] = (v & keep) ^ flip;
                     }
             }
 #pragma unroll
@@ -428,87 +474,99 @@ struct Mma {
 
     // scores of a unit's tokens and their weights; mask: the tokens read;
     // [all0, all1): tokens that every row sees
-    __device__ __forceinline__ void scores(const AttnParams &p, uint32_t slot, uint32_t mask, int tok0, int all0, int all1, int lane)
+    __device__ __forceinline__ void scores(const AttnParams &p, char *slot_ptr, uint32_t mask, int tok0, int all0, int all1, int lane)
     {
-        const int D = p.a.d.headdim;
+        const int D = dim(p), stride = row_bytes(p);
+        const uint32_t slot = smem_addr(slot_ptr);
 #pragma unroll
         for (int mt = 0; mt < NM; ++mt)
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < 2 * NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     s[mt][n][i] = 0.f;
         // lanes 0-7, 8-15: tokens 0-7, first and second 16 bytes; 16-23, 24-31: tokens 8-15
-        const uint32_t a = slot + ((lane & 7) + ((lane >> 4) << 3)) * p.stride + ((lane >> 3) & 1) * 16;
+        const uint32_t a = slot + ((lane & 7) + ((lane >> 4) << 3)) * stride + ((lane >> 3) & 1) * 16;
 #pragma unroll
         for (int k = 0; k < DP / 16; ++k) {
             if (16 * k < D) {
-                uint32_t b[4];
-                ldsm4(a + k * 32, b);
 #pragma unroll
-                for (int mt = 0; mt < NM; ++mt) {
-                    mma16816(s[mt][0], q[mt][k], b[0], b[1]);
-                    mma16816(s[mt][1], q[mt][k], b[2], b[3]);
+                for (int h = 0; h < NT; ++h) {
+                    uint32_t b[4];
+                    ldsm4(a + h * 16 * stride + k * 32, b);
+#pragma unroll
+                    for (int mt = 0; mt < NM; ++mt) {
+                        mma16816(s[mt][2 * h], q[mt][k], b[0], b[1]);
+                        mma16816(s[mt][2 * h + 1], q[mt][k], b[2], b[3]);
+                    }
                 }
             }
         }
-        const float f = p.a.d.scale * kLog2e;
-        const bool masked = mask != 0xffffu || tok0 < all0 || tok0 + kUnit > all1;
+        constexpr uint32_t kAll = NT == 1 ? 0xffffu : 0xffffffffu;
+        if (mask != kAll || tok0 < all0 || tok0 + kUnit > all1) {
 #pragma unroll
-        for (int mt = 0; mt < NM; ++mt)
+            for (int n = 0; n < 2 * NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int tt = 8 * n + 2 * (lane & 3) + i, tok = tok0 + tt;
+                    const bool there = (mask >> tt) & 1;
+#pragma unroll
+                    for (int mt = 0; mt < NM; ++mt)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+                            if (!there || tok < lo[mt][x] || tok >= hi[mt][x])
+                                s[mt][n][2 * x + i] = -INFINITY;
+                }
+        }
+#pragma unroll
+        for (int mt = 0; mt < NM; ++mt) {
+            float keep[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                float top = -INFINITY;
+                float top = m[mt][x];
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float &v = s[mt][n][2 * x + i];
-                        v *= f;
-                        if (masked) {
-                            const int tt = 8 * n + 2 * (lane & 3) + i, tok = tok0 + tt;
-                            if (!((mask >> tt) & 1) || tok < lo[mt][x] || tok >= hi[mt][x])
-                                v = -INFINITY;
-                        }
-                        top = fmaxf(top, v);
-                    }
+                for (int n = 0; n < 2 * NT; ++n)
+                    top = fmaxf(top, fmaxf(s[mt][n][2 * x], s[mt][n][2 * x + 1]));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const float mn = fmaxf(m[mt][x], top), base = mn == -INFINITY ? 0.f : mn;
-                const float keep = exp2_fast(m[mt][x] - base);
-                m[mt][x] = mn;
+                const float base = (top == -INFINITY ? 0.f : top) * p.f;
+                keep[x] = exp2_fast(m[mt][x] * p.f - base);
+                m[mt][x] = top;
                 float sum = 0.f;
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < 2 * NT; ++n)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         float &v = s[mt][n][2 * x + i];
-                        v = exp2_fast(v - base);
+                        v = exp2_fast(v * p.f - base);
                         sum += v;
                     }
-                l[mt][x] = l[mt][x] * keep + sum;
-                if (__any_sync(0xffffffffu, keep != 1.f)) {
-#pragma unroll
-                    for (int n = 0; n < DP / 8; ++n) {
-                        o[mt][n][2 * x] *= keep;
-                        o[mt][n][2 * x + 1] *= keep;
-                    }
-                }
+                l[mt][x] = l[mt][x] * keep[x] + sum;
             }
+            if (__any_sync(0xffffffffu, keep[0] != 1.f || keep[1] != 1.f)) {
+#pragma unroll
+                for (int n = 0; n < DP / 8; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        o[mt][n][i] *= keep[i >> 1];
+            }
+        }
     }
 
     // Tokens that some rows of the tile see and others do not are added row by
     // row, to those that see them, and then left out of the product: there a
     // weight 0 times an infinity or NaN of theirs would reach every row.
-    __device__ __forceinline__ void partial_tokens(const AttnParams &p, uint32_t slot, char *slot_ptr, uint32_t part, int tok0, int lane)
+    // (Unrolled over the tokens: a running token number would index the score
+    // registers at run time and put them in local memory.)
+    __device__ __forceinline__ void partial_tokens(const AttnParams &p, char *slot_ptr, uint32_t part, int tok0, int lane)
     {
-        // (unrolled over the tokens: a running token number would index the
-        // score registers at run time and put them in local memory)
+        const int stride = row_bytes(p);
+        const uint32_t slot = smem_addr(slot_ptr);
 #pragma unroll
         for (int tt = 0; tt < kUnit; ++tt) {
             if (!((part >> tt) & 1))
                 continue;
-            const uint32_t row = slot + tt * p.stride;
+            const uint32_t row = slot + tt * stride;
             float wgt[NM][2];
 #pragma unroll
             for (int mt = 0; mt < NM; ++mt)
@@ -524,7 +582,7 @@ struct Mma {
                 }
 #pragma unroll
             for (int n = 0; n < DP / 8; ++n) {
-                if (8 * n < p.a.d.headdim) {
+                if (8 * n < dim(p)) {
                     uint32_t v;
                     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(row + 16 * n + 4 * (lane & 3)) : "memory");
 #pragma unroll
@@ -539,55 +597,57 @@ struct Mma {
             }
             __syncwarp();
             for (int c = lane; c < p.seg; c += 32)
-                *reinterpret_cast<uint4 *>(slot_ptr + tt * p.stride + c * 16) = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4 *>(slot_ptr + tt * stride + c * 16) = make_uint4(0, 0, 0, 0);
         }
         __syncwarp();
     }
 
-    __device__ __forceinline__ void values(const AttnParams &p, uint32_t slot, char *slot_ptr, uint32_t mask, int tok0, int all0,
-                                           int all1, int lane)
+    __device__ __forceinline__ void values(const AttnParams &p, char *slot_ptr, uint32_t mask, int tok0, int all0, int all1, int lane)
     {
-        const int D = p.a.d.headdim;
+        const int D = dim(p), stride = row_bytes(p);
         if (tok0 < all0 || tok0 + kUnit > all1) {
             // bit tt: every row sees token tok0 + tt
             const int a0 = min(max(all0 - tok0, 0), kUnit), a1 = min(max(all1 - tok0, 0), kUnit);
-            const uint32_t all = a1 > a0 ? (0xffffu >> (16 - a1)) & (0xffffu << a0) : 0u;
+            const uint32_t all = a1 > a0 ? (0xffffffffu >> (32 - a1)) & (0xffffffffu << a0) : 0u;
             const uint32_t part = mask & ~all;
             if (part)
-                partial_tokens(p, slot, slot_ptr, part, tok0, lane);
+                partial_tokens(p, slot_ptr, part, tok0, lane);
         }
-        uint32_t hi4[NM][4], lo4[NM][4];
-#pragma unroll
-        for (int mt = 0; mt < NM; ++mt)
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const float a = s[mt][n][2 * x], b = s[mt][n][2 * x + 1];
-                    const uint32_t h = pack_bf16(a, b);
-                    hi4[mt][2 * n + x] = h;
-                    lo4[mt][2 * n + x] = pack_bf16(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xffff0000u));
-                }
         // lanes 0-7, 8-15: tokens 0-7, 8-15 of the first 16 bytes; 16-31: of the second
-        const uint32_t a = slot + ((lane & 7) + (((lane >> 3) & 1) << 3)) * p.stride + (lane >> 4) * 16;
+        const uint32_t a = smem_addr(slot_ptr) + ((lane & 7) + (((lane >> 3) & 1) << 3)) * stride + (lane >> 4) * 16;
 #pragma unroll
-        for (int n = 0; n < DP / 16; ++n) {
-            if (16 * n < D) {
-                uint32_t b[4];
-                ldsm4t(a + n * 32, b);
+        for (int h = 0; h < NT; ++h) {
+            uint32_t hi4[NM][4], lo4[NM][4];
 #pragma unroll
-                for (int mt = 0; mt < NM; ++mt) {
-                    mma16816(o[mt][2 * n], hi4[mt], b[0], b[1]);
-                    mma16816(o[mt][2 * n], lo4[mt], b[0], b[1]);
-                    mma16816(o[mt][2 * n + 1], hi4[mt], b[2], b[3]);
-                    mma16816(o[mt][2 * n + 1], lo4[mt], b[2], b[3]);
+            for (int mt = 0; mt < NM; ++mt)
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const float u = s[mt][2 * h + n][2 * x], v = s[mt][2 * h + n][2 * x + 1];
+                        const uint32_t w = pack_bf16(u, v);
+                        hi4[mt][2 * n + x] = w;
+                        lo4[mt][2 * n + x] = pack_bf16(u - __uint_as_float(w << 16), v - __uint_as_float(w & 0xffff0000u));
+                    }
+#pragma unroll
+            for (int n = 0; n < DP / 16; ++n) {
+                if (16 * n < D) {
+                    uint32_t b[4];
+                    ldsm4t(a + h * 16 * stride + n * 32, b);
+#pragma unroll
+                    for (int mt = 0; mt < NM; ++mt) {
+                        mma16816(o[mt][2 * n], hi4[mt], b[0], b[1]);
+                        mma16816(o[mt][2 * n + 1], hi4[mt], b[2], b[3]);
+                        mma16816(o[mt][2 * n], lo4[mt], b[0], b[1]);
+                        mma16816(o[mt][2 * n + 1], lo4[mt], b[2], b[3]);
+                    }
                 }
             }
         }
     }
 
-    // the sums over the four lanes of a row, and the rows' maxima and sums to shared memory
-    __device__ __forceinline__ void end(float *ml, int lane)
+    // the sums over the four lanes of a row; the rows' maxima (base 2) and sums to shared memory
+    __device__ __forceinline__ void end(const AttnParams &p, float *ml, int lane)
     {
 #pragma unroll
         for (int mt = 0; mt < NM; ++mt)
@@ -595,6 +655,7 @@ struct Mma {
             for (int x = 0; x < 2; ++x) {
                 l[mt][x] += __shfl_xor_sync(0xffffffffu, l[mt][x], 1);
                 l[mt][x] += __shfl_xor_sync(0xffffffffu, l[mt][x], 2);
+                m[mt][x] *= p.f;
                 if ((lane & 3) == 0) {
                     const int r = mt * 16 + x * 8 + (lane >> 2);
                     ml[2 * r] = m[mt][x];
@@ -616,7 +677,7 @@ struct Mma {
 #pragma unroll
                     for (int n = 0; n < DP / 8; ++n) {
                         const int c = 8 * n + 2 * (lane & 3);
-                        if (8 * n < p.a.d.headdim) {
+                        if (8 * n < dim(p)) {
                             float2 *at = reinterpret_cast<float2 *>(buf + r * ds + c);
                             float2 v = make_float2(o[mt][n][2 * x] * f, o[mt][n][2 * x + 1] * f);
                             if (ADD) {
@@ -638,19 +699,23 @@ struct Mma {
 // read from shared memory (the same address for all tokens: a broadcast), one
 // shuffle to add the halves.  Output: lane = elements 4 lane .. (+ 128), the
 // weights read back from shared memory by token.
-template <int MRows, int DP>
+template <int MRows, int DP, bool EX>
 struct Simt {
     using T = float;
-    static constexpr int MR = MRows;
+    static constexpr int MR = MRows, kDim = DP, kUnit = 16;
+    static constexpr bool kExact = EX;
     static constexpr int NV = (DP + 127) / 128;   // float4 of the output per lane and row
     float o[MR][NV][4];
-    float m[MR], l[MR];
+    float m[MR], l[MR];   // m: the running maximum of q.k (of -q.k for a negative scale)
     int lo[MR], hi[MR];
-    float *qs, *ps;   // the CTA's query rows [MR][DP], this warp's weights [MR][16]
+    float *qs, *ps;       // the CTA's query rows [MR][DP], this warp's weights [MR][16]
+
+    __device__ __forceinline__ static int dim(const AttnParams &p) { return EX ? DP : p.a.d.headdim; }
+    __device__ __forceinline__ static int row_bytes(const AttnParams &p) { return EX ? ((DP / 4) | 1) * 16 : p.stride; }
 
     __device__ __forceinline__ void begin(const AttnParams &p, const Tile &t, int item, int lane)
     {
-        const int kvh = item / p.nhb, hb = item - kvh * p.nhb, D = p.a.d.headdim;
+        const int kvh = item / p.nhb, hb = item - kvh * p.nhb, D = dim(p);
         const int h0 = hb * p.gh, nh = min(p.gh, p.group - h0), rows = t.nq * nh;
         const int limit = p.a.d.max_pages * p.a.d.page_size;
 #pragma unroll
@@ -664,9 +729,14 @@ struct Simt {
             const float *src = static_cast<const float *>(p.a.q) + (long long)(t.row + j) * p.a.d.q_stride[0] +
                                (long long)(kvh * p.group + h0 + g) * p.a.d.q_stride[1];
             if (r % kWarps == (int)(threadIdx.x >> 5))
-                for (int c = 4 * lane; c < DP; c += 128)
-                    *reinterpret_cast<float4 *>(qs + r * DP + c) =
-                        r < rows && c < D ? *reinterpret_cast<const float4 *>(src + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int c = 4 * lane; c < DP; c += 128) {
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (r < rows && c < D && p.sign != 0)
+                        v = *reinterpret_cast<const float4 *>(src + c);
+                    if (p.sign < 0)
+                        v = make_float4(-v.x, -v.y, -v.z, -v.w);
+                    *reinterpret_cast<float4 *>(qs + r * DP + c) = v;
+                }
 #pragma unroll
             for (int n = 0; n < NV; ++n)
 #pragma unroll
@@ -676,10 +746,10 @@ struct Simt {
         __syncthreads();   // (each warp has loaded some of the rows)
     }
 
-    __device__ __forceinline__ void scores(const AttnParams &p, const char *slot, uint32_t mask, int tok0, int all0, int all1, int lane)
+    __device__ __forceinline__ void scores(const AttnParams &p, char *slot, uint32_t mask, int tok0, int all0, int all1, int lane)
     {
-        const int tt = lane & 15, half = lane >> 4, D = p.a.d.headdim;
-        const float4 *k = reinterpret_cast<const float4 *>(slot + tt * p.stride);
+        const int tt = lane & 15, half = lane >> 4, D = dim(p);
+        const float4 *k = reinterpret_cast<const float4 *>(slot + tt * row_bytes(p));
         float acc[MR];
 #pragma unroll
         for (int r = 0; r < MR; ++r)
@@ -696,19 +766,18 @@ struct Simt {
                 acc[r] += qv.w * kv.w;
             }
         }
-        const float f = p.a.d.scale * kLog2e;
         const bool masked = mask != 0xffffu || tok0 < all0 || tok0 + kUnit > all1;
 #pragma unroll
         for (int r = 0; r < MR; ++r) {
-            float v = (acc[r] + __shfl_xor_sync(0xffffffffu, acc[r], 16)) * f;
+            float v = acc[r] + __shfl_xor_sync(0xffffffffu, acc[r], 16);
             if (masked && (!((mask >> tt) & 1) || tok0 + tt < lo[r] || tok0 + tt >= hi[r]))
                 v = -INFINITY;
             float top = v;
 #pragma unroll
             for (int x = 8; x >= 1; x >>= 1)
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-            const float mn = fmaxf(m[r], top), base = mn == -INFINITY ? 0.f : mn;
-            const float keep = exp2_fast(m[r] - base), e = exp2_fast(v - base);
+            const float mn = fmaxf(m[r], top), base = (mn == -INFINITY ? 0.f : mn) * p.f;
+            const float keep = exp2_fast(m[r] * p.f - base), e = exp2_fast(v * p.f - base);
             m[r] = mn;
             l[r] = l[r] * keep + (half == 0 ? e : 0.f);   // summed over the lanes at the end
             if (half == 0)
@@ -724,7 +793,7 @@ struct Simt {
         __syncwarp();
     }
 
-    __device__ __forceinline__ void values(const AttnParams &p, const char *slot, uint32_t mask, int tok0, int all0, int all1, int lane)
+    __device__ __forceinline__ void values(const AttnParams &p, char *slot, uint32_t mask, int tok0, int all0, int all1, int lane)
     {
         // tokens not read are zero in the slot; one that a row does not see is skipped for it
         const bool ragged = tok0 < all0 || tok0 + kUnit > all1;
@@ -734,7 +803,7 @@ struct Simt {
 #pragma unroll
             for (int n = 0; n < NV; ++n) {
                 const int c = 4 * lane + 128 * n;
-                v[n] = c < p.a.d.headdim ? *reinterpret_cast<const float4 *>(slot + tt * p.stride + 4 * c)
+                v[n] = c < dim(p) ? *reinterpret_cast<const float4 *>(slot + tt * row_bytes(p) + 4 * c)
                                          : make_float4(0.f, 0.f, 0.f, 0.f);
             }
 #pragma unroll
@@ -754,13 +823,14 @@ struct Simt {
         __syncwarp();
     }
 
-    __device__ __forceinline__ void end(float *ml, int lane)
+    __device__ __forceinline__ void end(const AttnParams &p, float *ml, int lane)
     {
 #pragma unroll
         for (int r = 0; r < MR; ++r) {
 #pragma unroll
             for (int x = 16; x >= 1; x >>= 1)
                 l[r] += __shfl_xor_sync(0xffffffffu, l[r], x);
+            m[r] *= p.f;
             if (lane == 0) {
                 ml[2 * r] = m[r];
                 ml[2 * r + 1] = l[r];
@@ -777,7 +847,7 @@ struct Simt {
 #pragma unroll
                 for (int n = 0; n < NV; ++n) {
                     const int c = 4 * lane + 128 * n;
-                    if (c < p.a.d.headdim) {
+                    if (c < dim(p)) {
                         float4 *at = reinterpret_cast<float4 *>(buf + r * ds + c);
                         float4 v = make_float4(o[r][n][0] * f, o[r][n][1] * f, o[r][n][2] * f, o[r][n][3] * f);
                         if (ADD) {
@@ -801,60 +871,43 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 v)
     *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
 }
 
-// shared memory: the warps' rings, two join buffers, (fp32) the warps' query
-// rows and weights -- all of whole 16-byte segments -- then maxima, sums and
-// slot masks
-template <typename M, int DP, int NH>
+// shared memory: the warps' rings, two join buffers, (fp32) the query rows and
+// the warps' weights -- all of whole 16-byte segments -- then maxima, sums and
+// slot masks.  NU: units in a warp's ring.
+template <typename M, int NU>
 struct Layout {
-    static constexpr int kMask = kWarps * NH;
-    static __host__ __device__ int join_stride(int D) { return D + 8; }
-    static __host__ __device__ int ring_bytes(int stride) { return kWarps * NH * kUnit * stride; }
-    static __host__ __device__ int join_bytes(int D) { return 2 * M::MR * join_stride(D) * 4; }
-    static constexpr int kSmall = (kWarps * M::MR * 2 + M::MR * 2 + kMask) * 4;
     static constexpr bool kSimt = sizeof(typename M::T) == 4;
-    static constexpr int kQuery = kSimt ? (M::MR * DP + kWarps * M::MR * 16) * 4 : 0;
+    static constexpr int kQuery = kSimt ? (M::MR * M::kDim + kWarps * M::MR * 16) * 4 : 0;
+    static constexpr int kSmall = (kWarps * M::MR * 2 + M::MR * 2 + kWarps * NU) * 4;
+    static __host__ __device__ int join_stride(int D) { return D + 8; }
+    static __host__ __device__ int ring_bytes(int stride) { return kWarps * NU * 2 * M::kUnit * stride; }
+    static __host__ __device__ int join_bytes(int D) { return 2 * M::MR * join_stride(D) * 4; }
     static __host__ __device__ int total(int D, int stride) { return ring_bytes(stride) + join_bytes(D) + kSmall + kQuery; }
 };
 
-template <int R, int DP>
-__device__ __forceinline__ void bind(Simt<R, DP> &m, float *q, float *s) { m.qs = q; m.ps = s; }
-template <int NM, int DP>
-__device__ __forceinline__ void bind(Mma<NM, DP> &, float *, float *) {}
-
-template <int R, int DP>
-__device__ __forceinline__ void do_scores(Simt<R, DP> &m, const AttnParams &p, char *slot, uint32_t mask, int tok0, int a0, int a1, int lane)
+template <typename M>
+__device__ __forceinline__ void bind(M &m, float *q, float *w)
 {
-    m.scores(p, slot, mask, tok0, a0, a1, lane);
-}
-template <int NM, int DP>
-__device__ __forceinline__ void do_scores(Mma<NM, DP> &m, const AttnParams &p, char *slot, uint32_t mask, int tok0, int a0, int a1, int lane)
-{
-    m.scores(p, smem_addr(slot), mask, tok0, a0, a1, lane);
-}
-template <int R, int DP>
-__device__ __forceinline__ void do_values(Simt<R, DP> &m, const AttnParams &p, char *slot, uint32_t mask, int tok0, int a0, int a1, int lane)
-{
-    m.values(p, slot, mask, tok0, a0, a1, lane);
-}
-template <int NM, int DP>
-__device__ __forceinline__ void do_values(Mma<NM, DP> &m, const AttnParams &p, char *slot, uint32_t mask, int tok0, int a0, int a1, int lane)
-{
-    m.values(p, smem_addr(slot), slot, mask, tok0, a0, a1, lane);
+    if constexpr (sizeof(typename M::T) == 4) {
+        m.qs = q;
+        m.ps = w;
+    }
 }
 
-template <typename M, int DP, int NH>
+template <typename M, int NU>
 __global__ void __launch_bounds__(kThreads) ssd_paged_attn_kernel(const __grid_constant__ AttnParams p)
 {
     using T = typename M::T;
-    using L = Layout<M, DP, NH>;
+    using L = Layout<M, NU>;
+    constexpr int UT = M::kUnit;
     extern __shared__ __align__(16) char smem[];
     __shared__ Found found;
     __shared__ long long tmp[kWarps];
-    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, D = p.a.d.headdim;
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, D = M::dim(p), stride = M::row_bytes(p);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     long long total, per, u0;
-    locate(p, reinterpret_cast<int *>(smem), tmp, &found, total, per, u0);
+    locate<UT>(p, reinterpret_cast<int *>(smem), tmp, &found, total, per, u0);
     // padding rows see nothing
     if (p.a.start) {
         const long long r0 = min((long long)max(p.a.start[p.a.d.nreq], 0), (long long)p.a.d.nrows);
@@ -872,58 +925,66 @@ __global__ void __launch_bounds__(kThreads) ssd_paged_attn_kernel(const __grid_c
     if (u0 >= total)
         return;
     const long long u1 = min(u0 + per, total);
-    char *ring = smem + (size_t)w * NH * kUnit * p.stride;
-    const int slot_bytes = kUnit * p.stride;
-    float *join = reinterpret_cast<float *>(smem + L::ring_bytes(p.stride));
+    const int half_bytes = UT * stride;
+    char *ring = smem + (size_t)w * NU * 2 * half_bytes;    // [NU][K, V][UT][stride]
+    float *join = reinterpret_cast<float *>(smem + L::ring_bytes(stride));
     float *qs = join + L::join_bytes(D) / 4;                 // (16-byte accesses up to here)
     float *ml = join + (L::join_bytes(D) + L::kQuery) / 4;   // [kWarps][MR][2]
     float *joint = ml + kWarps * M::MR * 2;                  // [MR] maxima, [MR] sums
-    uint32_t *masks = reinterpret_cast<uint32_t *>(joint + M::MR * 2) + w * NH;
+    uint32_t *masks = reinterpret_cast<uint32_t *>(joint + M::MR * 2) + w * NU;
     const int ds = L::join_stride(D);
     __syncthreads();   // (the schedule's use of the ring's memory is over)
     // segments past the head's elements are read by the products: zero once
-    for (int i = tid; i < kWarps * NH * kUnit; i += kThreads)
-        for (int c = p.seg; c * 16 < p.stride; ++c)
-            *reinterpret_cast<uint4 *>(smem + (size_t)i * p.stride + c * 16) = make_uint4(0, 0, 0, 0);
-    __syncthreads();
+    if (!M::kExact) {
+        for (int i = tid; i < kWarps * NU * 2 * UT; i += kThreads)
+            for (int c = p.seg; c * 16 < stride; ++c)
+                *reinterpret_cast<uint4 *>(smem + (size_t)i * stride + c * 16) = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+    }
 
     Cursor cur;
-    set_tile(p, cur.t, found.req, found.j);
+    set_tile<UT>(p, cur.t, found.req, found.j);
     cur.item = (int)((u0 - found.lin) / cur.t.units);
     cur.lin = found.lin + (long long)cur.item * cur.t.units;
 
-    Loader ld;
+    // Steps alternate: while a unit's K is used the V half of the ring's newest
+    // unit is loaded, while its V is used the next unit's K.  Every step is one
+    // group of asynchronous copies, empty past the share's end.
+    Loader<T, M::kDim, M::kExact, UT> ld;
     ld.c = cur;
     ld.u1 = u1;
+    ld.set_end();
     ld.u = (int)(u0 - cur.lin);
-    ld.page = -1;
-    loader_skip(p, ld, w);
-    loader_fetch_page(p, ld, lane);
-    int head = 0;        // ring slot of the next half to load
-    bool vhalf = false;  // the next half to load is V
-    auto load_half = [&]() {
+    ld.skip(p, w);
+    ld.fetch_page(p, lane);
+    int head = 0;
+    auto load_k = [&]() {
         if (ld.u >= 0) {
-            if (!vhalf) {
-                loader_offsets<T>(p, ld, lane);
-                if (lane == 0)
-                    masks[head] = ld.mask;
-                loader_copy<T, DP>(p, ld, p.a.kc, ld.koff, p.a.d.kc_stride[1], smem_addr(ring + head * slot_bytes), lane);
-            } else {
-                loader_copy<T, DP>(p, ld, p.a.vc, ld.voff, p.a.d.vc_stride[1], smem_addr(ring + head * slot_bytes), lane);
-                loader_skip(p, ld, kWarps);
-                loader_fetch_page(p, ld, lane);
-            }
-            vhalf = !vhalf;
-            head = head + 1 == NH ? 0 : head + 1;
+            ld.offsets(p, lane);
+            if (lane == 0)
+                masks[head] = ld.mask;
+            ld.copy(p, p.a.kc, ld.koff, p.a.d.kc_stride[1], smem_addr(ring + head * 2 * half_bytes), lane);
+        }
+        cp_commit();
+    };
+    auto load_v = [&]() {
+        if (ld.u >= 0) {
+            ld.copy(p, p.a.vc, ld.voff, p.a.d.vc_stride[1], smem_addr(ring + (head * 2 + 1) * half_bytes), lane);
+            ld.skip(p, kWarps);
+            ld.fetch_page(p, lane);
+            head = head + 1 == NU ? 0 : head + 1;
         }
         cp_commit();
     };
 #pragma unroll 1
-    for (int i = 0; i < NH - 1; ++i)
-        load_half();
+    for (int i = 0; i < NU - 1; ++i) {
+        load_k();
+        load_v();
+    }
+    load_k();
 
     M math;
-    bind(math, qs, qs + (size_t)M::MR * DP + w * M::MR * 16);
+    bind(math, qs, qs + (size_t)M::MR * M::kDim + w * M::MR * 16);
     int tail = 0;
     int u = (int)(u0 - cur.lin);   // first unit of the share in this item
     while (true) {
@@ -942,21 +1003,21 @@ __global__ void __launch_bounds__(kThreads) ssd_paged_attn_kernel(const __grid_c
         // this warp's units: those whose number in the share is w modulo the warps
         const int skip = (w - (int)((cur.lin + u - u0) % kWarps) + kWarps) % kWarps;
         for (int x = u + skip; x < ue; x += kWarps) {
-            const int tok0 = (cur.t.ub + x) * kUnit;
-            cp_wait<NH - 2>();
+            const int tok0 = (cur.t.ub + x) * UT;
+            char *slot = ring + tail * 2 * half_bytes;
+            cp_wait<2 * NU - 2>();
             __syncwarp();
-            load_half();
             const uint32_t mask = masks[tail];
-            do_scores(math, p, ring + tail * slot_bytes, mask, tok0, all0, all1, lane);
-            tail = tail + 1 == NH ? 0 : tail + 1;
-            cp_wait<NH - 2>();
+            load_v();
+            math.scores(p, slot, mask, tok0, all0, all1, lane);
+            cp_wait<2 * NU - 2>();
             __syncwarp();
-            load_half();
-            do_values(math, p, ring + tail * slot_bytes, mask, tok0, all0, all1, lane);
-            tail = tail + 1 == NH ? 0 : tail + 1;
+            load_k();
+            math.values(p, slot + half_bytes, mask, tok0, all0, all1, lane);
+            tail = tail + 1 == NU ? 0 : tail + 1;
         }
         // join the warps
-        math.end(ml + w * M::MR * 2, lane);
+        math.end(p, ml + w * M::MR * 2, lane);
         __syncthreads();
         if (tid < M::MR) {
             float mm = -INFINITY, ll = 0.f;
@@ -1010,7 +1071,7 @@ __global__ void __launch_bounds__(kThreads) ssd_paged_attn_kernel(const __grid_c
             break;
         __syncthreads();   // (the join buffers are free again)
         u = 0;
-        next_item(p, cur);
+        next_item<UT>(p, cur);
     }
     cp_wait<0>();
 }
@@ -1103,8 +1164,6 @@ int tile_rows(const ssd_attn_dims_t &d)
     const long long want = rows_wanted(d);
     if (d.dtype == SSD_DTYPE_BF16)
         return want > 16 && d.headdim <= 128 ? 32 : 16;
-    if (d.headdim > 128)
-        return want <= 2 ? 2 : 8;
     return want <= 1 ? 1 : want <= 2 ? 2 : want <= 4 ? 4 : 8;
 }
 
@@ -1121,13 +1180,13 @@ int sm_count()
     return n[dev];
 }
 
-template <typename M, int DP, int NH>
+template <typename M, int NU>
 cudaError_t launch(AttnParams &p, void *workspace, cudaStream_t stream)
 {
     using T = typename M::T;
     const int D = p.a.d.headdim;
-    const int smem = std::max(Layout<M, DP, NH>::total(D, p.stride), p.a.start ? (int)(p.a.d.nreq + 1) * 4 : 0);
-    auto kernel = ssd_paged_attn_kernel<M, DP, NH>;
+    const int smem = std::max(Layout<M, NU>::total(D, p.stride), p.a.start ? (int)(p.a.d.nreq + 1) * 4 : 0);
+    auto kernel = ssd_paged_attn_kernel<M, NU>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess)
         return e;
@@ -1159,6 +1218,41 @@ cudaError_t launch(AttnParams &p, void *workspace, cudaStream_t stream)
     return e;
 }
 
+cudaError_t launch_bf16(AttnParams &p, int mr, void *ws, cudaStream_t st)
+{
+    const int D = p.a.d.headdim;
+    if (D == 64)
+        return mr == 32 ? launch<Mma<2, 64, true, 1>, 4>(p, ws, st) : launch<Mma<1, 64, true, 2>, 2>(p, ws, st);
+    if (D == 128)
+        return mr == 32 ? launch<Mma<2, 128, true, 1>, 2>(p, ws, st) : launch<Mma<1, 128, true, 1>, 2>(p, ws, st);
+    if (D <= 128)
+        return mr == 32 ? launch<Mma<2, 128, false, 1>, 2>(p, ws, st) : launch<Mma<1, 128, false, 1>, 2>(p, ws, st);
+    return launch<Mma<1, 256, false, 1>, 2>(p, ws, st);
+}
+
+template <int MR>
+cudaError_t launch_f32_rows(AttnParams &p, void *ws, cudaStream_t st)
+{
+    const int D = p.a.d.headdim;
+    if (D == 64)
+        return launch<Simt<MR, 64, true>, 2>(p, ws, st);
+    if (D == 128)
+        return launch<Simt<MR, 128, true>, MR == 8 ? 1 : 2>(p, ws, st);
+    if (D <= 128)
+        return launch<Simt<MR, 128, false>, MR == 8 ? 1 : 2>(p, ws, st);
+    return launch<Simt<MR, 256, false>, 1>(p, ws, st);
+}
+
+cudaError_t launch_f32(AttnParams &p, int mr, void *ws, cudaStream_t st)
+{
+    switch (mr) {
+    case 1: return launch_f32_rows<1>(p, ws, st);
+    case 2: return launch_f32_rows<2>(p, ws, st);
+    case 4: return launch_f32_rows<4>(p, ws, st);
+    default: return launch_f32_rows<8>(p, ws, st);
+    }
+}
+
 }  // namespace
 
 size_t attn_workspace_bytes(const ssd_attn_dims_t &d)
@@ -1182,30 +1276,15 @@ cudaError_t attn_launch(const AttnArgs &a, void *workspace, cudaStream_t stream)
     // rows of an odd number of 16-byte segments: eight rows' segments lie in different banks
     const int seg = es == 2 ? (p.seg + 1) / 2 * 2 : p.seg;
     p.stride = (seg | 1) * 16;
-    p.same_page = a.d.page_size % kUnit == 0;
+    p.same16 = a.d.page_size % 16 == 0;
+    // scores are kept as q.k times the scale's sign, so that their maximum is that of the scaled ones
+    p.sign = a.d.scale > 0.f ? 1 : a.d.scale < 0.f ? -1 : 0;
+    p.f = p.sign ? fabsf(a.d.scale) * kLog2e : 1.f;
     p.page.sh = 31;
     while ((1u << (p.page.sh - 31)) < (uint32_t)a.d.page_size)
         ++p.page.sh;
     p.page.mul = (uint32_t)((1ull << p.page.sh) / (uint32_t)a.d.page_size + 1);
-    if (a.d.dtype == SSD_DTYPE_BF16) {
-        if (D <= 64)
-            return mr == 32 ? launch<Mma<2, 64>, 64, 8>(p, workspace, stream) : launch<Mma<1, 64>, 64, 9>(p, workspace, stream);
-        if (D <= 128)
-            return mr == 32 ? launch<Mma<2, 128>, 128, 4>(p, workspace, stream) : launch<Mma<1, 128>, 128, 5>(p, workspace, stream);
-        return launch<Mma<1, 256>, 256, 5>(p, workspace, stream);
-    }
-    if (D <= 64)
-        return mr == 1 ? launch<Simt<1, 64>, 64, 5>(p, workspace, stream)
-             : mr == 2 ? launch<Simt<2, 64>, 64, 5>(p, workspace, stream)
-             : mr == 4 ? launch<Simt<4, 64>, 64, 5>(p, workspace, stream)
-                       : launch<Simt<8, 64>, 64, 5>(p, workspace, stream);
-    if (D <= 128)
-        return mr == 1 ? launch<Simt<1, 128>, 128, 3>(p, workspace, stream)
-             : mr == 2 ? launch<Simt<2, 128>, 128, 3>(p, workspace, stream)
-             : mr == 4 ? launch<Simt<4, 128>, 128, 3>(p, workspace, stream)
-                       : launch<Simt<8, 128>, 128, 2>(p, workspace, stream);
-    return mr == 2 ? launch<Simt<2, 256>, 256, 3>(p, workspace, stream)
-                   : launch<Simt<8, 256>, 256, 3>(p, workspace, stream);
+    return a.d.dtype == SSD_DTYPE_BF16 ? launch_bf16(p, mr, workspace, stream) : launch_f32(p, mr, workspace, stream);
 }
 
 }  // namespace ssd
