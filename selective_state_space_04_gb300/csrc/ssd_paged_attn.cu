@@ -33,6 +33,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "f32x2.cuh"
 #include "ssd_internal.h"
 
 namespace ssd {
@@ -419,6 +420,17 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// the largest of the warps' maxima of row r (0 when no warp saw a token)
+template <int MR>
+__device__ __forceinline__ float joint_max(const float *ml, int r)
+{
+    float v = ml[2 * r];
+#pragma unroll
+    for (int i = 1; i < kWarps; ++i)
+        v = fmaxf(v, ml[(i * MR + r) * 2]);
+    return v == -INFINITY ? 0.f : v;
+}
+
 // NM: tiles of 16 query rows; DP: the head's elements, rounded up (EXACT: as
 // they are); NT: 16-token halves of a unit.  A lane holds results of rows
 // lane / 4 and lane / 4 + 8 of each tile.
@@ -663,9 +675,18 @@ struct Mma {
                 }
             }
     }
-    // rows scaled to the joint maximum `base[r]`, written to or added to buf [MR][ds]
+    // m becomes the factor that brings the warp's rows to the warps' joint maximum
+    __device__ __forceinline__ void rescale(const float *ml, int lane)
+    {
+#pragma unroll
+        for (int mt = 0; mt < NM; ++mt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                m[mt][x] = exp2_fast(m[mt][x] - joint_max<MR>(ml, mt * 16 + x * 8 + (lane >> 2)));
+    }
+    // the scaled rows, written to or added to buf [MR][ds]
     template <bool ADD>
-    __device__ __forceinline__ void put(const AttnParams &p, const float *base, float *buf, int ds, int rows, int lane)
+    __device__ __forceinline__ void put(const AttnParams &p, float *buf, int ds, int rows, int lane)
     {
 #pragma unroll
         for (int mt = 0; mt < NM; ++mt)
@@ -673,7 +694,7 @@ struct Mma {
             for (int x = 0; x < 2; ++x) {
                 const int r = mt * 16 + x * 8 + (lane >> 2);
                 if (r < rows) {
-                    const float f = exp2_fast(m[mt][x] - base[r]);
+                    const float f = m[mt][x];
 #pragma unroll
                     for (int n = 0; n < DP / 8; ++n) {
                         const int c = 8 * n + 2 * (lane & 3);
@@ -695,20 +716,24 @@ struct Mma {
 
 // ---- the arithmetic: fp32 ---------------------------------------------------
 
-// Scores: lane = token (16) and half of the head's elements (2), the query rows
-// read from shared memory (the same address for all tokens: a broadcast), one
-// shuffle to add the halves.  Output: lane = elements 4 lane .. (+ 128), the
-// weights read back from shared memory by token.
+// Scores: a unit's 32 tokens over the lanes (16 tokens, two lanes each, where
+// 32 rows of K for every warp do not fit shared memory), the query rows read
+// from shared memory at the same address by all lanes.  Output: a lane holds 4
+// elements of every row (8 for heads above 128); for heads of at most 64 the
+// half warps take tokens in turn.  The weights go through shared memory.
+// Products and sums are packed pairs of fp32 FMA.
 template <int MRows, int DP, bool EX>
 struct Simt {
     using T = float;
-    static constexpr int MR = MRows, kDim = DP, kUnit = 16;
+    static constexpr int MR = MRows, kDim = DP, kUnit = DP > 128 ? 16 : 32;
     static constexpr bool kExact = EX;
-    static constexpr int NV = (DP + 127) / 128;   // float4 of the output per lane and row
-    float o[MR][NV][4];
+    static constexpr int kPer = 32 / kUnit;              // lanes per token in the scores
+    static constexpr int kGroups = DP <= 64 ? 2 : 1;     // tokens at a time in the output
+    static constexpr int NV = (DP + 127) / 128;          // float4 of the output per lane and row
+    f32x2 o[MR][NV][2];
     float m[MR], l[MR];   // m: the running maximum of q.k (of -q.k for a negative scale)
     int lo[MR], hi[MR];
-    float *qs, *ps;       // the CTA's query rows [MR][DP], this warp's weights [MR][16]
+    float *qs, *ps;       // the CTA's query rows [MR][DP], this warp's weights [MR][kUnit]
 
     __device__ __forceinline__ static int dim(const AttnParams &p) { return EX ? DP : p.a.d.headdim; }
     __device__ __forceinline__ static int row_bytes(const AttnParams &p) { return EX ? ((DP / 4) | 1) * 16 : p.stride; }
@@ -739,55 +764,55 @@ struct Simt {
                 }
 #pragma unroll
             for (int n = 0; n < NV; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    o[r][n][i] = 0.f;
+                o[r][n][0] = o[r][n][1] = pk2(0.f, 0.f);
         }
         __syncthreads();   // (each warp has loaded some of the rows)
     }
 
     __device__ __forceinline__ void scores(const AttnParams &p, char *slot, uint32_t mask, int tok0, int all0, int all1, int lane)
     {
-        const int tt = lane & 15, half = lane >> 4, D = dim(p);
-        const float4 *k = reinterpret_cast<const float4 *>(slot + tt * row_bytes(p));
-        float acc[MR];
+        const int tt = lane % kUnit, part = lane / kUnit, D = dim(p);
+        const ulonglong2 *k = reinterpret_cast<const ulonglong2 *>(slot + tt * row_bytes(p));
+        f32x2 acc[MR][2];
 #pragma unroll
         for (int r = 0; r < MR; ++r)
-            acc[r] = 0.f;
-        // the halves take float4s in turn: 2c + half
-        for (int c = half; c < D / 4; c += 2) {
-            const float4 kv = k[c];
+            acc[r][0] = acc[r][1] = pk2(0.f, 0.f);
+#pragma unroll 4
+        for (int c = part; c < D / 4; c += kPer) {
+            const ulonglong2 kv = k[c];
 #pragma unroll
             for (int r = 0; r < MR; ++r) {
-                const float4 qv = *reinterpret_cast<const float4 *>(qs + r * DP + 4 * c);
-                acc[r] += qv.x * kv.x;
-                acc[r] += qv.y * kv.y;
-                acc[r] += qv.z * kv.z;
-                acc[r] += qv.w * kv.w;
+                const ulonglong2 qv = *reinterpret_cast<const ulonglong2 *>(qs + r * DP + 4 * c);
+                acc[r][0] = fma2(qv.x, kv.x, acc[r][0]);
+                acc[r][1] = fma2(qv.y, kv.y, acc[r][1]);
             }
         }
-        const bool masked = mask != 0xffffu || tok0 < all0 || tok0 + kUnit > all1;
+        constexpr uint32_t kAll = kUnit == 16 ? 0xffffu : 0xffffffffu;
+        const bool masked = mask != kAll || tok0 < all0 || tok0 + kUnit > all1;
 #pragma unroll
         for (int r = 0; r < MR; ++r) {
-            float v = acc[r] + __shfl_xor_sync(0xffffffffu, acc[r], 16);
+            float v = (lo2(acc[r][0]) + hi2(acc[r][0])) + (lo2(acc[r][1]) + hi2(acc[r][1]));
+            if (kPer == 2)
+                v += __shfl_xor_sync(0xffffffffu, v, 16);
             if (masked && (!((mask >> tt) & 1) || tok0 + tt < lo[r] || tok0 + tt >= hi[r]))
                 v = -INFINITY;
             float top = v;
 #pragma unroll
-            for (int x = 8; x >= 1; x >>= 1)
+            for (int x = kUnit / 2; x >= 1; x >>= 1)
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
             const float mn = fmaxf(m[r], top), base = (mn == -INFINITY ? 0.f : mn) * p.f;
             const float keep = exp2_fast(m[r] * p.f - base), e = exp2_fast(v * p.f - base);
             m[r] = mn;
-            l[r] = l[r] * keep + (half == 0 ? e : 0.f);   // summed over the lanes at the end
-            if (half == 0)
-                ps[r * 16 + tt] = e;
+            l[r] = l[r] * keep + (part == 0 ? e : 0.f);   // summed over the lanes at the end
+            if (part == 0)
+                ps[r * kUnit + tt] = e;
             if (keep != 1.f) {
+                const f32x2 kk = pk2(keep, keep);
 #pragma unroll
-                for (int n = 0; n < NV; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        o[r][n][i] *= keep;
+                for (int n = 0; n < NV; ++n) {
+                    o[r][n][0] = mul2(o[r][n][0], kk);
+                    o[r][n][1] = mul2(o[r][n][1], kk);
+                }
             }
         }
         __syncwarp();
@@ -795,28 +820,33 @@ struct Simt {
 
     __device__ __forceinline__ void values(const AttnParams &p, char *slot, uint32_t mask, int tok0, int all0, int all1, int lane)
     {
+        const int grp = kGroups == 2 ? lane >> 4 : 0, el = 4 * (kGroups == 2 ? lane & 15 : lane), stride = row_bytes(p);
         // tokens not read are zero in the slot; one that a row does not see is skipped for it
         const bool ragged = tok0 < all0 || tok0 + kUnit > all1;
-#pragma unroll 4
-        for (int tt = 0; tt < kUnit; ++tt) {
-            float4 v[NV];
+#pragma unroll 2
+        for (int t4 = 0; t4 < kUnit; t4 += 4) {
+            float w[MR][4];
 #pragma unroll
-            for (int n = 0; n < NV; ++n) {
-                const int c = 4 * lane + 128 * n;
-                v[n] = c < dim(p) ? *reinterpret_cast<const float4 *>(slot + tt * row_bytes(p) + 4 * c)
-                                         : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
+            for (int r = 0; r < MR; ++r)
+                *reinterpret_cast<float4 *>(w[r]) = *reinterpret_cast<const float4 *>(ps + r * kUnit + t4);
 #pragma unroll
-            for (int r = 0; r < MR; ++r) {
-                if (ragged && (tok0 + tt < lo[r] || tok0 + tt >= hi[r]))
-                    continue;
-                const float w = ps[r * 16 + tt];
+            for (int i = 0; i < 4 / kGroups; ++i) {
+                const int tt = t4 + i * kGroups + grp;
 #pragma unroll
                 for (int n = 0; n < NV; ++n) {
-                    o[r][n][0] += w * v[n].x;
-                    o[r][n][1] += w * v[n].y;
-                    o[r][n][2] += w * v[n].z;
-                    o[r][n][3] += w * v[n].w;
+                    const int c = el + 128 * n;
+                    ulonglong2 v = make_ulonglong2(0, 0);
+                    if (EX || c < dim(p))
+                        v = *reinterpret_cast<const ulonglong2 *>(slot + tt * stride + 4 * c);
+#pragma unroll
+                    for (int r = 0; r < MR; ++r) {
+                        const float e = kGroups == 2 && grp ? w[r][(kGroups * i + 1) & 3] : w[r][kGroups * i];
+                        if (!ragged || (tok0 + tt >= lo[r] && tok0 + tt < hi[r])) {
+                            const f32x2 ee = pk2(e, e);
+                            o[r][n][0] = fma2(ee, v.x, o[r][n][0]);
+                            o[r][n][1] = fma2(ee, v.y, o[r][n][1]);
+                        }
+                    }
                 }
             }
         }
@@ -835,21 +865,35 @@ struct Simt {
                 ml[2 * r] = m[r];
                 ml[2 * r + 1] = l[r];
             }
+            if (kGroups == 2) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    o[r][0][i] = pk2(lo2(o[r][0][i]) + __shfl_xor_sync(0xffffffffu, lo2(o[r][0][i]), 16),
+                                     hi2(o[r][0][i]) + __shfl_xor_sync(0xffffffffu, hi2(o[r][0][i]), 16));
+            }
         }
     }
-    template <bool ADD>
-    __device__ __forceinline__ void put(const AttnParams &p, const float *base, float *buf, int ds, int rows, int lane)
+    __device__ __forceinline__ void rescale(const float *ml, int)
     {
+#pragma unroll
+        for (int r = 0; r < MR; ++r)
+            m[r] = exp2_fast(m[r] - joint_max<MR>(ml, r));
+    }
+    template <bool ADD>
+    __device__ __forceinline__ void put(const AttnParams &p, float *buf, int ds, int rows, int lane)
+    {
+        if (kGroups == 2 && lane >= 16)
+            return;
 #pragma unroll
         for (int r = 0; r < MR; ++r) {
             if (r < rows) {
-                const float f = exp2_fast(m[r] - base[r]);
+                const float f = m[r];
 #pragma unroll
                 for (int n = 0; n < NV; ++n) {
                     const int c = 4 * lane + 128 * n;
                     if (c < dim(p)) {
                         float4 *at = reinterpret_cast<float4 *>(buf + r * ds + c);
-                        float4 v = make_float4(o[r][n][0] * f, o[r][n][1] * f, o[r][n][2] * f, o[r][n][3] * f);
+                        float4 v = make_float4(lo2(o[r][n][0]) * f, hi2(o[r][n][0]) * f, lo2(o[r][n][1]) * f, hi2(o[r][n][1]) * f);
                         if (ADD) {
                             const float4 u = *at;
                             v.x += u.x;
@@ -877,7 +921,7 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 v)
 template <typename M, int NU>
 struct Layout {
     static constexpr bool kSimt = sizeof(typename M::T) == 4;
-    static constexpr int kQuery = kSimt ? (M::MR * M::kDim + kWarps * M::MR * 16) * 4 : 0;
+    static constexpr int kQuery = kSimt ? (M::MR * M::kDim + kWarps * M::MR * M::kUnit) * 4 : 0;
     static constexpr int kSmall = (kWarps * M::MR * 2 + M::MR * 2 + kWarps * NU) * 4;
     static __host__ __device__ int join_stride(int D) { return D + 8; }
     static __host__ __device__ int ring_bytes(int stride) { return kWarps * NU * 2 * M::kUnit * stride; }
@@ -904,6 +948,9 @@ __global__ void __launch_bounds__(kThreads) ssd_paged_attn_kernel(const __grid_c
     __shared__ Found found;
     __shared__ long long tmp[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, D = M::dim(p), stride = M::row_bytes(p);
+    // The call's launches are programmatic dependents: each starts while the one
+    // before it runs out and waits here for all of it.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     long long total, per, u0;
@@ -984,7 +1031,7 @@ __global__ void __launch_bounds__(kThreads) ssd_paged_attn_kernel(const __grid_c
     load_k();
 
     M math;
-    bind(math, qs, qs + (size_t)M::MR * M::kDim + w * M::MR * 16);
+    bind(math, qs, qs + (size_t)M::MR * M::kDim + w * M::MR * M::kUnit);
     int tail = 0;
     int u = (int)(u0 - cur.lin);   // first unit of the share in this item
     while (true) {
@@ -1016,28 +1063,26 @@ __global__ void __launch_bounds__(kThreads) ssd_paged_attn_kernel(const __grid_c
             math.values(p, slot + half_bytes, mask, tok0, all0, all1, lane);
             tail = tail + 1 == NU ? 0 : tail + 1;
         }
-        // join the warps
+        // join the warps: three barriers; the next tile's writes to ml, joint and
+        // the buffers come after its own first or second one
         math.end(p, ml + w * M::MR * 2, lane);
         __syncthreads();
         if (tid < M::MR) {
-            float mm = -INFINITY, ll = 0.f;
-#pragma unroll
-            for (int i = 0; i < kWarps; ++i)
-                mm = fmaxf(mm, ml[(i * M::MR + tid) * 2]);
-            const float base = mm == -INFINITY ? 0.f : mm;
+            float ll = 0.f;
+            const float base = joint_max<M::MR>(ml, tid);
 #pragma unroll
             for (int i = 0; i < kWarps; ++i)
                 ll += ml[(i * M::MR + tid) * 2 + 1] * exp2_fast(ml[(i * M::MR + tid) * 2] - base);
             joint[tid] = base;
             joint[M::MR + tid] = ll;
         }
-        __syncthreads();
+        math.rescale(ml, lane);
         float *buf = join + (w & 1) * M::MR * ds;
         if (w >= 2)
-            math.template put<false>(p, joint, buf, ds, rows, lane);
+            math.template put<false>(p, buf, ds, rows, lane);
         __syncthreads();
         if (w < 2)
-            math.template put<true>(p, joint, buf, ds, rows, lane);
+            math.template put<true>(p, buf, ds, rows, lane);
         __syncthreads();
         const bool whole = u == 0 && ue == cur.t.units;
         const int slot = u > 0 ? 0 : 1;   // a tile begun in an earlier share, or in this one
@@ -1069,7 +1114,6 @@ __global__ void __launch_bounds__(kThreads) ssd_paged_attn_kernel(const __grid_c
             p.desc[blockIdx.x] = make_int4(cur.t.row, cur.t.nq, cur.item, (int)((cur.lin + cur.t.units - 1) / per));
         if (cur.lin + ue >= u1)
             break;
-        __syncthreads();   // (the join buffers are free again)
         u = 0;
         next_item<UT>(p, cur);
     }
@@ -1085,6 +1129,7 @@ __global__ void __launch_bounds__(128) ssd_paged_attn_join_kernel(const __grid_c
     __shared__ float sm[4][2];
     __shared__ float so[4][256];
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int4 d = p.desc[blockIdx.x];
     if (d.x < 0)
         return;
@@ -1096,32 +1141,47 @@ __global__ void __launch_bounds__(128) ssd_paged_attn_join_kernel(const __grid_c
     // part i lies in share c0 + i: slot 1 of the first, slot 0 of the others
     auto part = [&](int i) { return ((size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * MR + r; };
     const int n = c1 - c0 + 1;
-    float mm = -INFINITY;
-    for (int i = threadIdx.x; i < n; i += 128)
-        mm = fmaxf(mm, p.part_ml[2 * part(i) + 1] == 0.f ? -INFINITY : p.part_ml[2 * part(i)]);
+    // each warp joins its parts in the running form, so that their maxima and
+    // rows are loaded together, four parts at a time
+    float mm = -INFINITY, ll = 0.f, o[2][4] = {};
+    for (int i = w; i < n; i += 16) {
+        float pm[4], pl[4];
+        float4 v[4][2];
 #pragma unroll
-    for (int x = 16; x >= 1; x >>= 1)
-        mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x));
-    if (lane == 0)
-        sm[w][0] = mm;
-    __syncthreads();
-    mm = fmaxf(fmaxf(sm[0][0], sm[1][0]), fmaxf(sm[2][0], sm[3][0]));
-    const float base = mm == -INFINITY ? 0.f : mm;
-    float ll = 0.f, o[2][4] = {};
-#pragma unroll 4
-    for (int i = w; i < n; i += 4) {
-        const size_t at = part(i);
-        const float lp = p.part_ml[2 * at + 1], f = lp == 0.f ? 0.f : exp2_fast(p.part_ml[2 * at] - base);
-        ll += lp * f;
+        for (int b = 0; b < 4; ++b) {
+            pm[b] = -INFINITY;
+            pl[b] = 0.f;
+            v[b][0] = v[b][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i + 4 * b < n) {
+                const size_t at = part(i + 4 * b);
+                const float2 t = *reinterpret_cast<const float2 *>(p.part_ml + 2 * at);
+                pm[b] = t.y == 0.f ? -INFINITY : t.x;   // (a part that saw nothing)
+                pl[b] = t.y;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int c = 4 * lane + 128 * k;
-            if (c < D) {
-                const float4 v = *reinterpret_cast<const float4 *>(p.part_o + at * D + c);
-                o[k][0] += f * v.x;
-                o[k][1] += f * v.y;
-                o[k][2] += f * v.z;
-                o[k][3] += f * v.w;
+                for (int k = 0; k < 2; ++k)
+                    if (4 * lane + 128 * k < D)
+                        v[b][k] = *reinterpret_cast<const float4 *>(p.part_o + at * D + 4 * lane + 128 * k);
+            }
+        }
+        const float mn = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])), mm), base = mn == -INFINITY ? 0.f : mn;
+        const float keep = exp2_fast(mm - base);
+        mm = mn;
+        ll *= keep;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                o[k][e] *= keep;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const float f = exp2_fast(pm[b] - base);
+            ll += pl[b] * f;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                o[k][0] += f * v[b][k].x;
+                o[k][1] += f * v[b][k].y;
+                o[k][2] += f * v[b][k].z;
+                o[k][3] += f * v[b][k].w;
             }
         }
     }
@@ -1130,10 +1190,18 @@ __global__ void __launch_bounds__(128) ssd_paged_attn_join_kernel(const __grid_c
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             so[w][4 * lane + 128 * k + e] = o[k][e];
-    if (lane == 0)
+    if (lane == 0) {
+        sm[w][0] = mm;
         sm[w][1] = ll;
+    }
     __syncthreads();
-    ll = (sm[0][1] + sm[1][1]) + (sm[2][1] + sm[3][1]);
+    mm = fmaxf(fmaxf(sm[0][0], sm[1][0]), fmaxf(sm[2][0], sm[3][0]));
+    const float base = mm == -INFINITY ? 0.f : mm;
+    float f[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        f[i] = exp2_fast(sm[i][0] - base);
+    ll = (sm[0][1] * f[0] + sm[1][1] * f[1]) + (sm[2][1] * f[2] + sm[3][1] * f[3]);
     const float inv = ll == 0.f ? 0.f : 1.f / ll;
     const int j = r / nh, h = kvh * p.group + hb * p.gh + (r - j * nh);
     for (int c = 4 * threadIdx.x; c < D; c += 512) {
@@ -1141,7 +1209,7 @@ __global__ void __launch_bounds__(128) ssd_paged_attn_join_kernel(const __grid_c
         float *e = &v.x;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            e[k] = ((so[0][c + k] + so[1][c + k]) + (so[2][c + k] + so[3][c + k])) * inv;
+            e[k] = ((so[0][c + k] * f[0] + so[1][c + k] * f[1]) + (so[2][c + k] * f[2] + so[3][c + k] * f[3])) * inv;
         store4(static_cast<T *>(p.a.out) + (long long)(row + j) * p.a.d.o_stride[0] + (long long)h * p.a.d.o_stride[1] + c, v);
     }
     if (p.a.lse && threadIdx.x == 0)
@@ -1167,7 +1235,8 @@ int tile_rows(const ssd_attn_dims_t &d)
     return want <= 1 ? 1 : want <= 2 ? 2 : want <= 4 ? 4 : 8;
 }
 
-constexpr int kMaxCtas = 1024;   // workspace is sized for at most this many CTAs
+constexpr int kMaxPerSm = 4;     // CTAs
+constexpr int kMaxCtas = 1024;   // the workspace is sized for at most this many
 
 int sm_count()
 {
@@ -1187,31 +1256,38 @@ cudaError_t launch(AttnParams &p, void *workspace, cudaStream_t stream)
     const int D = p.a.d.headdim;
     const int smem = std::max(Layout<M, NU>::total(D, p.stride), p.a.start ? (int)(p.a.d.nreq + 1) * 4 : 0);
     auto kernel = ssd_paged_attn_kernel<M, NU>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess)
+    // CTAs per SM by shared memory (227 KB for them, 1 KB of the system's each) and registers
+    static int regs = 0;   // (the same for every device)
+    cudaError_t e;
+    if (!regs) {
+        cudaFuncAttributes at;
+        if ((e = cudaFuncGetAttributes(&at, kernel)) != cudaSuccess)
+            return e;
+        regs = (at.numRegs + 7) / 8 * 8;
+    }
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
         return e;
-    int per_sm = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, smem);
-    if (e != cudaSuccess)
-        return e;
-    const int grid = std::min(kMaxCtas, sm_count() * std::max(1, std::min(per_sm, 4)));
+    const int per_sm = std::max(1, std::min({kMaxPerSm, (228 << 10) / (smem + 1024 + 256), 65536 / (regs * kThreads)}));
+    const int grid = std::min(kMaxCtas, sm_count() * per_sm);
     p.part_o = static_cast<float *>(workspace);
     p.part_ml = p.part_o + (size_t)grid * 2 * M::MR * D;
     p.desc = reinterpret_cast<int4 *>(p.part_ml + (size_t)grid * 2 * M::MR * 2);
-    kernel<<<grid, kThreads, smem, stream>>>(p);
-    e = cudaGetLastError();
-    if (e != cudaSuccess)
-        return e;
-    note_launches(1);
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, p.tok * p.gh);
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, kernel, p)) != cudaSuccess)
+        return e;
+    note_launches(1);
+    cfg.gridDim = dim3(grid, p.tok * p.gh);
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&cfg, ssd_paged_attn_join_kernel<T, M::MR>, p);
     if (e == cudaSuccess)
         note_launches(1);
@@ -1235,11 +1311,11 @@ cudaError_t launch_f32_rows(AttnParams &p, void *ws, cudaStream_t st)
 {
     const int D = p.a.d.headdim;
     if (D == 64)
-        return launch<Simt<MR, 64, true>, 2>(p, ws, st);
+        return launch<Simt<MR, 64, true>, 1>(p, ws, st);
     if (D == 128)
-        return launch<Simt<MR, 128, true>, MR == 8 ? 1 : 2>(p, ws, st);
+        return launch<Simt<MR, 128, true>, 1>(p, ws, st);
     if (D <= 128)
-        return launch<Simt<MR, 128, false>, MR == 8 ? 1 : 2>(p, ws, st);
+        return launch<Simt<MR, 128, false>, 1>(p, ws, st);
     return launch<Simt<MR, 256, false>, 1>(p, ws, st);
 }
 
@@ -1257,7 +1333,7 @@ cudaError_t launch_f32(AttnParams &p, int mr, void *ws, cudaStream_t st)
 
 size_t attn_workspace_bytes(const ssd_attn_dims_t &d)
 {
-    const int grid = std::min(kMaxCtas, sm_count() * 4);
+    const int grid = std::min(kMaxCtas, sm_count() * kMaxPerSm);
     return (size_t)grid * (2 * tile_rows(d) * (d.headdim + 2) * sizeof(float) + sizeof(int4));
 }
 
