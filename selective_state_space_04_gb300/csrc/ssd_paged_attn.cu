@@ -2,19 +2,25 @@
 //
 // A tile is up to MR query rows that read the same keys: the query heads of one
 // key-value head for one or several consecutive new tokens of a request.  The
-// tile's visible positions are cut into units of 16 or 32 tokens.  All units of all
-// tiles and key-value heads, laid end to end, are dealt to the CTAs in equal
-// contiguous shares, whatever the requests' lengths; one CTA per resident slot
-// stays for the whole launch.  Within its share a CTA's warps take units in
-// turn; each warp streams its own units through a ring of shared-memory slots
-// (asynchronous 16-byte copies, K and V halves alternating, zero-filled where a
-// token is not to be seen) and keeps its own running maximum, sum and output
-// rows in registers, so no barrier stands between loads and arithmetic.  Loads
-// run ahead across tile boundaries.  At the end of a tile's part in a share the
-// warps' results are joined in shared memory; a tile that lies in one share
-// is finished there, one that is cut leaves a partial result (maximum, sum,
-// unnormalised rows) for the second launch, which joins the parts in order of
-// their CTAs.
+// tile's visible positions are cut into units of 16 or 32 tokens.  All units of
+// all tiles and key-value heads, laid end to end, are dealt out in equal
+// contiguous shares, whatever the requests' lengths; the CTAs that fit the GPU
+// at once stay for the whole launch.  A warp streams its units through a ring of
+// shared-memory slots of its own, K and V halves in turn, and keeps a running
+// maximum, sum and output rows in registers: no barrier stands between loads and
+// arithmetic, and loads run ahead across tile boundaries.
+//
+// Shares belong to warps, or to CTAs, whose warps then take units in turn and
+// are joined in shared memory at the end of a tile (many tiles, or few: see
+// kernel).  A tile that lies in one share is finished there; one that is cut
+// leaves partial results (maximum, sum, unnormalised rows), which a second
+// launch joins in the order of their shares.
+//
+// Two ways into the ring: 16-byte asynchronous copies, each lane at a fixed
+// segment of every row, where sizes are known at compile time and 16 aligned
+// tokens never cross a page; else one bulk copy per token and half, which takes
+// any row length and any page (at most one row per about 9 cycles and SM, which
+// bounds rows of 128 bytes at 4.1 TB/s, rows of 256 at the memory's rate).
 //
 // The running form: with s2 = scale log2(e) q.k, m = max s2 so far,
 // p = 2^(s2 - m), l = sum p, o = sum p v; when m grows by d, l and o are
@@ -34,6 +40,7 @@
 #include <cstdint>
 
 #include "f32x2.cuh"
+#include "ptx.cuh"
 #include "ssd_internal.h"
 
 namespace ssd {
@@ -52,9 +59,10 @@ struct FastDiv {
 struct AttnParams {
     AttnArgs a;
     FastDiv page;
-    float *part_o;      // [grid][2][MR][D] partial rows
-    float *part_ml;     // [grid][2][MR][2] their maxima (base 2) and sums
-    int4 *desc;         // [grid] the cut tile that starts in a CTA's share: first row, tokens | item << 8, last CTA; or x = -1
+    float *part_o;      // [shares][2][MR][D] partial rows
+    float *part_ml;     // [shares][2][MR][2] their maxima (base 2) and sums
+    int4 *desc;         // [shares] the cut tile that starts in a share: first row, tokens, item, last share (~ of it
+                        // for shares of warps); x -1: none
     int group;          // query heads per key-value head
     int gh;             // query heads of a tile (group, or a part of it when it is larger than MR)
     int nhb;            // head blocks per key-value head
@@ -62,7 +70,7 @@ struct AttnParams {
     int items;          // nkv * nhb: tiles of the same rows
     int seg;            // 16-byte segments per row of K or V
     int stride;         // bytes from row to row of a ring slot (an odd number of segments)
-    int same16;         // 16 tokens from a multiple of 16 on never cross a page
+    int bulk;           // rows come by bulk copies
     float f;            // |scale| log2(e), or 1 for scale 0
     int sign;           // of scale
 };
@@ -204,12 +212,17 @@ struct Found {
     long long lin;   // the linear unit where the tile's first item begins
 };
 
-// Where the CTA's share begins.  Every CTA sums all tiles' units (a contiguous
-// run of tiles per thread); the thread whose run holds unit u0 finds the tile.
-// `counts` (shared memory, nreq + 1 ints) is used when there is a start array.
+struct Shares {
+    bool solo;           // one share per warp, not per CTA
+    long long total, per;   // units, and units of a share
+};
+
+// Where the CTA's shares begin (found[i]: of warp i's share, or found[0]).
+// Every CTA sums all tiles' units (a contiguous run of tiles per thread); the
+// thread whose run holds a share's first unit finds its tile.  `counts` (shared
+// memory, nreq + 1 ints) is used when there is a start array.
 template <int UT>
-__device__ void locate(const AttnParams &p, int *counts, long long *tmp, Found *found, long long &total, long long &per,
-                       long long &u0)
+__device__ Shares locate(const AttnParams &p, int *counts, long long *tmp, Found *found)
 {
     const int tid = threadIdx.x, nreq = (int)p.a.d.nreq;
     long long ntiles = p.a.d.nrows;
@@ -262,27 +275,33 @@ __device__ void locate(const AttnParams &p, int *counts, long long *tmp, Found *
     }
     long long sum;
     const long long before = block_exclusive(n, &sum, tmp) * p.items;
-    total = sum * p.items;
-    per = max((long long)kWarps, (total + gridDim.x - 1) / gridDim.x);
-    u0 = (long long)blockIdx.x * per;
-    if (t0 < t1 && u0 >= before && u0 < before + n * p.items) {
+    Shares sh;
+    sh.total = sum * p.items;
+    sh.solo = ntiles * p.items >= (long long)gridDim.x;
+    sh.per = sh.solo ? max(1ll, (sh.total + (long long)gridDim.x * kWarps - 1) / ((long long)gridDim.x * kWarps))
+                     : max((long long)kWarps, (sh.total + gridDim.x - 1) / gridDim.x);
+    if (t0 < t1) {
         long long lin = before;
-        for (long long i = t0; i < t1; ++i) {
-            if (i == t0)
+        const long long end = before + n * p.items;
+        for (int i = 0; i < (sh.solo ? kWarps : 1); ++i) {
+            const long long u0 = ((long long)blockIdx.x * (sh.solo ? kWarps : 1) + i) * sh.per;
+            if (u0 < before || u0 >= end)
+                continue;
+            if (i == 0 || lin == before) {   // (the walk goes on from share to share)
                 set_tile<UT>(p, t, f.req, f.j);
-            else
-                next_tile<UT>(p, t);
-            const long long here = (long long)t.units * p.items;
-            if (u0 < lin + here) {
-                found->req = t.req;
-                found->j = t.j;
-                found->lin = lin;
-                break;
+                lin = before;
             }
-            lin += here;
+            while (u0 >= lin + (long long)t.units * p.items) {
+                lin += (long long)t.units * p.items;
+                next_tile<UT>(p, t);
+            }
+            found[i].req = t.req;
+            found[i].j = t.j;
+            found[i].lin = lin;
         }
     }
     __syncthreads();
+    return sh;
 }
 
 // ---- the loader -------------------------------------------------------------
@@ -295,9 +314,9 @@ struct Loader {
     Cursor c;
     int u, u_end;          // the unit within the item (-1: none left); the share's units of the item
     long long u1;          // end of the share
-    int page;              // table entry read ahead (same16: of the lane's 16 tokens, else of the lane's token)
+    int page;              // table entry read ahead (bulk: of the lane's token, else of the lane's 16 tokens)
     uint32_t mask;         // the unit's tokens that are to be read
-    // byte offsets in the caches; same16: of the first token of each 16, else [0] is the lane's token's
+    // byte offsets in the caches: of the first token of each 16; bulk: [0] of the lane's token
     long long koff[kSub], voff[kSub];
 
     __device__ __forceinline__ void set_end() { u_end = (int)min((long long)c.t.units, u1 - c.lin); }
@@ -319,8 +338,8 @@ struct Loader {
     {
         page = -1;
         if (u >= 0) {
-            const int tok = (c.t.ub + u) * UT + (p.same16 ? (kSub > 1 ? lane & 16 : 0) : lane % UT);
-            if (tok < c.t.end)   // (same16: the page of 16 tokens is that of the first of them)
+            const int tok = (c.t.ub + u) * UT + (p.bulk ? lane % UT : kSub > 1 ? lane & 16 : 0);
+            if (tok < c.t.end)   // (16 tokens are in the page of the first of them)
                 page = __ldg(p.a.table + (long long)c.t.req * p.a.d.table_stride + div_page(p.page, tok));
         }
     }
@@ -332,7 +351,7 @@ struct Loader {
         if (UT == 16)
             mask &= 0xffffu;
         const int kvh = p.nhb == 1 ? c.item : c.item / p.nhb;
-        if (p.same16) {
+        if (!p.bulk) {
 #pragma unroll
             for (int b = 0; b < kSub; ++b) {
                 // (an entry out of range masks all 16 tokens: nothing is read at its offset)
@@ -348,53 +367,76 @@ struct Loader {
             voff[0] = (pg * p.a.d.vc_stride[0] + off * p.a.d.vc_stride[1] + kvh * p.a.d.vc_stride[2]) * (long long)sizeof(T);
         }
     }
-    // copies one half (UT tokens of K or V) into a ring slot
+    // one half (UT tokens of K or V) into a ring slot, by 16-byte copies
     __device__ __forceinline__ void copy(const AttnParams &p, const void *base, const long long (&off)[kSub], long long tstride,
                                          uint32_t slot, int lane)
     {
         const char *src = static_cast<const char *>(base);
         constexpr uint32_t kAll = UT == 16 ? 0xffffu : 0xffffffffu;
-        if (EXACT && p.same16) {
-            // a lane's segment is the same in each of its rows, which lie kRows apart
-            constexpr int kRows = 32 / kSegMax > 0 ? 32 / kSegMax : 1;   // rows per instruction
-            constexpr int kParts = kSegMax / 32 > 0 ? kSegMax / 32 : 1;  // instructions per row
-            constexpr int kStride = (kSegMax | 1) * 16;
-            const int r0 = lane / kSegMax, seg = lane % kSegMax;
-            const uint32_t dst = slot + r0 * kStride + seg * 16;
-            const long long ts = tstride * (long long)sizeof(T);
+        // a lane's segment is the same in each of its rows, which lie kRows apart
+        constexpr int kRows = 32 / kSegMax > 0 ? 32 / kSegMax : 1;   // rows per instruction
+        constexpr int kParts = kSegMax / 32 > 0 ? kSegMax / 32 : 1;  // instructions per row
+        constexpr int kStride = (kSegMax | 1) * 16;
+        const int r0 = lane / kSegMax, seg = lane % kSegMax;
+        const uint32_t dst = slot + r0 * kStride + seg * 16;
+        const long long ts = tstride * (long long)sizeof(T);
 #pragma unroll
-            for (int b = 0; b < kSub; ++b) {
-                const char *s = src + off[b] + r0 * ts + seg * 16;
+        for (int b = 0; b < kSub; ++b) {
+            const char *s = src + off[b] + r0 * ts + seg * 16;
 #pragma unroll
-                for (int i = 0; i < 16 / kRows; ++i) {
+            for (int i = 0; i < 16 / kRows; ++i) {
 #pragma unroll
-                    for (int x = 0; x < kParts; ++x) {
-                        const uint32_t d = dst + (16 * b + i * kRows) * kStride + x * 512;
-                        if (mask == kAll)
-                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(s + x * 512) : "memory");
-                        else {
-                            const bool on = (mask >> (16 * b + i * kRows + r0)) & 1;
-                            cp_async16(d, on ? s + x * 512 : static_cast<const char *>(p.a.q), on);
-                        }
+                for (int x = 0; x < kParts; ++x) {
+                    const uint32_t d = dst + (16 * b + i * kRows) * kStride + x * 512;
+                    if (mask == kAll)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(s + x * 512) : "memory");
+                    else {
+                        const bool on = (mask >> (16 * b + i * kRows + r0)) & 1;
+                        cp_async16(d, on ? s + x * 512 : static_cast<const char *>(p.a.q), on);
                     }
-                    s += kRows * ts;
                 }
-            }
-        } else {
-            const uint32_t inv = 65536u / (uint32_t)p.seg + 1;
-            const long long ts = tstride * (long long)sizeof(T);
-#pragma unroll 4
-            for (int i = 0; i < (UT * p.seg + 31) / 32; ++i) {
-                const int idx = lane + 32 * i, r = (int)((idx * inv) >> 16), s = idx - r * p.seg;
-                const bool in = r < UT, on = in && ((mask >> r) & 1);
-                const long long o = p.same16 ? (kSub > 1 && r >= 16 ? off[kSub - 1] : off[0]) + (r & 15) * ts
-                                             : __shfl_sync(0xffffffffu, off[0], r % UT);
-                if (in)
-                    cp_async16(slot + r * p.stride + s * 16, on ? src + o + s * 16 : static_cast<const char *>(p.a.q), on);
+                s += kRows * ts;
             }
         }
     }
+    // ... by one bulk copy per token; `bar` completes when all are there.  Rows
+    // of V that are not read are zeroed (those of K only give scores that are
+    // masked).
+    __device__ __forceinline__ void copy_bulk(const AttnParams &p, const void *base, long long off, char *slot, uint64_t *bar,
+                                              bool zero, int lane)
+    {
+        const int bytes = p.seg * 16;
+        char *dst = slot + (lane % UT) * p.stride;
+        const bool mine = lane < UT, on = mine && ((mask >> (lane % UT)) & 1);
+        if (zero && mine && !on) {
+            for (int c = 0; c < p.seg; ++c)
+                *reinterpret_cast<uint4 *>(dst + c * 16) = make_uint4(0, 0, 0, 0);
+            ptx::fence_proxy_async_smem();   // (later bulk copies write the row)
+        }
+        if (lane == 0)
+            ptx::mbar_arrive_expect_tx(bar, (uint32_t)(__popc(mask) * bytes));
+        __syncwarp();
+        if (on)
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                             smem_addr(dst)), "l"(static_cast<const char *>(base) + off), "r"(bytes), "r"(smem_addr(bar))
+                         : "memory");
+    }
 };
+
+// Set (to SSD_ERR_TIMEOUT) by a warp that gave up a wait for its copies.
+__device__ unsigned int g_attn_error;
+
+// A bounded wait for a bulk copy's barrier (about 2 s; after one that ran out,
+// the warp's next ones only poll).  A copy cannot fail to arrive in a healthy
+// context; if one did, the warp would go on with whatever its slot holds.
+__device__ __noinline__ bool wait_bulk(uint64_t *bar, uint32_t parity, bool healthy)
+{
+    for (int i = 0; i < (healthy ? 2000 : 1); ++i)
+        if (ptx::mbar_wait_for(bar, parity, 1000000))
+            return healthy;
+    atomicExch(&g_attn_error, (unsigned int)SSD_ERR_TIMEOUT);
+    return false;
+}
 
 // ---- the arithmetic: bf16 on mma.sync --------------------------------------
 
@@ -439,7 +481,14 @@ struct Mma {
     using T = __nv_bfloat16;
     static constexpr int MR = 16 * NM, kDim = DP, kUnit = 16 * NT;
     static constexpr bool kExact = EX;
-    uint32_t q[NM][DP / 16][4];
+    // Query rows stay in registers, but for 64 KB of output rows per warp and
+    // more (256 of a lane's registers are not enough for both): then in shared
+    // memory, read anew for each unit.
+    static constexpr bool kQSmem = NM * DP >= 256;
+    static constexpr int kQStride = (DP / 8 | 1) * 16;
+    static constexpr int kQBytes = kQSmem ? MR * kQStride : 0;   // per warp
+    uint32_t q[kQSmem ? 1 : NM][kQSmem ? 1 : DP / 16][4];
+    char *qs;
     float o[NM][DP / 8][4];
     float s[NM][2 * NT][4];
     float m[NM][2], l[NM][2];   // m: the running maximum of q.k (of -q.k for a negative scale)
@@ -471,10 +520,16 @@ struct Mma {
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
                         const int c = 16 * k + 8 * y + 2 * (lane & 3);
-                        const uint32_t v = r < rows && c < D ? *reinterpret_cast<const uint32_t *>(src + c) : 0u;
-                        q[mt][k][x + 2 * y] = (v & keep) ^ flip;
+                        uint32_t v = r < rows && c < D ? *reinterpret_cast<const uint32_t *>(src + c) : 0u;
+                        v = (v & keep) ^ flip;
+                        if constexpr (kQSmem)
+                            *reinterpret_cast<uint32_t *>(qs + r * kQStride + c * 2) = v;
+                        else
+                            q[mt][k][x + 2 * y] = v;
                     }
             }
+        if (kQSmem)
+            __syncwarp();
 #pragma unroll
         for (int mt = 0; mt < NM; ++mt)
 #pragma unroll
@@ -499,17 +554,30 @@ struct Mma {
                     s[mt][n][i] = 0.f;
         // lanes 0-7, 8-15: tokens 0-7, first and second 16 bytes; 16-23, 24-31: tokens 8-15
         const uint32_t a = slot + ((lane & 7) + ((lane >> 4) << 3)) * stride + ((lane >> 3) & 1) * 16;
+        // (query rows in shared memory) lanes 0-7, 8-15: rows 0-7, 8-15, first 16 bytes; 16-31: second
+        const uint32_t qa = kQSmem ? smem_addr(qs) + ((lane & 7) + (((lane >> 3) & 1) << 3)) * kQStride + (lane >> 4) * 16 : 0;
 #pragma unroll
         for (int k = 0; k < DP / 16; ++k) {
             if (16 * k < D) {
+                uint32_t qf[NM][4];
+#pragma unroll
+                for (int mt = 0; mt < NM; ++mt) {
+                    if constexpr (kQSmem)
+                        ldsm4(qa + mt * 16 * kQStride + k * 32, qf[mt]);
+                    else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            qf[mt][i] = q[mt][k][i];
+                    }
+                }
 #pragma unroll
                 for (int h = 0; h < NT; ++h) {
                     uint32_t b[4];
                     ldsm4(a + h * 16 * stride + k * 32, b);
 #pragma unroll
                     for (int mt = 0; mt < NM; ++mt) {
-                        mma16816(s[mt][2 * h], q[mt][k], b[0], b[1]);
-                        mma16816(s[mt][2 * h + 1], q[mt][k], b[2], b[3]);
+                        mma16816(s[mt][2 * h], qf[mt], b[0], b[1]);
+                        mma16816(s[mt][2 * h + 1], qf[mt], b[2], b[3]);
                     }
                 }
             }
@@ -611,6 +679,7 @@ struct Mma {
             for (int c = lane; c < p.seg; c += 32)
                 *reinterpret_cast<uint4 *>(slot_ptr + tt * stride + c * 16) = make_uint4(0, 0, 0, 0);
         }
+        ptx::fence_proxy_async_smem();   // (later bulk copies write the rows)
         __syncwarp();
     }
 
@@ -675,6 +744,31 @@ struct Mma {
                 }
             }
     }
+    // The warp's rows as they are, without a join: `out(r, c, x, y)` takes elements
+    // c, c + 1 of row r, scaled by `scale(m, l)`, and `stat(r, m, l)` the rows'
+    // maxima (base 2, 0 for a row that saw nothing) and sums.
+    template <typename Scale, typename Out, typename Stat>
+    __device__ __forceinline__ void finish(const AttnParams &p, int rows, int lane, Scale scale, Out out, Stat stat)
+    {
+#pragma unroll
+        for (int mt = 0; mt < NM; ++mt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int r = mt * 16 + x * 8 + (lane >> 2);
+                float ll = l[mt][x];
+                ll += __shfl_xor_sync(0xffffffffu, ll, 1);
+                ll += __shfl_xor_sync(0xffffffffu, ll, 2);
+                const float mm = m[mt][x] == -INFINITY ? 0.f : m[mt][x] * p.f, f = scale(ll);
+                if (r < rows) {
+                    if ((lane & 3) == 0)
+                        stat(r, mm, ll);
+#pragma unroll
+                    for (int n = 0; n < DP / 8; ++n)
+                        if (8 * n < dim(p))
+                            out(r, 8 * n + 2 * (lane & 3), o[mt][n][2 * x] * f, o[mt][n][2 * x + 1] * f);
+                }
+            }
+    }
     // m becomes the factor that brings the warp's rows to the warps' joint maximum
     __device__ __forceinline__ void rescale(const float *ml, int lane)
     {
@@ -733,7 +827,9 @@ struct Simt {
     f32x2 o[MR][NV][2];
     float m[MR], l[MR];   // m: the running maximum of q.k (of -q.k for a negative scale)
     int lo[MR], hi[MR];
-    float *qs, *ps;       // the CTA's query rows [MR][DP], this warp's weights [MR][kUnit]
+    float *qs, *ps;       // the warp's query rows [MR][DP] and weights [MR][kUnit]
+    static constexpr int kQBytes = MR * (DP + kUnit) * 4;   // per warp
+    static constexpr bool kQSmem = false;
 
     __device__ __forceinline__ static int dim(const AttnParams &p) { return EX ? DP : p.a.d.headdim; }
     __device__ __forceinline__ static int row_bytes(const AttnParams &p) { return EX ? ((DP / 4) | 1) * 16 : p.stride; }
@@ -753,20 +849,19 @@ struct Simt {
             l[r] = 0.f;
             const float *src = static_cast<const float *>(p.a.q) + (long long)(t.row + j) * p.a.d.q_stride[0] +
                                (long long)(kvh * p.group + h0 + g) * p.a.d.q_stride[1];
-            if (r % kWarps == (int)(threadIdx.x >> 5))
-                for (int c = 4 * lane; c < DP; c += 128) {
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (r < rows && c < D && p.sign != 0)
-                        v = *reinterpret_cast<const float4 *>(src + c);
-                    if (p.sign < 0)
-                        v = make_float4(-v.x, -v.y, -v.z, -v.w);
-                    *reinterpret_cast<float4 *>(qs + r * DP + c) = v;
-                }
+            for (int c = 4 * lane; c < DP; c += 128) {
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (r < rows && c < D && p.sign != 0)
+                    v = *reinterpret_cast<const float4 *>(src + c);
+                if (p.sign < 0)
+                    v = make_float4(-v.x, -v.y, -v.z, -v.w);
+                *reinterpret_cast<float4 *>(qs + r * DP + c) = v;
+            }
 #pragma unroll
             for (int n = 0; n < NV; ++n)
                 o[r][n][0] = o[r][n][1] = pk2(0.f, 0.f);
         }
-        __syncthreads();   // (each warp has loaded some of the rows)
+        __syncwarp();
     }
 
     __device__ __forceinline__ void scores(const AttnParams &p, char *slot, uint32_t mask, int tok0, int all0, int all1, int lane)
@@ -853,6 +948,43 @@ struct Simt {
         __syncwarp();
     }
 
+    __device__ __forceinline__ void add_groups()
+    {
+        if (kGroups == 2) {
+#pragma unroll
+            for (int r = 0; r < MR; ++r)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    o[r][0][i] = pk2(lo2(o[r][0][i]) + __shfl_xor_sync(0xffffffffu, lo2(o[r][0][i]), 16),
+                                     hi2(o[r][0][i]) + __shfl_xor_sync(0xffffffffu, hi2(o[r][0][i]), 16));
+        }
+    }
+    // as Mma's
+    template <typename Scale, typename Out, typename Stat>
+    __device__ __forceinline__ void finish(const AttnParams &p, int rows, int lane, Scale scale, Out out, Stat stat)
+    {
+        add_groups();
+#pragma unroll
+        for (int r = 0; r < MR; ++r) {
+            float ll = l[r];
+#pragma unroll
+            for (int x = 16; x >= 1; x >>= 1)
+                ll += __shfl_xor_sync(0xffffffffu, ll, x);
+            const float mm = m[r] == -INFINITY ? 0.f : m[r] * p.f, f = scale(ll);
+            if (r < rows && (kGroups == 1 || lane < 16)) {
+                if (lane == 0)
+                    stat(r, mm, ll);
+#pragma unroll
+                for (int n = 0; n < NV; ++n) {
+                    const int c = 4 * lane + 128 * n;
+                    if (c < dim(p)) {
+                        out(r, c, lo2(o[r][n][0]) * f, hi2(o[r][n][0]) * f);
+                        out(r, c + 2, lo2(o[r][n][1]) * f, hi2(o[r][n][1]) * f);
+                    }
+                }
+            }
+        }
+    }
     __device__ __forceinline__ void end(const AttnParams &p, float *ml, int lane)
     {
 #pragma unroll
@@ -865,13 +997,8 @@ struct Simt {
                 ml[2 * r] = m[r];
                 ml[2 * r + 1] = l[r];
             }
-            if (kGroups == 2) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    o[r][0][i] = pk2(lo2(o[r][0][i]) + __shfl_xor_sync(0xffffffffu, lo2(o[r][0][i]), 16),
-                                     hi2(o[r][0][i]) + __shfl_xor_sync(0xffffffffu, hi2(o[r][0][i]), 16));
-            }
         }
+        add_groups();
     }
     __device__ __forceinline__ void rescale(const float *ml, int)
     {
@@ -915,29 +1042,32 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 v)
     *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
 }
 
-// shared memory: the warps' rings, two join buffers, (fp32) the query rows and
-// the warps' weights -- all of whole 16-byte segments -- then maxima, sums and
-// slot masks.  NU: units in a warp's ring.
+__device__ __forceinline__ void store2(float *p, float x, float y) { *reinterpret_cast<float2 *>(p) = make_float2(x, y); }
+__device__ __forceinline__ void store2(__nv_bfloat16 *p, float x, float y) { *reinterpret_cast<uint32_t *>(p) = pack_bf16(x, y); }
+
+// shared memory: the warps' rings, their query rows (and fp32 weights), two
+// join buffers (in the query rows' place where those are bf16) -- all of whole
+// 16-byte segments -- then maxima, sums, barriers and slot masks.  NU: units in
+// a warp's ring.
 template <typename M, int NU>
 struct Layout {
-    static constexpr bool kSimt = sizeof(typename M::T) == 4;
-    static constexpr int kQuery = kSimt ? (M::MR * M::kDim + kWarps * M::MR * M::kUnit) * 4 : 0;
-    static constexpr int kSmall = (kWarps * M::MR * 2 + M::MR * 2 + kWarps * NU) * 4;
+    static constexpr int kQuery = kWarps * M::kQBytes;
+    static constexpr int kSmall = kWarps * NU * 2 * 8 + (kWarps * M::MR * 2 + M::MR * 2 + kWarps * NU) * 4;
     static __host__ __device__ int join_stride(int D) { return D + 8; }
     static __host__ __device__ int ring_bytes(int stride) { return kWarps * NU * 2 * M::kUnit * stride; }
     static __host__ __device__ int join_bytes(int D) { return 2 * M::MR * join_stride(D) * 4; }
-    static __host__ __device__ int total(int D, int stride) { return ring_bytes(stride) + join_bytes(D) + kSmall + kQuery; }
+    static __host__ __device__ int middle_bytes(int D)
+    {
+        return M::kQSmem ? (kQuery > join_bytes(D) ? kQuery : join_bytes(D)) : kQuery + join_bytes(D);
+    }
+    static __host__ __device__ int total(int D, int stride) { return ring_bytes(stride) + middle_bytes(D) + kSmall; }
 };
 
-template <typename M>
-__device__ __forceinline__ void bind(M &m, float *q, float *w)
-{
-    if constexpr (sizeof(typename M::T) == 4) {
-        m.qs = q;
-        m.ps = w;
-    }
-}
-
+// Shares of warps where there are at least as many tiles (times key-value heads)
+// as CTAs: a warp then goes through whole tiles without a barrier, and a tile
+// is cut into a few parts at most.  Shares of CTAs where there are fewer: a
+// tile is then cut into many parts, and joining a CTA's warps first leaves a
+// quarter of them to the second launch.
 template <typename M, int NU>
 __global__ void __launch_bounds__(kThreads) ssd_paged_attn_kernel(const __grid_constant__ AttnParams p)
 {
@@ -945,7 +1075,7 @@ __global__ void __launch_bounds__(kThreads) ssd_paged_attn_kernel(const __grid_c
     using L = Layout<M, NU>;
     constexpr int UT = M::kUnit;
     extern __shared__ __align__(16) char smem[];
-    __shared__ Found found;
+    __shared__ Found found[kWarps];
     __shared__ long long tmp[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, D = M::dim(p), stride = M::row_bytes(p);
     // The call's launches are programmatic dependents: each starts while the one
@@ -953,8 +1083,7 @@ __global__ void __launch_bounds__(kThreads) ssd_paged_attn_kernel(const __grid_c
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    long long total, per, u0;
-    locate<UT>(p, reinterpret_cast<int *>(smem), tmp, &found, total, per, u0);
+    const Shares sh = locate<UT>(p, reinterpret_cast<int *>(smem), tmp, found);
     // padding rows see nothing
     if (p.a.start) {
         const long long r0 = min((long long)max(p.a.start[p.a.d.nreq], 0), (long long)p.a.d.nrows);
@@ -967,57 +1096,80 @@ __global__ void __launch_bounds__(kThreads) ssd_paged_attn_kernel(const __grid_c
                 p.a.lse[i] = -INFINITY;
         }
     }
-    if (tid == 0)
-        p.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    if (u0 >= total)
-        return;
-    const long long u1 = min(u0 + per, total);
+    const bool solo = sh.solo;
+    const long long share = solo ? (long long)blockIdx.x * kWarps + w : blockIdx.x;
+    const long long u0 = share * sh.per, u1 = min(u0 + sh.per, sh.total);
+    if (solo ? lane == 0 : lane < kWarps && w == 0)   // (a CTA's share has its first warp's number in desc)
+        p.desc[solo ? share : (long long)blockIdx.x * kWarps + lane] = make_int4(-1, 0, 0, 0);
     const int half_bytes = UT * stride;
     char *ring = smem + (size_t)w * NU * 2 * half_bytes;    // [NU][K, V][UT][stride]
-    float *join = reinterpret_cast<float *>(smem + L::ring_bytes(stride));
-    float *qs = join + L::join_bytes(D) / 4;                 // (16-byte accesses up to here)
-    float *ml = join + (L::join_bytes(D) + L::kQuery) / 4;   // [kWarps][MR][2]
-    float *joint = ml + kWarps * M::MR * 2;                  // [MR] maxima, [MR] sums
+    char *middle = smem + L::ring_bytes(stride);
+    char *qs = middle + w * M::kQBytes;
+    float *join = reinterpret_cast<float *>(middle + (M::kQSmem ? 0 : L::kQuery));   // (16-byte accesses up to here)
+    uint64_t *bars = reinterpret_cast<uint64_t *>(middle + L::middle_bytes(D)) + w * NU * 2;
+    float *ml = reinterpret_cast<float *>(bars - w * NU * 2 + kWarps * NU * 2);      // [kWarps][MR][2]
+    float *joint = ml + kWarps * M::MR * 2;                                          // [MR] maxima, [MR] sums
     uint32_t *masks = reinterpret_cast<uint32_t *>(joint + M::MR * 2) + w * NU;
     const int ds = L::join_stride(D);
     __syncthreads();   // (the schedule's use of the ring's memory is over)
     // segments past the head's elements are read by the products: zero once
     if (!M::kExact) {
-        for (int i = tid; i < kWarps * NU * 2 * UT; i += kThreads)
+        for (int i = lane; i < NU * 2 * UT; i += 32)
             for (int c = p.seg; c * 16 < stride; ++c)
-                *reinterpret_cast<uint4 *>(smem + (size_t)i * stride + c * 16) = make_uint4(0, 0, 0, 0);
-        __syncthreads();
+                *reinterpret_cast<uint4 *>(ring + (size_t)i * stride + c * 16) = make_uint4(0, 0, 0, 0);
     }
+    const bool bulk = p.bulk;
+    if (bulk) {
+        if (lane < NU * 2)
+            ptx::mbar_init(bars + lane, 1);
+        ptx::fence_mbar_init();
+        ptx::fence_proxy_async_smem();
+    }
+    __syncwarp();
+    if (u0 >= sh.total)
+        return;   // (the whole CTA where it has one share; no barrier follows where it has four)
 
     Cursor cur;
-    set_tile<UT>(p, cur.t, found.req, found.j);
-    cur.item = (int)((u0 - found.lin) / cur.t.units);
-    cur.lin = found.lin + (long long)cur.item * cur.t.units;
+    {
+        const Found f = found[solo ? w : 0];
+        set_tile<UT>(p, cur.t, f.req, f.j);
+        cur.item = (int)((u0 - f.lin) / cur.t.units);
+        cur.lin = f.lin + (long long)cur.item * cur.t.units;
+    }
 
     // Steps alternate: while a unit's K is used the V half of the ring's newest
     // unit is loaded, while its V is used the next unit's K.  Every step is one
     // group of asynchronous copies, empty past the share's end.
+    const int step = solo ? 1 : kWarps;
     Loader<T, M::kDim, M::kExact, UT> ld;
     ld.c = cur;
     ld.u1 = u1;
     ld.set_end();
     ld.u = (int)(u0 - cur.lin);
-    ld.skip(p, w);
+    ld.skip(p, solo ? 0 : w);
     ld.fetch_page(p, lane);
     int head = 0;
     auto load_k = [&]() {
         if (ld.u >= 0) {
+            char *slot = ring + head * 2 * half_bytes;
             ld.offsets(p, lane);
             if (lane == 0)
                 masks[head] = ld.mask;
-            ld.copy(p, p.a.kc, ld.koff, p.a.d.kc_stride[1], smem_addr(ring + head * 2 * half_bytes), lane);
+            if (M::kExact && !bulk)
+                ld.copy(p, p.a.kc, ld.koff, p.a.d.kc_stride[1], smem_addr(slot), lane);
+            else
+                ld.copy_bulk(p, p.a.kc, ld.koff[0], slot, bars + head * 2, false, lane);
         }
         cp_commit();
     };
     auto load_v = [&]() {
         if (ld.u >= 0) {
-            ld.copy(p, p.a.vc, ld.voff, p.a.d.vc_stride[1], smem_addr(ring + (head * 2 + 1) * half_bytes), lane);
-            ld.skip(p, kWarps);
+            char *slot = ring + (head * 2 + 1) * half_bytes;
+            if (M::kExact && !bulk)
+                ld.copy(p, p.a.vc, ld.voff, p.a.d.vc_stride[1], smem_addr(slot), lane);
+            else
+                ld.copy_bulk(p, p.a.vc, ld.voff[0], slot, bars + head * 2 + 1, true, lane);
+            ld.skip(p, step);
             ld.fetch_page(p, lane);
             head = head + 1 == NU ? 0 : head + 1;
         }
@@ -1031,8 +1183,12 @@ __global__ void __launch_bounds__(kThreads) ssd_paged_attn_kernel(const __grid_c
     load_k();
 
     M math;
-    bind(math, qs, qs + (size_t)M::MR * M::kDim + w * M::MR * M::kUnit);
+    math.qs = reinterpret_cast<decltype(math.qs)>(qs);
+    if constexpr (sizeof(T) == 4)
+        math.ps = math.qs + M::MR * M::kDim;
     int tail = 0;
+    uint32_t parity = 0;
+    bool healthy = true;
     int u = (int)(u0 - cur.lin);   // first unit of the share in this item
     while (true) {
         const int ue = (int)min((long long)cur.t.units, u1 - cur.lin);   // the share's units of the item: [u, ue)
@@ -1047,71 +1203,100 @@ __global__ void __launch_bounds__(kThreads) ssd_paged_attn_kernel(const __grid_c
         math.begin(p, cur.t, cur.item, lane);
         const int kvh = cur.item / p.nhb, hb = cur.item - kvh * p.nhb;
         const int h0 = kvh * p.group + hb * p.gh, nh = min(p.gh, p.group - hb * p.gh), rows = cur.t.nq * nh;
-        // this warp's units: those whose number in the share is w modulo the warps
-        const int skip = (w - (int)((cur.lin + u - u0) % kWarps) + kWarps) % kWarps;
-        for (int x = u + skip; x < ue; x += kWarps) {
+        // this warp's units: all, or those whose number in the CTA's share is w modulo the warps
+        const int skip = solo ? 0 : (w - (int)((cur.lin + u - u0) % kWarps) + kWarps) % kWarps;
+        for (int x = u + skip; x < ue; x += step) {
             const int tok0 = (cur.t.ub + x) * UT;
             char *slot = ring + tail * 2 * half_bytes;
             cp_wait<2 * NU - 2>();
+            if (bulk)
+                healthy = wait_bulk(bars + tail * 2, parity, healthy);
             __syncwarp();
             const uint32_t mask = masks[tail];
             load_v();
             math.scores(p, slot, mask, tok0, all0, all1, lane);
             cp_wait<2 * NU - 2>();
+            if (bulk)
+                healthy = wait_bulk(bars + tail * 2 + 1, parity, healthy);
             __syncwarp();
             load_k();
             math.values(p, slot + half_bytes, mask, tok0, all0, all1, lane);
-            tail = tail + 1 == NU ? 0 : tail + 1;
-        }
-        // join the warps: three barriers; the next tile's writes to ml, joint and
-        // the buffers come after its own first or second one
-        math.end(p, ml + w * M::MR * 2, lane);
-        __syncthreads();
-        if (tid < M::MR) {
-            float ll = 0.f;
-            const float base = joint_max<M::MR>(ml, tid);
-#pragma unroll
-            for (int i = 0; i < kWarps; ++i)
-                ll += ml[(i * M::MR + tid) * 2 + 1] * exp2_fast(ml[(i * M::MR + tid) * 2] - base);
-            joint[tid] = base;
-            joint[M::MR + tid] = ll;
-        }
-        math.rescale(ml, lane);
-        float *buf = join + (w & 1) * M::MR * ds;
-        if (w >= 2)
-            math.template put<false>(p, buf, ds, rows, lane);
-        __syncthreads();
-        if (w < 2)
-            math.template put<true>(p, buf, ds, rows, lane);
-        __syncthreads();
-        const bool whole = u == 0 && ue == cur.t.units;
-        const int slot = u > 0 ? 0 : 1;   // a tile begun in an earlier share, or in this one
-        const int n4 = D / 4;
-        for (int i = tid; i < rows * n4; i += kThreads) {
-            const int r = i / n4, c = 4 * (i - r * n4);
-            const float4 x = *reinterpret_cast<const float4 *>(join + r * ds + c);
-            const float4 y = *reinterpret_cast<const float4 *>(join + (M::MR + r) * ds + c);
-            float4 v = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
-            if (whole) {
-                const float ll = joint[M::MR + r], inv = ll == 0.f ? 0.f : 1.f / ll;
-                const int j = r / nh, g = r - j * nh;
-                v.x *= inv; v.y *= inv; v.z *= inv; v.w *= inv;
-                store4(static_cast<T *>(p.a.out) + (long long)(cur.t.row + j) * p.a.d.o_stride[0] +
-                           (long long)(h0 + g) * p.a.d.o_stride[1] + c, v);
-                if (c == 0 && p.a.lse)
-                    p.a.lse[(long long)(cur.t.row + j) * p.a.d.nheads + h0 + g] =
-                        ll == 0.f ? -INFINITY : kLn2 * (joint[r] + log2f(ll));
-            } else {
-                const size_t at = ((size_t)blockIdx.x * 2 + slot) * M::MR + r;
-                *reinterpret_cast<float4 *>(p.part_o + at * D + c) = v;
-                if (c == 0) {
-                    p.part_ml[2 * at] = joint[r];
-                    p.part_ml[2 * at + 1] = joint[M::MR + r];
-                }
+            if (++tail == NU) {
+                tail = 0;
+                parity ^= 1;
             }
         }
-        if (!whole && slot == 1 && tid == 0)   // the cut tile's first part: where the others are
-            p.desc[blockIdx.x] = make_int4(cur.t.row, cur.t.nq, cur.item, (int)((cur.lin + cur.t.units - 1) / per));
+        const bool whole = u == 0 && ue == cur.t.units;
+        const int slot = u > 0 ? 0 : 1;   // a tile begun in an earlier share, or in this one
+        T *out = static_cast<T *>(p.a.out) + (long long)cur.t.row * p.a.d.o_stride[0] + (long long)h0 * p.a.d.o_stride[1];
+        float *lse = p.a.lse ? p.a.lse + (long long)cur.t.row * p.a.d.nheads + h0 : nullptr;
+        float *po = p.part_o + ((size_t)share * 2 + slot) * M::MR * D, *pml = p.part_ml + ((size_t)share * 2 + slot) * M::MR * 2;
+        auto put_lse = [&](int r, float mm, float ll) {
+            if (lse) {
+                const int j = r / nh;
+                lse[(long long)j * p.a.d.nheads + (r - j * nh)] = ll == 0.f ? -INFINITY : kLn2 * (mm + log2f(ll));
+            }
+        };
+        if (solo) {
+            if (whole)
+                math.finish(p, rows, lane, [](float ll) { return ll == 0.f ? 0.f : 1.f / ll; },
+                            [&](int r, int c, float a, float b) {
+                                const int j = r / nh;
+                                store2(out + (long long)j * p.a.d.o_stride[0] + (long long)(r - j * nh) * p.a.d.o_stride[1] + c, a, b);
+                            }, put_lse);
+            else
+                math.finish(p, rows, lane, [](float) { return 1.f; },
+                            [&](int r, int c, float a, float b) { store2(po + (size_t)r * D + c, a, b); },
+                            [&](int r, float mm, float ll) { store2(pml + 2 * r, mm, ll); });
+        } else {
+            // join the warps: three barriers; the next tile's writes to ml, joint
+            // and the buffers come after its own first or second one
+            math.end(p, ml + w * M::MR * 2, lane);
+            __syncthreads();
+            if (tid < M::MR) {
+                float ll = 0.f;
+                const float base = joint_max<M::MR>(ml, tid);
+#pragma unroll
+                for (int i = 0; i < kWarps; ++i)
+                    ll += ml[(i * M::MR + tid) * 2 + 1] * exp2_fast(ml[(i * M::MR + tid) * 2] - base);
+                joint[tid] = base;
+                joint[M::MR + tid] = ll;
+            }
+            math.rescale(ml, lane);
+            float *buf = join + (w & 1) * M::MR * ds;
+            if (w >= 2)
+                math.template put<false>(p, buf, ds, rows, lane);
+            __syncthreads();
+            if (w < 2)
+                math.template put<true>(p, buf, ds, rows, lane);
+            __syncthreads();
+            const int n4 = D / 4;
+            for (int i = tid; i < rows * n4; i += kThreads) {
+                const int r = i / n4, c = 4 * (i - r * n4);
+                const float4 x = *reinterpret_cast<const float4 *>(join + r * ds + c);
+                const float4 y = *reinterpret_cast<const float4 *>(join + (M::MR + r) * ds + c);
+                float4 v = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+                const float ll = joint[M::MR + r];
+                if (whole) {
+                    const float inv = ll == 0.f ? 0.f : 1.f / ll;
+                    const int j = r / nh;
+                    v.x *= inv; v.y *= inv; v.z *= inv; v.w *= inv;
+                    store4(out + (long long)j * p.a.d.o_stride[0] + (long long)(r - j * nh) * p.a.d.o_stride[1] + c, v);
+                    if (c == 0)
+                        put_lse(r, joint[r], ll);
+                } else {
+                    store4(po + (size_t)r * D + c, v);
+                    if (c == 0)
+                        store2(pml + 2 * r, joint[r], ll);
+                }
+            }
+            if (M::kQSmem)
+                __syncthreads();   // (the next tile's query rows go where the buffers are)
+        }
+        if (!whole && slot == 1 && (solo ? lane == 0 : tid == 0))   // the cut tile's first part: where the others are
+            p.desc[solo ? share : (long long)blockIdx.x * kWarps] =
+                make_int4(cur.t.row, cur.t.nq, cur.item,
+                          solo ? ~(int)((cur.lin + cur.t.units - 1) / sh.per) : (int)((cur.lin + cur.t.units - 1) / sh.per));
         if (cur.lin + ue >= u1)
             break;
         u = 0;
@@ -1120,100 +1305,115 @@ __global__ void __launch_bounds__(kThreads) ssd_paged_attn_kernel(const __grid_c
     cp_wait<0>();
 }
 
-// Joins the parts of the tile that starts in share blockIdx.x and goes on in
-// the next ones, row blockIdx.y of it: warps take parts in turn, lanes the
-// elements.
+// Joins the parts of the tiles that start in a share of CTA blockIdx.x and go
+// on in the next shares, row blockIdx.y of them: warps take parts in turn,
+// lanes the elements.
+constexpr int kJoinWarps = 8;
+
 template <typename T, int MR>
-__global__ void __launch_bounds__(128) ssd_paged_attn_join_kernel(const __grid_constant__ AttnParams p)
+__global__ void __launch_bounds__(32 * kJoinWarps) ssd_paged_attn_join_kernel(const __grid_constant__ AttnParams p)
 {
-    __shared__ float sm[4][2];
-    __shared__ float so[4][256];
+    __shared__ float sm[kJoinWarps][2];
+    __shared__ __align__(16) float so[kJoinWarps][256];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int4 d = p.desc[blockIdx.x];
-    if (d.x < 0)
-        return;
-    const int row = d.x, nq = d.y, item = d.z, c0 = blockIdx.x, c1 = d.w, r = blockIdx.y, D = p.a.d.headdim;
-    const int kvh = item / p.nhb, hb = item - kvh * p.nhb, nh = min(p.gh, p.group - hb * p.gh);
-    if (r >= nq * nh)
-        return;
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    // part i lies in share c0 + i: slot 1 of the first, slot 0 of the others
-    auto part = [&](int i) { return ((size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * MR + r; };
-    const int n = c1 - c0 + 1;
-    // each warp joins its parts in the running form, so that their maxima and
-    // rows are loaded together, four parts at a time
-    float mm = -INFINITY, ll = 0.f, o[2][4] = {};
-    for (int i = w; i < n; i += 16) {
-        float pm[4], pl[4];
-        float4 v[4][2];
+    int4 descs[kWarps];
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            pm[b] = -INFINITY;
-            pl[b] = 0.f;
-            v[b][0] = v[b][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (i + 4 * b < n) {
-                const size_t at = part(i + 4 * b);
-                const float2 t = *reinterpret_cast<const float2 *>(p.part_ml + 2 * at);
-                pm[b] = t.y == 0.f ? -INFINITY : t.x;   // (a part that saw nothing)
-                pl[b] = t.y;
+    for (int k = 0; k < kWarps; ++k)
+        descs[k] = p.desc[(long long)blockIdx.x * kWarps + k];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, r = blockIdx.y, D = p.a.d.headdim;
+#pragma unroll 1
+    for (int k = 0; k < kWarps; ++k) {
+        const int4 d = k == 0 ? descs[0] : k == 1 ? descs[1] : k == 2 ? descs[2] : descs[3];
+        const int row = d.x, nq = d.y, item = d.z;
+        const int kvh = item / p.nhb, hb = item - kvh * p.nhb, nh = min(p.gh, p.group - hb * p.gh);
+        if (row < 0 || r >= nq * nh)
+            continue;
+        // (numbers of shares: a CTA's one share has the CTA's number, four have 4 CTA + warp)
+        const bool solo = d.w < 0;
+        const int c0 = solo ? blockIdx.x * kWarps + k : blockIdx.x, c1 = solo ? ~d.w : d.w;
+        // part i lies in share c0 + i: slot 1 of the first, slot 0 of the others
+        const int n = c1 - c0 + 1;
+        // each warp joins its parts in the running form, so that their maxima and
+        // rows are loaded together, four parts at a time
+        float mm = -INFINITY, ll = 0.f, o[2][4] = {};
+        for (int i = w; i < n; i += 4 * kJoinWarps) {
+            float pm[4], pl[4];
+            float4 v[4][2];
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    if (4 * lane + 128 * k < D)
-                        v[b][k] = *reinterpret_cast<const float4 *>(p.part_o + at * D + 4 * lane + 128 * k);
+            for (int b = 0; b < 4; ++b) {
+                pm[b] = -INFINITY;
+                pl[b] = 0.f;
+                v[b][0] = v[b][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+                const int part = i + kJoinWarps * b;
+                if (part < n) {
+                    const size_t at = ((size_t)(c0 + part) * 2 + (part == 0 ? 1 : 0)) * MR + r;
+                    const float2 t = *reinterpret_cast<const float2 *>(p.part_ml + 2 * at);
+                    pm[b] = t.y == 0.f ? -INFINITY : t.x;   // (a part that saw nothing)
+                    pl[b] = t.y;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        if (4 * lane + 128 * x < D)
+                            v[b][x] = *reinterpret_cast<const float4 *>(p.part_o + at * D + 4 * lane + 128 * x);
+                }
+            }
+            const float mn = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])), mm), base = mn == -INFINITY ? 0.f : mn;
+            const float keep = exp2_fast(mm - base);
+            mm = mn;
+            ll *= keep;
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    o[x][e] *= keep;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const float f = exp2_fast(pm[b] - base);
+                ll += pl[b] * f;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    o[x][0] += f * v[b][x].x;
+                    o[x][1] += f * v[b][x].y;
+                    o[x][2] += f * v[b][x].z;
+                    o[x][3] += f * v[b][x].w;
+                }
             }
         }
-        const float mn = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])), mm), base = mn == -INFINITY ? 0.f : mn;
-        const float keep = exp2_fast(mm - base);
-        mm = mn;
-        ll *= keep;
+        __syncthreads();   // (the previous tile's sums have been read)
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                o[k][e] *= keep;
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const float f = exp2_fast(pm[b] - base);
-            ll += pl[b] * f;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                o[k][0] += f * v[b][k].x;
-                o[k][1] += f * v[b][k].y;
-                o[k][2] += f * v[b][k].z;
-                o[k][3] += f * v[b][k].w;
-            }
+        for (int x = 0; x < 2; ++x)
+            *reinterpret_cast<float4 *>(&so[w][4 * lane + 128 * x]) = make_float4(o[x][0], o[x][1], o[x][2], o[x][3]);
+        if (lane == 0) {
+            sm[w][0] = mm;
+            sm[w][1] = ll;
         }
+        __syncthreads();
+        float top = sm[0][0];
+#pragma unroll
+        for (int i = 1; i < kJoinWarps; ++i)
+            top = fmaxf(top, sm[i][0]);
+        const float base = top == -INFINITY ? 0.f : top;
+        float f[kJoinWarps], total = 0.f;
+#pragma unroll
+        for (int i = 0; i < kJoinWarps; ++i) {
+            f[i] = exp2_fast(sm[i][0] - base);
+            total += sm[i][1] * f[i];
+        }
+        const float inv = total == 0.f ? 0.f : 1.f / total;
+        const int j = r / nh, h = kvh * p.group + hb * p.gh + (r - j * nh);
+        for (int c = 2 * threadIdx.x; c < D; c += 64 * kJoinWarps) {
+            float a = 0.f, b = 0.f;
+#pragma unroll
+            for (int i = 0; i < kJoinWarps; ++i) {
+                a += so[i][c] * f[i];
+                b += so[i][c + 1] * f[i];
+            }
+            store2(static_cast<T *>(p.a.out) + (long long)(row + j) * p.a.d.o_stride[0] + (long long)h * p.a.d.o_stride[1] + c,
+                   a * inv, b * inv);
+        }
+        if (p.a.lse && threadIdx.x == 0)
+            p.a.lse[(long long)(row + j) * p.a.d.nheads + h] = total == 0.f ? -INFINITY : kLn2 * (base + log2f(total));
     }
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            so[w][4 * lane + 128 * k + e] = o[k][e];
-    if (lane == 0) {
-        sm[w][0] = mm;
-        sm[w][1] = ll;
-    }
-    __syncthreads();
-    mm = fmaxf(fmaxf(sm[0][0], sm[1][0]), fmaxf(sm[2][0], sm[3][0]));
-    const float base = mm == -INFINITY ? 0.f : mm;
-    float f[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        f[i] = exp2_fast(sm[i][0] - base);
-    ll = (sm[0][1] * f[0] + sm[1][1] * f[1]) + (sm[2][1] * f[2] + sm[3][1] * f[3]);
-    const float inv = ll == 0.f ? 0.f : 1.f / ll;
-    const int j = r / nh, h = kvh * p.group + hb * p.gh + (r - j * nh);
-    for (int c = 4 * threadIdx.x; c < D; c += 512) {
-        float4 v;
-        float *e = &v.x;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            e[k] = ((so[0][c + k] * f[0] + so[1][c + k] * f[1]) + (so[2][c + k] * f[2] + so[3][c + k] * f[3])) * inv;
-        store4(static_cast<T *>(p.a.out) + (long long)(row + j) * p.a.d.o_stride[0] + (long long)h * p.a.d.o_stride[1] + c, v);
-    }
-    if (p.a.lse && threadIdx.x == 0)
-        p.a.lse[(long long)(row + j) * p.a.d.nheads + h] = ll == 0.f ? -INFINITY : kLn2 * (base + log2f(ll));
 }
 
 // ---- host: variant, sizes, launch -------------------------------------------
@@ -1270,8 +1470,9 @@ cudaError_t launch(AttnParams &p, void *workspace, cudaStream_t stream)
     const int per_sm = std::max(1, std::min({kMaxPerSm, (228 << 10) / (smem + 1024 + 256), 65536 / (regs * kThreads)}));
     const int grid = std::min(kMaxCtas, sm_count() * per_sm);
     p.part_o = static_cast<float *>(workspace);
-    p.part_ml = p.part_o + (size_t)grid * 2 * M::MR * D;
-    p.desc = reinterpret_cast<int4 *>(p.part_ml + (size_t)grid * 2 * M::MR * 2);
+    const size_t shares = (size_t)grid * kWarps;
+    p.part_ml = p.part_o + shares * 2 * M::MR * D;
+    p.desc = reinterpret_cast<int4 *>(p.part_ml + shares * 2 * M::MR * 2);
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1286,7 +1487,7 @@ cudaError_t launch(AttnParams &p, void *workspace, cudaStream_t stream)
         return e;
     note_launches(1);
     cfg.gridDim = dim3(grid, p.tok * p.gh);
-    cfg.blockDim = dim3(128);
+    cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&cfg, ssd_paged_attn_join_kernel<T, M::MR>, p);
     if (e == cudaSuccess)
@@ -1301,6 +1502,8 @@ cudaError_t launch_bf16(AttnParams &p, int mr, void *ws, cudaStream_t st)
         return mr == 32 ? launch<Mma<2, 64, true, 1>, 4>(p, ws, st) : launch<Mma<1, 64, true, 2>, 2>(p, ws, st);
     if (D == 128)
         return mr == 32 ? launch<Mma<2, 128, true, 1>, 2>(p, ws, st) : launch<Mma<1, 128, true, 1>, 2>(p, ws, st);
+    if (D == 256)
+        return launch<Mma<1, 256, true, 1>, 2>(p, ws, st);
     if (D <= 128)
         return mr == 32 ? launch<Mma<2, 128, false, 1>, 2>(p, ws, st) : launch<Mma<1, 128, false, 1>, 2>(p, ws, st);
     return launch<Mma<1, 256, false, 1>, 2>(p, ws, st);
@@ -1316,6 +1519,8 @@ cudaError_t launch_f32_rows(AttnParams &p, void *ws, cudaStream_t st)
         return launch<Simt<MR, 128, true>, 1>(p, ws, st);
     if (D <= 128)
         return launch<Simt<MR, 128, false>, 1>(p, ws, st);
+    if (D == 256)
+        return launch<Simt<MR, 256, true>, 1>(p, ws, st);
     return launch<Simt<MR, 256, false>, 1>(p, ws, st);
 }
 
@@ -1334,7 +1539,7 @@ cudaError_t launch_f32(AttnParams &p, int mr, void *ws, cudaStream_t st)
 size_t attn_workspace_bytes(const ssd_attn_dims_t &d)
 {
     const int grid = std::min(kMaxCtas, sm_count() * kMaxPerSm);
-    return (size_t)grid * (2 * tile_rows(d) * (d.headdim + 2) * sizeof(float) + sizeof(int4));
+    return (size_t)grid * kWarps * (2 * tile_rows(d) * (d.headdim + 2) * sizeof(float) + sizeof(int4));
 }
 
 cudaError_t attn_launch(const AttnArgs &a, void *workspace, cudaStream_t stream)
@@ -1352,7 +1557,7 @@ cudaError_t attn_launch(const AttnArgs &a, void *workspace, cudaStream_t stream)
     // rows of an odd number of 16-byte segments: eight rows' segments lie in different banks
     const int seg = es == 2 ? (p.seg + 1) / 2 * 2 : p.seg;
     p.stride = (seg | 1) * 16;
-    p.same16 = a.d.page_size % 16 == 0;
+    p.bulk = a.d.page_size % 16 != 0 || (D != 64 && D != 128 && D != 256);
     // scores are kept as q.k times the scale's sign, so that their maximum is that of the scaled ones
     p.sign = a.d.scale > 0.f ? 1 : a.d.scale < 0.f ? -1 : 0;
     p.f = p.sign ? fabsf(a.d.scale) * kLog2e : 1.f;
@@ -1361,6 +1566,16 @@ cudaError_t attn_launch(const AttnArgs &a, void *workspace, cudaStream_t stream)
         ++p.page.sh;
     p.page.mul = (uint32_t)((1ull << p.page.sh) / (uint32_t)a.d.page_size + 1);
     return a.d.dtype == SSD_DTYPE_BF16 ? launch_bf16(p, mr, workspace, stream) : launch_f32(p, mr, workspace, stream);
+}
+
+ssd_status_t attn_read_device_error(uint32_t *code)
+{
+    unsigned int v = 0, zero = 0;
+    if (cudaMemcpyFromSymbol(&v, g_attn_error, sizeof(v)) != cudaSuccess ||
+        (v != 0 && cudaMemcpyToSymbol(g_attn_error, &zero, sizeof(zero)) != cudaSuccess))
+        return SSD_ERR_CUDA;
+    *code = v;
+    return SSD_OK;
 }
 
 }  // namespace ssd
