@@ -61,8 +61,9 @@ struct AttnParams {
     FastDiv page;
     float *part_o;      // [shares][2][MR][D] partial rows
     float *part_ml;     // [shares][2][MR][2] their maxima (base 2) and sums
-    int4 *desc;         // [shares] the cut tile that starts in a share: first row, tokens, item, last share (~ of it
-                        // for shares of warps); x -1: none
+    int4 *desc;         // the cut tiles: first row, tokens | item << 8, first and last share; x -1: none.  Shares of
+                        // warps: [shares], of the tile that starts in a share; shares of CTAs: [most tiles x items]
+    int ndesc;          // entries of it
     int group;          // query heads per key-value head
     int gh;             // query heads of a tile (group, or a part of it when it is larger than MR)
     int nhb;            // head blocks per key-value head
@@ -70,7 +71,6 @@ struct AttnParams {
     int items;          // nkv * nhb: tiles of the same rows
     int seg;            // 16-byte segments per row of K or V
     int stride;         // bytes from row to row of a ring slot (an odd number of segments)
-    int bulk;           // rows come by bulk copies
     float f;            // |scale| log2(e), or 1 for scale 0
     int sign;           // of scale
 };
@@ -166,7 +166,7 @@ __device__ __forceinline__ void next_tile(const AttnParams &p, Tile &t)
 // of it, and the linear number of the item's first unit.
 struct Cursor {
     Tile t;
-    int item;
+    int item, tile;   // (tile: counted over all requests; shares of CTAs)
     long long lin;
 };
 
@@ -176,6 +176,7 @@ __device__ __forceinline__ void next_item(const AttnParams &p, Cursor &c)
     c.lin += c.t.units;
     if (++c.item == p.items) {
         c.item = 0;
+        ++c.tile;
         next_tile<UT>(p, c.t);
     }
 }
@@ -208,20 +209,20 @@ __device__ __forceinline__ long long block_exclusive(long long v, long long *tot
 }
 
 struct Found {
-    int req, j;
+    int req, j, tile;
     long long lin;   // the linear unit where the tile's first item begins
 };
 
 struct Shares {
-    bool solo;           // one share per warp, not per CTA
     long long total, per;   // units, and units of a share
+    long long ntiles;
 };
 
 // Where the CTA's shares begin (found[i]: of warp i's share, or found[0]).
 // Every CTA sums all tiles' units (a contiguous run of tiles per thread); the
 // thread whose run holds a share's first unit finds its tile.  `counts` (shared
 // memory, nreq + 1 ints) is used when there is a start array.
-template <int UT>
+template <int UT, bool SOLO>
 __device__ Shares locate(const AttnParams &p, int *counts, long long *tmp, Found *found)
 {
     const int tid = threadIdx.x, nreq = (int)p.a.d.nreq;
@@ -248,7 +249,7 @@ __device__ Shares locate(const AttnParams &p, int *counts, long long *tmp, Found
     }
     const long long run = (ntiles + kThreads - 1) / kThreads, t0 = min((long long)tid * run, ntiles), t1 = min(t0 + run, ntiles);
     // the run's first tile
-    Found f{0, 0, 0};
+    Found f{0, 0, 0, 0};
     if (t0 < t1) {
         if (p.a.start) {
             int lo = 0, hi = nreq;
@@ -277,26 +278,29 @@ __device__ Shares locate(const AttnParams &p, int *counts, long long *tmp, Found
     const long long before = block_exclusive(n, &sum, tmp) * p.items;
     Shares sh;
     sh.total = sum * p.items;
-    sh.solo = ntiles * p.items >= (long long)gridDim.x;
-    sh.per = sh.solo ? max(1ll, (sh.total + (long long)gridDim.x * kWarps - 1) / ((long long)gridDim.x * kWarps))
-                     : max((long long)kWarps, (sh.total + gridDim.x - 1) / gridDim.x);
+    sh.ntiles = ntiles;
+    sh.per = SOLO ? max(1ll, (sh.total + (long long)gridDim.x * kWarps - 1) / ((long long)gridDim.x * kWarps))
+                  : max((long long)kWarps, (sh.total + gridDim.x - 1) / gridDim.x);
     if (t0 < t1) {
-        long long lin = before;
+        long long lin = before, tile = t0;
         const long long end = before + n * p.items;
-        for (int i = 0; i < (sh.solo ? kWarps : 1); ++i) {
-            const long long u0 = ((long long)blockIdx.x * (sh.solo ? kWarps : 1) + i) * sh.per;
+        bool at_start = false;
+        for (int i = 0; i < (SOLO ? kWarps : 1); ++i) {
+            const long long u0 = ((long long)blockIdx.x * (SOLO ? kWarps : 1) + i) * sh.per;
             if (u0 < before || u0 >= end)
                 continue;
-            if (i == 0 || lin == before) {   // (the walk goes on from share to share)
+            if (!at_start) {   // (the walk goes on from share to share)
                 set_tile<UT>(p, t, f.req, f.j);
-                lin = before;
+                at_start = true;
             }
             while (u0 >= lin + (long long)t.units * p.items) {
                 lin += (long long)t.units * p.items;
                 next_tile<UT>(p, t);
+                ++tile;
             }
             found[i].req = t.req;
             found[i].j = t.j;
+            found[i].tile = (int)tile;
             found[i].lin = lin;
         }
     }
@@ -307,7 +311,7 @@ __device__ Shares locate(const AttnParams &p, int *counts, long long *tmp, Found
 // ---- the loader -------------------------------------------------------------
 
 // Streams a warp's units into its ring, K halves and V halves in turn.
-template <typename T, int DP, bool EXACT, int UT>
+template <typename T, int DP, bool BULK, int UT>
 struct Loader {
     static constexpr int kSegMax = DP * (int)sizeof(T) / 16;
     static constexpr int kSub = UT / 16;
@@ -338,7 +342,7 @@ struct Loader {
     {
         page = -1;
         if (u >= 0) {
-            const int tok = (c.t.ub + u) * UT + (p.bulk ? lane % UT : kSub > 1 ? lane & 16 : 0);
+            const int tok = (c.t.ub + u) * UT + (BULK ? lane % UT : kSub > 1 ? lane & 16 : 0);
             if (tok < c.t.end)   // (16 tokens are in the page of the first of them)
                 page = __ldg(p.a.table + (long long)c.t.req * p.a.d.table_stride + div_page(p.page, tok));
         }
@@ -351,7 +355,7 @@ struct Loader {
         if (UT == 16)
             mask &= 0xffffu;
         const int kvh = p.nhb == 1 ? c.item : c.item / p.nhb;
-        if (!p.bulk) {
+        if (!BULK) {
 #pragma unroll
             for (int b = 0; b < kSub; ++b) {
                 // (an entry out of range masks all 16 tokens: nothing is read at its offset)
@@ -429,8 +433,9 @@ __device__ unsigned int g_attn_error;
 // A bounded wait for a bulk copy's barrier (about 2 s; after one that ran out,
 // the warp's next ones only poll).  A copy cannot fail to arrive in a healthy
 // context; if one did, the warp would go on with whatever its slot holds.
-__device__ __noinline__ bool wait_bulk(uint64_t *bar, uint32_t parity, bool healthy)
+__device__ __forceinline__ bool wait_bulk(uint64_t *bar, uint32_t parity, bool healthy)
 {
+#pragma unroll 1
     for (int i = 0; i < (healthy ? 2000 : 1); ++i)
         if (ptx::mbar_wait_for(bar, parity, 1000000))
             return healthy;
@@ -1049,13 +1054,13 @@ __device__ __forceinline__ void store2(__nv_bfloat16 *p, float x, float y) { *re
 // join buffers (in the query rows' place where those are bf16) -- all of whole
 // 16-byte segments -- then maxima, sums, barriers and slot masks.  NU: units in
 // a warp's ring.
-template <typename M, int NU>
+template <typename M, int NU, bool SOLO>
 struct Layout {
     static constexpr int kQuery = kWarps * M::kQBytes;
     static constexpr int kSmall = kWarps * NU * 2 * 8 + (kWarps * M::MR * 2 + M::MR * 2 + kWarps * NU) * 4;
     static __host__ __device__ int join_stride(int D) { return D + 8; }
     static __host__ __device__ int ring_bytes(int stride) { return kWarps * NU * 2 * M::kUnit * stride; }
-    static __host__ __device__ int join_bytes(int D) { return 2 * M::MR * join_stride(D) * 4; }
+    static __host__ __device__ int join_bytes(int D) { return SOLO ? 0 : 2 * M::MR * join_stride(D) * 4; }
     static __host__ __device__ int middle_bytes(int D)
     {
         return M::kQSmem ? (kQuery > join_bytes(D) ? kQuery : join_bytes(D)) : kQuery + join_bytes(D);
@@ -1063,16 +1068,15 @@ struct Layout {
     static __host__ __device__ int total(int D, int stride) { return ring_bytes(stride) + middle_bytes(D) + kSmall; }
 };
 
-// Shares of warps where there are at least as many tiles (times key-value heads)
-// as CTAs: a warp then goes through whole tiles without a barrier, and a tile
-// is cut into a few parts at most.  Shares of CTAs where there are fewer: a
-// tile is then cut into many parts, and joining a CTA's warps first leaves a
-// quarter of them to the second launch.
-template <typename M, int NU>
+// SOLO: shares of warps, for many tiles: a warp goes through whole tiles without
+// a barrier, and a tile is cut into a few parts at most.  Else shares of CTAs,
+// for few: a tile is then cut into many parts, and joining a CTA's warps first
+// leaves a quarter of them to the second launch.
+template <typename M, int NU, bool SOLO, bool BULK>
 __global__ void __launch_bounds__(kThreads) ssd_paged_attn_kernel(const __grid_constant__ AttnParams p)
 {
     using T = typename M::T;
-    using L = Layout<M, NU>;
+    using L = Layout<M, NU, SOLO>;
     constexpr int UT = M::kUnit;
     extern __shared__ __align__(16) char smem[];
     __shared__ Found found[kWarps];
@@ -1083,7 +1087,7 @@ __global__ void __launch_bounds__(kThreads) ssd_paged_attn_kernel(const __grid_c
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    const Shares sh = locate<UT>(p, reinterpret_cast<int *>(smem), tmp, found);
+    const Shares sh = locate<UT, SOLO>(p, reinterpret_cast<int *>(smem), tmp, found);
     // padding rows see nothing
     if (p.a.start) {
         const long long r0 = min((long long)max(p.a.start[p.a.d.nreq], 0), (long long)p.a.d.nrows);
@@ -1096,11 +1100,15 @@ __global__ void __launch_bounds__(kThreads) ssd_paged_attn_kernel(const __grid_c
                 p.a.lse[i] = -INFINITY;
         }
     }
-    const bool solo = sh.solo;
-    const long long share = solo ? (long long)blockIdx.x * kWarps + w : blockIdx.x;
+    const long long share = SOLO ? (long long)blockIdx.x * kWarps + w : blockIdx.x;
     const long long u0 = share * sh.per, u1 = min(u0 + sh.per, sh.total);
-    if (solo ? lane == 0 : lane < kWarps && w == 0)   // (a CTA's share has its first warp's number in desc)
-        p.desc[solo ? share : (long long)blockIdx.x * kWarps + lane] = make_int4(-1, 0, 0, 0);
+    if (SOLO) {
+        if (lane == 0)
+            p.desc[share] = make_int4(-1, 0, 0, 0);
+    } else {   // (there may be fewer tiles than the host could tell)
+        for (long long i = sh.ntiles * p.items + blockIdx.x * kThreads + tid; i < p.ndesc; i += gridDim.x * kThreads)
+            p.desc[i] = make_int4(-1, 0, 0, 0);
+    }
     const int half_bytes = UT * stride;
     char *ring = smem + (size_t)w * NU * 2 * half_bytes;    // [NU][K, V][UT][stride]
     char *middle = smem + L::ring_bytes(stride);
@@ -1118,8 +1126,7 @@ __global__ void __launch_bounds__(kThreads) ssd_paged_attn_kernel(const __grid_c
             for (int c = p.seg; c * 16 < stride; ++c)
                 *reinterpret_cast<uint4 *>(ring + (size_t)i * stride + c * 16) = make_uint4(0, 0, 0, 0);
     }
-    const bool bulk = p.bulk;
-    if (bulk) {
+    if (BULK) {
         if (lane < NU * 2)
             ptx::mbar_init(bars + lane, 1);
         ptx::fence_mbar_init();
@@ -1131,22 +1138,23 @@ __global__ void __launch_bounds__(kThreads) ssd_paged_attn_kernel(const __grid_c
 
     Cursor cur;
     {
-        const Found f = found[solo ? w : 0];
+        const Found f = found[SOLO ? w : 0];
         set_tile<UT>(p, cur.t, f.req, f.j);
         cur.item = (int)((u0 - f.lin) / cur.t.units);
         cur.lin = f.lin + (long long)cur.item * cur.t.units;
+        cur.tile = f.tile;
     }
 
     // Steps alternate: while a unit's K is used the V half of the ring's newest
     // unit is loaded, while its V is used the next unit's K.  Every step is one
     // group of asynchronous copies, empty past the share's end.
-    const int step = solo ? 1 : kWarps;
-    Loader<T, M::kDim, M::kExact, UT> ld;
+    constexpr int step = SOLO ? 1 : kWarps;
+    Loader<T, M::kDim, BULK, UT> ld;
     ld.c = cur;
     ld.u1 = u1;
     ld.set_end();
     ld.u = (int)(u0 - cur.lin);
-    ld.skip(p, solo ? 0 : w);
+    ld.skip(p, SOLO ? 0 : w);
     ld.fetch_page(p, lane);
     int head = 0;
     auto load_k = [&]() {
@@ -1155,17 +1163,18 @@ __global__ void __launch_bounds__(kThreads) ssd_paged_attn_kernel(const __grid_c
             ld.offsets(p, lane);
             if (lane == 0)
                 masks[head] = ld.mask;
-            if (M::kExact && !bulk)
+            if constexpr (!BULK)
                 ld.copy(p, p.a.kc, ld.koff, p.a.d.kc_stride[1], smem_addr(slot), lane);
             else
                 ld.copy_bulk(p, p.a.kc, ld.koff[0], slot, bars + head * 2, false, lane);
         }
-        cp_commit();
+        if (!BULK)
+            cp_commit();
     };
     auto load_v = [&]() {
         if (ld.u >= 0) {
             char *slot = ring + (head * 2 + 1) * half_bytes;
-            if (M::kExact && !bulk)
+            if constexpr (!BULK)
                 ld.copy(p, p.a.vc, ld.voff, p.a.d.vc_stride[1], smem_addr(slot), lane);
             else
                 ld.copy_bulk(p, p.a.vc, ld.voff[0], slot, bars + head * 2 + 1, true, lane);
@@ -1173,7 +1182,8 @@ __global__ void __launch_bounds__(kThreads) ssd_paged_attn_kernel(const __grid_c
             ld.fetch_page(p, lane);
             head = head + 1 == NU ? 0 : head + 1;
         }
-        cp_commit();
+        if (!BULK)
+            cp_commit();
     };
 #pragma unroll 1
     for (int i = 0; i < NU - 1; ++i) {
@@ -1204,20 +1214,22 @@ __global__ void __launch_bounds__(kThreads) ssd_paged_attn_kernel(const __grid_c
         const int kvh = cur.item / p.nhb, hb = cur.item - kvh * p.nhb;
         const int h0 = kvh * p.group + hb * p.gh, nh = min(p.gh, p.group - hb * p.gh), rows = cur.t.nq * nh;
         // this warp's units: all, or those whose number in the CTA's share is w modulo the warps
-        const int skip = solo ? 0 : (w - (int)((cur.lin + u - u0) % kWarps) + kWarps) % kWarps;
+        const int skip = SOLO ? 0 : (w - (int)((cur.lin + u - u0) % kWarps) + kWarps) % kWarps;
         for (int x = u + skip; x < ue; x += step) {
             const int tok0 = (cur.t.ub + x) * UT;
             char *slot = ring + tail * 2 * half_bytes;
-            cp_wait<2 * NU - 2>();
-            if (bulk)
+            if constexpr (BULK)
                 healthy = wait_bulk(bars + tail * 2, parity, healthy);
+            else
+                cp_wait<2 * NU - 2>();
             __syncwarp();
             const uint32_t mask = masks[tail];
             load_v();
             math.scores(p, slot, mask, tok0, all0, all1, lane);
-            cp_wait<2 * NU - 2>();
-            if (bulk)
+            if constexpr (BULK)
                 healthy = wait_bulk(bars + tail * 2 + 1, parity, healthy);
+            else
+                cp_wait<2 * NU - 2>();
             __syncwarp();
             load_k();
             math.values(p, slot + half_bytes, mask, tok0, all0, all1, lane);
@@ -1237,7 +1249,7 @@ __global__ void __launch_bounds__(kThreads) ssd_paged_attn_kernel(const __grid_c
                 lse[(long long)j * p.a.d.nheads + (r - j * nh)] = ll == 0.f ? -INFINITY : kLn2 * (mm + log2f(ll));
             }
         };
-        if (solo) {
+        if constexpr (SOLO) {
             if (whole)
                 math.finish(p, rows, lane, [](float ll) { return ll == 0.f ? 0.f : 1.f / ll; },
                             [&](int r, int c, float a, float b) {
@@ -1293,93 +1305,74 @@ __global__ void __launch_bounds__(kThreads) ssd_paged_attn_kernel(const __grid_c
             if (M::kQSmem)
                 __syncthreads();   // (the next tile's query rows go where the buffers are)
         }
-        if (!whole && slot == 1 && (solo ? lane == 0 : tid == 0))   // the cut tile's first part: where the others are
-            p.desc[solo ? share : (long long)blockIdx.x * kWarps] =
-                make_int4(cur.t.row, cur.t.nq, cur.item,
-                          solo ? ~(int)((cur.lin + cur.t.units - 1) / sh.per) : (int)((cur.lin + cur.t.units - 1) / sh.per));
+        // where the parts of a cut tile are
+        if (SOLO ? !whole && slot == 1 && lane == 0 : slot == 1 && tid == 0)
+            p.desc[SOLO ? share : (long long)cur.tile * p.items + cur.item] =
+                make_int4(whole ? -1 : cur.t.row, cur.t.nq | cur.item << 8, (int)share, (int)((cur.lin + cur.t.units - 1) / sh.per));
         if (cur.lin + ue >= u1)
             break;
         u = 0;
         next_item<UT>(p, cur);
     }
-    cp_wait<0>();
+    if (!BULK)
+        cp_wait<0>();
 }
 
-// Joins the parts of the tiles that start in a share of CTA blockIdx.x and go
-// on in the next shares, row blockIdx.y of them: warps take parts in turn,
-// lanes the elements.
-constexpr int kJoinWarps = 8;
-
-template <typename T, int MR>
-__global__ void __launch_bounds__(32 * kJoinWarps) ssd_paged_attn_join_kernel(const __grid_constant__ AttnParams p)
+// Joins parts of row r of a cut tile: NW warps take parts in turn, lanes the
+// elements, each warp in the running form, so that the parts' maxima and rows
+// are loaded together, four at a time; then the warps through shared memory
+// (sm, so: of the NW warps).
+template <typename T, int MR, int NW>
+__device__ __forceinline__ void join_row(const AttnParams &p, const int4 &d, int r, int w, int lane, float (*sm)[2], float (*so)[256])
 {
-    __shared__ float sm[kJoinWarps][2];
-    __shared__ __align__(16) float so[kJoinWarps][256];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    int4 descs[kWarps];
+    const int row = d.x, item = d.y >> 8, c0 = d.z, n = d.w - d.z + 1, D = p.a.d.headdim;
+    const int kvh = item / p.nhb, hb = item - kvh * p.nhb, nh = min(p.gh, p.group - hb * p.gh);
+    float mm = -INFINITY, ll = 0.f, o[2][4] = {};
+    // part i lies in share c0 + i: slot 1 of the first, slot 0 of the others
+    for (int i = w; i < n; i += 4 * NW) {
+        float pm[4], pl[4];
+        float4 v[4][2];
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k)
-        descs[k] = p.desc[(long long)blockIdx.x * kWarps + k];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, r = blockIdx.y, D = p.a.d.headdim;
-#pragma unroll 1
-    for (int k = 0; k < kWarps; ++k) {
-        const int4 d = k == 0 ? descs[0] : k == 1 ? descs[1] : k == 2 ? descs[2] : descs[3];
-        const int row = d.x, nq = d.y, item = d.z;
-        const int kvh = item / p.nhb, hb = item - kvh * p.nhb, nh = min(p.gh, p.group - hb * p.gh);
-        if (row < 0 || r >= nq * nh)
-            continue;
-        // (numbers of shares: a CTA's one share has the CTA's number, four have 4 CTA + warp)
-        const bool solo = d.w < 0;
-        const int c0 = solo ? blockIdx.x * kWarps + k : blockIdx.x, c1 = solo ? ~d.w : d.w;
-        // part i lies in share c0 + i: slot 1 of the first, slot 0 of the others
-        const int n = c1 - c0 + 1;
-        // each warp joins its parts in the running form, so that their maxima and
-        // rows are loaded together, four parts at a time
-        float mm = -INFINITY, ll = 0.f, o[2][4] = {};
-        for (int i = w; i < n; i += 4 * kJoinWarps) {
-            float pm[4], pl[4];
-            float4 v[4][2];
+        for (int b = 0; b < 4; ++b) {
+            pm[b] = -INFINITY;
+            pl[b] = 0.f;
+            v[b][0] = v[b][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+            const int part = i + NW * b;
+            if (part < n) {
+                const size_t at = ((size_t)(c0 + part) * 2 + (part == 0 ? 1 : 0)) * MR + r;
+                const float2 t = *reinterpret_cast<const float2 *>(p.part_ml + 2 * at);
+                pm[b] = t.y == 0.f ? -INFINITY : t.x;   // (a part that saw nothing)
+                pl[b] = t.y;
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                pm[b] = -INFINITY;
-                pl[b] = 0.f;
-                v[b][0] = v[b][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-                const int part = i + kJoinWarps * b;
-                if (part < n) {
-                    const size_t at = ((size_t)(c0 + part) * 2 + (part == 0 ? 1 : 0)) * MR + r;
-                    const float2 t = *reinterpret_cast<const float2 *>(p.part_ml + 2 * at);
-                    pm[b] = t.y == 0.f ? -INFINITY : t.x;   // (a part that saw nothing)
-                    pl[b] = t.y;
-#pragma unroll
-                    for (int x = 0; x < 2; ++x)
-                        if (4 * lane + 128 * x < D)
-                            v[b][x] = *reinterpret_cast<const float4 *>(p.part_o + at * D + 4 * lane + 128 * x);
-                }
-            }
-            const float mn = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])), mm), base = mn == -INFINITY ? 0.f : mn;
-            const float keep = exp2_fast(mm - base);
-            mm = mn;
-            ll *= keep;
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    o[x][e] *= keep;
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const float f = exp2_fast(pm[b] - base);
-                ll += pl[b] * f;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    o[x][0] += f * v[b][x].x;
-                    o[x][1] += f * v[b][x].y;
-                    o[x][2] += f * v[b][x].z;
-                    o[x][3] += f * v[b][x].w;
-                }
+                for (int x = 0; x < 2; ++x)
+                    if (4 * lane + 128 * x < D)
+                        v[b][x] = *reinterpret_cast<const float4 *>(p.part_o + at * D + 4 * lane + 128 * x);
             }
         }
-        __syncthreads();   // (the previous tile's sums have been read)
+        const float mn = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])), mm), base = mn == -INFINITY ? 0.f : mn;
+        const float keep = exp2_fast(mm - base);
+        mm = mn;
+        ll *= keep;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                o[x][e] *= keep;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const float f = exp2_fast(pm[b] - base);
+            ll += pl[b] * f;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                o[x][0] += f * v[b][x].x;
+                o[x][1] += f * v[b][x].y;
+                o[x][2] += f * v[b][x].z;
+                o[x][3] += f * v[b][x].w;
+            }
+        }
+    }
+    float base = mm == -INFINITY ? 0.f : mm;
+    if (NW > 1) {
 #pragma unroll
         for (int x = 0; x < 2; ++x)
             *reinterpret_cast<float4 *>(&so[w][4 * lane + 128 * x]) = make_float4(o[x][0], o[x][1], o[x][2], o[x][3]);
@@ -1388,31 +1381,79 @@ __global__ void __launch_bounds__(32 * kJoinWarps) ssd_paged_attn_join_kernel(co
             sm[w][1] = ll;
         }
         __syncthreads();
-        float top = sm[0][0];
+        if (w != 0)
+            return;
+        float top = -INFINITY;
 #pragma unroll
-        for (int i = 1; i < kJoinWarps; ++i)
+        for (int i = 0; i < NW; ++i)
             top = fmaxf(top, sm[i][0]);
-        const float base = top == -INFINITY ? 0.f : top;
-        float f[kJoinWarps], total = 0.f;
+        base = top == -INFINITY ? 0.f : top;
+        ll = 0.f;
 #pragma unroll
-        for (int i = 0; i < kJoinWarps; ++i) {
-            f[i] = exp2_fast(sm[i][0] - base);
-            total += sm[i][1] * f[i];
-        }
-        const float inv = total == 0.f ? 0.f : 1.f / total;
-        const int j = r / nh, h = kvh * p.group + hb * p.gh + (r - j * nh);
-        for (int c = 2 * threadIdx.x; c < D; c += 64 * kJoinWarps) {
-            float a = 0.f, b = 0.f;
+        for (int x = 0; x < 2; ++x)
 #pragma unroll
-            for (int i = 0; i < kJoinWarps; ++i) {
-                a += so[i][c] * f[i];
-                b += so[i][c + 1] * f[i];
+            for (int e = 0; e < 4; ++e)
+                o[x][e] = 0.f;
+#pragma unroll
+        for (int i = 0; i < NW; ++i) {
+            const float f = exp2_fast(sm[i][0] - base);
+            ll += sm[i][1] * f;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const float4 v = *reinterpret_cast<const float4 *>(&so[i][4 * lane + 128 * x]);
+                o[x][0] += f * v.x;
+                o[x][1] += f * v.y;
+                o[x][2] += f * v.z;
+                o[x][3] += f * v.w;
             }
-            store2(static_cast<T *>(p.a.out) + (long long)(row + j) * p.a.d.o_stride[0] + (long long)h * p.a.d.o_stride[1] + c,
-                   a * inv, b * inv);
         }
-        if (p.a.lse && threadIdx.x == 0)
-            p.a.lse[(long long)(row + j) * p.a.d.nheads + h] = total == 0.f ? -INFINITY : kLn2 * (base + log2f(total));
+    }
+    const float inv = ll == 0.f ? 0.f : 1.f / ll;
+    const int j = r / nh, h = kvh * p.group + hb * p.gh + (r - j * nh);
+    T *out = static_cast<T *>(p.a.out) + (long long)(row + j) * p.a.d.o_stride[0] + (long long)h * p.a.d.o_stride[1];
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+        if (4 * lane + 128 * x < D)
+            store4(out + 4 * lane + 128 * x, make_float4(o[x][0] * inv, o[x][1] * inv, o[x][2] * inv, o[x][3] * inv));
+    if (p.a.lse && lane == 0)
+        p.a.lse[(long long)(row + j) * p.a.d.nheads + h] = ll == 0.f ? -INFINITY : kLn2 * (base + log2f(ll));
+}
+
+__device__ __forceinline__ int desc_rows(const AttnParams &p, const int4 &d)
+{
+    const int hb = (d.y >> 8) % p.nhb;
+    return d.x < 0 ? 0 : (d.y & 0xff) * min(p.gh, p.group - hb * p.gh);
+}
+
+constexpr int kJoinWarps = 8;
+
+// SOLO: few parts; a warp per row, a block per CTA of the first launch.  Else many
+// parts: a block per tile and row.
+template <typename T, int MR, bool SOLO>
+__global__ void __launch_bounds__(32 * kJoinWarps) ssd_paged_attn_join_kernel(const __grid_constant__ AttnParams p)
+{
+    __shared__ float sm[kJoinWarps][2];
+    __shared__ __align__(16) float so[SOLO ? 1 : kJoinWarps][256];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (SOLO) {
+        int4 d[kWarps];
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k)
+            d[k] = p.desc[(long long)blockIdx.x * kWarps + k];
+        int at = w;   // rows of all four, dealt to the warps
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) {
+            const int rows = desc_rows(p, d[k]);
+            for (; at < rows; at += kJoinWarps)
+                join_row<T, MR, 1>(p, d[k], at, 0, lane, sm, so);
+            at -= rows;
+        }
+    } else {
+        const int4 d = p.desc[blockIdx.x];
+        if ((int)blockIdx.y < desc_rows(p, d))
+            join_row<T, MR, kJoinWarps>(p, d, blockIdx.y, w, lane, sm, so);
     }
 }
 
@@ -1435,6 +1476,21 @@ int tile_rows(const ssd_attn_dims_t &d)
     return want <= 1 ? 1 : want <= 2 ? 2 : want <= 4 ? 4 : 8;
 }
 
+// tiles that the sizes allow at most (one per row, or per `tok` rows of a request)
+long long most_tiles(const AttnParams &p)
+{
+    if (!p.a.start)
+        return p.a.d.nrows;
+    return std::max<long long>(1, std::min<long long>(p.a.d.nrows, p.a.d.nrows / p.tok + p.a.d.nreq));
+}
+
+int sm_count();
+
+// Shares of warps for at least two tiles (times key-value heads) per SM: below
+// that a tile would be cut into more than four parts of warps, the join of
+// which costs more than the CTAs' own joins.
+bool solo_shares(const AttnParams &p) { return most_tiles(p) * p.items >= 2 * sm_count(); }
+
 constexpr int kMaxPerSm = 4;     // CTAs
 constexpr int kMaxCtas = 1024;   // the workspace is sized for at most this many
 
@@ -1449,14 +1505,14 @@ int sm_count()
     return n[dev];
 }
 
-template <typename M, int NU>
+template <typename M, int NU, bool SOLO, bool BULK>
 cudaError_t launch(AttnParams &p, void *workspace, cudaStream_t stream)
 {
     using T = typename M::T;
     const int D = p.a.d.headdim;
-    const int smem = std::max(Layout<M, NU>::total(D, p.stride), p.a.start ? (int)(p.a.d.nreq + 1) * 4 : 0);
-    auto kernel = ssd_paged_attn_kernel<M, NU>;
-    // CTAs per SM by shared memory (227 KB for them, 1 KB of the system's each) and registers
+    const int smem = std::max(Layout<M, NU, SOLO>::total(D, p.stride), p.a.start ? (int)(p.a.d.nreq + 1) * 4 : 0);
+    auto kernel = ssd_paged_attn_kernel<M, NU, SOLO, BULK>;
+    // CTAs per SM by shared memory (1 KB of the system's each) and registers
     static int regs = 0;   // (the same for every device)
     cudaError_t e;
     if (!regs) {
@@ -1469,10 +1525,11 @@ cudaError_t launch(AttnParams &p, void *workspace, cudaStream_t stream)
         return e;
     const int per_sm = std::max(1, std::min({kMaxPerSm, (228 << 10) / (smem + 1024 + 256), 65536 / (regs * kThreads)}));
     const int grid = std::min(kMaxCtas, sm_count() * per_sm);
+    const size_t shares = (size_t)grid * (SOLO ? kWarps : 1);
     p.part_o = static_cast<float *>(workspace);
-    const size_t shares = (size_t)grid * kWarps;
     p.part_ml = p.part_o + shares * 2 * M::MR * D;
     p.desc = reinterpret_cast<int4 *>(p.part_ml + shares * 2 * M::MR * 2);
+    p.ndesc = SOLO ? (int)shares : (int)(most_tiles(p) * p.items);
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1486,42 +1543,49 @@ cudaError_t launch(AttnParams &p, void *workspace, cudaStream_t stream)
     if ((e = cudaLaunchKernelEx(&cfg, kernel, p)) != cudaSuccess)
         return e;
     note_launches(1);
-    cfg.gridDim = dim3(grid, p.tok * p.gh);
+    cfg.gridDim = SOLO ? dim3(grid) : dim3(p.ndesc, p.tok * p.gh);
     cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, ssd_paged_attn_join_kernel<T, M::MR>, p);
+    e = cudaLaunchKernelEx(&cfg, ssd_paged_attn_join_kernel<T, M::MR, SOLO>, p);
     if (e == cudaSuccess)
         note_launches(1);
     return e;
 }
 
+template <typename M, int NU, int NUS, bool BULK>
+cudaError_t launch_shares(AttnParams &p, void *ws, cudaStream_t st)
+{
+    return solo_shares(p) ? launch<M, NUS, true, BULK>(p, ws, st) : launch<M, NU, false, BULK>(p, ws, st);
+}
+
 cudaError_t launch_bf16(AttnParams &p, int mr, void *ws, cudaStream_t st)
 {
     const int D = p.a.d.headdim;
-    if (D == 64)
-        return mr == 32 ? launch<Mma<2, 64, true, 1>, 4>(p, ws, st) : launch<Mma<1, 64, true, 2>, 2>(p, ws, st);
-    if (D == 128)
-        return mr == 32 ? launch<Mma<2, 128, true, 1>, 2>(p, ws, st) : launch<Mma<1, 128, true, 1>, 2>(p, ws, st);
-    if (D == 256)
-        return launch<Mma<1, 256, true, 1>, 2>(p, ws, st);
+    if (p.a.d.page_size % 16 == 0) {
+        if (D == 64)
+            return mr == 32 ? launch_shares<Mma<2, 64, true, 1>, 4, 4, false>(p, ws, st)
+                            : launch_shares<Mma<1, 64, true, 2>, 2, 2, false>(p, ws, st);
+        if (D == 128)
+            return mr == 32 ? launch_shares<Mma<2, 128, true, 1>, 2, 2, false>(p, ws, st)
+                            : launch_shares<Mma<1, 128, true, 1>, 2, 2, false>(p, ws, st);
+        if (D == 256)
+            return launch_shares<Mma<1, 256, true, 1>, 2, 2, false>(p, ws, st);
+    }
     if (D <= 128)
-        return mr == 32 ? launch<Mma<2, 128, false, 1>, 2>(p, ws, st) : launch<Mma<1, 128, false, 1>, 2>(p, ws, st);
-    return launch<Mma<1, 256, false, 1>, 2>(p, ws, st);
+        return mr == 32 ? launch_shares<Mma<2, 128, false, 1>, 2, 2, true>(p, ws, st)
+                        : launch_shares<Mma<1, 128, false, 1>, 2, 2, true>(p, ws, st);
+    return launch_shares<Mma<1, 256, false, 1>, 2, 2, true>(p, ws, st);
 }
 
 template <int MR>
 cudaError_t launch_f32_rows(AttnParams &p, void *ws, cudaStream_t st)
 {
     const int D = p.a.d.headdim;
-    if (D == 64)
-        return launch<Simt<MR, 64, true>, 1>(p, ws, st);
-    if (D == 128)
-        return launch<Simt<MR, 128, true>, 1>(p, ws, st);
+    if (D <= 64)
+        return launch_shares<Simt<MR, 64, false>, 1, 1, true>(p, ws, st);
     if (D <= 128)
-        return launch<Simt<MR, 128, false>, 1>(p, ws, st);
-    if (D == 256)
-        return launch<Simt<MR, 256, true>, 1>(p, ws, st);
-    return launch<Simt<MR, 256, false>, 1>(p, ws, st);
+        return launch_shares<Simt<MR, 128, false>, 1, 1, true>(p, ws, st);
+    return launch_shares<Simt<MR, 256, false>, 1, 1, true>(p, ws, st);
 }
 
 cudaError_t launch_f32(AttnParams &p, int mr, void *ws, cudaStream_t st)
@@ -1557,7 +1621,6 @@ cudaError_t attn_launch(const AttnArgs &a, void *workspace, cudaStream_t stream)
     // rows of an odd number of 16-byte segments: eight rows' segments lie in different banks
     const int seg = es == 2 ? (p.seg + 1) / 2 * 2 : p.seg;
     p.stride = (seg | 1) * 16;
-    p.bulk = a.d.page_size % 16 != 0 || (D != 64 && D != 128 && D != 256);
     // scores are kept as q.k times the scale's sign, so that their maximum is that of the scaled ones
     p.sign = a.d.scale > 0.f ? 1 : a.d.scale < 0.f ? -1 : 0;
     p.f = p.sign ? fabsf(a.d.scale) * kLog2e : 1.f;
