@@ -473,6 +473,9 @@ ssd_status_t check_attn_dims(const ssd_attn_dims_t *d)
     if (!strides_ok(d->q_stride, 2, nq, es, &why) || !strides_ok(d->o_stride, 2, nq, es, &why) ||
         !strides_ok(d->kc_stride, 3, nc, es, &why) || !strides_ok(d->vc_stride, 3, nc, es, &why))
         return why;
+    for (int i = 0; i < 2; ++i)   // the kernels hold page and token strides as 32-bit counts of 16 bytes
+        if (nc[i] > 1 && (d->kc_stride[i] * es / 16 >= (INT64_C(1) << 32) || d->vc_stride[i] * es / 16 >= (INT64_C(1) << 32)))
+            return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
 }
 

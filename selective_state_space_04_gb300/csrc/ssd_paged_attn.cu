@@ -1,1463 +1,17 @@
-// ssd_paged_attn.cu -- attention of new tokens over a paged key-value cache.
-//
-// A tile is up to MR query rows that read the same keys: the query heads of one
-// key-value head for one or several consecutive new tokens of a request.  The
-// tile's visible positions are cut into units of 16 or 32 tokens.  All units of
-// all tiles and key-value heads, laid end to end, are dealt out in equal
-// contiguous shares, whatever the requests' lengths; the CTAs that fit the GPU
-// at once stay for the whole launch.  A warp streams its units through a ring of
-// shared-memory slots of its own, K and V halves in turn, and keeps a running
-// maximum, sum and output rows in registers: no barrier stands between loads and
-// arithmetic, and loads run ahead across tile boundaries.
-//
-// Shares belong to warps, or to CTAs, whose warps then take units in turn and
-// are joined in shared memory at the end of a tile (many tiles, or few: see
-// kernel).  A tile that lies in one share is finished there; one that is cut
-// leaves partial results (maximum, sum, unnormalised rows), which a second
-// launch joins in the order of their shares.
-//
-// Two ways into the ring: 16-byte asynchronous copies, each lane at a fixed
-// segment of every row, where sizes are known at compile time and 16 aligned
-// tokens never cross a page; else one bulk copy per token and half, which takes
-// any row length and any page (at most one row per about 9 cycles and SM, which
-// bounds rows of 128 bytes at 4.1 TB/s, rows of 256 at the memory's rate).
-//
-// The running form: with s2 = scale log2(e) q.k, m = max s2 so far,
-// p = 2^(s2 - m), l = sum p, o = sum p v; when m grows by d, l and o are
-// scaled by 2^-d.  out = o / l, lse = ln 2 (m + log2 l).
-//
-// bf16: both products run on mma.sync m16n8k16 (scores: 16 query rows x 8
-// tokens; output: 16 rows x 8 elements over 16 tokens).  A score tile's
-// accumulator registers are, as they stand, the second product's A operand.
-// The weights p enter it as two bf16 terms, so that they carry 16 bits: one
-// bf16 term would add an error as large as the output's own rounding.
-// fp32: fp32 FMA (see Simt below).
-#include <cuda_bf16.h>
+// ssd_paged_attn.cu -- paged attention: sizes, variants and parameters.  The
+// kernels are in ssd_paged_attn.cuh.
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
 
-#include "f32x2.cuh"
-#include "ptx.cuh"
-#include "ssd_internal.h"
+#include "ssd_paged_attn.h"
 
 namespace ssd {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
-constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.4426950408889634f;
-
-// exact floor(n / d) for 0 <= n < 2^31: (n * mul) >> sh
-struct FastDiv {
-    uint32_t mul, sh;
-};
-
-struct AttnParams {
-    AttnArgs a;
-    FastDiv page;
-    float *part_o;      // [shares][2][MR][D] partial rows
-    float *part_ml;     // [shares][2][MR][2] their maxima (base 2) and sums
-    int4 *desc;         // the cut tiles: first row, tokens | item << 8, first and last share; x -1: none.  Shares of
-                        // warps: [shares], of the tile that starts in a share; shares of CTAs: [most tiles x items]
-    int ndesc;          // entries of it
-    int group;          // query heads per key-value head
-    int gh;             // query heads of a tile (group, or a part of it when it is larger than MR)
-    int nhb;            // head blocks per key-value head
-    int tok;            // most new tokens of a tile
-    int items;          // nkv * nhb: tiles of the same rows
-    int seg;            // 16-byte segments per row of K or V
-    int stride;         // bytes from row to row of a ring slot (an odd number of segments)
-    float f;            // |scale| log2(e), or 1 for scale 0
-    int sign;           // of scale
-};
-
-__device__ __forceinline__ int div_page(const FastDiv &f, int n) { return (int)(((uint64_t)(uint32_t)n * f.mul) >> f.sh); }
-
-__device__ __forceinline__ float exp2_fast(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
-// 16 bytes, or zeros when !on (nothing is read then, but the address must be valid all the same)
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool on)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-// ---- the walk over tiles, items and units ---------------------------------
-
-// One tile of query rows: nq tokens from row `row` of request `req`; the tokens
-// they see lie in [first, end), in `units` units from unit `ub` on.
-struct Tile {
-    int req, j, row, nq, rows_left;   // j: tile of the request; rows_left: the request's rows after this tile
-    int first, end, ub, units;
-};
-
-template <int UT>
-__device__ __forceinline__ void tile_extent(const AttnParams &p, Tile &t)
-{
-    const int limit = p.a.d.max_pages * p.a.d.page_size;
-    const int p0 = p.a.positions[t.row], p1 = t.nq > 1 ? p.a.positions[t.row + t.nq - 1] : p0;
-    t.end = p1 < 0 ? 0 : min(p1, limit - 1) + 1;
-    t.first = p.a.d.window > 0 ? max(0, p0 - p.a.d.window + 1) : 0;
-    t.first = min(t.first, t.end);
-    t.ub = t.first / UT;
-    t.units = max(1, (t.end + UT - 1) / UT - t.ub);   // (a tile that sees nothing still writes its rows)
-}
-
-// rows [s, e) of request r, clamped to the rows there are
-__device__ __forceinline__ void request_rows(const AttnParams &p, int r, int &s, int &e)
-{
-    const int n = (int)p.a.d.nrows;
-    s = min(max(p.a.start[r], 0), n);
-    e = min(max(p.a.start[r + 1], s), n);
-}
-
-template <int UT>
-__device__ __forceinline__ void set_tile(const AttnParams &p, Tile &t, int req, int j)
-{
-    t.req = req;
-    t.j = j;
-    if (p.a.start) {
-        int s, e;
-        request_rows(p, req, s, e);
-        t.row = s + j * p.tok;
-        t.nq = min(p.tok, e - t.row);
-        t.rows_left = e - t.row - t.nq;
-    } else {
-        t.row = req;
-        t.nq = 1;
-        t.rows_left = 0;
-    }
-    tile_extent<UT>(p, t);
-}
-
-// the next tile (there is one)
-template <int UT>
-__device__ __forceinline__ void next_tile(const AttnParams &p, Tile &t)
-{
-    if (t.rows_left > 0) {
-        set_tile<UT>(p, t, t.req, t.j + 1);
-        return;
-    }
-    int r = t.req + 1;
-    if (p.a.start) {
-        int s, e;
-        while (r < (int)p.a.d.nreq - 1) {
-            request_rows(p, r, s, e);
-            if (e > s)
-                break;
-            ++r;
-        }
-    }
-    set_tile<UT>(p, t, r, 0);
-}
-
-// A place in the CTA's share: a tile, an item (key-value head and head block)
-// of it, and the linear number of the item's first unit.
-struct Cursor {
-    Tile t;
-    int item, tile;   // (tile: counted over all requests; shares of CTAs)
-    long long lin;
-};
-
-template <int UT>
-__device__ __forceinline__ void next_item(const AttnParams &p, Cursor &c)
-{
-    c.lin += c.t.units;
-    if (++c.item == p.items) {
-        c.item = 0;
-        ++c.tile;
-        next_tile<UT>(p, c.t);
-    }
-}
-
-// ---- block scan for the schedule ------------------------------------------
-
-__device__ __forceinline__ long long block_exclusive(long long v, long long *total, long long *tmp)
-{
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    long long inc = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o)
-            inc += u;
-    }
-    __syncthreads();
-    if (lane == 31)
-        tmp[w] = inc;
-    __syncthreads();
-    long long before = 0, all = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-        if (i < w)
-            before += tmp[i];
-        all += tmp[i];
-    }
-    *total = all;
-    return before + inc - v;
-}
-
-struct Found {
-    int req, j, tile;
-    long long lin;   // the linear unit where the tile's first item begins
-};
-
-struct Shares {
-    long long total, per;   // units, and units of a share
-    long long ntiles;
-};
-
-// Where the CTA's shares begin (found[i]: of warp i's share, or found[0]).
-// Every CTA sums all tiles' units (a contiguous run of tiles per thread); the
-// thread whose run holds a share's first unit finds its tile.  `counts` (shared
-// memory, nreq + 1 ints) is used when there is a start array.
-template <int UT, bool SOLO>
-__device__ Shares locate(const AttnParams &p, int *counts, long long *tmp, Found *found)
-{
-    const int tid = threadIdx.x, nreq = (int)p.a.d.nreq;
-    long long ntiles = p.a.d.nrows;
-    if (p.a.start) {
-        const int run = (nreq + kThreads - 1) / kThreads, r0 = min(tid * run, nreq), r1 = min(r0 + run, nreq);
-        long long n = 0, all;
-        for (int r = r0; r < r1; ++r) {
-            int s, e;
-            request_rows(p, r, s, e);
-            n += (e - s + p.tok - 1) / p.tok;
-        }
-        long long at = block_exclusive(n, &all, tmp);
-        for (int r = r0; r < r1; ++r) {
-            int s, e;
-            request_rows(p, r, s, e);
-            counts[r] = (int)at;
-            at += (e - s + p.tok - 1) / p.tok;
-        }
-        if (tid == 0)
-            counts[nreq] = (int)all;
-        ntiles = all;
-        __syncthreads();
-    }
-    const long long run = (ntiles + kThreads - 1) / kThreads, t0 = min((long long)tid * run, ntiles), t1 = min(t0 + run, ntiles);
-    // the run's first tile
-    Found f{0, 0, 0, 0};
-    if (t0 < t1) {
-        if (p.a.start) {
-            int lo = 0, hi = nreq;
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (counts[mid] <= t0)
-                    lo = mid;
-                else
-                    hi = mid;
-            }
-            f.req = lo;
-            f.j = (int)(t0 - counts[lo]);
-        } else
-            f.req = (int)t0;
-    }
-    long long n = 0;
-    Tile t;
-    for (long long i = t0; i < t1; ++i) {
-        if (i == t0)
-            set_tile<UT>(p, t, f.req, f.j);
-        else
-            next_tile<UT>(p, t);
-        n += t.units;
-    }
-    long long sum;
-    const long long before = block_exclusive(n, &sum, tmp) * p.items;
-    Shares sh;
-    sh.total = sum * p.items;
-    sh.ntiles = ntiles;
-    sh.per = SOLO ? max(1ll, (sh.total + (long long)gridDim.x * kWarps - 1) / ((long long)gridDim.x * kWarps))
-                  : max((long long)kWarps, (sh.total + gridDim.x - 1) / gridDim.x);
-    if (t0 < t1) {
-        long long lin = before, tile = t0;
-        const long long end = before + n * p.items;
-        bool at_start = false;
-        for (int i = 0; i < (SOLO ? kWarps : 1); ++i) {
-            const long long u0 = ((long long)blockIdx.x * (SOLO ? kWarps : 1) + i) * sh.per;
-            if (u0 < before || u0 >= end)
-                continue;
-            if (!at_start) {   // (the walk goes on from share to share)
-                set_tile<UT>(p, t, f.req, f.j);
-                at_start = true;
-            }
-            while (u0 >= lin + (long long)t.units * p.items) {
-                lin += (long long)t.units * p.items;
-                next_tile<UT>(p, t);
-                ++tile;
-            }
-            found[i].req = t.req;
-            found[i].j = t.j;
-            found[i].tile = (int)tile;
-            found[i].lin = lin;
-        }
-    }
-    __syncthreads();
-    return sh;
-}
-
-// ---- the loader -------------------------------------------------------------
-
-// Streams a warp's units into its ring, K halves and V halves in turn.
-template <typename T, int DP, bool BULK, int UT>
-struct Loader {
-    static constexpr int kSegMax = DP * (int)sizeof(T) / 16;
-    static constexpr int kSub = UT / 16;
-    Cursor c;
-    int u, u_end;          // the unit within the item (-1: none left); the share's units of the item
-    long long u1;          // end of the share
-    int page;              // table entry read ahead (bulk: of the lane's token, else of the lane's 16 tokens)
-    uint32_t mask;         // the unit's tokens that are to be read
-    // byte offsets in the caches: of the first token of each 16; bulk: [0] of the lane's token
-    long long koff[kSub], voff[kSub];
-
-    __device__ __forceinline__ void set_end() { u_end = (int)min((long long)c.t.units, u1 - c.lin); }
-    // the unit `by` further on in the share
-    __device__ __forceinline__ void skip(const AttnParams &p, int by)
-    {
-        u += by;
-        while (u >= u_end) {
-            if (c.lin + u >= u1) {
-                u = -1;
-                return;
-            }
-            u -= c.t.units;
-            next_item<UT>(p, c);
-            set_end();
-        }
-    }
-    __device__ __forceinline__ void fetch_page(const AttnParams &p, int lane)
-    {
-        page = -1;
-        if (u >= 0) {
-            const int tok = (c.t.ub + u) * UT + (BULK ? lane % UT : kSub > 1 ? lane & 16 : 0);
-            if (tok < c.t.end)   // (16 tokens are in the page of the first of them)
-                page = __ldg(p.a.table + (long long)c.t.req * p.a.d.table_stride + div_page(p.page, tok));
-        }
-    }
-    __device__ __forceinline__ void offsets(const AttnParams &p, int lane)
-    {
-        const int tok0 = (c.t.ub + u) * UT, tok = tok0 + lane % UT;
-        const bool there = (unsigned)page < (unsigned)p.a.d.npages;
-        mask = __ballot_sync(0xffffffffu, tok >= c.t.first && tok < c.t.end && there);
-        if (UT == 16)
-            mask &= 0xffffu;
-        const int kvh = p.nhb == 1 ? c.item : c.item / p.nhb;
-        if (!BULK) {
-#pragma unroll
-            for (int b = 0; b < kSub; ++b) {
-                // (an entry out of range masks all 16 tokens: nothing is read at its offset)
-                const long long pg = max(kSub > 1 ? __shfl_sync(0xffffffffu, page, 16 * b) : page, 0);
-                const int at = tok0 + 16 * b, off = at - div_page(p.page, at) * p.a.d.page_size;
-                koff[b] = (pg * p.a.d.kc_stride[0] + off * p.a.d.kc_stride[1] + kvh * p.a.d.kc_stride[2]) * (long long)sizeof(T);
-                voff[b] = (pg * p.a.d.vc_stride[0] + off * p.a.d.vc_stride[1] + kvh * p.a.d.vc_stride[2]) * (long long)sizeof(T);
-            }
-        } else {
-            const long long pg = max(page, 0);
-            const int off = tok - div_page(p.page, tok) * p.a.d.page_size;
-            koff[0] = (pg * p.a.d.kc_stride[0] + off * p.a.d.kc_stride[1] + kvh * p.a.d.kc_stride[2]) * (long long)sizeof(T);
-            voff[0] = (pg * p.a.d.vc_stride[0] + off * p.a.d.vc_stride[1] + kvh * p.a.d.vc_stride[2]) * (long long)sizeof(T);
-        }
-    }
-    // one half (UT tokens of K or V) into a ring slot, by 16-byte copies
-    __device__ __forceinline__ void copy(const AttnParams &p, const void *base, const long long (&off)[kSub], long long tstride,
-                                         uint32_t slot, int lane)
-    {
-        const char *src = static_cast<const char *>(base);
-        constexpr uint32_t kAll = UT == 16 ? 0xffffu : 0xffffffffu;
-        // a lane's segment is the same in each of its rows, which lie kRows apart
-        constexpr int kRows = 32 / kSegMax > 0 ? 32 / kSegMax : 1;   // rows per instruction
-        constexpr int kParts = kSegMax / 32 > 0 ? kSegMax / 32 : 1;  // instructions per row
-        constexpr int kStride = (kSegMax | 1) * 16;
-        const int r0 = lane / kSegMax, seg = lane % kSegMax;
-        const uint32_t dst = slot + r0 * kStride + seg * 16;
-        const long long ts = tstride * (long long)sizeof(T);
-#pragma unroll
-        for (int b = 0; b < kSub; ++b) {
-            const char *s = src + off[b] + r0 * ts + seg * 16;
-#pragma unroll
-            for (int i = 0; i < 16 / kRows; ++i) {
-#pragma unroll
-                for (int x = 0; x < kParts; ++x) {
-                    const uint32_t d = dst + (16 * b + i * kRows) * kStride + x * 512;
-                    if (mask == kAll)
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(s + x * 512) : "memory");
-                    else {
-                        const bool on = (mask >> (16 * b + i * kRows + r0)) & 1;
-                        cp_async16(d, on ? s + x * 512 : static_cast<const char *>(p.a.q), on);
-                    }
-                }
-                s += kRows * ts;
-            }
-        }
-    }
-    // ... by one bulk copy per token; `bar` completes when all are there.  Rows
-    // of V that are not read are zeroed (those of K only give scores that are
-    // masked).
-    __device__ __forceinline__ void copy_bulk(const AttnParams &p, const void *base, long long off, char *slot, uint64_t *bar,
-                                              bool zero, int lane)
-    {
-        const int bytes = p.seg * 16;
-        char *dst = slot + (lane % UT) * p.stride;
-        const bool mine = lane < UT, on = mine && ((mask >> (lane % UT)) & 1);
-        if (zero && mine && !on) {
-            for (int c = 0; c < p.seg; ++c)
-                *reinterpret_cast<uint4 *>(dst + c * 16) = make_uint4(0, 0, 0, 0);
-            ptx::fence_proxy_async_smem();   // (later bulk copies write the row)
-        }
-        if (lane == 0)
-            ptx::mbar_arrive_expect_tx(bar, (uint32_t)(__popc(mask) * bytes));
-        __syncwarp();
-        if (on)
-            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                             smem_addr(dst)), "l"(static_cast<const char *>(base) + off), "r"(bytes), "r"(smem_addr(bar))
-                         : "memory");
-    }
-};
-
-// Set (to SSD_ERR_TIMEOUT) by a warp that gave up a wait for its copies.
-__device__ unsigned int g_attn_error;
-
-// A bounded wait for a bulk copy's barrier (about 2 s; after one that ran out,
-// the warp's next ones only poll).  A copy cannot fail to arrive in a healthy
-// context; if one did, the warp would go on with whatever its slot holds.
-__device__ __forceinline__ bool wait_bulk(uint64_t *bar, uint32_t parity, bool healthy)
-{
-#pragma unroll 1
-    for (int i = 0; i < (healthy ? 2000 : 1); ++i)
-        if (ptx::mbar_wait_for(bar, parity, 1000000))
-            return healthy;
-    atomicExch(&g_attn_error, (unsigned int)SSD_ERR_TIMEOUT);
-    return false;
-}
-
-// ---- the arithmetic: bf16 on mma.sync --------------------------------------
-
-__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4])
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
-}
-__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4])
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
-}
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
-{
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
-{
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-// the largest of the warps' maxima of row r (0 when no warp saw a token)
-template <int MR>
-__device__ __forceinline__ float joint_max(const float *ml, int r)
-{
-    float v = ml[2 * r];
-#pragma unroll
-    for (int i = 1; i < kWarps; ++i)
-        v = fmaxf(v, ml[(i * MR + r) * 2]);
-    return v == -INFINITY ? 0.f : v;
-}
-
-// NM: tiles of 16 query rows; DP: the head's elements, rounded up (EXACT: as
-// they are); NT: 16-token halves of a unit.  A lane holds results of rows
-// lane / 4 and lane / 4 + 8 of each tile.
-template <int NM, int DP, bool EX, int NT>
-struct Mma {
-    using T = __nv_bfloat16;
-    static constexpr int MR = 16 * NM, kDim = DP, kUnit = 16 * NT;
-    static constexpr bool kExact = EX;
-    // Query rows stay in registers, but for 64 KB of output rows per warp and
-    // more (256 of a lane's registers are not enough for both): then in shared
-    // memory, read anew for each unit.
-    static constexpr bool kQSmem = NM * DP >= 256;
-    static constexpr int kQStride = (DP / 8 | 1) * 16;
-    static constexpr int kQBytes = kQSmem ? MR * kQStride : 0;   // per warp
-    uint32_t q[kQSmem ? 1 : NM][kQSmem ? 1 : DP / 16][4];
-    char *qs;
-    float o[NM][DP / 8][4];
-    float s[NM][2 * NT][4];
-    float m[NM][2], l[NM][2];   // m: the running maximum of q.k (of -q.k for a negative scale)
-    int lo[NM][2], hi[NM][2];   // positions a row sees
-
-    __device__ __forceinline__ static int dim(const AttnParams &p) { return EX ? DP : p.a.d.headdim; }
-    __device__ __forceinline__ static int row_bytes(const AttnParams &p) { return EX ? ((DP / 8) | 1) * 16 : p.stride; }
-
-    __device__ __forceinline__ void begin(const AttnParams &p, const Tile &t, int item, int lane)
-    {
-        const int kvh = item / p.nhb, hb = item - kvh * p.nhb, D = dim(p);
-        const int h0 = hb * p.gh, nh = min(p.gh, p.group - h0), rows = t.nq * nh;
-        const int limit = p.a.d.max_pages * p.a.d.page_size;
-        const uint32_t keep = p.sign == 0 ? 0u : 0xffffffffu, flip = p.sign < 0 ? 0x80008000u : 0u;
-#pragma unroll
-        for (int mt = 0; mt < NM; ++mt)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int r = mt * 16 + x * 8 + (lane >> 2), rr = min(r, rows - 1), j = rr / nh, g = rr - j * nh;
-                const int pos = p.a.positions[t.row + j];
-                hi[mt][x] = pos < 0 ? 0 : min(pos, limit - 1) + 1;
-                lo[mt][x] = p.a.d.window > 0 ? max(0, pos - p.a.d.window + 1) : 0;
-                m[mt][x] = -INFINITY;
-                l[mt][x] = 0.f;
-                const T *src = static_cast<const T *>(p.a.q) + (long long)(t.row + j) * p.a.d.q_stride[0] +
-                               (long long)(kvh * p.group + h0 + g) * p.a.d.q_stride[1];
-#pragma unroll
-                for (int k = 0; k < DP / 16; ++k)
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const int c = 16 * k + 8 * y + 2 * (lane & 3);
-                        uint32_t v = r < rows && c < D ? *reinterpret_cast<const uint32_t *>(src + c) : 0u;
-                        v = (v & keep) ^ flip;
-                        if constexpr (kQSmem)
-                            *reinterpret_cast<uint32_t *>(qs + r * kQStride + c * 2) = v;
-                        else
-                            q[mt][k][x + 2 * y] = v;
-                    }
-            }
-        if (kQSmem)
-            __syncwarp();
-#pragma unroll
-        for (int mt = 0; mt < NM; ++mt)
-#pragma unroll
-            for (int n = 0; n < DP / 8; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    o[mt][n][i] = 0.f;
-    }
-
-    // scores of a unit's tokens and their weights; mask: the tokens read;
-    // [all0, all1): tokens that every row sees
-    __device__ __forceinline__ void scores(const AttnParams &p, char *slot_ptr, uint32_t mask, int tok0, int all0, int all1, int lane)
-    {
-        const int D = dim(p), stride = row_bytes(p);
-        const uint32_t slot = smem_addr(slot_ptr);
-#pragma unroll
-        for (int mt = 0; mt < NM; ++mt)
-#pragma unroll
-            for (int n = 0; n < 2 * NT; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    s[mt][n][i] = 0.f;
-        // lanes 0-7, 8-15: tokens 0-7, first and second 16 bytes; 16-23, 24-31: tokens 8-15
-        const uint32_t a = slot + ((lane & 7) + ((lane >> 4) << 3)) * stride + ((lane >> 3) & 1) * 16;
-        // (query rows in shared memory) lanes 0-7, 8-15: rows 0-7, 8-15, first 16 bytes; 16-31: second
-        const uint32_t qa = kQSmem ? smem_addr(qs) + ((lane & 7) + (((lane >> 3) & 1) << 3)) * kQStride + (lane >> 4) * 16 : 0;
-#pragma unroll
-        for (int k = 0; k < DP / 16; ++k) {
-            if (16 * k < D) {
-                uint32_t qf[NM][4];
-#pragma unroll
-                for (int mt = 0; mt < NM; ++mt) {
-                    if constexpr (kQSmem)
-                        ldsm4(qa + mt * 16 * kQStride + k * 32, qf[mt]);
-                    else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            qf[mt][i] = q[mt][k][i];
-                    }
-                }
-#pragma unroll
-                for (int h = 0; h < NT; ++h) {
-                    uint32_t b[4];
-                    ldsm4(a + h * 16 * stride + k * 32, b);
-#pragma unroll
-                    for (int mt = 0; mt < NM; ++mt) {
-                        mma16816(s[mt][2 * h], qf[mt], b[0], b[1]);
-                        mma16816(s[mt][2 * h + 1], qf[mt], b[2], b[3]);
-                    }
-                }
-            }
-        }
-        constexpr uint32_t kAll = NT == 1 ? 0xffffu : 0xffffffffu;
-        if (mask != kAll || tok0 < all0 || tok0 + kUnit > all1) {
-#pragma unroll
-            for (int n = 0; n < 2 * NT; ++n)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int tt = 8 * n + 2 * (lane & 3) + i, tok = tok0 + tt;
-                    const bool there = (mask >> tt) & 1;
-#pragma unroll
-                    for (int mt = 0; mt < NM; ++mt)
-#pragma unroll
-                        for (int x = 0; x < 2; ++x)
-                            if (!there || tok < lo[mt][x] || tok >= hi[mt][x])
-                                s[mt][n][2 * x + i] = -INFINITY;
-                }
-        }
-#pragma unroll
-        for (int mt = 0; mt < NM; ++mt) {
-            float keep[2];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                float top = m[mt][x];
-#pragma unroll
-                for (int n = 0; n < 2 * NT; ++n)
-                    top = fmaxf(top, fmaxf(s[mt][n][2 * x], s[mt][n][2 * x + 1]));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const float base = (top == -INFINITY ? 0.f : top) * p.f;
-                keep[x] = exp2_fast(m[mt][x] * p.f - base);
-                m[mt][x] = top;
-                float sum = 0.f;
-#pragma unroll
-                for (int n = 0; n < 2 * NT; ++n)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float &v = s[mt][n][2 * x + i];
-                        v = exp2_fast(v * p.f - base);
-                        sum += v;
-                    }
-                l[mt][x] = l[mt][x] * keep[x] + sum;
-            }
-            if (__any_sync(0xffffffffu, keep[0] != 1.f || keep[1] != 1.f)) {
-#pragma unroll
-                for (int n = 0; n < DP / 8; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        o[mt][n][i] *= keep[i >> 1];
-            }
-        }
-    }
-
-    // Tokens that some rows of the tile see and others do not are added row by
-    // row, to those that see them, and then left out of the product: there a
-    // weight 0 times an infinity or NaN of theirs would reach every row.
-    // (Unrolled over the tokens: a running token number would index the score
-    // registers at run time and put them in local memory.)
-    __device__ __forceinline__ void partial_tokens(const AttnParams &p, char *slot_ptr, uint32_t part, int tok0, int lane)
-    {
-        const int stride = row_bytes(p);
-        const uint32_t slot = smem_addr(slot_ptr);
-#pragma unroll
-        for (int tt = 0; tt < kUnit; ++tt) {
-            if (!((part >> tt) & 1))
-                continue;
-            const uint32_t row = slot + tt * stride;
-            float wgt[NM][2];
-#pragma unroll
-            for (int mt = 0; mt < NM; ++mt)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    float &own = s[mt][tt >> 3][2 * x + (tt & 1)];
-                    const bool sees = tok0 + tt >= lo[mt][x] && tok0 + tt < hi[mt][x];
-                    wgt[mt][x] = __shfl_sync(0xffffffffu, own, (lane & ~3) | ((tt & 7) >> 1));
-                    if (!sees)
-                        wgt[mt][x] = -1.f;
-                    if ((lane & 3) == ((tt & 7) >> 1))
-                        own = 0.f;
-                }
-#pragma unroll
-            for (int n = 0; n < DP / 8; ++n) {
-                if (8 * n < dim(p)) {
-                    uint32_t v;
-                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(row + 16 * n + 4 * (lane & 3)) : "memory");
-#pragma unroll
-                    for (int mt = 0; mt < NM; ++mt)
-#pragma unroll
-                        for (int x = 0; x < 2; ++x)
-                            if (!(wgt[mt][x] < 0.f)) {
-                                o[mt][n][2 * x] += wgt[mt][x] * __uint_as_float(v << 16);
-                                o[mt][n][2 * x + 1] += wgt[mt][x] * __uint_as_float(v & 0xffff0000u);
-                            }
-                }
-            }
-            __syncwarp();
-            for (int c = lane; c < p.seg; c += 32)
-                *reinterpret_cast<uint4 *>(slot_ptr + tt * stride + c * 16) = make_uint4(0, 0, 0, 0);
-        }
-        ptx::fence_proxy_async_smem();   // (later bulk copies write the rows)
-        __syncwarp();
-    }
-
-    __device__ __forceinline__ void values(const AttnParams &p, char *slot_ptr, uint32_t mask, int tok0, int all0, int all1, int lane)
-    {
-        const int D = dim(p), stride = row_bytes(p);
-        if (tok0 < all0 || tok0 + kUnit > all1) {
-            // bit tt: every row sees token tok0 + tt
-            const int a0 = min(max(all0 - tok0, 0), kUnit), a1 = min(max(all1 - tok0, 0), kUnit);
-            const uint32_t all = a1 > a0 ? (0xffffffffu >> (32 - a1)) & (0xffffffffu << a0) : 0u;
-            const uint32_t part = mask & ~all;
-            if (part)
-                partial_tokens(p, slot_ptr, part, tok0, lane);
-        }
-        // lanes 0-7, 8-15: tokens 0-7, 8-15 of the first 16 bytes; 16-31: of the second
-        const uint32_t a = smem_addr(slot_ptr) + ((lane & 7) + (((lane >> 3) & 1) << 3)) * stride + (lane >> 4) * 16;
-#pragma unroll
-        for (int h = 0; h < NT; ++h) {
-            uint32_t hi4[NM][4], lo4[NM][4];
-#pragma unroll
-            for (int mt = 0; mt < NM; ++mt)
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const float u = s[mt][2 * h + n][2 * x], v = s[mt][2 * h + n][2 * x + 1];
-                        const uint32_t w = pack_bf16(u, v);
-                        hi4[mt][2 * n + x] = w;
-                        lo4[mt][2 * n + x] = pack_bf16(u - __uint_as_float(w << 16), v - __uint_as_float(w & 0xffff0000u));
-                    }
-#pragma unroll
-            for (int n = 0; n < DP / 16; ++n) {
-                if (16 * n < D) {
-                    uint32_t b[4];
-                    ldsm4t(a + h * 16 * stride + n * 32, b);
-#pragma unroll
-                    for (int mt = 0; mt < NM; ++mt) {
-                        mma16816(o[mt][2 * n], hi4[mt], b[0], b[1]);
-                        mma16816(o[mt][2 * n + 1], hi4[mt], b[2], b[3]);
-                        mma16816(o[mt][2 * n], lo4[mt], b[0], b[1]);
-                        mma16816(o[mt][2 * n + 1], lo4[mt], b[2], b[3]);
-                    }
-                }
-            }
-        }
-    }
-
-    // the sums over the four lanes of a row; the rows' maxima (base 2) and sums to shared memory
-    __device__ __forceinline__ void end(const AttnParams &p, float *ml, int lane)
-    {
-#pragma unroll
-        for (int mt = 0; mt < NM; ++mt)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                l[mt][x] += __shfl_xor_sync(0xffffffffu, l[mt][x], 1);
-                l[mt][x] += __shfl_xor_sync(0xffffffffu, l[mt][x], 2);
-                m[mt][x] *= p.f;
-                if ((lane & 3) == 0) {
-                    const int r = mt * 16 + x * 8 + (lane >> 2);
-                    ml[2 * r] = m[mt][x];
-                    ml[2 * r + 1] = l[mt][x];
-                }
-            }
-    }
-    // The warp's rows as they are, without a join: `out(r, c, x, y)` takes elements
-    // c, c + 1 of row r, scaled by `scale(m, l)`, and `stat(r, m, l)` the rows'
-    // maxima (base 2, 0 for a row that saw nothing) and sums.
-    template <typename Scale, typename Out, typename Stat>
-    __device__ __forceinline__ void finish(const AttnParams &p, int rows, int lane, Scale scale, Out out, Stat stat)
-    {
-#pragma unroll
-        for (int mt = 0; mt < NM; ++mt)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int r = mt * 16 + x * 8 + (lane >> 2);
-                float ll = l[mt][x];
-                ll += __shfl_xor_sync(0xffffffffu, ll, 1);
-                ll += __shfl_xor_sync(0xffffffffu, ll, 2);
-                const float mm = m[mt][x] == -INFINITY ? 0.f : m[mt][x] * p.f, f = scale(ll);
-                if (r < rows) {
-                    if ((lane & 3) == 0)
-                        stat(r, mm, ll);
-#pragma unroll
-                    for (int n = 0; n < DP / 8; ++n)
-                        if (8 * n < dim(p))
-                            out(r, 8 * n + 2 * (lane & 3), o[mt][n][2 * x] * f, o[mt][n][2 * x + 1] * f);
-                }
-            }
-    }
-    // m becomes the factor that brings the warp's rows to the warps' joint maximum
-    __device__ __forceinline__ void rescale(const float *ml, int lane)
-    {
-#pragma unroll
-        for (int mt = 0; mt < NM; ++mt)
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-                m[mt][x] = exp2_fast(m[mt][x] - joint_max<MR>(ml, mt * 16 + x * 8 + (lane >> 2)));
-    }
-    // the scaled rows, written to or added to buf [MR][ds]
-    template <bool ADD>
-    __device__ __forceinline__ void put(const AttnParams &p, float *buf, int ds, int rows, int lane)
-    {
-#pragma unroll
-        for (int mt = 0; mt < NM; ++mt)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int r = mt * 16 + x * 8 + (lane >> 2);
-                if (r < rows) {
-                    const float f = m[mt][x];
-#pragma unroll
-                    for (int n = 0; n < DP / 8; ++n) {
-                        const int c = 8 * n + 2 * (lane & 3);
-                        if (8 * n < dim(p)) {
-                            float2 *at = reinterpret_cast<float2 *>(buf + r * ds + c);
-                            float2 v = make_float2(o[mt][n][2 * x] * f, o[mt][n][2 * x + 1] * f);
-                            if (ADD) {
-                                const float2 u = *at;
-                                v.x += u.x;
-                                v.y += u.y;
-                            }
-                            *at = v;
-                        }
-                    }
-                }
-            }
-    }
-};
-
-// ---- the arithmetic: fp32 ---------------------------------------------------
-
-// Scores: a unit's 32 tokens over the lanes (16 tokens, two lanes each, where
-// 32 rows of K for every warp do not fit shared memory), the query rows read
-// from shared memory at the same address by all lanes.  Output: a lane holds 4
-// elements of every row (8 for heads above 128); for heads of at most 64 the
-// half warps take tokens in turn.  The weights go through shared memory.
-// Products and sums are packed pairs of fp32 FMA.
-template <int MRows, int DP, bool EX>
-struct Simt {
-    using T = float;
-    static constexpr int MR = MRows, kDim = DP, kUnit = DP > 128 ? 16 : 32;
-    static constexpr bool kExact = EX;
-    static constexpr int kPer = 32 / kUnit;              // lanes per token in the scores
-    static constexpr int kGroups = DP <= 64 ? 2 : 1;     // tokens at a time in the output
-    static constexpr int NV = (DP + 127) / 128;          // float4 of the output per lane and row
-    f32x2 o[MR][NV][2];
-    float m[MR], l[MR];   // m: the running maximum of q.k (of -q.k for a negative scale)
-    int lo[MR], hi[MR];
-    float *qs, *ps;       // the warp's query rows [MR][DP] and weights [MR][kUnit]
-    static constexpr int kQBytes = MR * (DP + kUnit) * 4;   // per warp
-    static constexpr bool kQSmem = false;
-
-    __device__ __forceinline__ static int dim(const AttnParams &p) { return EX ? DP : p.a.d.headdim; }
-    __device__ __forceinline__ static int row_bytes(const AttnParams &p) { return EX ? ((DP / 4) | 1) * 16 : p.stride; }
-
-    __device__ __forceinline__ void begin(const AttnParams &p, const Tile &t, int item, int lane)
-    {
-        const int kvh = item / p.nhb, hb = item - kvh * p.nhb, D = dim(p);
-        const int h0 = hb * p.gh, nh = min(p.gh, p.group - h0), rows = t.nq * nh;
-        const int limit = p.a.d.max_pages * p.a.d.page_size;
-#pragma unroll
-        for (int r = 0; r < MR; ++r) {
-            const int rr = min(r, rows - 1), j = rr / nh, g = rr - j * nh;
-            const int pos = p.a.positions[t.row + j];
-            hi[r] = pos < 0 ? 0 : min(pos, limit - 1) + 1;
-            lo[r] = p.a.d.window > 0 ? max(0, pos - p.a.d.window + 1) : 0;
-            m[r] = -INFINITY;
-            l[r] = 0.f;
-            const float *src = static_cast<const float *>(p.a.q) + (long long)(t.row + j) * p.a.d.q_stride[0] +
-                               (long long)(kvh * p.group + h0 + g) * p.a.d.q_stride[1];
-            for (int c = 4 * lane; c < DP; c += 128) {
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (r < rows && c < D && p.sign != 0)
-                    v = *reinterpret_cast<const float4 *>(src + c);
-                if (p.sign < 0)
-                    v = make_float4(-v.x, -v.y, -v.z, -v.w);
-                *reinterpret_cast<float4 *>(qs + r * DP + c) = v;
-            }
-#pragma unroll
-            for (int n = 0; n < NV; ++n)
-                o[r][n][0] = o[r][n][1] = pk2(0.f, 0.f);
-        }
-        __syncwarp();
-    }
-
-    __device__ __forceinline__ void scores(const AttnParams &p, char *slot, uint32_t mask, int tok0, int all0, int all1, int lane)
-    {
-        const int tt = lane % kUnit, part = lane / kUnit, D = dim(p);
-        const ulonglong2 *k = reinterpret_cast<const ulonglong2 *>(slot + tt * row_bytes(p));
-        f32x2 acc[MR][2];
-#pragma unroll
-        for (int r = 0; r < MR; ++r)
-            acc[r][0] = acc[r][1] = pk2(0.f, 0.f);
-#pragma unroll 4
-        for (int c = part; c < D / 4; c += kPer) {
-            const ulonglong2 kv = k[c];
-#pragma unroll
-            for (int r = 0; r < MR; ++r) {
-                const ulonglong2 qv = *reinterpret_cast<const ulonglong2 *>(qs + r * DP + 4 * c);
-                acc[r][0] = fma2(qv.x, kv.x, acc[r][0]);
-                acc[r][1] = fma2(qv.y, kv.y, acc[r][1]);
-            }
-        }
-        constexpr uint32_t kAll = kUnit == 16 ? 0xffffu : 0xffffffffu;
-        const bool masked = mask != kAll || tok0 < all0 || tok0 + kUnit > all1;
-#pragma unroll
-        for (int r = 0; r < MR; ++r) {
-            float v = (lo2(acc[r][0]) + hi2(acc[r][0])) + (lo2(acc[r][1]) + hi2(acc[r][1]));
-            if (kPer == 2)
-                v += __shfl_xor_sync(0xffffffffu, v, 16);
-            if (masked && (!((mask >> tt) & 1) || tok0 + tt < lo[r] || tok0 + tt >= hi[r]))
-                v = -INFINITY;
-            float top = v;
-#pragma unroll
-            for (int x = kUnit / 2; x >= 1; x >>= 1)
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-            const float mn = fmaxf(m[r], top), base = (mn == -INFINITY ? 0.f : mn) * p.f;
-            const float keep = exp2_fast(m[r] * p.f - base), e = exp2_fast(v * p.f - base);
-            m[r] = mn;
-            l[r] = l[r] * keep + (part == 0 ? e : 0.f);   // summed over the lanes at the end
-            if (part == 0)
-                ps[r * kUnit + tt] = e;
-            if (keep != 1.f) {
-                const f32x2 kk = pk2(keep, keep);
-#pragma unroll
-                for (int n = 0; n < NV; ++n) {
-                    o[r][n][0] = mul2(o[r][n][0], kk);
-                    o[r][n][1] = mul2(o[r][n][1], kk);
-                }
-            }
-        }
-        __syncwarp();
-    }
-
-    __device__ __forceinline__ void values(const AttnParams &p, char *slot, uint32_t mask, int tok0, int all0, int all1, int lane)
-    {
-        const int grp = kGroups == 2 ? lane >> 4 : 0, el = 4 * (kGroups == 2 ? lane & 15 : lane), stride = row_bytes(p);
-        // tokens not read are zero in the slot; one that a row does not see is skipped for it
-        const bool ragged = tok0 < all0 || tok0 + kUnit > all1;
-#pragma unroll 2
-        for (int t4 = 0; t4 < kUnit; t4 += 4) {
-            float w[MR][4];
-#pragma unroll
-            for (int r = 0; r < MR; ++r)
-                *reinterpret_cast<float4 *>(w[r]) = *reinterpret_cast<const float4 *>(ps + r * kUnit + t4);
-#pragma unroll
-            for (int i = 0; i < 4 / kGroups; ++i) {
-                const int tt = t4 + i * kGroups + grp;
-#pragma unroll
-                for (int n = 0; n < NV; ++n) {
-                    const int c = el + 128 * n;
-                    ulonglong2 v = make_ulonglong2(0, 0);
-                    if (EX || c < dim(p))
-                        v = *reinterpret_cast<const ulonglong2 *>(slot + tt * stride + 4 * c);
-#pragma unroll
-                    for (int r = 0; r < MR; ++r) {
-                        const float e = kGroups == 2 && grp ? w[r][(kGroups * i + 1) & 3] : w[r][kGroups * i];
-                        if (!ragged || (tok0 + tt >= lo[r] && tok0 + tt < hi[r])) {
-                            const f32x2 ee = pk2(e, e);
-                            o[r][n][0] = fma2(ee, v.x, o[r][n][0]);
-                            o[r][n][1] = fma2(ee, v.y, o[r][n][1]);
-                        }
-                    }
-                }
-            }
-        }
-        __syncwarp();
-    }
-
-    __device__ __forceinline__ void add_groups()
-    {
-        if (kGroups == 2) {
-#pragma unroll
-            for (int r = 0; r < MR; ++r)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    o[r][0][i] = pk2(lo2(o[r][0][i]) + __shfl_xor_sync(0xffffffffu, lo2(o[r][0][i]), 16),
-                                     hi2(o[r][0][i]) + __shfl_xor_sync(0xffffffffu, hi2(o[r][0][i]), 16));
-        }
-    }
-    // as Mma's
-    template <typename Scale, typename Out, typename Stat>
-    __device__ __forceinline__ void finish(const AttnParams &p, int rows, int lane, Scale scale, Out out, Stat stat)
-    {
-        add_groups();
-#pragma unroll
-        for (int r = 0; r < MR; ++r) {
-            float ll = l[r];
-#pragma unroll
-            for (int x = 16; x >= 1; x >>= 1)
-                ll += __shfl_xor_sync(0xffffffffu, ll, x);
-            const float mm = m[r] == -INFINITY ? 0.f : m[r] * p.f, f = scale(ll);
-            if (r < rows && (kGroups == 1 || lane < 16)) {
-                if (lane == 0)
-                    stat(r, mm, ll);
-#pragma unroll
-                for (int n = 0; n < NV; ++n) {
-                    const int c = 4 * lane + 128 * n;
-                    if (c < dim(p)) {
-                        out(r, c, lo2(o[r][n][0]) * f, hi2(o[r][n][0]) * f);
-                        out(r, c + 2, lo2(o[r][n][1]) * f, hi2(o[r][n][1]) * f);
-                    }
-                }
-            }
-        }
-    }
-    __device__ __forceinline__ void end(const AttnParams &p, float *ml, int lane)
-    {
-#pragma unroll
-        for (int r = 0; r < MR; ++r) {
-#pragma unroll
-            for (int x = 16; x >= 1; x >>= 1)
-                l[r] += __shfl_xor_sync(0xffffffffu, l[r], x);
-            m[r] *= p.f;
-            if (lane == 0) {
-                ml[2 * r] = m[r];
-                ml[2 * r + 1] = l[r];
-            }
-        }
-        add_groups();
-    }
-    __device__ __forceinline__ void rescale(const float *ml, int)
-    {
-#pragma unroll
-        for (int r = 0; r < MR; ++r)
-            m[r] = exp2_fast(m[r] - joint_max<MR>(ml, r));
-    }
-    template <bool ADD>
-    __device__ __forceinline__ void put(const AttnParams &p, float *buf, int ds, int rows, int lane)
-    {
-        if (kGroups == 2 && lane >= 16)
-            return;
-#pragma unroll
-        for (int r = 0; r < MR; ++r) {
-            if (r < rows) {
-                const float f = m[r];
-#pragma unroll
-                for (int n = 0; n < NV; ++n) {
-                    const int c = 4 * lane + 128 * n;
-                    if (c < dim(p)) {
-                        float4 *at = reinterpret_cast<float4 *>(buf + r * ds + c);
-                        float4 v = make_float4(lo2(o[r][n][0]) * f, hi2(o[r][n][0]) * f, lo2(o[r][n][1]) * f, hi2(o[r][n][1]) * f);
-                        if (ADD) {
-                            const float4 u = *at;
-                            v.x += u.x;
-                            v.y += u.y;
-                            v.z += u.z;
-                            v.w += u.w;
-                        }
-                        *at = v;
-                    }
-                }
-            }
-        }
-    }
-};
-
-__device__ __forceinline__ void store4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
-__device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 v)
-{
-    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-}
-
-__device__ __forceinline__ void store2(float *p, float x, float y) { *reinterpret_cast<float2 *>(p) = make_float2(x, y); }
-__device__ __forceinline__ void store2(__nv_bfloat16 *p, float x, float y) { *reinterpret_cast<uint32_t *>(p) = pack_bf16(x, y); }
-
-// shared memory: the warps' rings, their query rows (and fp32 weights), two
-// join buffers (in the query rows' place where those are bf16) -- all of whole
-// 16-byte segments -- then maxima, sums, barriers and slot masks.  NU: units in
-// a warp's ring.
-template <typename M, int NU, bool SOLO>
-struct Layout {
-    static constexpr int kQuery = kWarps * M::kQBytes;
-    static constexpr int kSmall = kWarps * NU * 2 * 8 + (kWarps * M::MR * 2 + M::MR * 2 + kWarps * NU) * 4;
-    static __host__ __device__ int join_stride(int D) { return D + 8; }
-    static __host__ __device__ int ring_bytes(int stride) { return kWarps * NU * 2 * M::kUnit * stride; }
-    static __host__ __device__ int join_bytes(int D) { return SOLO ? 0 : 2 * M::MR * join_stride(D) * 4; }
-    static __host__ __device__ int middle_bytes(int D)
-    {
-        return M::kQSmem ? (kQuery > join_bytes(D) ? kQuery : join_bytes(D)) : kQuery + join_bytes(D);
-    }
-    static __host__ __device__ int total(int D, int stride) { return ring_bytes(stride) + middle_bytes(D) + kSmall; }
-};
-
-// SOLO: shares of warps, for many tiles: a warp goes through whole tiles without
-// a barrier, and a tile is cut into a few parts at most.  Else shares of CTAs,
-// for few: a tile is then cut into many parts, and joining a CTA's warps first
-// leaves a quarter of them to the second launch.
-template <typename M, int NU, bool SOLO, bool BULK>
-__global__ void __launch_bounds__(kThreads) ssd_paged_attn_kernel(const __grid_constant__ AttnParams p)
-{
-    using T = typename M::T;
-    using L = Layout<M, NU, SOLO>;
-    constexpr int UT = M::kUnit;
-    extern __shared__ __align__(16) char smem[];
-    __shared__ Found found[kWarps];
-    __shared__ long long tmp[kWarps];
-    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, D = M::dim(p), stride = M::row_bytes(p);
-    // The call's launches are programmatic dependents: each starts while the one
-    // before it runs out and waits here for all of it.
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
-    const Shares sh = locate<UT, SOLO>(p, reinterpret_cast<int *>(smem), tmp, found);
-    // padding rows see nothing
-    if (p.a.start) {
-        const long long r0 = min((long long)max(p.a.start[p.a.d.nreq], 0), (long long)p.a.d.nrows);
-        for (long long i = r0 * p.a.d.nheads + blockIdx.x; i < p.a.d.nrows * p.a.d.nheads; i += gridDim.x) {
-            const long long row = i / p.a.d.nheads, h = i - row * p.a.d.nheads;
-            T *out = static_cast<T *>(p.a.out) + row * p.a.d.o_stride[0] + h * p.a.d.o_stride[1];
-            for (int c = 4 * tid; c < D; c += 4 * kThreads)
-                store4(out + c, make_float4(0.f, 0.f, 0.f, 0.f));
-            if (p.a.lse && tid == 0)
-                p.a.lse[i] = -INFINITY;
-        }
-    }
-    const long long share = SOLO ? (long long)blockIdx.x * kWarps + w : blockIdx.x;
-    const long long u0 = share * sh.per, u1 = min(u0 + sh.per, sh.total);
-    if (SOLO) {
-        if (lane == 0)
-            p.desc[share] = make_int4(-1, 0, 0, 0);
-    } else {   // (there may be fewer tiles than the host could tell)
-        for (long long i = sh.ntiles * p.items + blockIdx.x * kThreads + tid; i < p.ndesc; i += gridDim.x * kThreads)
-            p.desc[i] = make_int4(-1, 0, 0, 0);
-    }
-    const int half_bytes = UT * stride;
-    char *ring = smem + (size_t)w * NU * 2 * half_bytes;    // [NU][K, V][UT][stride]
-    char *middle = smem + L::ring_bytes(stride);
-    char *qs = middle + w * M::kQBytes;
-    float *join = reinterpret_cast<float *>(middle + (M::kQSmem ? 0 : L::kQuery));   // (16-byte accesses up to here)
-    uint64_t *bars = reinterpret_cast<uint64_t *>(middle + L::middle_bytes(D)) + w * NU * 2;
-    float *ml = reinterpret_cast<float *>(bars - w * NU * 2 + kWarps * NU * 2);      // [kWarps][MR][2]
-    float *joint = ml + kWarps * M::MR * 2;                                          // [MR] maxima, [MR] sums
-    uint32_t *masks = reinterpret_cast<uint32_t *>(joint + M::MR * 2) + w * NU;
-    const int ds = L::join_stride(D);
-    __syncthreads();   // (the schedule's use of the ring's memory is over)
-    // segments past the head's elements are read by the products: zero once
-    if (!M::kExact) {
-        for (int i = lane; i < NU * 2 * UT; i += 32)
-            for (int c = p.seg; c * 16 < stride; ++c)
-                *reinterpret_cast<uint4 *>(ring + (size_t)i * stride + c * 16) = make_uint4(0, 0, 0, 0);
-    }
-    if (BULK) {
-        if (lane < NU * 2)
-            ptx::mbar_init(bars + lane, 1);
-        ptx::fence_mbar_init();
-        ptx::fence_proxy_async_smem();
-    }
-    __syncwarp();
-    if (u0 >= sh.total)
-        return;   // (the whole CTA where it has one share; no barrier follows where it has four)
-
-    Cursor cur;
-    {
-        const Found f = found[SOLO ? w : 0];
-        set_tile<UT>(p, cur.t, f.req, f.j);
-        cur.item = (int)((u0 - f.lin) / cur.t.units);
-        cur.lin = f.lin + (long long)cur.item * cur.t.units;
-        cur.tile = f.tile;
-    }
-
-    // Steps alternate: while a unit's K is used the V half of the ring's newest
-    // unit is loaded, while its V is used the next unit's K.  Every step is one
-    // group of asynchronous copies, empty past the share's end.
-    constexpr int step = SOLO ? 1 : kWarps;
-    Loader<T, M::kDim, BULK, UT> ld;
-    ld.c = cur;
-    ld.u1 = u1;
-    ld.set_end();
-    ld.u = (int)(u0 - cur.lin);
-    ld.skip(p, SOLO ? 0 : w);
-    ld.fetch_page(p, lane);
-    int head = 0;
-    auto load_k = [&]() {
-        if (ld.u >= 0) {
-            char *slot = ring + head * 2 * half_bytes;
-            ld.offsets(p, lane);
-            if (lane == 0)
-                masks[head] = ld.mask;
-            if constexpr (!BULK)
-                ld.copy(p, p.a.kc, ld.koff, p.a.d.kc_stride[1], smem_addr(slot), lane);
-            else
-                ld.copy_bulk(p, p.a.kc, ld.koff[0], slot, bars + head * 2, false, lane);
-        }
-        if (!BULK)
-            cp_commit();
-    };
-    auto load_v = [&]() {
-        if (ld.u >= 0) {
-            char *slot = ring + (head * 2 + 1) * half_bytes;
-            if constexpr (!BULK)
-                ld.copy(p, p.a.vc, ld.voff, p.a.d.vc_stride[1], smem_addr(slot), lane);
-            else
-                ld.copy_bulk(p, p.a.vc, ld.voff[0], slot, bars + head * 2 + 1, true, lane);
-            ld.skip(p, step);
-            ld.fetch_page(p, lane);
-            head = head + 1 == NU ? 0 : head + 1;
-        }
-        if (!BULK)
-            cp_commit();
-    };
-#pragma unroll 1
-    for (int i = 0; i < NU - 1; ++i) {
-        load_k();
-        load_v();
-    }
-    load_k();
-
-    M math;
-    math.qs = reinterpret_cast<decltype(math.qs)>(qs);
-    if constexpr (sizeof(T) == 4)
-        math.ps = math.qs + M::MR * M::kDim;
-    int tail = 0;
-    uint32_t parity = 0;
-    bool healthy = true;
-    int u = (int)(u0 - cur.lin);   // first unit of the share in this item
-    while (true) {
-        const int ue = (int)min((long long)cur.t.units, u1 - cur.lin);   // the share's units of the item: [u, ue)
-        // tokens that every row of the tile sees: from the last row's first to the first row's last
-        int all0, all1;
-        {
-            const int limit = p.a.d.max_pages * p.a.d.page_size;
-            const int p0 = p.a.positions[cur.t.row], p1 = p.a.positions[cur.t.row + cur.t.nq - 1];
-            all1 = p0 < 0 ? 0 : min(p0, limit - 1) + 1;
-            all0 = p.a.d.window > 0 ? max(0, p1 - p.a.d.window + 1) : 0;
-        }
-        math.begin(p, cur.t, cur.item, lane);
-        const int kvh = cur.item / p.nhb, hb = cur.item - kvh * p.nhb;
-        const int h0 = kvh * p.group + hb * p.gh, nh = min(p.gh, p.group - hb * p.gh), rows = cur.t.nq * nh;
-        // this warp's units: all, or those whose number in the CTA's share is w modulo the warps
-        const int skip = SOLO ? 0 : (w - (int)((cur.lin + u - u0) % kWarps) + kWarps) % kWarps;
-        for (int x = u + skip; x < ue; x += step) {
-            const int tok0 = (cur.t.ub + x) * UT;
-            char *slot = ring + tail * 2 * half_bytes;
-            if constexpr (BULK)
-                healthy = wait_bulk(bars + tail * 2, parity, healthy);
-            else
-                cp_wait<2 * NU - 2>();
-            __syncwarp();
-            const uint32_t mask = masks[tail];
-            load_v();
-            math.scores(p, slot, mask, tok0, all0, all1, lane);
-            if constexpr (BULK)
-                healthy = wait_bulk(bars + tail * 2 + 1, parity, healthy);
-            else
-                cp_wait<2 * NU - 2>();
-            __syncwarp();
-            load_k();
-            math.values(p, slot + half_bytes, mask, tok0, all0, all1, lane);
-            if (++tail == NU) {
-                tail = 0;
-                parity ^= 1;
-            }
-        }
-        const bool whole = u == 0 && ue == cur.t.units;
-        const int slot = u > 0 ? 0 : 1;   // a tile begun in an earlier share, or in this one
-        T *out = static_cast<T *>(p.a.out) + (long long)cur.t.row * p.a.d.o_stride[0] + (long long)h0 * p.a.d.o_stride[1];
-        float *lse = p.a.lse ? p.a.lse + (long long)cur.t.row * p.a.d.nheads + h0 : nullptr;
-        float *po = p.part_o + ((size_t)share * 2 + slot) * M::MR * D, *pml = p.part_ml + ((size_t)share * 2 + slot) * M::MR * 2;
-        auto put_lse = [&](int r, float mm, float ll) {
-            if (lse) {
-                const int j = r / nh;
-                lse[(long long)j * p.a.d.nheads + (r - j * nh)] = ll == 0.f ? -INFINITY : kLn2 * (mm + log2f(ll));
-            }
-        };
-        if constexpr (SOLO) {
-            if (whole)
-                math.finish(p, rows, lane, [](float ll) { return ll == 0.f ? 0.f : 1.f / ll; },
-                            [&](int r, int c, float a, float b) {
-                                const int j = r / nh;
-                                store2(out + (long long)j * p.a.d.o_stride[0] + (long long)(r - j * nh) * p.a.d.o_stride[1] + c, a, b);
-                            }, put_lse);
-            else
-                math.finish(p, rows, lane, [](float) { return 1.f; },
-                            [&](int r, int c, float a, float b) { store2(po + (size_t)r * D + c, a, b); },
-                            [&](int r, float mm, float ll) { store2(pml + 2 * r, mm, ll); });
-        } else {
-            // join the warps: three barriers; the next tile's writes to ml, joint
-            // and the buffers come after its own first or second one
-            math.end(p, ml + w * M::MR * 2, lane);
-            __syncthreads();
-            if (tid < M::MR) {
-                float ll = 0.f;
-                const float base = joint_max<M::MR>(ml, tid);
-#pragma unroll
-                for (int i = 0; i < kWarps; ++i)
-                    ll += ml[(i * M::MR + tid) * 2 + 1] * exp2_fast(ml[(i * M::MR + tid) * 2] - base);
-                joint[tid] = base;
-                joint[M::MR + tid] = ll;
-            }
-            math.rescale(ml, lane);
-            float *buf = join + (w & 1) * M::MR * ds;
-            if (w >= 2)
-                math.template put<false>(p, buf, ds, rows, lane);
-            __syncthreads();
-            if (w < 2)
-                math.template put<true>(p, buf, ds, rows, lane);
-            __syncthreads();
-            const int n4 = D / 4;
-            for (int i = tid; i < rows * n4; i += kThreads) {
-                const int r = i / n4, c = 4 * (i - r * n4);
-                const float4 x = *reinterpret_cast<const float4 *>(join + r * ds + c);
-                const float4 y = *reinterpret_cast<const float4 *>(join + (M::MR + r) * ds + c);
-                float4 v = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
-                const float ll = joint[M::MR + r];
-                if (whole) {
-                    const float inv = ll == 0.f ? 0.f : 1.f / ll;
-                    const int j = r / nh;
-                    v.x *= inv; v.y *= inv; v.z *= inv; v.w *= inv;
-                    store4(out + (long long)j * p.a.d.o_stride[0] + (long long)(r - j * nh) * p.a.d.o_stride[1] + c, v);
-                    if (c == 0)
-                        put_lse(r, joint[r], ll);
-                } else {
-                    store4(po + (size_t)r * D + c, v);
-                    if (c == 0)
-                        store2(pml + 2 * r, joint[r], ll);
-                }
-            }
-            if (M::kQSmem)
-                __syncthreads();   // (the next tile's query rows go where the buffers are)
-        }
-        // where the parts of a cut tile are
-        if (SOLO ? !whole && slot == 1 && lane == 0 : slot == 1 && tid == 0)
-            p.desc[SOLO ? share : (long long)cur.tile * p.items + cur.item] =
-                make_int4(whole ? -1 : cur.t.row, cur.t.nq | cur.item << 8, (int)share, (int)((cur.lin + cur.t.units - 1) / sh.per));
-        if (cur.lin + ue >= u1)
-            break;
-        u = 0;
-        next_item<UT>(p, cur);
-    }
-    if (!BULK)
-        cp_wait<0>();
-}
-
-// Joins parts of row r of a cut tile: NW warps take parts in turn, lanes the
-// elements, each warp in the running form, so that the parts' maxima and rows
-// are loaded together, four at a time; then the warps through shared memory
-// (sm, so: of the NW warps).
-template <typename T, int MR, int NW>
-__device__ __forceinline__ void join_row(const AttnParams &p, const int4 &d, int r, int w, int lane, float (*sm)[2], float (*so)[256])
-{
-    const int row = d.x, item = d.y >> 8, c0 = d.z, n = d.w - d.z + 1, D = p.a.d.headdim;
-    const int kvh = item / p.nhb, hb = item - kvh * p.nhb, nh = min(p.gh, p.group - hb * p.gh);
-    float mm = -INFINITY, ll = 0.f, o[2][4] = {};
-    // part i lies in share c0 + i: slot 1 of the first, slot 0 of the others
-    for (int i = w; i < n; i += 4 * NW) {
-        float pm[4], pl[4];
-        float4 v[4][2];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            pm[b] = -INFINITY;
-            pl[b] = 0.f;
-            v[b][0] = v[b][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-            const int part = i + NW * b;
-            if (part < n) {
-                const size_t at = ((size_t)(c0 + part) * 2 + (part == 0 ? 1 : 0)) * MR + r;
-                const float2 t = *reinterpret_cast<const float2 *>(p.part_ml + 2 * at);
-                pm[b] = t.y == 0.f ? -INFINITY : t.x;   // (a part that saw nothing)
-                pl[b] = t.y;
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-                    if (4 * lane + 128 * x < D)
-                        v[b][x] = *reinterpret_cast<const float4 *>(p.part_o + at * D + 4 * lane + 128 * x);
-            }
-        }
-        const float mn = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])), mm), base = mn == -INFINITY ? 0.f : mn;
-        const float keep = exp2_fast(mm - base);
-        mm = mn;
-        ll *= keep;
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                o[x][e] *= keep;
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const float f = exp2_fast(pm[b] - base);
-            ll += pl[b] * f;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                o[x][0] += f * v[b][x].x;
-                o[x][1] += f * v[b][x].y;
-                o[x][2] += f * v[b][x].z;
-                o[x][3] += f * v[b][x].w;
-            }
-        }
-    }
-    float base = mm == -INFINITY ? 0.f : mm;
-    if (NW > 1) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-            *reinterpret_cast<float4 *>(&so[w][4 * lane + 128 * x]) = make_float4(o[x][0], o[x][1], o[x][2], o[x][3]);
-        if (lane == 0) {
-            sm[w][0] = mm;
-            sm[w][1] = ll;
-        }
-        __syncthreads();
-        if (w != 0)
-            return;
-        float top = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < NW; ++i)
-            top = fmaxf(top, sm[i][0]);
-        base = top == -INFINITY ? 0.f : top;
-        ll = 0.f;
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                o[x][e] = 0.f;
-#pragma unroll
-        for (int i = 0; i < NW; ++i) {
-            const float f = exp2_fast(sm[i][0] - base);
-            ll += sm[i][1] * f;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const float4 v = *reinterpret_cast<const float4 *>(&so[i][4 * lane + 128 * x]);
-                o[x][0] += f * v.x;
-                o[x][1] += f * v.y;
-                o[x][2] += f * v.z;
-                o[x][3] += f * v.w;
-            }
-        }
-    }
-    const float inv = ll == 0.f ? 0.f : 1.f / ll;
-    const int j = r / nh, h = kvh * p.group + hb * p.gh + (r - j * nh);
-    T *out = static_cast<T *>(p.a.out) + (long long)(row + j) * p.a.d.o_stride[0] + (long long)h * p.a.d.o_stride[1];
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-        if (4 * lane + 128 * x < D)
-            store4(out + 4 * lane + 128 * x, make_float4(o[x][0] * inv, o[x][1] * inv, o[x][2] * inv, o[x][3] * inv));
-    if (p.a.lse && lane == 0)
-        p.a.lse[(long long)(row + j) * p.a.d.nheads + h] = ll == 0.f ? -INFINITY : kLn2 * (base + log2f(ll));
-}
-
-__device__ __forceinline__ int desc_rows(const AttnParams &p, const int4 &d)
-{
-    const int hb = (d.y >> 8) % p.nhb;
-    return d.x < 0 ? 0 : (d.y & 0xff) * min(p.gh, p.group - hb * p.gh);
-}
-
-constexpr int kJoinWarps = 8;
-
-// SOLO: few parts; a warp per row, a block per CTA of the first launch.  Else many
-// parts: a block per tile and row.
-template <typename T, int MR, bool SOLO>
-__global__ void __launch_bounds__(32 * kJoinWarps) ssd_paged_attn_join_kernel(const __grid_constant__ AttnParams p)
-{
-    __shared__ float sm[kJoinWarps][2];
-    __shared__ __align__(16) float so[SOLO ? 1 : kJoinWarps][256];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (SOLO) {
-        int4 d[kWarps];
-#pragma unroll
-        for (int k = 0; k < kWarps; ++k)
-            d[k] = p.desc[(long long)blockIdx.x * kWarps + k];
-        int at = w;   // rows of all four, dealt to the warps
-#pragma unroll
-        for (int k = 0; k < kWarps; ++k) {
-            const int rows = desc_rows(p, d[k]);
-            for (; at < rows; at += kJoinWarps)
-                join_row<T, MR, 1>(p, d[k], at, 0, lane, sm, so);
-            at -= rows;
-        }
-    } else {
-        const int4 d = p.desc[blockIdx.x];
-        if ((int)blockIdx.y < desc_rows(p, d))
-            join_row<T, MR, kJoinWarps>(p, d, blockIdx.y, w, lane, sm, so);
-    }
-}
-
-// ---- host: variant, sizes, launch -------------------------------------------
 
 // How many query rows of a key-value head one request brings, as far as the
 // sizes tell: the variant's rows per tile follow it.
@@ -1476,24 +30,6 @@ int tile_rows(const ssd_attn_dims_t &d)
     return want <= 1 ? 1 : want <= 2 ? 2 : want <= 4 ? 4 : 8;
 }
 
-// tiles that the sizes allow at most (one per row, or per `tok` rows of a request)
-long long most_tiles(const AttnParams &p)
-{
-    if (!p.a.start)
-        return p.a.d.nrows;
-    return std::max<long long>(1, std::min<long long>(p.a.d.nrows, p.a.d.nrows / p.tok + p.a.d.nreq));
-}
-
-int sm_count();
-
-// Shares of warps for at least two tiles (times key-value heads) per SM: below
-// that a tile would be cut into more than four parts of warps, the join of
-// which costs more than the CTAs' own joins.
-bool solo_shares(const AttnParams &p) { return most_tiles(p) * p.items >= 2 * sm_count(); }
-
-constexpr int kMaxPerSm = 4;     // CTAs
-constexpr int kMaxCtas = 1024;   // the workspace is sized for at most this many
-
 int sm_count()
 {
     static int n[64] = {};
@@ -1503,99 +39,6 @@ int sm_count()
     if (!n[dev] && cudaDeviceGetAttribute(&n[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return 152;
     return n[dev];
-}
-
-template <typename M, int NU, bool SOLO, bool BULK>
-cudaError_t launch(AttnParams &p, void *workspace, cudaStream_t stream)
-{
-    using T = typename M::T;
-    const int D = p.a.d.headdim;
-    const int smem = std::max(Layout<M, NU, SOLO>::total(D, p.stride), p.a.start ? (int)(p.a.d.nreq + 1) * 4 : 0);
-    auto kernel = ssd_paged_attn_kernel<M, NU, SOLO, BULK>;
-    // CTAs per SM by shared memory (1 KB of the system's each) and registers
-    static int regs = 0;   // (the same for every device)
-    cudaError_t e;
-    if (!regs) {
-        cudaFuncAttributes at;
-        if ((e = cudaFuncGetAttributes(&at, kernel)) != cudaSuccess)
-            return e;
-        regs = (at.numRegs + 7) / 8 * 8;
-    }
-    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
-        return e;
-    const int per_sm = std::max(1, std::min({kMaxPerSm, (228 << 10) / (smem + 1024 + 256), 65536 / (regs * kThreads)}));
-    const int grid = std::min(kMaxCtas, sm_count() * per_sm);
-    const size_t shares = (size_t)grid * (SOLO ? kWarps : 1);
-    p.part_o = static_cast<float *>(workspace);
-    p.part_ml = p.part_o + shares * 2 * M::MR * D;
-    p.desc = reinterpret_cast<int4 *>(p.part_ml + shares * 2 * M::MR * 2);
-    p.ndesc = SOLO ? (int)shares : (int)(most_tiles(p) * p.items);
-    cudaLaunchAttribute pdl[1];
-    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    pdl[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = pdl;
-    cfg.numAttrs = 1;
-    if ((e = cudaLaunchKernelEx(&cfg, kernel, p)) != cudaSuccess)
-        return e;
-    note_launches(1);
-    cfg.gridDim = SOLO ? dim3(grid) : dim3(p.ndesc, p.tok * p.gh);
-    cfg.blockDim = dim3(32 * kJoinWarps);
-    cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, ssd_paged_attn_join_kernel<T, M::MR, SOLO>, p);
-    if (e == cudaSuccess)
-        note_launches(1);
-    return e;
-}
-
-template <typename M, int NU, int NUS, bool BULK>
-cudaError_t launch_shares(AttnParams &p, void *ws, cudaStream_t st)
-{
-    return solo_shares(p) ? launch<M, NUS, true, BULK>(p, ws, st) : launch<M, NU, false, BULK>(p, ws, st);
-}
-
-cudaError_t launch_bf16(AttnParams &p, int mr, void *ws, cudaStream_t st)
-{
-    const int D = p.a.d.headdim;
-    if (p.a.d.page_size % 16 == 0) {
-        if (D == 64)
-            return mr == 32 ? launch_shares<Mma<2, 64, true, 1>, 4, 4, false>(p, ws, st)
-                            : launch_shares<Mma<1, 64, true, 2>, 2, 2, false>(p, ws, st);
-        if (D == 128)
-            return mr == 32 ? launch_shares<Mma<2, 128, true, 1>, 2, 2, false>(p, ws, st)
-                            : launch_shares<Mma<1, 128, true, 1>, 2, 2, false>(p, ws, st);
-        if (D == 256)
-            return launch_shares<Mma<1, 256, true, 1>, 2, 2, false>(p, ws, st);
-    }
-    if (D <= 128)
-        return mr == 32 ? launch_shares<Mma<2, 128, false, 1>, 2, 2, true>(p, ws, st)
-                        : launch_shares<Mma<1, 128, false, 1>, 2, 2, true>(p, ws, st);
-    return launch_shares<Mma<1, 256, false, 1>, 2, 2, true>(p, ws, st);
-}
-
-template <int MR>
-cudaError_t launch_f32_rows(AttnParams &p, void *ws, cudaStream_t st)
-{
-    const int D = p.a.d.headdim;
-    if (D <= 64)
-        return launch_shares<Simt<MR, 64, false>, 1, 1, true>(p, ws, st);
-    if (D <= 128)
-        return launch_shares<Simt<MR, 128, false>, 1, 1, true>(p, ws, st);
-    return launch_shares<Simt<MR, 256, false>, 1, 1, true>(p, ws, st);
-}
-
-cudaError_t launch_f32(AttnParams &p, int mr, void *ws, cudaStream_t st)
-{
-    switch (mr) {
-    case 1: return launch_f32_rows<1>(p, ws, st);
-    case 2: return launch_f32_rows<2>(p, ws, st);
-    case 4: return launch_f32_rows<4>(p, ws, st);
-    default: return launch_f32_rows<8>(p, ws, st);
-    }
 }
 
 }  // namespace
@@ -1618,6 +61,14 @@ cudaError_t attn_launch(const AttnArgs &a, void *workspace, cudaStream_t stream)
     p.tok = a.start ? std::max(1, mr / p.gh) : 1;
     p.items = a.d.nkv * p.nhb;
     p.seg = D * es / 16;
+    // (a stride that no second page, token or head uses may be anything)
+    auto used = [](int64_t n, int64_t stride) { return n > 1 ? stride : 0; };
+    p.kpage = (uint32_t)(used(a.d.npages, a.d.kc_stride[0]) * es / 16);
+    p.vpage = (uint32_t)(used(a.d.npages, a.d.vc_stride[0]) * es / 16);
+    p.ktok = (uint32_t)(used(a.d.page_size, a.d.kc_stride[1]) * es / 16);
+    p.vtok = (uint32_t)(used(a.d.page_size, a.d.vc_stride[1]) * es / 16);
+    p.khead = used(a.d.nkv, a.d.kc_stride[2]) * es;
+    p.vhead = used(a.d.nkv, a.d.vc_stride[2]) * es;
     // rows of an odd number of 16-byte segments: eight rows' segments lie in different banks
     const int seg = es == 2 ? (p.seg + 1) / 2 * 2 : p.seg;
     p.stride = (seg | 1) * 16;
@@ -1628,16 +79,19 @@ cudaError_t attn_launch(const AttnArgs &a, void *workspace, cudaStream_t stream)
     while ((1u << (p.page.sh - 31)) < (uint32_t)a.d.page_size)
         ++p.page.sh;
     p.page.mul = (uint32_t)((1ull << p.page.sh) / (uint32_t)a.d.page_size + 1);
-    return a.d.dtype == SSD_DTYPE_BF16 ? launch_bf16(p, mr, workspace, stream) : launch_f32(p, mr, workspace, stream);
+    p.sms = sm_count();
+    if (a.d.dtype == SSD_DTYPE_F32)
+        return attn_launch_f32(p, mr, workspace, stream);
+    const bool sized = a.d.page_size % 16 == 0 && (D == 64 || D == 128 || D == 256);
+    return sized ? attn_launch_bf16(p, mr, workspace, stream) : attn_launch_bf16_any(p, mr, workspace, stream);
 }
 
 ssd_status_t attn_read_device_error(uint32_t *code)
 {
-    unsigned int v = 0, zero = 0;
-    if (cudaMemcpyFromSymbol(&v, g_attn_error, sizeof(v)) != cudaSuccess ||
-        (v != 0 && cudaMemcpyToSymbol(g_attn_error, &zero, sizeof(zero)) != cudaSuccess))
+    uint32_t b = 0, f = 0;
+    if (attn_bf16_any_error(&b) != cudaSuccess || attn_f32_error(&f) != cudaSuccess)
         return SSD_ERR_CUDA;
-    *code = v;
+    *code = b ? b : f;
     return SSD_OK;
 }
 

@@ -1,0 +1,32 @@
+// ssd_paged_attn_f32.cu -- paged attention: fp32.
+#include "ssd_paged_attn.cuh"
+
+namespace ssd {
+namespace {
+
+template <int MR>
+cudaError_t launch_rows(AttnParams &p, void *ws, cudaStream_t st)
+{
+    const int D = p.a.d.headdim;
+    if (D <= 64)
+        return launch_shares<Simt<MR, 64, false>, 1, 1, 2, true>(p, ws, st);
+    if (D <= 128)
+        return launch_shares<Simt<MR, 128, false>, MR == 8 ? 2 : 3, 3, 1, true>(p, ws, st);
+    return launch_shares<Simt<MR, 256, false>, 1, 1, 1, true>(p, ws, st);
+}
+
+}  // namespace
+
+cudaError_t attn_launch_f32(AttnParams &p, int mr, void *ws, cudaStream_t st)
+{
+    switch (mr) {
+    case 1: return launch_rows<1>(p, ws, st);
+    case 2: return launch_rows<2>(p, ws, st);
+    case 4: return launch_rows<4>(p, ws, st);
+    default: return launch_rows<8>(p, ws, st);
+    }
+}
+
+cudaError_t attn_f32_error(uint32_t *code) { return take_error(code); }
+
+}  // namespace ssd
