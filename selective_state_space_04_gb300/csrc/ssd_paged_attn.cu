@@ -46,7 +46,10 @@ int sm_count()
 size_t attn_workspace_bytes(const ssd_attn_dims_t &d)
 {
     const int grid = std::min(kMaxCtas, sm_count() * kMaxPerSm);
-    return (size_t)grid * kWarps * (2 * tile_rows(d) * (d.headdim + 2) * sizeof(float) + sizeof(int4));
+    // shares: as many as warps, or one per key-value head (and head block) where those are more
+    const long long group = d.nheads / d.nkv, mr = tile_rows(d), items = d.nkv * ((group + mr - 1) / mr);
+    const size_t shares = (size_t)std::max<long long>((long long)grid * kWarps, items);
+    return shares * (2 * tile_rows(d) * (d.headdim + 2) * sizeof(float) + sizeof(int4));
 }
 
 cudaError_t attn_launch(const AttnArgs &a, void *workspace, cudaStream_t stream)

@@ -2,10 +2,12 @@
 //
 // A tile is up to MR query rows that read the same keys: the query heads of one
 // key-value head for one or several consecutive new tokens of a request.  The
-// tile's visible positions are cut into units of 16 or 32 tokens.  All units of
-// all tiles and key-value heads, laid end to end, are dealt out in equal
-// contiguous shares, whatever the requests' lengths; the CTAs that fit the GPU
-// at once stay for the whole launch.  A warp streams its units through a ring of
+// tile's visible positions are cut into units of 16 or 32 tokens.  The units of
+// all tiles, laid end to end, are dealt out in equal contiguous shares, whatever
+// the requests' lengths, the same shares for every key-value head.  Neighbouring
+// warps (or CTAs) take the same share of neighbouring heads, so that a token's
+// heads, which lie side by side in a token-major cache, are read at about the
+// same time.  The CTAs that fit the GPU at once stay for the whole launch.  A warp streams its units through a ring of
 // shared-memory slots of its own, K and V halves in turn, and keeps a running
 // maximum, sum and output rows in registers: no barrier stands between loads and
 // arithmetic, and loads run ahead across tile boundaries.
@@ -139,23 +141,19 @@ __device__ __forceinline__ void next_tile(const AttnParams &p, Tile &t)
     set_tile<UT>(p, t, r, 0);
 }
 
-// A place in the CTA's share: a tile, an item (key-value head and head block)
-// of it, and the linear number of the item's first unit.
+// A place in a share: a tile and the number of its first unit.
 struct Cursor {
     Tile t;
-    int item, tile;   // (tile: counted over all requests; shares of CTAs)
+    int tile;   // counted over all requests
     long long lin;
 };
 
 template <int UT>
-__device__ __forceinline__ void next_item(const AttnParams &p, Cursor &c)
+__device__ __forceinline__ void advance(const AttnParams &p, Cursor &c)
 {
     c.lin += c.t.units;
-    if (++c.item == p.items) {
-        c.item = 0;
-        ++c.tile;
-        next_tile<UT>(p, c.t);
-    }
+    ++c.tile;
+    next_tile<UT>(p, c.t);
 }
 
 // ---- block scan for the schedule ------------------------------------------
@@ -191,14 +189,15 @@ struct Found {
 };
 
 struct Shares {
-    long long total, per;   // units, and units of a share
+    long long total, per;   // units of a key-value head, and of a share
     long long ntiles;
+    int of_head;            // shares of a head; all shares: of_head * items
 };
 
-// Where the CTA's shares begin (found[i]: of warp i's share, or found[0]).
-// Every CTA sums all tiles' units (a contiguous run of tiles per thread); the
-// thread whose run holds a share's first unit finds its tile.  `counts` (shared
-// memory, nreq + 1 ints) is used when there is a start array.
+// Finds where share j of a head begins (found[i] for warp i's share, or
+// found[0]).  Every CTA sums all tiles' units (a contiguous run of tiles per
+// thread); the thread whose run holds a share's first unit finds its tile.
+// `counts` (shared memory, nreq + 1 ints) is used when there is a start array.
 template <int UT, bool SOLO>
 __device__ Shares locate(const AttnParams &p, int *counts, long long *tmp, Found *found)
 {
@@ -252,26 +251,29 @@ __device__ Shares locate(const AttnParams &p, int *counts, long long *tmp, Found
         n += t.units;
     }
     long long sum;
-    const long long before = block_exclusive(n, &sum, tmp) * p.items;
+    const long long before = block_exclusive(n, &sum, tmp);
+    constexpr int kOwn = SOLO ? kWarps : 1;   // shares of a CTA at a time
     Shares sh;
-    sh.total = sum * p.items;
+    sh.total = sum;
     sh.ntiles = ntiles;
-    sh.per = SOLO ? max(1ll, (sh.total + (long long)gridDim.x * kWarps - 1) / ((long long)gridDim.x * kWarps))
-                  : max((long long)kWarps, (sh.total + gridDim.x - 1) / gridDim.x);
+    sh.of_head = max(1, (int)gridDim.x * kOwn / p.items);
+    sh.per = max((long long)(SOLO ? 1 : kWarps), (sh.total + sh.of_head - 1) / sh.of_head);
     if (t0 < t1) {
         long long lin = before, tile = t0;
-        const long long end = before + n * p.items;
+        const long long end = before + n;
         bool at_start = false;
-        for (int i = 0; i < (SOLO ? kWarps : 1); ++i) {
-            const long long u0 = ((long long)blockIdx.x * (SOLO ? kWarps : 1) + i) * sh.per;
+        for (int i = 0; i < kOwn; ++i) {
+            // (more heads than CTAs' shares: one share per head, from the first unit on)
+            const int share = blockIdx.x * kOwn + i, j = sh.of_head == 1 ? 0 : share / p.items;
+            const long long u0 = j * sh.per;
             if (u0 < before || u0 >= end)
                 continue;
             if (!at_start) {   // (the walk goes on from share to share)
                 set_tile<UT>(p, t, f.req, f.j);
                 at_start = true;
             }
-            while (u0 >= lin + (long long)t.units * p.items) {
-                lin += (long long)t.units * p.items;
+            while (u0 >= lin + t.units) {
+                lin += t.units;
                 next_tile<UT>(p, t);
                 ++tile;
             }
@@ -298,29 +300,31 @@ struct Loader {
     static constexpr int kStride = (kSegMax | 1) * 16;
     static constexpr uint32_t kAll = UT == 16 ? 0xffffu : 0xffffffffu;
     Cursor c;
-    int u, u_end;          // the unit within the item (-1: none left); the share's units of the item
+    int u, u_end;          // the unit within the tile (-1: none left); the share's units of the tile
     long long u1;          // end of the share
-    const char *kb, *vb;   // the item's key-value head in the caches (16-byte copies: at the lane's row and segment)
+    const char *kb, *vb;   // the key-value head in the caches (16-byte copies: at the lane's row and segment)
     const int32_t *table;  // the request's row
     int page;              // table entry read ahead (bulk: of the lane's token, else of the lane's 16 tokens)
     uint32_t mask;         // the unit's tokens that are to be read
     // offsets in 16 bytes: of the first token of each 16; bulk: of the lane's token
     uint64_t koff[kSub], voff[kSub];
 
-    __device__ __forceinline__ void set_item(const AttnParams &p, int lane)
+    __device__ __forceinline__ void set_head(const AttnParams &p, int kvh, int lane)
     {
-        u_end = (int)min((long long)c.t.units, u1 - c.lin);
-        const long long kvh = p.nhb == 1 ? c.item : c.item / p.nhb;
         kb = static_cast<const char *>(p.a.kc) + kvh * p.khead;
         vb = static_cast<const char *>(p.a.vc) + kvh * p.vhead;
         if (!BULK) {
             kb += (lane / kSegMax) * (long long)p.ktok * 16 + (lane % kSegMax) * 16;
             vb += (lane / kSegMax) * (long long)p.vtok * 16 + (lane % kSegMax) * 16;
         }
+    }
+    __device__ __forceinline__ void set_tile_end(const AttnParams &p)
+    {
+        u_end = (int)min((long long)c.t.units, u1 - c.lin);
         table = p.a.table + (long long)c.t.req * p.a.d.table_stride;
     }
     // the unit `by` further on in the share
-    __device__ __forceinline__ void skip(const AttnParams &p, int by, int lane)
+    __device__ __forceinline__ void skip(const AttnParams &p, int by)
     {
         u += by;
         while (u >= u_end) {
@@ -329,8 +333,8 @@ struct Loader {
                 return;
             }
             u -= c.t.units;
-            next_item<UT>(p, c);
-            set_item(p, lane);
+            advance<UT>(p, c);
+            set_tile_end(p);
         }
     }
     __device__ __forceinline__ void fetch_page(const AttnParams &p, int lane)
@@ -1037,14 +1041,14 @@ __device__ __forceinline__ void store2(__nv_bfloat16 *p, float x, float y) { *re
 
 // shared memory: the warps' rings, their query rows (and fp32 weights), two
 // join buffers (in the query rows' place where those are bf16) -- all of whole
-// 16-byte segments -- then maxima, sums, barriers and slot masks.  NU: units in
+// 16-byte segments -- then maxima, sums, barriers and slot masks.  NH: halves in
 // a warp's ring.
-template <typename M, int NU, bool SOLO>
+template <typename M, int NH, bool SOLO>
 struct Layout {
     static constexpr int kQuery = kWarps * M::kQBytes;
-    static constexpr int kSmall = kWarps * NU * 2 * 8 + (kWarps * M::MR * 2 + M::MR * 2 + kWarps * NU) * 4;
+    static constexpr int kSmall = kWarps * NH * 8 + (kWarps * M::MR * 2 + M::MR * 2 + kWarps * NH) * 4;
     static __host__ __device__ int join_stride(int D) { return D + 8; }
-    static __host__ __device__ int ring_bytes(int stride) { return kWarps * NU * 2 * M::kUnit * stride; }
+    static __host__ __device__ int ring_bytes(int stride) { return kWarps * NH * M::kUnit * stride; }
     static __host__ __device__ int join_bytes(int D) { return SOLO ? 0 : 2 * M::MR * join_stride(D) * 4; }
     static __host__ __device__ int middle_bytes(int D)
     {
@@ -1057,11 +1061,11 @@ struct Layout {
 // a barrier, and a tile is cut into a few parts at most.  Else shares of CTAs,
 // for few: a tile is then cut into many parts, and joining a CTA's warps first
 // leaves a quarter of them to the second launch.
-template <typename M, int NU, bool SOLO, bool BULK, int MB>
+template <typename M, int NH, bool SOLO, bool BULK, int MB>
 __global__ void __launch_bounds__(kThreads, MB) ssd_paged_attn_kernel(const __grid_constant__ AttnParams p)
 {
     using T = typename M::T;
-    using L = Layout<M, NU, SOLO>;
+    using L = Layout<M, NH, SOLO>;
     constexpr int UT = M::kUnit;
     extern __shared__ __align__(16) char smem[];
     __shared__ Found found[kWarps];
@@ -1085,108 +1089,114 @@ __global__ void __launch_bounds__(kThreads, MB) ssd_paged_attn_kernel(const __gr
                 p.a.lse[i] = -INFINITY;
         }
     }
-    const long long share = SOLO ? (long long)blockIdx.x * kWarps + w : blockIdx.x;
-    const long long u0 = share * sh.per, u1 = min(u0 + sh.per, sh.total);
-    if (SOLO) {
-        if (lane == 0)
-            p.desc[share] = make_int4(-1, 0, 0, 0);
-    } else {   // (there may be fewer tiles than the host could tell)
+    if (!SOLO)   // (there may be fewer tiles than the host could tell)
         for (long long i = sh.ntiles * p.items + blockIdx.x * kThreads + tid; i < p.ndesc; i += gridDim.x * kThreads)
             p.desc[i] = make_int4(-1, 0, 0, 0);
-    }
     const int half_bytes = UT * stride;
-    char *ring = smem + (size_t)w * NU * 2 * half_bytes;    // [NU][K, V][UT][stride]
+    char *ring = smem + (size_t)w * NH * half_bytes;        // [NH][UT][stride]
     char *middle = smem + L::ring_bytes(stride);
     char *qs = middle + w * M::kQBytes;
     float *join = reinterpret_cast<float *>(middle + (M::kQSmem ? 0 : L::kQuery));   // (16-byte accesses up to here)
-    uint64_t *bars = reinterpret_cast<uint64_t *>(middle + L::middle_bytes(D)) + w * NU * 2;
-    float *ml = reinterpret_cast<float *>(bars - w * NU * 2 + kWarps * NU * 2);      // [kWarps][MR][2]
-    float *joint = ml + kWarps * M::MR * 2;                                          // [MR] maxima, [MR] sums
-    uint32_t *masks = reinterpret_cast<uint32_t *>(joint + M::MR * 2) + w * NU;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(middle + L::middle_bytes(D)) + w * NH;
+    float *ml = reinterpret_cast<float *>(bars - w * NH + kWarps * NH);   // [kWarps][MR][2]
+    float *joint = ml + kWarps * M::MR * 2;                               // [MR] maxima, [MR] sums
+    uint32_t *masks = reinterpret_cast<uint32_t *>(joint + M::MR * 2) + w * NH;
     const int ds = L::join_stride(D);
     __syncthreads();   // (the schedule's use of the ring's memory is over)
     // segments past the head's elements are read by the products: zero once
     if (!M::kExact) {
-        for (int i = lane; i < NU * 2 * UT; i += 32)
+        for (int i = lane; i < NH * UT; i += 32)
             for (int c = p.seg; c * 16 < stride; ++c)
                 *reinterpret_cast<uint4 *>(ring + (size_t)i * stride + c * 16) = make_uint4(0, 0, 0, 0);
     }
     if (BULK) {
-        if (lane < NU * 2)
+        if (lane < NH)
             ptx::mbar_init(bars + lane, 1);
         ptx::fence_mbar_init();
         ptx::fence_proxy_async_smem();
     }
     __syncwarp();
+
+    // Half h (K of unit h / 2, V when odd) goes to slot h % NH; at step h the half
+    // h + NH - 1 is loaded: with an even ring V of a unit while K of one is used,
+    // with an odd one K while K.  Every step is one group of asynchronous copies,
+    // empty past the share's end.
+    constexpr int step = SOLO ? 1 : kWarps;
+    int head = 0, tail = 0;   // slots of the next half to load, to use
+    uint32_t parity = 0;
+    bool healthy = true;
+    const long long nshares = (long long)sh.of_head * p.items;
+    // (one round, but for more heads than there are warps or CTAs)
+    for (long long share = SOLO ? (long long)blockIdx.x * kWarps + w : blockIdx.x; share < nshares;
+         share += (long long)gridDim.x * (SOLO ? kWarps : 1)) {
+    const int item = (int)(share % p.items);
+    const long long u0 = sh.of_head == 1 ? 0 : share / p.items * sh.per, u1 = min(u0 + sh.per, sh.total);
+    if (SOLO && lane == 0)
+        p.desc[share] = make_int4(-1, 0, 0, 0);
     if (u0 >= sh.total)
-        return;   // (the whole CTA where it has one share; no barrier follows where it has four)
+        break;
+    const int kvh = item / p.nhb, hb = item - kvh * p.nhb;
+    const int h0 = kvh * p.group + hb * p.gh, nh = min(p.gh, p.group - hb * p.gh);
 
     Cursor cur;
     {
         const Found f = found[SOLO ? w : 0];
         set_tile<UT>(p, cur.t, f.req, f.j);
-        cur.item = (int)((u0 - f.lin) / cur.t.units);
-        cur.lin = f.lin + (long long)cur.item * cur.t.units;
         cur.tile = f.tile;
+        cur.lin = f.lin;
     }
-
-    // Steps alternate: while a unit's K is used the V half of the ring's newest
-    // unit is loaded, while its V is used the next unit's K.  Every step is one
-    // group of asynchronous copies, empty past the share's end.
-    constexpr int step = SOLO ? 1 : kWarps;
     Loader<T, M::kDim, BULK, UT> ld;
     ld.c = cur;
     ld.u1 = u1;
-    ld.set_item(p, lane);
+    ld.set_head(p, kvh, lane);
+    ld.set_tile_end(p);
     ld.u = (int)(u0 - cur.lin);
-    ld.skip(p, SOLO ? 0 : w, lane);
+    ld.skip(p, SOLO ? 0 : w);
     ld.fetch_page(p, lane);
-    int head = 0;
     auto load_k = [&]() {
         if (ld.u >= 0) {
-            char *slot = ring + head * 2 * half_bytes;
+            char *slot = ring + head * half_bytes;
             ld.offsets(p, lane);
             if (lane == 0)
                 masks[head] = ld.mask;
             if constexpr (!BULK)
                 ld.copy(p, ld.kb, ld.koff, p.ktok, smem_addr(slot), lane);
             else
-                ld.copy_bulk(p, ld.kb, ld.koff[0], slot, bars + head * 2, false, lane);
+                ld.copy_bulk(p, ld.kb, ld.koff[0], slot, bars + head, false, lane);
+            head = head + 1 == NH ? 0 : head + 1;
         }
         if (!BULK)
             cp_commit();
     };
     auto load_v = [&]() {
         if (ld.u >= 0) {
-            char *slot = ring + (head * 2 + 1) * half_bytes;
+            char *slot = ring + head * half_bytes;
             if constexpr (!BULK)
                 ld.copy(p, ld.vb, ld.voff, p.vtok, smem_addr(slot), lane);
             else
-                ld.copy_bulk(p, ld.vb, ld.voff[0], slot, bars + head * 2 + 1, true, lane);
-            ld.skip(p, step, lane);
+                ld.copy_bulk(p, ld.vb, ld.voff[0], slot, bars + head, true, lane);
+            ld.skip(p, step);
             ld.fetch_page(p, lane);
-            head = head + 1 == NU ? 0 : head + 1;
+            head = head + 1 == NH ? 0 : head + 1;
         }
         if (!BULK)
             cp_commit();
     };
 #pragma unroll 1
-    for (int i = 0; i < NU - 1; ++i) {
+    for (int i = 0; i < (NH - 1) / 2; ++i) {
         load_k();
         load_v();
     }
-    load_k();
+    if (NH % 2 == 0)
+        load_k();
 
     M math;
     math.qs = reinterpret_cast<decltype(math.qs)>(qs);
     if constexpr (sizeof(T) == 4)
         math.ps = math.qs + M::MR * M::kDim;
-    int tail = 0;
-    uint32_t parity = 0;
-    bool healthy = true;
-    int u = (int)(u0 - cur.lin);   // first unit of the share in this item
+    int u = (int)(u0 - cur.lin);   // first unit of the share in this tile
     while (true) {
-        const int ue = (int)min((long long)cur.t.units, u1 - cur.lin);   // the share's units of the item: [u, ue)
+        const int ue = (int)min((long long)cur.t.units, u1 - cur.lin);   // the share's units of the tile: [u, ue)
         // tokens that every row of the tile sees: from the last row's first to the first row's last
         int all0, all1;
         {
@@ -1195,30 +1205,38 @@ __global__ void __launch_bounds__(kThreads, MB) ssd_paged_attn_kernel(const __gr
             all1 = p0 < 0 ? 0 : min(p0, limit - 1) + 1;
             all0 = p.a.d.window > 0 ? max(0, p1 - p.a.d.window + 1) : 0;
         }
-        math.begin(p, cur.t, cur.item, lane);
-        const int kvh = cur.item / p.nhb, hb = cur.item - kvh * p.nhb;
-        const int h0 = kvh * p.group + hb * p.gh, nh = min(p.gh, p.group - hb * p.gh), rows = cur.t.nq * nh;
+        math.begin(p, cur.t, item, lane);
+        const int rows = cur.t.nq * nh;
         // this warp's units: all, or those whose number in the CTA's share is w modulo the warps
         const int skip = SOLO ? 0 : (w - (int)((cur.lin + u - u0) % kWarps) + kWarps) % kWarps;
         for (int x = u + skip; x < ue; x += step) {
             const int tok0 = (cur.t.ub + x) * UT;
-            char *slot = ring + tail * 2 * half_bytes;
             if constexpr (BULK)
-                healthy = wait_bulk(bars + tail * 2, parity, healthy);
+                healthy = wait_bulk(bars + tail, parity, healthy);
             else
-                cp_wait<2 * NU - 2>();
+                cp_wait<NH - 2>();
             __syncwarp();
             const uint32_t mask = masks[tail];
-            load_v();
-            math.scores(p, slot, mask, tok0, all0, all1, lane);
-            if constexpr (BULK)
-                healthy = wait_bulk(bars + tail * 2 + 1, parity, healthy);
+            if (NH % 2 == 0)
+                load_v();
             else
-                cp_wait<2 * NU - 2>();
+                load_k();
+            math.scores(p, ring + tail * half_bytes, mask, tok0, all0, all1, lane);
+            if (++tail == NH) {
+                tail = 0;
+                parity ^= 1;
+            }
+            if constexpr (BULK)
+                healthy = wait_bulk(bars + tail, parity, healthy);
+            else
+                cp_wait<NH - 2>();
             __syncwarp();
-            load_k();
-            math.values(p, slot + half_bytes, mask, tok0, all0, all1, lane);
-            if (++tail == NU) {
+            if (NH % 2 == 0)
+                load_k();
+            else
+                load_v();
+            math.values(p, ring + tail * half_bytes, mask, tok0, all0, all1, lane);
+            if (++tail == NH) {
                 tail = 0;
                 parity ^= 1;
             }
@@ -1290,17 +1308,20 @@ __global__ void __launch_bounds__(kThreads, MB) ssd_paged_attn_kernel(const __gr
             if (M::kQSmem)
                 __syncthreads();   // (the next tile's query rows go where the buffers are)
         }
-        // where the parts of a cut tile are
+        // where the parts of a cut tile are: this share and the head's next ones
         if (SOLO ? !whole && slot == 1 && lane == 0 : slot == 1 && tid == 0)
-            p.desc[SOLO ? share : (long long)cur.tile * p.items + cur.item] =
-                make_int4(whole ? -1 : cur.t.row, cur.t.nq | cur.item << 8, (int)share, (int)((cur.lin + cur.t.units - 1) / sh.per));
+            p.desc[SOLO ? share : (long long)cur.tile * p.items + item] =
+                make_int4(whole ? -1 : cur.t.row, cur.t.nq | item << 8, (int)share,
+                          (int)((cur.lin + cur.t.units - 1) / sh.per - (cur.lin + u) / sh.per) + 1);
         if (cur.lin + ue >= u1)
             break;
         u = 0;
-        next_item<UT>(p, cur);
+        advance<UT>(p, cur);
     }
     if (!BULK)
         cp_wait<0>();
+    __syncwarp();
+    }
 }
 
 // Joins parts of row r of a cut tile: NW warps take parts in turn, lanes the
@@ -1310,10 +1331,10 @@ __global__ void __launch_bounds__(kThreads, MB) ssd_paged_attn_kernel(const __gr
 template <typename T, int MR, int NW>
 __device__ __forceinline__ void join_row(const AttnParams &p, const int4 &d, int r, int w, int lane, float (*sm)[2], float (*so)[256])
 {
-    const int row = d.x, item = d.y >> 8, c0 = d.z, n = d.w - d.z + 1, D = p.a.d.headdim;
+    const int row = d.x, item = d.y >> 8, n = d.w, D = p.a.d.headdim;
     const int kvh = item / p.nhb, hb = item - kvh * p.nhb, nh = min(p.gh, p.group - hb * p.gh);
     float mm = -INFINITY, ll = 0.f, o[2][4] = {};
-    // part i lies in share c0 + i: slot 1 of the first, slot 0 of the others
+    // part i lies in the head's i-th share from d.z on: slot 1 of the first, slot 0 of the others
     for (int i = w; i < n; i += 4 * NW) {
         float pm[4], pl[4];
         float4 v[4][2];
@@ -1324,7 +1345,7 @@ __device__ __forceinline__ void join_row(const AttnParams &p, const int4 &d, int
             v[b][0] = v[b][1] = make_float4(0.f, 0.f, 0.f, 0.f);
             const int part = i + NW * b;
             if (part < n) {
-                const size_t at = ((size_t)(c0 + part) * 2 + (part == 0 ? 1 : 0)) * MR + r;
+                const size_t at = (((size_t)d.z + (size_t)part * p.items) * 2 + (part == 0 ? 1 : 0)) * MR + r;
                 const float2 t = *reinterpret_cast<const float2 *>(p.part_ml + 2 * at);
                 pm[b] = t.y == 0.f ? -INFINITY : t.x;   // (a part that saw nothing)
                 pl[b] = t.y;
@@ -1425,8 +1446,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) ssd_paged_attn_join_kernel(co
     if (SOLO) {
         int4 d[kWarps];
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k)
-            d[k] = p.desc[(long long)blockIdx.x * kWarps + k];
+        for (int k = 0; k < kWarps; ++k) {
+            const int i = blockIdx.x * kWarps + k;
+            d[k] = i < p.ndesc ? p.desc[i] : make_int4(-1, 0, 0, 0);
+        }
         int at = w;   // rows of all four, dealt to the warps
 #pragma unroll
         for (int k = 0; k < kWarps; ++k) {
@@ -1444,13 +1467,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) ssd_paged_attn_join_kernel(co
 
 // ---- host: one variant's launches ---------------------------------------------
 
-template <typename M, int NU, bool SOLO, bool BULK, int MB>
+template <typename M, int NH, bool SOLO, bool BULK, int MB>
 cudaError_t launch(AttnParams &p, void *workspace, cudaStream_t stream)
 {
     using T = typename M::T;
     const int D = p.a.d.headdim;
-    const int smem = std::max(Layout<M, NU, SOLO>::total(D, p.stride), p.a.start ? (int)(p.a.d.nreq + 1) * 4 : 0);
-    auto kernel = ssd_paged_attn_kernel<M, NU, SOLO, BULK, MB>;
+    const int smem = std::max(Layout<M, NH, SOLO>::total(D, p.stride), p.a.start ? (int)(p.a.d.nreq + 1) * 4 : 0);
+    auto kernel = ssd_paged_attn_kernel<M, NH, SOLO, BULK, MB>;
     // CTAs per SM by shared memory (1 KB of the system's each) and registers
     static int regs = 0;   // (the same for every device)
     cudaError_t e;
@@ -1464,7 +1487,8 @@ cudaError_t launch(AttnParams &p, void *workspace, cudaStream_t stream)
         return e;
     const int per_sm = std::max(1, std::min({kMaxPerSm, (228 << 10) / (smem + 1024 + 256), 65536 / (regs * kThreads)}));
     const int grid = std::min(kMaxCtas, p.sms * per_sm);
-    const size_t shares = (size_t)grid * (SOLO ? kWarps : 1);
+    const int own = grid * (SOLO ? kWarps : 1);
+    const size_t shares = (size_t)std::max(1, own / p.items) * p.items;
     p.part_o = static_cast<float *>(workspace);
     p.part_ml = p.part_o + shares * 2 * M::MR * D;
     p.desc = reinterpret_cast<int4 *>(p.part_ml + shares * 2 * M::MR * 2);
@@ -1482,7 +1506,7 @@ cudaError_t launch(AttnParams &p, void *workspace, cudaStream_t stream)
     if ((e = cudaLaunchKernelEx(&cfg, kernel, p)) != cudaSuccess)
         return e;
     note_launches(1);
-    cfg.gridDim = SOLO ? dim3(grid) : dim3(p.ndesc, p.tok * p.gh);
+    cfg.gridDim = SOLO ? dim3((p.ndesc + kWarps - 1) / kWarps) : dim3(p.ndesc, p.tok * p.gh);
     cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&cfg, ssd_paged_attn_join_kernel<T, M::MR, SOLO>, p);
@@ -1491,12 +1515,12 @@ cudaError_t launch(AttnParams &p, void *workspace, cudaStream_t stream)
     return e;
 }
 
-// NU, NUS: ring units with shares of CTAs, of warps; MB: CTAs per SM that the
+// NH, NHS: halves in the ring with shares of CTAs, of warps; MB: CTAs per SM that the
 // registers must leave room for with shares of warps
-template <typename M, int NU, int NUS, int MB, bool BULK>
+template <typename M, int NH, int NHS, int MB, bool BULK>
 cudaError_t launch_shares(AttnParams &p, void *ws, cudaStream_t st)
 {
-    return solo_shares(p) ? launch<M, NUS, true, BULK, MB>(p, ws, st) : launch<M, NU, false, BULK, 1>(p, ws, st);
+    return solo_shares(p) ? launch<M, NHS, true, BULK, MB>(p, ws, st) : launch<M, NH, false, BULK, 1>(p, ws, st);
 }
 
 cudaError_t take_error(uint32_t *code)

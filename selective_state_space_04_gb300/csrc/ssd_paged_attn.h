@@ -19,7 +19,7 @@ struct AttnParams {
     FastDiv page;
     float *part_o;      // [shares][2][MR][D] partial rows
     float *part_ml;     // [shares][2][MR][2] their maxima (base 2) and sums
-    int4 *desc;         // the cut tiles: first row, tokens | item << 8, first and last share; x -1: none.  Shares of
+    int4 *desc;         // the cut tiles: first row, tokens | item << 8, first share, parts; x -1: none.  Shares of
                         // warps: [shares], of the tile that starts in a share; shares of CTAs: [most tiles x items]
     int ndesc;          // entries of it
     int group;          // query heads per key-value head

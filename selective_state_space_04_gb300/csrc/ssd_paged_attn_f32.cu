@@ -9,10 +9,10 @@ cudaError_t launch_rows(AttnParams &p, void *ws, cudaStream_t st)
 {
     const int D = p.a.d.headdim;
     if (D <= 64)
-        return launch_shares<Simt<MR, 64, false>, 1, 1, 2, true>(p, ws, st);
+        return launch_shares<Simt<MR, 64, false>, 2, 2, 2, true>(p, ws, st);
     if (D <= 128)
-        return launch_shares<Simt<MR, 128, false>, MR == 8 ? 2 : 3, 3, 1, true>(p, ws, st);
-    return launch_shares<Simt<MR, 256, false>, 1, 1, 1, true>(p, ws, st);
+        return launch_shares<Simt<MR, 128, false>, MR == 8 ? 5 : 6, 6, 1, true>(p, ws, st);
+    return launch_shares<Simt<MR, 256, false>, 2, 2, 1, true>(p, ws, st);
 }
 
 }  // namespace
