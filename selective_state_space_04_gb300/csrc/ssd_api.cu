@@ -505,6 +505,8 @@ ssd_status_t with_workspace(void *workspace, uint64_t have, size_t need, cudaStr
 
 }  // namespace
 
+uint64_t context_id() { return current_context_id(); }
+
 void note_launches(int n) { g_launches.fetch_add((uint64_t)n, std::memory_order_relaxed); }
 
 }  // namespace ssd

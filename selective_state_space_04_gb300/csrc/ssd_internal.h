@@ -4,6 +4,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "ssd.h"
@@ -256,5 +257,22 @@ ssd_status_t attn_read_device_error(uint32_t *code);
 
 // launch accounting
 void note_launches(int n);
+// a number that no other CUDA context of the process has or had, for the one
+// current on this thread; 0 when it has none or the driver cannot say
+uint64_t context_id();
+
+// Prepares a kernel once per context for up to `smem` bytes of dynamic shared
+// memory (`done`: a static of the caller's, the context it is prepared in).
+template <typename K>
+inline cudaError_t allow_smem(K *kernel, int smem, std::atomic<uint64_t> &done)
+{
+    const uint64_t ctx = context_id();
+    if (ctx != 0 && done.load(std::memory_order_acquire) == ctx)
+        return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess)
+        done.store(context_id(), std::memory_order_release);   // (the context exists now)
+    return e;
+}
 
 }  // namespace ssd

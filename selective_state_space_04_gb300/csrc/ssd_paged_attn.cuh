@@ -1467,6 +1467,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) ssd_paged_attn_join_kernel(co
 
 // ---- host: one variant's launches ---------------------------------------------
 
+constexpr int kSmemMost = (227 << 10) - 1024;   // dynamic, beside the kernel's few static bytes
+
 template <typename M, int NH, bool SOLO, bool BULK, int MB>
 cudaError_t launch(AttnParams &p, void *workspace, cudaStream_t stream)
 {
@@ -1474,18 +1476,20 @@ cudaError_t launch(AttnParams &p, void *workspace, cudaStream_t stream)
     const int D = p.a.d.headdim;
     const int smem = std::max(Layout<M, NH, SOLO>::total(D, p.stride), p.a.start ? (int)(p.a.d.nreq + 1) * 4 : 0);
     auto kernel = ssd_paged_attn_kernel<M, NH, SOLO, BULK, MB>;
-    // CTAs per SM by shared memory (1 KB of the system's each) and registers
-    static int regs = 0;   // (the same for every device)
-    cudaError_t e;
-    if (!regs) {
+    static std::atomic<uint64_t> done{0};
+    static std::atomic<int> regs{0};   // (the same for every device)
+    cudaError_t e = allow_smem(kernel, kSmemMost, done);
+    if (e != cudaSuccess)
+        return e;
+    int r = regs.load(std::memory_order_relaxed);
+    if (r == 0) {
         cudaFuncAttributes at;
         if ((e = cudaFuncGetAttributes(&at, kernel)) != cudaSuccess)
             return e;
-        regs = (at.numRegs + 7) / 8 * 8;
+        regs.store(r = (at.numRegs + 7) / 8 * 8, std::memory_order_relaxed);
     }
-    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
-        return e;
-    const int per_sm = std::max(1, std::min({kMaxPerSm, (228 << 10) / (smem + 1024 + 256), 65536 / (regs * kThreads)}));
+    // CTAs per SM by shared memory (1 KB of the system's each) and registers
+    const int per_sm = std::max(1, std::min({kMaxPerSm, (228 << 10) / (smem + 1024 + 256), 65536 / (r * kThreads)}));
     const int grid = std::min(kMaxCtas, p.sms * per_sm);
     const int own = grid * (SOLO ? kWarps : 1);
     const size_t shares = (size_t)std::max(1, own / p.items) * p.items;

@@ -226,8 +226,8 @@ cudaError_t plan_launch(const PlanArgs &a, cudaStream_t stream)
     SSD_NVTX_RANGE("plan_launch");
     const int pad = (a.nreq + 4) & ~3;
     const size_t smem = (size_t)pad * 4 * sizeof(int);
-    cudaError_t e = cudaFuncSetAttribute(ssd_paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)(((SSD_PLAN_MAX_REQUESTS + 4) & ~3) * 4 * sizeof(int)));
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(ssd_paged_plan_kernel, ((SSD_PLAN_MAX_REQUESTS + 4) & ~3) * 4 * (int)sizeof(int), done);
     if (e != cudaSuccess)
         return e;
     cudaLaunchAttribute attr[1];

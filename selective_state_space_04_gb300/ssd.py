@@ -500,7 +500,25 @@ def _addr(t):
 
 
 def _stream_ptr(device, stream):
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+
+
+def _layout(t):
+    """What the checks of an argument go by: everything but its address."""
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+
+
+# Call structures of argument layouts that have passed the checks below: a serving loop calls with the same few
+# layouts again and again, and the checks and the structure cost several times the call itself.  Nothing of an
+# argument's address or contents is kept.
+_known = {}
+
+
+def _remember(key, d):
+    if len(_known) >= 4096:
+        _known.clear()
+    _known[key] = d
+    return d
 
 
 def _vectors(device, named, dtype):
@@ -552,11 +570,6 @@ def paged_plan(lens, new_lens, block_table, free_ring, ring_pos, *, page_size, m
     write, as such a dict; its ``lens`` and ``ring_pos`` may be the inputs (in place).
     """
     R, dev = lens.shape[0], lens.device
-    if not lens.is_cuda:
-        raise ValueError("lens must be a CUDA tensor")
-    if block_table.dtype != torch.int32 or block_table.device != dev or block_table.dim() != 2 or \
-            block_table.shape[0] != R or not block_table.is_contiguous():
-        raise ValueError(f"block_table must be a contiguous [{R}, max_pages] int32 tensor on {dev}")
     if out is None:
         i32 = dict(dtype=torch.int32, device=dev)
         i64 = dict(dtype=torch.int64, device=dev)
@@ -564,12 +577,21 @@ def paged_plan(lens, new_lens, block_table, free_ring, ring_pos, *, page_size, m
                    positions=torch.empty(max_tokens, **i32), token_req=torch.empty(max_tokens, **i32),
                    slots=torch.empty(max_tokens, **i64), ring_pos=torch.empty(2, **i64), counts=torch.empty(4, **i32))
     o = out
-    _vectors(dev, (("lens", lens, R), ("new_lens", new_lens, R), ("free_ring", free_ring, None), ("out lens", o["lens"], R),
-                   ("granted", o["granted"], R), ("start", o["start"], R + 1), ("positions", o["positions"], max_tokens),
-                   ("token_req", o["token_req"], max_tokens), ("counts", o["counts"], 4)), torch.int32)
-    _vectors(dev, (("ring_pos", ring_pos, 2), ("out ring_pos", o["ring_pos"], 2), ("slots", o["slots"], max_tokens)),
-             torch.int64)
-    d = SsdPlanDims(R, max_tokens, free_ring.shape[0], page_size, block_table.shape[1], 0, 0)
+    key = (paged_plan, *map(_layout, (lens, new_lens, block_table, free_ring, ring_pos, o["lens"], o["granted"], o["start"],
+                                      o["positions"], o["token_req"], o["slots"], o["ring_pos"], o["counts"])), page_size, max_tokens)
+    d = _known.get(key)
+    if d is None:
+        if not lens.is_cuda:
+            raise ValueError("lens must be a CUDA tensor")
+        if block_table.dtype != torch.int32 or block_table.device != dev or block_table.dim() != 2 or \
+                block_table.shape[0] != R or not block_table.is_contiguous():
+            raise ValueError(f"block_table must be a contiguous [{R}, max_pages] int32 tensor on {dev}")
+        _vectors(dev, (("lens", lens, R), ("new_lens", new_lens, R), ("free_ring", free_ring, None), ("out lens", o["lens"], R),
+                       ("granted", o["granted"], R), ("start", o["start"], R + 1), ("positions", o["positions"], max_tokens),
+                       ("token_req", o["token_req"], max_tokens), ("counts", o["counts"], 4)), torch.int32)
+        _vectors(dev, (("ring_pos", ring_pos, 2), ("out ring_pos", o["ring_pos"], 2), ("slots", o["slots"], max_tokens)),
+                 torch.int64)
+        d = _remember(key, SsdPlanDims(R, max_tokens, free_ring.shape[0], page_size, block_table.shape[1], 0, 0))
     _check(_lib.ssd_paged_plan(lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), free_ring.data_ptr(),
                                ring_pos.data_ptr(), o["lens"].data_ptr(), o["granted"].data_ptr(), o["start"].data_ptr(),
                                o["positions"].data_ptr(), o["token_req"].data_ptr(), o["slots"].data_ptr(),
@@ -618,25 +640,29 @@ def qk_norm_rope_fwd(q, k, q_weight, k_weight, cos, sin, positions, *, eps=1e-6,
     [npages, page_size, Hk, D]`` (any strides, contiguous last axis) and ``slots [T]`` int64, keys and values go into
     the cache as well; ``return_k=False`` then leaves ``k_out`` out (None).  ``q_out`` may be ``q`` and ``k_out`` ``k``.
     """
-    d = _qk_dims(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
     dev = q.device
+    key = (qk_norm_rope_fwd, *map(_layout, (q, k, q_weight, k_weight, cos, sin, positions, v, k_cache, v_cache, slots, q_out,
+                                            k_out)), eps, interleaved, return_k)
+    d = _known.get(key)
+    if d is None:   # (first of all, so that only tensors that are CUDA tensors get outputs)
+        d = _qk_dims(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
+        _rows(dev, (("q_out", q_out, q.shape), ("k_out", k_out, k.shape), ("v", v, k.shape)), q.dtype)
+        d.qo_stride = (q.shape[1] * q.shape[2], q.shape[2]) if q_out is None else q_out.stride()[:2]
+        d.ko_stride = (k.shape[1] * k.shape[2], k.shape[2]) if k_out is None else k_out.stride()[:2]
+        if k_cache is not None or v_cache is not None or slots is not None:
+            if k_cache is None or v_cache is None or slots is None or v is None:
+                raise ValueError("writing the cache takes v, k_cache, v_cache and slots")
+            _cache_args(dev, q.dtype, k_cache, v_cache, k.shape[1], q.shape[2])
+            _vectors(dev, (("slots", slots, q.shape[0]),), torch.int64)
+            d.npages, d.page_size = k_cache.shape[0], k_cache.shape[1]
+            d.v_stride, d.kc_stride, d.vc_stride = v.stride()[:2], k_cache.stride()[:3], v_cache.stride()[:3]
+        elif k_out is None and not return_k:
+            raise ValueError("return_k=False takes a cache to write the keys to")
+        _remember(key, d)
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
     if k_out is None and return_k:
         k_out = torch.empty(k.shape, dtype=q.dtype, device=dev)
-    _rows(dev, (("q_out", q_out, q.shape), ("k_out", k_out, k.shape), ("v", v, k.shape)), q.dtype)
-    d.qo_stride = q_out.stride()[:2]
-    if k_out is not None:
-        d.ko_stride = k_out.stride()[:2]
-    if k_cache is not None or v_cache is not None or slots is not None:
-        if k_cache is None or v_cache is None or slots is None or v is None:
-            raise ValueError("writing the cache takes v, k_cache, v_cache and slots")
-        _cache_args(dev, q.dtype, k_cache, v_cache, k.shape[1], q.shape[2])
-        _vectors(dev, (("slots", slots, q.shape[0]),), torch.int64)
-        d.npages, d.page_size = k_cache.shape[0], k_cache.shape[1]
-        d.v_stride, d.kc_stride, d.vc_stride = v.stride()[:2], k_cache.stride()[:3], v_cache.stride()[:3]
-    elif k_out is None:
-        raise ValueError("return_k=False takes a cache to write the keys to")
     _check(_lib.ssd_qk_norm_rope_fwd(q.data_ptr(), k.data_ptr(), _addr(v), _addr(q_weight), _addr(k_weight), cos.data_ptr(),
                                      sin.data_ptr(), positions.data_ptr(), q_out.data_ptr(), _addr(k_out), _addr(k_cache),
                                      _addr(v_cache), _addr(slots), d, _stream_ptr(dev, stream)), "ssd_qk_norm_rope_fwd")
@@ -648,15 +674,21 @@ def qk_norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_o
     """Gradients of :func:`qk_norm_rope_fwd` given those of its outputs.  Returns a dict: ``dq, dk`` in the inputs'
     dtype, ``dq_weight, dk_weight [D]`` fp32.  ``dq`` and ``dk`` may be given (views of a fused gradient, or ``dq_out``
     and ``dk_out`` themselves)."""
-    d = _qk_dims(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
     dev, D = q.device, q.shape[2]
+    key = (qk_norm_rope_bwd, *map(_layout, (q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_out, dq, dk)), eps,
+           interleaved)
+    d = _known.get(key)
+    if d is None:
+        d = _qk_dims(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
+        _rows(dev, (("dq_out", dq_out, q.shape), ("dk_out", dk_out, k.shape), ("dq", dq, q.shape), ("dk", dk, k.shape)), q.dtype)
+        d.qo_stride, d.ko_stride = dq_out.stride()[:2], dk_out.stride()[:2]
+        d.dq_stride = (q.shape[1] * D, D) if dq is None else dq.stride()[:2]
+        d.dk_stride = (k.shape[1] * D, D) if dk is None else dk.stride()[:2]
+        _remember(key, d)
     if dq is None:
         dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
     if dk is None:
         dk = torch.empty(k.shape, dtype=q.dtype, device=dev)
-    _rows(dev, (("dq_out", dq_out, q.shape), ("dk_out", dk_out, k.shape), ("dq", dq, q.shape), ("dk", dk, k.shape)), q.dtype)
-    d.qo_stride, d.ko_stride = dq_out.stride()[:2], dk_out.stride()[:2]
-    d.dq_stride, d.dk_stride = dq.stride()[:2], dk.stride()[:2]
     dw = torch.empty((2, (D + 3) // 4 * 4), dtype=torch.float32, device=dev)
     dqw, dkw = dw[0, :D], dw[1, :D]
     ws, nws = _workspace(workspace)
@@ -703,17 +735,22 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, positions, start=None, *, s
     them.  Rows that see nothing get 0 (lse -inf).  ``scale`` defaults to D^-1/2.  ``out [rows,H,D]`` is in q's dtype,
     ``lse [rows,H]`` fp32.
     """
-    d = _attn_dims(q, k_cache, v_cache, block_table, scale, window)
-    dev, n, H = q.device, q.shape[0], q.shape[1]
+    dev = q.device
+    key = (paged_attn_fwd, *map(_layout, (q, k_cache, v_cache, block_table, positions, start, out, lse)), scale, window)
+    d = _known.get(key)
+    if d is None:
+        d = _attn_dims(q, k_cache, v_cache, block_table, scale, window)
+        n, H, D = q.shape
+        _rows(dev, (("out", out, q.shape),), q.dtype)
+        if lse is not None and (lse.dtype != torch.float32 or lse.device != dev or lse.shape != (n, H) or not lse.is_contiguous()):
+            raise ValueError(f"lse must be a contiguous [{n}, {H}] fp32 tensor on {dev}")
+        _vectors(dev, (("positions", positions, n), ("start", start, block_table.shape[0] + 1)), torch.int32)
+        d.o_stride = (H * D, D) if out is None else out.stride()[:2]
+        _remember(key, d)
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=dev)
     if lse is None and return_lse:
-        lse = torch.empty((n, H), dtype=torch.float32, device=dev)
-    _rows(dev, (("out", out, q.shape),), q.dtype)
-    if lse is not None and (lse.dtype != torch.float32 or lse.device != dev or lse.shape != (n, H) or not lse.is_contiguous()):
-        raise ValueError(f"lse must be a contiguous [{n}, {H}] fp32 tensor on {dev}")
-    _vectors(dev, (("positions", positions, n), ("start", start, block_table.shape[0] + 1)), torch.int32)
-    d.o_stride = out.stride()[:2]
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
     ws, nws = _workspace(workspace)
     _check(_lib.ssd_paged_attn_fwd(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
                                    positions.data_ptr(), _addr(start), out.data_ptr(), _addr(lse), ws, nws, d,
