@@ -505,6 +505,21 @@ ssd_status_t with_workspace(void *workspace, uint64_t have, size_t need, cudaStr
 
 }  // namespace
 
+int sm_count()
+{
+    static std::atomic<int> known[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+        return 152;
+    n = known[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+            return 152;
+        known[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
 uint64_t context_id() { return current_context_id(); }
 
 void note_launches(int n) { g_launches.fetch_add((uint64_t)n, std::memory_order_relaxed); }

@@ -257,6 +257,8 @@ ssd_status_t attn_read_device_error(uint32_t *code);
 
 // launch accounting
 void note_launches(int n);
+// SMs of the current device (152 when the driver cannot say)
+int sm_count();
 // a number that no other CUDA context of the process has or had, for the one
 // current on this thread; 0 when it has none or the driver cannot say
 uint64_t context_id();

@@ -30,17 +30,6 @@ int tile_rows(const ssd_attn_dims_t &d)
     return want <= 1 ? 1 : want <= 2 ? 2 : want <= 4 ? 4 : 8;
 }
 
-int sm_count()
-{
-    static int n[64] = {};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
-        return 152;
-    if (!n[dev] && cudaDeviceGetAttribute(&n[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 152;
-    return n[dev];
-}
-
 }  // namespace
 
 size_t attn_workspace_bytes(const ssd_attn_dims_t &d)

@@ -699,9 +699,9 @@ def qk_norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_o
     return dict(dq=dq, dk=dk, dq_weight=dqw, dk_weight=dkw)
 
 
-def qk_norm_rope_bwd_workspace_size(ntokens, headdim) -> int:
-    """Bytes of scratch ``qk_norm_rope_bwd`` needs."""
-    d = SsdQkDims(ntokens, 0, 0, 1, 1, headdim, 0, 0, DTYPE_BF16, 0, 0.0)
+def qk_norm_rope_bwd_workspace_size(q, k) -> int:
+    """Bytes of scratch ``qk_norm_rope_bwd`` needs for such tensors on the current device."""
+    d = SsdQkDims(q.shape[0], 0, 0, q.shape[1], k.shape[1], q.shape[2], 0, 0, _DTYPES[q.dtype], 0, 0.0)
     n = ctypes.c_uint64(0)
     _check(_lib.ssd_qk_norm_rope_bwd_workspace_size(ctypes.byref(d), ctypes.byref(n)), "ssd_qk_norm_rope_bwd_workspace_size")
     return int(n.value)

@@ -171,7 +171,7 @@ def test_in_place_and_strided_gradients(ssd):
     got = ssd.qk_norm_rope_bwd(g["q"], g["k"], *tab, g["dq"], g["dk"], dq=fused[:, :Hq], dk=fused[:, Hq:Hq + Hk])
     assert torch.equal(fused[:, :Hq], ref["dq"]) and torch.equal(fused[:, Hq:Hq + Hk], ref["dk"])
     assert (fused[:, Hq + Hk:] == 9).all() and torch.equal(got["dq_weight"], ref["dq_weight"])
-    ws = torch.full((ssd.qk_norm_rope_bwd_workspace_size(T, D),), 255, dtype=torch.uint8, device="cuda")
+    ws = torch.full((ssd.qk_norm_rope_bwd_workspace_size(g["q"], g["k"]),), 255, dtype=torch.uint8, device="cuda")
     got = ssd.qk_norm_rope_bwd(g["q"], g["k"], *tab, g["dq"], g["dk"], dq=g["dq"], dk=g["dk"], workspace=ws)
     for n in ref:
         assert torch.equal(got[n], ref[n])
