@@ -504,7 +504,7 @@ ssd_status_t ssd_paged_plan(const int32_t *lens, const int32_t *new_lens, int32_
 #define SSD_ROPE_INTERLEAVED 1u
 
 typedef struct ssd_qk_dims {
-    int64_t ntokens;     /* >= 0 */
+    int64_t ntokens;     /* >= 0; times either number of heads at most 2^30 */
     int64_t max_pos;     /* rows of cos and sin, >= 0 */
     int64_t npages;      /* pages of the cache (0 without one) */
     int32_t nheads_q;    /* >= 1 */

@@ -419,7 +419,8 @@ ssd_status_t check_qk_dims(const ssd_qk_dims_t *d, bool cache, bool bwd)
         return SSD_ERR_INVALID_DIMS;
     if (d->dtype != SSD_DTYPE_F32 && d->dtype != SSD_DTYPE_BF16)
         return SSD_ERR_UNSUPPORTED_DTYPE;
-    if (d->headdim % 8 != 0 || d->headdim > 256 || d->rotary_dim % 16 != 0)
+    if (d->headdim % 8 != 0 || d->headdim > 256 || d->rotary_dim % 16 != 0 ||
+        d->ntokens * std::max(d->nheads_q, d->nheads_k) > (INT64_C(1) << 30))   // (rows are counted in 32 bits)
         return SSD_ERR_UNSUPPORTED;
     const int64_t es = (int64_t)elem_size(d->dtype);
     const int64_t nq[] = {d->ntokens, d->nheads_q}, nk[] = {d->ntokens, d->nheads_k};
