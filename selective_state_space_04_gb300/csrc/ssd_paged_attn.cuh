@@ -804,18 +804,19 @@ struct Mma {
 
 // ---- the arithmetic: fp32 ---------------------------------------------------
 
-// Scores: a unit's 32 tokens over the lanes (16 tokens, two lanes each, where
-// 32 rows of K for every warp do not fit shared memory), the query rows read
-// from shared memory at the same address by all lanes.  Output: a lane holds 4
-// elements of every row (8 for heads above 128); for heads of at most 64 the
-// half warps take tokens in turn.  The weights go through shared memory.
-// Products and sums are packed pairs of fp32 FMA.
+// Scores: a lane takes two tokens (half a unit apart) and a part of the head's
+// elements, so that a query segment read from shared memory (the same for all
+// lanes of a part) serves two tokens: those reads bound the scores of several
+// rows.  The parts are added by shuffles, after which lane l has token l.
+// Output: a lane holds 4 elements of every row (8 for heads above 128); for heads
+// of at most 64 the half warps take tokens in turn.  The weights go through
+// shared memory.  Products and sums are packed pairs of fp32 FMA.
 template <int MRows, int DP, bool EX>
 struct Simt {
     using T = float;
     static constexpr int MR = MRows, kDim = DP, kUnit = DP > 64 ? 16 : 32;
     static constexpr bool kExact = EX;
-    static constexpr int kPer = 32 / kUnit;              // lanes per token in the scores
+    static constexpr int kParts = 64 / kUnit;            // parts of the elements in the scores
     static constexpr int kGroups = DP <= 64 ? 2 : 1;     // tokens at a time in the output
     static constexpr int NV = (DP + 127) / 128;          // float4 of the output per lane and row
     f32x2 o[MR][NV][2];
@@ -860,28 +861,42 @@ struct Simt {
 
     __device__ __forceinline__ void scores(const AttnParams &p, char *slot, uint32_t mask, int tok0, int all0, int all1, int lane)
     {
-        const int tt = lane % kUnit, part = lane / kUnit, D = dim(p);
-        const ulonglong2 *k = reinterpret_cast<const ulonglong2 *>(slot + tt * row_bytes(p));
-        f32x2 acc[MR][2];
+        constexpr int kHalf = kUnit / 2, NC = MR > 4 ? 1 : 2;   // NC: sums per row and token
+        const int part = lane / kHalf, tt = lane % kUnit, D = dim(p);
+        const ulonglong2 *k0 = reinterpret_cast<const ulonglong2 *>(slot + (lane % kHalf) * row_bytes(p));
+        const ulonglong2 *k1 = reinterpret_cast<const ulonglong2 *>(slot + (lane % kHalf + kHalf) * row_bytes(p));
+        f32x2 acc[MR][2][NC];
 #pragma unroll
         for (int r = 0; r < MR; ++r)
-            acc[r][0] = acc[r][1] = pk2(0.f, 0.f);
-#pragma unroll 4
-        for (int c = part; c < D / 4; c += kPer) {
-            const ulonglong2 kv = k[c];
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < NC; ++i)
+                    acc[r][t][i] = pk2(0.f, 0.f);
+#pragma unroll 2
+        for (int c = part; c < D / 4; c += kParts) {
+            const ulonglong2 ka = k0[c], kb = k1[c];
 #pragma unroll
             for (int r = 0; r < MR; ++r) {
                 const ulonglong2 qv = *reinterpret_cast<const ulonglong2 *>(qs + r * DP + 4 * c);
-                acc[r][0] = fma2(qv.x, kv.x, acc[r][0]);
-                acc[r][1] = fma2(qv.y, kv.y, acc[r][1]);
+                acc[r][0][0] = fma2(qv.x, ka.x, acc[r][0][0]);
+                acc[r][1][0] = fma2(qv.x, kb.x, acc[r][1][0]);
+                acc[r][0][NC - 1] = fma2(qv.y, ka.y, acc[r][0][NC - 1]);
+                acc[r][1][NC - 1] = fma2(qv.y, kb.y, acc[r][1][NC - 1]);
             }
         }
         constexpr uint32_t kAll = kUnit == 16 ? 0xffffu : 0xffffffffu;
         const bool masked = mask != kAll || tok0 < all0 || tok0 + kUnit > all1;
 #pragma unroll
         for (int r = 0; r < MR; ++r) {
-            float v = (lo2(acc[r][0]) + hi2(acc[r][0])) + (lo2(acc[r][1]) + hi2(acc[r][1]));
-            if (kPer == 2)
+            float s0 = lo2(acc[r][0][0]) + hi2(acc[r][0][0]), s1 = lo2(acc[r][1][0]) + hi2(acc[r][1][0]);
+            if (NC == 2) {
+                s0 += lo2(acc[r][0][NC - 1]) + hi2(acc[r][0][NC - 1]);
+                s1 += lo2(acc[r][1][NC - 1]) + hi2(acc[r][1][NC - 1]);
+            }
+            // neighbouring parts exchange: one keeps the first token, one the second
+            float v = (part & 1 ? s1 : s0) + __shfl_xor_sync(0xffffffffu, part & 1 ? s0 : s1, kHalf);
+            if (kParts == 4)
                 v += __shfl_xor_sync(0xffffffffu, v, 16);
             if (masked && (!((mask >> tt) & 1) || tok0 + tt < lo[r] || tok0 + tt >= hi[r]))
                 v = -INFINITY;
@@ -892,8 +907,8 @@ struct Simt {
             const float mn = fmaxf(m[r], top), base = (mn == -INFINITY ? 0.f : mn) * p.f;
             const float keep = exp2_fast(m[r] * p.f - base), e = exp2_fast(v * p.f - base);
             m[r] = mn;
-            l[r] = l[r] * keep + (part == 0 ? e : 0.f);   // summed over the lanes at the end
-            if (part == 0)
+            l[r] = l[r] * keep + (lane < kUnit ? e : 0.f);   // summed over the lanes at the end
+            if (lane < kUnit)
                 ps[r * kUnit + tt] = e;
             if (keep != 1.f) {
                 const f32x2 kk = pk2(keep, keep);
