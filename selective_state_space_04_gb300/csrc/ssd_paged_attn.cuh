@@ -922,38 +922,47 @@ struct Simt {
         __syncwarp();
     }
 
-    __device__ __forceinline__ void values(const AttnParams &p, char *slot, uint32_t mask, int tok0, int all0, int all1, int lane)
+    // RAGGED: some rows do not see all of the tokens; one that a row does not see is
+    // skipped for it (tokens not read are zero in the slot, with weight 0)
+    template <bool RAGGED>
+    __device__ __forceinline__ void add_values(const AttnParams &p, const char *slot, int tok0, int lane)
     {
+        constexpr int kTok = kUnit / kGroups;   // tokens of a half warp, or of the warp
         const int grp = kGroups == 2 ? lane >> 4 : 0, el = 4 * (kGroups == 2 ? lane & 15 : lane), stride = row_bytes(p);
-        // tokens not read are zero in the slot; one that a row does not see is skipped for it
-        const bool ragged = tok0 < all0 || tok0 + kUnit > all1;
-#pragma unroll 2
-        for (int t4 = 0; t4 < kUnit; t4 += 4) {
-            float w[MR][4];
+        const char *v0 = slot + grp * kTok * stride + 4 * el;
+        const float *w0 = ps + grp * kTok;
+#pragma unroll RAGGED ? 1 : 2
+        for (int t4 = 0; t4 < kTok; t4 += 4) {
+            float4 w[MR];
 #pragma unroll
             for (int r = 0; r < MR; ++r)
-                *reinterpret_cast<float4 *>(w[r]) = *reinterpret_cast<const float4 *>(ps + r * kUnit + t4);
+                w[r] = *reinterpret_cast<const float4 *>(w0 + r * kUnit + t4);
 #pragma unroll
-            for (int i = 0; i < 4 / kGroups; ++i) {
-                const int tt = t4 + i * kGroups + grp;
+            for (int i = 0; i < 4; ++i) {
+                const int tok = tok0 + grp * kTok + t4 + i;
 #pragma unroll
                 for (int n = 0; n < NV; ++n) {
-                    const int c = el + 128 * n;
                     ulonglong2 v = make_ulonglong2(0, 0);
-                    if (EX || c < dim(p))
-                        v = *reinterpret_cast<const ulonglong2 *>(slot + tt * stride + 4 * c);
+                    if (EX || el + 128 * n < dim(p))
+                        v = *reinterpret_cast<const ulonglong2 *>(v0 + (t4 + i) * stride + 512 * n);
 #pragma unroll
                     for (int r = 0; r < MR; ++r) {
-                        const float e = kGroups == 2 && grp ? w[r][(kGroups * i + 1) & 3] : w[r][kGroups * i];
-                        if (!ragged || (tok0 + tt >= lo[r] && tok0 + tt < hi[r])) {
-                            const f32x2 ee = pk2(e, e);
-                            o[r][n][0] = fma2(ee, v.x, o[r][n][0]);
-                            o[r][n][1] = fma2(ee, v.y, o[r][n][1]);
+                        const float e = i == 0 ? w[r].x : i == 1 ? w[r].y : i == 2 ? w[r].z : w[r].w;
+                        if (!RAGGED || (tok >= lo[r] && tok < hi[r])) {
+                            o[r][n][0] = fma2(pk2(e, e), v.x, o[r][n][0]);
+                            o[r][n][1] = fma2(pk2(e, e), v.y, o[r][n][1]);
                         }
                     }
                 }
             }
         }
+    }
+    __device__ __forceinline__ void values(const AttnParams &p, char *slot, uint32_t mask, int tok0, int all0, int all1, int lane)
+    {
+        if (tok0 < all0 || tok0 + kUnit > all1)
+            add_values<true>(p, slot, tok0, lane);
+        else
+            add_values<false>(p, slot, tok0, lane);
         __syncwarp();
     }
 
