@@ -81,11 +81,11 @@ struct Tile {
     int first, end, ub, units;
 };
 
+// the extent from the positions of the first and the last row
 template <int UT>
-__device__ __forceinline__ void tile_extent(const AttnParams &p, Tile &t)
+__device__ __forceinline__ void tile_extent(const AttnParams &p, Tile &t, int p0, int p1)
 {
     const int limit = p.a.d.max_pages * p.a.d.page_size;
-    const int p0 = p.a.positions[t.row], p1 = t.nq > 1 ? p.a.positions[t.row + t.nq - 1] : p0;
     t.end = p1 < 0 ? 0 : min(p1, limit - 1) + 1;
     t.first = p.a.d.window > 0 ? max(0, p0 - p.a.d.window + 1) : 0;
     t.first = min(t.first, t.end);
@@ -117,7 +117,8 @@ __device__ __forceinline__ void set_tile(const AttnParams &p, Tile &t, int req, 
         t.nq = 1;
         t.rows_left = 0;
     }
-    tile_extent<UT>(p, t);
+    const int p0 = p.a.positions[t.row];
+    tile_extent<UT>(p, t, p0, t.nq > 1 ? p.a.positions[t.row + t.nq - 1] : p0);
 }
 
 // the next tile (there is one)
@@ -154,6 +155,13 @@ __device__ __forceinline__ void advance(const AttnParams &p, Cursor &c)
     c.lin += c.t.units;
     ++c.tile;
     next_tile<UT>(p, c.t);
+}
+
+// a / b for a >= 0, b > 0: in 32 bits where they fit (a 64-bit division takes some
+// hundred cycles)
+__device__ __forceinline__ long long div_units(long long a, long long b)
+{
+    return ((unsigned long long)a | (unsigned long long)b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
 }
 
 // ---- block scan for the schedule ------------------------------------------
@@ -194,12 +202,71 @@ struct Shares {
     int of_head;            // shares of a head; all shares: of_head * items
 };
 
+// units of a share of `total` when a head has `of_head` of them
+template <bool SOLO>
+__device__ __forceinline__ long long share_units(long long total, int of_head)
+{
+    return max((long long)(SOLO ? 1 : kWarps), div_units(total + of_head - 1, of_head));
+}
+
+constexpr int kFewRows = 128;
+
+// For at most kFewRows rows, one per request: each warp sums all rows' units (four
+// rows a lane) and finds its own share's beginning, without a barrier.
+template <int UT, bool SOLO>
+__device__ __forceinline__ Shares locate_few(const AttnParams &p, int of_head, int j, Cursor &cur)
+{
+    const int lane = threadIdx.x & 31, n = (int)p.a.d.nrows;
+    int pos[4], units[4];
+    long long sum = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        pos[i] = 4 * lane + i < n ? p.a.positions[4 * lane + i] : -1;
+    Tile t{0, 0, 0, 1, 0, 0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        tile_extent<UT>(p, t, pos[i], pos[i]);
+        units[i] = 4 * lane + i < n ? t.units : 0;
+        sum += units[i];
+    }
+    long long inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o)
+            inc += u;
+    }
+    Shares sh;
+    sh.total = __shfl_sync(0xffffffffu, inc, 31);
+    sh.per = share_units<SOLO>(sh.total, of_head);
+    sh.ntiles = n;
+    sh.of_head = of_head;
+    const long long u0 = j * sh.per;
+    // the last lane that begins at or before u0, and the row of its four
+    const int from = 31 - __clz(__ballot_sync(0xffffffffu, inc - sum <= u0));
+    long long lin = inc - sum;
+    int row = 4 * lane, at = pos[0];
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+        if (row == 4 * lane + i && units[i + 1] > 0 && u0 >= lin + units[i]) {
+            lin += units[i];
+            ++row;
+            at = pos[i + 1];
+        }
+    t.req = t.row = cur.tile = __shfl_sync(0xffffffffu, row, from);
+    at = __shfl_sync(0xffffffffu, at, from);
+    cur.lin = __shfl_sync(0xffffffffu, lin, from);
+    tile_extent<UT>(p, t, at, at);
+    cur.t = t;
+    return sh;
+}
+
 // Finds where share j of a head begins (found[i] for warp i's share, or
 // found[0]).  Every CTA sums all tiles' units (a contiguous run of tiles per
 // thread); the thread whose run holds a share's first unit finds its tile.
 // `counts` (shared memory, nreq + 1 ints) is used when there is a start array.
 template <int UT, bool SOLO>
-__device__ Shares locate(const AttnParams &p, int *counts, long long *tmp, Found *found)
+__device__ __forceinline__ Shares locate(const AttnParams &p, int of_head, int *counts, long long *tmp, Found *found)
 {
     const int tid = threadIdx.x, nreq = (int)p.a.d.nreq;
     long long ntiles = p.a.d.nrows;
@@ -256,8 +323,8 @@ __device__ Shares locate(const AttnParams &p, int *counts, long long *tmp, Found
     Shares sh;
     sh.total = sum;
     sh.ntiles = ntiles;
-    sh.of_head = max(1, (int)gridDim.x * kOwn / p.items);
-    sh.per = max((long long)(SOLO ? 1 : kWarps), (sh.total + sh.of_head - 1) / sh.of_head);
+    sh.of_head = of_head;
+    sh.per = share_units<SOLO>(sum, of_head);
     if (t0 < t1) {
         long long lin = before, tile = t0;
         const long long end = before + n;
@@ -515,7 +582,8 @@ struct Mma {
                     for (int y = 0; y < 2; ++y) {
                         const int c = 16 * k + 8 * y + 2 * (lane & 3);
                         uint32_t v = r < rows && c < D ? *reinterpret_cast<const uint32_t *>(src + c) : 0u;
-                        v = (v & keep) ^ flip;
+                        if (p.sign != 1)
+                            v = (v & keep) ^ flip;
                         if constexpr (kQSmem)
                             *reinterpret_cast<uint32_t *>(qs + r * kQStride + c * 2) = v;
                         else
@@ -1095,12 +1163,40 @@ __global__ void __launch_bounds__(kThreads, MB) ssd_paged_attn_kernel(const __gr
     __shared__ Found found[kWarps];
     __shared__ long long tmp[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, D = M::dim(p), stride = M::row_bytes(p);
+    // The shares, as far as sizes tell; and the parameters' cache lines, which cost
+    // some hundred cycles each when first touched: before the wait.
+    constexpr int kOwn = SOLO ? kWarps : 1;
+    const int of_head = max(1, (int)gridDim.x * kOwn / p.items), nshares = of_head * p.items;
+    const int first_share = SOLO ? blockIdx.x * kWarps + w : blockIdx.x;
+    {
+        uint32_t x = 0;
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(AttnParams) / 4; i += 16)
+            x ^= reinterpret_cast<const uint32_t *>(&p)[i];
+        asm volatile("" ::"r"(x));
+    }
+    const int half_bytes = UT * stride;
+    char *ring = smem + (size_t)w * NH * half_bytes;        // [NH][UT][stride]
+    char *middle = smem + L::ring_bytes(stride);
+    char *qs = middle + w * M::kQBytes;
+    float *join = reinterpret_cast<float *>(middle + (M::kQSmem ? 0 : L::kQuery));   // (16-byte accesses up to here)
+    uint64_t *bars = reinterpret_cast<uint64_t *>(middle + L::middle_bytes(D)) + w * NH;
+    float *ml = reinterpret_cast<float *>(bars - w * NH + kWarps * NH);   // [kWarps][MR][2]
+    float *joint = ml + kWarps * M::MR * 2;                               // [MR] maxima, [MR] sums
+    uint32_t *masks = reinterpret_cast<uint32_t *>(joint + M::MR * 2) + w * NH;
+    const int ds = L::join_stride(D);
     // The call's launches are programmatic dependents: each starts while the one
     // before it runs out and waits here for all of it.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    const Shares sh = locate<UT, SOLO>(p, reinterpret_cast<int *>(smem), tmp, found);
+    Shares sh;
+    Cursor cur;
+    const bool few = !p.a.start && p.a.d.nrows <= kFewRows;
+    if (few)
+        sh = locate_few<UT, SOLO>(p, of_head, of_head == 1 ? 0 : first_share / p.items, cur);
+    else
+        sh = locate<UT, SOLO>(p, of_head, reinterpret_cast<int *>(smem), tmp, found);
     // padding rows see nothing
     if (p.a.start) {
         const long long r0 = min((long long)max(p.a.start[p.a.d.nreq], 0), (long long)p.a.d.nrows);
@@ -1116,17 +1212,8 @@ __global__ void __launch_bounds__(kThreads, MB) ssd_paged_attn_kernel(const __gr
     if (!SOLO)   // (there may be fewer tiles than the host could tell)
         for (long long i = sh.ntiles * p.items + blockIdx.x * kThreads + tid; i < p.ndesc; i += gridDim.x * kThreads)
             p.desc[i] = make_int4(-1, 0, 0, 0);
-    const int half_bytes = UT * stride;
-    char *ring = smem + (size_t)w * NH * half_bytes;        // [NH][UT][stride]
-    char *middle = smem + L::ring_bytes(stride);
-    char *qs = middle + w * M::kQBytes;
-    float *join = reinterpret_cast<float *>(middle + (M::kQSmem ? 0 : L::kQuery));   // (16-byte accesses up to here)
-    uint64_t *bars = reinterpret_cast<uint64_t *>(middle + L::middle_bytes(D)) + w * NH;
-    float *ml = reinterpret_cast<float *>(bars - w * NH + kWarps * NH);   // [kWarps][MR][2]
-    float *joint = ml + kWarps * M::MR * 2;                               // [MR] maxima, [MR] sums
-    uint32_t *masks = reinterpret_cast<uint32_t *>(joint + M::MR * 2) + w * NH;
-    const int ds = L::join_stride(D);
-    __syncthreads();   // (the schedule's use of the ring's memory is over)
+    if (!few)
+        __syncthreads();   // (the schedule's use of the ring's memory is over)
     // segments past the head's elements are read by the products: zero once
     if (!M::kExact) {
         for (int i = lane; i < NH * UT; i += 32)
@@ -1149,12 +1236,10 @@ __global__ void __launch_bounds__(kThreads, MB) ssd_paged_attn_kernel(const __gr
     int head = 0, tail = 0;   // slots of the next half to load, to use
     uint32_t parity = 0;
     bool healthy = true;
-    const long long nshares = (long long)sh.of_head * p.items;
     // (one round, but for more heads than there are warps or CTAs)
-    for (long long share = SOLO ? (long long)blockIdx.x * kWarps + w : blockIdx.x; share < nshares;
-         share += (long long)gridDim.x * (SOLO ? kWarps : 1)) {
-    const int item = (int)(share % p.items);
-    const long long u0 = sh.of_head == 1 ? 0 : share / p.items * sh.per, u1 = min(u0 + sh.per, sh.total);
+    for (int share = first_share; share < nshares; share += gridDim.x * kOwn) {
+    const int j = share / p.items, item = share - j * p.items;
+    const long long u0 = of_head == 1 ? 0 : j * sh.per, u1 = min(u0 + sh.per, sh.total);
     if (SOLO && lane == 0)
         p.desc[share] = make_int4(-1, 0, 0, 0);
     if (u0 >= sh.total)
@@ -1162,9 +1247,8 @@ __global__ void __launch_bounds__(kThreads, MB) ssd_paged_attn_kernel(const __gr
     const int kvh = item / p.nhb, hb = item - kvh * p.nhb;
     const int h0 = kvh * p.group + hb * p.gh, nh = min(p.gh, p.group - hb * p.gh);
 
-    Cursor cur;
-    {
-        const Found f = found[SOLO ? w : 0];
+    if (!few || share != first_share) {   // (another round begins where every head does)
+        const Found f = few ? Found{0, 0, 0, 0} : found[SOLO ? w : 0];
         set_tile<UT>(p, cur.t, f.req, f.j);
         cur.tile = f.tile;
         cur.lin = f.lin;
@@ -1206,6 +1290,20 @@ __global__ void __launch_bounds__(kThreads, MB) ssd_paged_attn_kernel(const __gr
         if (!BULK)
             cp_commit();
     };
+    M math;
+    math.qs = reinterpret_cast<decltype(math.qs)>(qs);
+    if constexpr (sizeof(T) == 4)
+        math.ps = math.qs + M::MR * M::kDim;
+    // tokens that every row of the tile sees: from the last row's first to the first row's last
+    int all0, all1;
+    auto begin = [&]() {
+        const int limit = p.a.d.max_pages * p.a.d.page_size;
+        const int p0 = p.a.positions[cur.t.row], p1 = p.a.positions[cur.t.row + cur.t.nq - 1];
+        all1 = p0 < 0 ? 0 : min(p0, limit - 1) + 1;
+        all0 = p.a.d.window > 0 ? max(0, p1 - p.a.d.window + 1) : 0;
+        math.begin(p, cur.t, item, lane);
+    };
+    begin();   // (its loads are on their way beside the first table entry's)
 #pragma unroll 1
     for (int i = 0; i < (NH - 1) / 2; ++i) {
         load_k();
@@ -1214,22 +1312,9 @@ __global__ void __launch_bounds__(kThreads, MB) ssd_paged_attn_kernel(const __gr
     if (NH % 2 == 0)
         load_k();
 
-    M math;
-    math.qs = reinterpret_cast<decltype(math.qs)>(qs);
-    if constexpr (sizeof(T) == 4)
-        math.ps = math.qs + M::MR * M::kDim;
     int u = (int)(u0 - cur.lin);   // first unit of the share in this tile
     while (true) {
         const int ue = (int)min((long long)cur.t.units, u1 - cur.lin);   // the share's units of the tile: [u, ue)
-        // tokens that every row of the tile sees: from the last row's first to the first row's last
-        int all0, all1;
-        {
-            const int limit = p.a.d.max_pages * p.a.d.page_size;
-            const int p0 = p.a.positions[cur.t.row], p1 = p.a.positions[cur.t.row + cur.t.nq - 1];
-            all1 = p0 < 0 ? 0 : min(p0, limit - 1) + 1;
-            all0 = p.a.d.window > 0 ? max(0, p1 - p.a.d.window + 1) : 0;
-        }
-        math.begin(p, cur.t, item, lane);
         const int rows = cur.t.nq * nh;
         // this warp's units: all, or those whose number in the CTA's share is w modulo the warps
         const int skip = SOLO ? 0 : (w - (int)((cur.lin + u - u0) % kWarps) + kWarps) % kWarps;
@@ -1336,11 +1421,12 @@ __global__ void __launch_bounds__(kThreads, MB) ssd_paged_attn_kernel(const __gr
         if (SOLO ? !whole && slot == 1 && lane == 0 : slot == 1 && tid == 0)
             p.desc[SOLO ? share : (long long)cur.tile * p.items + item] =
                 make_int4(whole ? -1 : cur.t.row, cur.t.nq | item << 8, (int)share,
-                          (int)((cur.lin + cur.t.units - 1) / sh.per - (cur.lin + u) / sh.per) + 1);
+                          (int)div_units(cur.lin + cur.t.units - 1 - u0, sh.per) + 1);
         if (cur.lin + ue >= u1)
             break;
         u = 0;
         advance<UT>(p, cur);
+        begin();
     }
     if (!BULK)
         cp_wait<0>();
