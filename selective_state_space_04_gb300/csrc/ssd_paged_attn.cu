@@ -67,10 +67,10 @@ cudaError_t attn_launch(const AttnArgs &a, void *workspace, cudaStream_t stream)
     // scores are kept as q.k times the scale's sign, so that their maximum is that of the scaled ones
     p.sign = a.d.scale > 0.f ? 1 : a.d.scale < 0.f ? -1 : 0;
     p.f = p.sign ? fabsf(a.d.scale) * kLog2e : 1.f;
-    p.page.sh = 31;
-    while ((1u << (p.page.sh - 31)) < (uint32_t)a.d.page_size)
-        ++p.page.sh;
-    p.page.mul = (uint32_t)((1ull << p.page.sh) / (uint32_t)a.d.page_size + 1);
+    p.page = fast_div(a.d.page_size);
+    p.by_items = fast_div(p.items);
+    p.few = !a.start && a.d.nrows <= kFewRows &&
+            a.d.nrows * ((int64_t)a.d.page_size * a.d.max_pages / 16 + 2) < (INT64_C(1) << 31);
     p.sms = sm_count();
     if (a.d.dtype == SSD_DTYPE_F32)
         return attn_launch_f32(p, mr, workspace, stream);

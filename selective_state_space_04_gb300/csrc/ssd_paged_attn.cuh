@@ -54,7 +54,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ int div_page(const FastDiv &f, int n) { return (int)(((uint64_t)(uint32_t)n * f.mul) >> f.sh); }
+__device__ __forceinline__ int div_fast(const FastDiv &f, int n) { return (int)(((uint64_t)(uint32_t)n * f.mul) >> f.sh); }
 
 __device__ __forceinline__ float exp2_fast(float x)
 {
@@ -199,26 +199,15 @@ struct Found {
 struct Shares {
     long long total, per;   // units of a key-value head, and of a share
     long long ntiles;
-    int of_head;            // shares of a head; all shares: of_head * items
 };
-
-// units of a share of `total` when a head has `of_head` of them
-template <bool SOLO>
-__device__ __forceinline__ long long share_units(long long total, int of_head)
-{
-    return max((long long)(SOLO ? 1 : kWarps), div_units(total + of_head - 1, of_head));
-}
-
-constexpr int kFewRows = 128;
 
 // For at most kFewRows rows, one per request: each warp sums all rows' units (four
 // rows a lane) and finds its own share's beginning, without a barrier.
 template <int UT, bool SOLO>
-__device__ __forceinline__ Shares locate_few(const AttnParams &p, int of_head, int j, Cursor &cur)
+__device__ __forceinline__ Shares locate_few(const AttnParams &p, int j, Cursor &cur)
 {
     const int lane = threadIdx.x & 31, n = (int)p.a.d.nrows;
-    int pos[4], units[4];
-    long long sum = 0;
+    int pos[4], units[4], sum = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         pos[i] = 4 * lane + i < n ? p.a.positions[4 * lane + i] : -1;
@@ -229,23 +218,20 @@ __device__ __forceinline__ Shares locate_few(const AttnParams &p, int of_head, i
         units[i] = 4 * lane + i < n ? t.units : 0;
         sum += units[i];
     }
-    long long inc = sum;
+    int inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, inc, o);
+        const int u = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o)
             inc += u;
     }
-    Shares sh;
-    sh.total = __shfl_sync(0xffffffffu, inc, 31);
-    sh.per = share_units<SOLO>(sh.total, of_head);
-    sh.ntiles = n;
-    sh.of_head = of_head;
-    const long long u0 = j * sh.per;
+    const int total = __shfl_sync(0xffffffffu, inc, 31);
+    const int per = max(SOLO ? 1 : kWarps, (int)(((unsigned)total + p.of_head - 1) / (unsigned)p.of_head));
+    const Shares sh{total, per, n};
+    const int u0 = (int)min((long long)j * per, (long long)total);   // (total: the share is empty)
     // the last lane that begins at or before u0, and the row of its four
     const int from = 31 - __clz(__ballot_sync(0xffffffffu, inc - sum <= u0));
-    long long lin = inc - sum;
-    int row = 4 * lane, at = pos[0];
+    int lin = inc - sum, row = 4 * lane, at = pos[0];
 #pragma unroll
     for (int i = 0; i < 3; ++i)
         if (row == 4 * lane + i && units[i + 1] > 0 && u0 >= lin + units[i]) {
@@ -266,7 +252,7 @@ __device__ __forceinline__ Shares locate_few(const AttnParams &p, int of_head, i
 // thread); the thread whose run holds a share's first unit finds its tile.
 // `counts` (shared memory, nreq + 1 ints) is used when there is a start array.
 template <int UT, bool SOLO>
-__device__ __forceinline__ Shares locate(const AttnParams &p, int of_head, int *counts, long long *tmp, Found *found)
+__device__ __forceinline__ Shares locate(const AttnParams &p, int *counts, long long *tmp, Found *found)
 {
     const int tid = threadIdx.x, nreq = (int)p.a.d.nreq;
     long long ntiles = p.a.d.nrows;
@@ -323,15 +309,14 @@ __device__ __forceinline__ Shares locate(const AttnParams &p, int of_head, int *
     Shares sh;
     sh.total = sum;
     sh.ntiles = ntiles;
-    sh.of_head = of_head;
-    sh.per = share_units<SOLO>(sum, of_head);
+    sh.per = max((long long)(SOLO ? 1 : kWarps), div_units(sum + p.of_head - 1, p.of_head));
     if (t0 < t1) {
         long long lin = before, tile = t0;
         const long long end = before + n;
         bool at_start = false;
         for (int i = 0; i < kOwn; ++i) {
             // (more heads than CTAs' shares: one share per head, from the first unit on)
-            const int share = blockIdx.x * kOwn + i, j = sh.of_head == 1 ? 0 : share / p.items;
+            const int share = blockIdx.x * kOwn + i, j = p.of_head == 1 ? 0 : div_fast(p.by_items, share);
             const long long u0 = j * sh.per;
             if (u0 < before || u0 >= end)
                 continue;
@@ -410,7 +395,7 @@ struct Loader {
         if (u >= 0) {
             const int tok = (c.t.ub + u) * UT + (BULK ? lane % UT : kSub > 1 ? lane & 16 : 0);
             if (tok < c.t.end)   // (16 tokens are in the page of the first of them)
-                page = __ldg(table + div_page(p.page, tok));
+                page = __ldg(table + div_fast(p.page, tok));
         }
     }
     __device__ __forceinline__ void offsets(const AttnParams &p, int lane)
@@ -425,7 +410,7 @@ struct Loader {
             // (an entry out of range masks its tokens: nothing is read at its offset)
             const uint32_t pg = (uint32_t)max(!BULK && kSub > 1 ? __shfl_sync(0xffffffffu, page, 16 * b) : page, 0);
             const int at = BULK ? tok : tok0 + 16 * b;
-            const uint32_t off = at - div_page(p.page, at) * p.a.d.page_size;
+            const uint32_t off = at - div_fast(p.page, at) * p.a.d.page_size;
             koff[b] = (uint64_t)pg * p.kpage + (uint64_t)off * p.ktok;
             voff[b] = (uint64_t)pg * p.vpage + (uint64_t)off * p.vtok;
         }
@@ -560,7 +545,7 @@ struct Mma {
 
     __device__ __forceinline__ void begin(const AttnParams &p, const Tile &t, int item, int lane)
     {
-        const int kvh = item / p.nhb, hb = item - kvh * p.nhb, D = dim(p);
+        const int kvh = p.nhb == 1 ? item : item / p.nhb, hb = item - kvh * p.nhb, D = dim(p);
         const int h0 = hb * p.gh, nh = min(p.gh, p.group - h0), rows = t.nq * nh;
         const int limit = p.a.d.max_pages * p.a.d.page_size;
         const uint32_t keep = p.sign == 0 ? 0u : 0xffffffffu, flip = p.sign < 0 ? 0x80008000u : 0u;
@@ -568,7 +553,7 @@ struct Mma {
         for (int mt = 0; mt < NM; ++mt)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                const int r = mt * 16 + x * 8 + (lane >> 2), rr = min(r, rows - 1), j = rr / nh, g = rr - j * nh;
+                const int r = mt * 16 + x * 8 + (lane >> 2), rr = min(r, rows - 1), j = t.nq == 1 ? 0 : rr / nh, g = rr - j * nh;
                 const int pos = p.a.positions[t.row + j];
                 hi[mt][x] = pos < 0 ? 0 : min(pos, limit - 1) + 1;
                 lo[mt][x] = p.a.d.window > 0 ? max(0, pos - p.a.d.window + 1) : 0;
@@ -899,12 +884,12 @@ struct Simt {
 
     __device__ __forceinline__ void begin(const AttnParams &p, const Tile &t, int item, int lane)
     {
-        const int kvh = item / p.nhb, hb = item - kvh * p.nhb, D = dim(p);
+        const int kvh = p.nhb == 1 ? item : item / p.nhb, hb = item - kvh * p.nhb, D = dim(p);
         const int h0 = hb * p.gh, nh = min(p.gh, p.group - h0), rows = t.nq * nh;
         const int limit = p.a.d.max_pages * p.a.d.page_size;
 #pragma unroll
         for (int r = 0; r < MR; ++r) {
-            const int rr = min(r, rows - 1), j = rr / nh, g = rr - j * nh;
+            const int rr = min(r, rows - 1), j = t.nq == 1 ? 0 : rr / nh, g = rr - j * nh;
             const int pos = p.a.positions[t.row + j];
             hi[r] = pos < 0 ? 0 : min(pos, limit - 1) + 1;
             lo[r] = p.a.d.window > 0 ? max(0, pos - p.a.d.window + 1) : 0;
@@ -1163,11 +1148,10 @@ __global__ void __launch_bounds__(kThreads, MB) ssd_paged_attn_kernel(const __gr
     __shared__ Found found[kWarps];
     __shared__ long long tmp[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, D = M::dim(p), stride = M::row_bytes(p);
-    // The shares, as far as sizes tell; and the parameters' cache lines, which cost
-    // some hundred cycles each when first touched: before the wait.
-    constexpr int kOwn = SOLO ? kWarps : 1;
-    const int of_head = max(1, (int)gridDim.x * kOwn / p.items), nshares = of_head * p.items;
+    constexpr int kOwn = SOLO ? kWarps : 1;   // shares of a CTA at a time
     const int first_share = SOLO ? blockIdx.x * kWarps + w : blockIdx.x;
+    // The parameters' cache lines cost some hundred cycles each when first
+    // touched: before the wait.
     {
         uint32_t x = 0;
 #pragma unroll
@@ -1192,11 +1176,11 @@ __global__ void __launch_bounds__(kThreads, MB) ssd_paged_attn_kernel(const __gr
 
     Shares sh;
     Cursor cur;
-    const bool few = !p.a.start && p.a.d.nrows <= kFewRows;
+    const bool few = p.few;
     if (few)
-        sh = locate_few<UT, SOLO>(p, of_head, of_head == 1 ? 0 : first_share / p.items, cur);
+        sh = locate_few<UT, SOLO>(p, p.of_head == 1 ? 0 : div_fast(p.by_items, first_share), cur);
     else
-        sh = locate<UT, SOLO>(p, of_head, reinterpret_cast<int *>(smem), tmp, found);
+        sh = locate<UT, SOLO>(p, reinterpret_cast<int *>(smem), tmp, found);
     // padding rows see nothing
     if (p.a.start) {
         const long long r0 = min((long long)max(p.a.start[p.a.d.nreq], 0), (long long)p.a.d.nrows);
@@ -1208,10 +1192,10 @@ __global__ void __launch_bounds__(kThreads, MB) ssd_paged_attn_kernel(const __gr
             if (p.a.lse && tid == 0)
                 p.a.lse[i] = -INFINITY;
         }
+        if (!SOLO)   // (there may be fewer tiles than the host could tell)
+            for (long long i = sh.ntiles * p.items + blockIdx.x * kThreads + tid; i < p.ndesc; i += gridDim.x * kThreads)
+                p.desc[i] = make_int4(-1, 0, 0, 0);
     }
-    if (!SOLO)   // (there may be fewer tiles than the host could tell)
-        for (long long i = sh.ntiles * p.items + blockIdx.x * kThreads + tid; i < p.ndesc; i += gridDim.x * kThreads)
-            p.desc[i] = make_int4(-1, 0, 0, 0);
     if (!few)
         __syncthreads();   // (the schedule's use of the ring's memory is over)
     // segments past the head's elements are read by the products: zero once
@@ -1237,14 +1221,14 @@ __global__ void __launch_bounds__(kThreads, MB) ssd_paged_attn_kernel(const __gr
     uint32_t parity = 0;
     bool healthy = true;
     // (one round, but for more heads than there are warps or CTAs)
-    for (int share = first_share; share < nshares; share += gridDim.x * kOwn) {
-    const int j = share / p.items, item = share - j * p.items;
-    const long long u0 = of_head == 1 ? 0 : j * sh.per, u1 = min(u0 + sh.per, sh.total);
+    for (int share = first_share; share < p.nshares; share += gridDim.x * kOwn) {
+    const int j = div_fast(p.by_items, share), item = share - j * p.items;
+    const long long u0 = p.of_head == 1 ? 0 : j * sh.per, u1 = min(u0 + sh.per, sh.total);
     if (SOLO && lane == 0)
         p.desc[share] = make_int4(-1, 0, 0, 0);
     if (u0 >= sh.total)
         break;
-    const int kvh = item / p.nhb, hb = item - kvh * p.nhb;
+    const int kvh = p.nhb == 1 ? item : item / p.nhb, hb = item - kvh * p.nhb;
     const int h0 = kvh * p.group + hb * p.gh, nh = min(p.gh, p.group - hb * p.gh);
 
     if (!few || share != first_share) {   // (another round begins where every head does)
@@ -1442,7 +1426,7 @@ template <typename T, int MR, int NW>
 __device__ __forceinline__ void join_row(const AttnParams &p, const int4 &d, int r, int w, int lane, float (*sm)[2], float (*so)[256])
 {
     const int row = d.x, item = d.y >> 8, n = d.w, D = p.a.d.headdim;
-    const int kvh = item / p.nhb, hb = item - kvh * p.nhb, nh = min(p.gh, p.group - hb * p.gh);
+    const int kvh = p.nhb == 1 ? item : item / p.nhb, hb = item - kvh * p.nhb, nh = min(p.gh, p.group - hb * p.gh);
     float mm = -INFINITY, ll = 0.f, o[2][4] = {};
     // part i lies in the head's i-th share from d.z on: slot 1 of the first, slot 0 of the others
     for (int i = w; i < n; i += 4 * NW) {
@@ -1498,7 +1482,7 @@ __device__ __forceinline__ void join_row(const AttnParams &p, const int4 &d, int
         }
         __syncthreads();
         if (w != 0)
-            return;
+            return;   // (the row is the first warp's)
         float top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < NW; ++i)
@@ -1525,7 +1509,7 @@ __device__ __forceinline__ void join_row(const AttnParams &p, const int4 &d, int
         }
     }
     const float inv = ll == 0.f ? 0.f : 1.f / ll;
-    const int j = r / nh, h = kvh * p.group + hb * p.gh + (r - j * nh);
+    const int j = (d.y & 0xff) == 1 ? 0 : r / nh, h = kvh * p.group + hb * p.gh + (r - j * nh);
     T *out = static_cast<T *>(p.a.out) + (long long)(row + j) * p.a.d.o_stride[0] + (long long)h * p.a.d.o_stride[1];
 #pragma unroll
     for (int x = 0; x < 2; ++x)
@@ -1537,7 +1521,7 @@ __device__ __forceinline__ void join_row(const AttnParams &p, const int4 &d, int
 
 __device__ __forceinline__ int desc_rows(const AttnParams &p, const int4 &d)
 {
-    const int hb = (d.y >> 8) % p.nhb;
+    const int hb = p.nhb == 1 ? 0 : (d.y >> 8) % p.nhb;
     return d.x < 0 ? 0 : (d.y & 0xff) * min(p.gh, p.group - hb * p.gh);
 }
 
@@ -1549,7 +1533,7 @@ template <typename T, int MR, bool SOLO>
 __global__ void __launch_bounds__(32 * kJoinWarps) ssd_paged_attn_join_kernel(const __grid_constant__ AttnParams p)
 {
     __shared__ float sm[kJoinWarps][2];
-    __shared__ __align__(16) float so[SOLO ? 1 : kJoinWarps][256];
+    __shared__ __align__(16) float so[kJoinWarps][256];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -1560,13 +1544,22 @@ __global__ void __launch_bounds__(32 * kJoinWarps) ssd_paged_attn_join_kernel(co
             const int i = blockIdx.x * kWarps + k;
             d[k] = i < p.ndesc ? p.desc[i] : make_int4(-1, 0, 0, 0);
         }
-        int at = w;   // rows of all four, dealt to the warps
+        int at = w;   // rows of all four, dealt to the warps; those of many parts are left to all of them
 #pragma unroll
         for (int k = 0; k < kWarps; ++k) {
-            const int rows = desc_rows(p, d[k]);
+            const int rows = d[k].w > 16 ? 0 : desc_rows(p, d[k]);
             for (; at < rows; at += kJoinWarps)
                 join_row<T, MR, 1>(p, d[k], at, 0, lane, sm, so);
             at -= rows;
+        }
+#pragma unroll 1
+        for (int k = 0; k < kWarps; ++k) {
+            const int4 t = k == 0 ? d[0] : k == 1 ? d[1] : k == 2 ? d[2] : d[3];
+            const int rows = t.w > 16 ? desc_rows(p, t) : 0;
+            for (int r = 0; r < rows; ++r) {
+                join_row<T, MR, kJoinWarps>(p, t, r, w, lane, sm, so);
+                __syncthreads();   // (the next row's sums go where these are)
+            }
         }
     } else {
         const int4 d = p.desc[blockIdx.x];
@@ -1602,7 +1595,9 @@ cudaError_t launch(AttnParams &p, void *workspace, cudaStream_t stream)
     const int per_sm = std::max(1, std::min({kMaxPerSm, (228 << 10) / (smem + 1024 + 256), 65536 / (r * kThreads)}));
     const int grid = std::min(kMaxCtas, p.sms * per_sm);
     const int own = grid * (SOLO ? kWarps : 1);
-    const size_t shares = (size_t)std::max(1, own / p.items) * p.items;
+    p.of_head = std::max(1, own / p.items);
+    p.nshares = p.of_head * p.items;
+    const size_t shares = (size_t)p.nshares;
     p.part_o = static_cast<float *>(workspace);
     p.part_ml = p.part_o + shares * 2 * M::MR * D;
     p.desc = reinterpret_cast<int4 *>(p.part_ml + shares * 2 * M::MR * 2);

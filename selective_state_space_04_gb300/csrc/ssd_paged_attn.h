@@ -22,6 +22,10 @@ struct AttnParams {
     int4 *desc;         // the cut tiles: first row, tokens | item << 8, first share, parts; x -1: none.  Shares of
                         // warps: [shares], of the tile that starts in a share; shares of CTAs: [most tiles x items]
     int ndesc;          // entries of it
+    int of_head;        // shares of a key-value head (and head block)
+    int nshares;        // of_head * items
+    int few;            // at most kFewRows rows, one per request, whose units fit 32 bits
+    FastDiv by_items;
     int group;          // query heads per key-value head
     int gh;             // query heads of a tile (group, or a part of it when it is larger than MR)
     int nhb;            // head blocks per key-value head
@@ -35,6 +39,17 @@ struct AttnParams {
     int sign;           // of scale
     int sms;            // the device's SMs
 };
+
+constexpr int kFewRows = 128;
+
+inline FastDiv fast_div(int d)
+{
+    FastDiv f{0, 31};
+    while ((1u << (f.sh - 31)) < (uint32_t)d)
+        ++f.sh;
+    f.mul = (uint32_t)((1ull << f.sh) / (uint32_t)d + 1);
+    return f;
+}
 
 // tiles that the sizes allow at most (one per row, or per `tok` rows of a request)
 inline long long most_tiles(const AttnParams &p)

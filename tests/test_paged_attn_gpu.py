@@ -121,6 +121,26 @@ def test_one_token_each(ssd, dtype, lens, H, hk, D, ps, layout):
 
 
 @pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("lens,H,hk,D,ps", [
+    ([30000] + [3] * 160, 4, 2, 64, 16),      # one long request among many short ones: cut into many parts
+    ([20] * 150 + [9000, 1] + [33] * 9, 8, 4, 128, 24),
+    ([300, 41], 1300, 1300, 8, 16),           # more heads than the GPU has warps
+    ([90, 17, 5], 700, 350, 64, 16),
+    ([2, 40, 18] * 70, 32, 1, 128, 16),
+])
+def test_uneven_work(ssd, dtype, lens, H, hk, D, ps):
+    c = make(27, lens, None, H, hk, D, ps, dtype)
+    check(*run(ssd, c), c)
+
+
+@pytest.mark.parametrize("scale", [-0.7, 0.0, 1e-3])
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_any_scale(ssd, dtype, scale):
+    c = make(28, [50, 200], None, 4, 2, 64, 16, dtype)
+    check(*run(ssd, c, scale=scale), c, scale=scale)
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
 @pytest.mark.parametrize("lens,new,H,hk,D,ps", [
     ([40, 9, 300], [4, 9, 1], 8, 2, 128, 16),
     ([40, 9, 300, 17], [0, 5, 0, 17], 6, 2, 64, 8),     # requests that bring nothing; whole prompts
