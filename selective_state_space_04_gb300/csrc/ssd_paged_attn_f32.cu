@@ -1,12 +1,6 @@
 // ssd_paged_attn_f32.cu -- paged attention: fp32.
 #include "ssd_paged_attn.cuh"
 
-#ifndef F128
-#define F128 3
-#define F128S 2
-#define F64 2
-#define F64S 2
-#endif
 namespace ssd {
 namespace {
 
@@ -15,9 +9,9 @@ cudaError_t launch_rows(AttnParams &p, void *ws, cudaStream_t st)
 {
     const int D = p.a.d.headdim;
     if (D <= 64)
-        return launch_shares<Simt<MR, 64, false>, F64, F64S, 2, true>(p, ws, st);
+        return launch_shares<Simt<MR, 64, false>, 2, 2, 2, true>(p, ws, st);
     if (D <= 128)
-        return launch_shares<Simt<MR, 128, false>, MR == 8 ? 2 : F128, F128S, 2, true>(p, ws, st);
+        return launch_shares<Simt<MR, 128, false>, MR == 8 ? 2 : 3, 2, 2, true>(p, ws, st);
     return launch_shares<Simt<MR, 256, false>, 2, 2, 1, true>(p, ws, st);
 }
 
