@@ -1220,18 +1220,18 @@ __global__ void __launch_bounds__(kThreads, MB) ssd_paged_attn_kernel(const __gr
     int head = 0, tail = 0;   // slots of the next half to load, to use
     uint32_t parity = 0;
     bool healthy = true;
-    // (one round, but for more heads than there are warps or CTAs)
+    // (one share each, but for more heads than there are warps or CTAs)
     for (int share = first_share; share < p.nshares; share += gridDim.x * kOwn) {
     const int j = div_fast(p.by_items, share), item = share - j * p.items;
     const long long u0 = p.of_head == 1 ? 0 : j * sh.per, u1 = min(u0 + sh.per, sh.total);
     if (SOLO && lane == 0)
         p.desc[share] = make_int4(-1, 0, 0, 0);
-    if (u0 >= sh.total)
-        break;
+    if (u0 >= sh.total)   // (empty)
+        continue;
     const int kvh = p.nhb == 1 ? item : item / p.nhb, hb = item - kvh * p.nhb;
     const int h0 = kvh * p.group + hb * p.gh, nh = min(p.gh, p.group - hb * p.gh);
 
-    if (!few || share != first_share) {   // (another round begins where every head does)
+    if (!few || share != first_share) {   // (a further share begins where its head does)
         const Found f = few ? Found{0, 0, 0, 0} : found[SOLO ? w : 0];
         set_tile<UT>(p, cur.t, f.req, f.j);
         cur.tile = f.tile;
@@ -1402,10 +1402,10 @@ __global__ void __launch_bounds__(kThreads, MB) ssd_paged_attn_kernel(const __gr
                 __syncthreads();   // (the next tile's query rows go where the buffers are)
         }
         // where the parts of a cut tile are: this share and the head's next ones
-        if (SOLO ? !whole && slot == 1 && lane == 0 : slot == 1 && tid == 0)
-            p.desc[SOLO ? share : (long long)cur.tile * p.items + item] =
-                make_int4(whole ? -1 : cur.t.row, cur.t.nq | item << 8, (int)share,
-                          (int)div_units(cur.lin + cur.t.units - 1 - u0, sh.per) + 1);
+        const long long at = SOLO ? share : (long long)cur.tile * p.items + item;
+        if ((SOLO ? !whole && slot == 1 && lane == 0 : slot == 1 && tid == 0) && at < p.ndesc)   // (a start array that descends has more tiles)
+            p.desc[at] = make_int4(whole ? -1 : cur.t.row, cur.t.nq | item << 8, (int)share,
+                                   (int)div_units(cur.lin + cur.t.units - 1 - u0, sh.per) + 1);
         if (cur.lin + ue >= u1)
             break;
         u = 0;

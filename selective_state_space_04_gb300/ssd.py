@@ -689,8 +689,7 @@ def qk_norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_o
         dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
     if dk is None:
         dk = torch.empty(k.shape, dtype=q.dtype, device=dev)
-    dw = torch.empty((2, (D + 3) // 4 * 4), dtype=torch.float32, device=dev)
-    dqw, dkw = dw[0, :D], dw[1, :D]
+    dqw, dkw = torch.empty(D, dtype=torch.float32, device=dev), torch.empty(D, dtype=torch.float32, device=dev)
     ws, nws = _workspace(workspace)
     _check(_lib.ssd_qk_norm_rope_bwd(q.data_ptr(), k.data_ptr(), _addr(q_weight), _addr(k_weight), cos.data_ptr(),
                                      sin.data_ptr(), positions.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(),

@@ -184,5 +184,16 @@ def test_attn_pointer_refusals(ssd, ptrs, status):
     assert attn(ssd, ptrs) == status
 
 
+@pytest.mark.parametrize("name", ["kc_stride", "vc_stride"])
+def test_attn_page_and_token_strides_have_a_limit(ssd, name):
+    big = 2 ** 35   # bf16: 2^32 times 16 bytes
+    assert attn(ssd, **{name: (big, 128, 64)}) == UNSUPPORTED
+    assert attn(ssd, **{name: (128, big, 64)}) == UNSUPPORTED
+
+
+def test_qk_rows_have_a_limit(ssd):
+    assert qk(ssd, ntokens=2 ** 30 // 4, nheads_q=8) == UNSUPPORTED
+
+
 def test_attn_rows_without_start_are_requests(ssd):
     assert attn(ssd, dict(start=None)) == INVALID

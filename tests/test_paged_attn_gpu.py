@@ -177,6 +177,17 @@ def test_rows_that_see_nothing(ssd, dtype):
     check(out, lse, c)
 
 
+def test_padding_only_with_more_heads_than_warps(ssd):
+    # a step without tokens leaves every share empty, those after a warp's first one too: nothing of a used workspace
+    # may be taken for parts (here: one part, of row 1, in each entry)
+    c = make(29, [20, 30], [0, 0], 1300, 1300, 8, 16, BF)
+    c = dict(c, q=torch.ones(3, 1300, 8, dtype=BF), pos=torch.full((3,), 7, dtype=torch.int32))
+    g = {k: to_gpu(c[k]) for k in ("q", "kc", "vc", "table")}
+    ws = torch.ones(ssd.paged_attn_workspace_size(*g.values()) // 4, dtype=torch.int32, device="cuda")
+    out, lse = run(ssd, c, workspace=ws)
+    assert (out == 0).all() and torch.isneginf(lse).all()
+
+
 def test_no_rows_and_no_requests(ssd):
     c = make(16, [8], None, 4, 2, 64, 16, BF)
     out, lse = ssd.paged_attn_fwd(torch.empty(0, 4, 64, dtype=BF, device="cuda"), to_gpu(c["kc"]), to_gpu(c["vc"]),
