@@ -861,16 +861,14 @@ ssd_status_t ssd_get_device_error(void *stream, uint32_t *code)
     const ssd_status_t s = chunk_read_device_error(static_cast<cudaStream_t>(stream), code);
     if (s != SSD_OK)
         return s;
-    uint32_t bwd = 0, cplx = 0, attn = 0;   // the backward's, the complex chunk form's and the attention's kernels keep their own words
+    uint32_t bwd = 0, cplx = 0;   // the backward's and the complex chunk form's kernels keep their own words
     ssd_status_t s2 = bwd_tc_read_device_error(&bwd);
     if (s2 == SSD_OK)
         s2 = complex_tc_read_device_error(&cplx);
-    if (s2 == SSD_OK)
-        s2 = attn_read_device_error(&attn);
     if (s2 != SSD_OK)
         return s2;
     if (*code == 0)
-        *code = bwd ? bwd : cplx ? cplx : attn;
+        *code = bwd ? bwd : cplx;
     return SSD_OK;
 }
 

@@ -253,7 +253,6 @@ struct AttnArgs {
 };
 size_t attn_workspace_bytes(const ssd_attn_dims_t &d);
 cudaError_t attn_launch(const AttnArgs &a, void *workspace, cudaStream_t stream);
-ssd_status_t attn_read_device_error(uint32_t *code);
 
 // launch accounting
 void note_launches(int n);

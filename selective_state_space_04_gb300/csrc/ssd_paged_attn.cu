@@ -61,30 +61,19 @@ cudaError_t attn_launch(const AttnArgs &a, void *workspace, cudaStream_t stream)
     p.vtok = (uint32_t)(used(a.d.page_size, a.d.vc_stride[1]) * es / 16);
     p.khead = used(a.d.nkv, a.d.kc_stride[2]) * es;
     p.vhead = used(a.d.nkv, a.d.vc_stride[2]) * es;
-    // rows of an odd number of 16-byte segments: eight rows' segments lie in different banks
-    const int seg = es == 2 ? (p.seg + 1) / 2 * 2 : p.seg;
-    p.stride = (seg | 1) * 16;
     // scores are kept as q.k times the scale's sign, so that their maximum is that of the scaled ones
     p.sign = a.d.scale > 0.f ? 1 : a.d.scale < 0.f ? -1 : 0;
     p.f = p.sign ? fabsf(a.d.scale) * kLog2e : 1.f;
     p.page = fast_div(a.d.page_size);
     p.by_items = fast_div(p.items);
-    p.few = !a.start && a.d.nrows <= kFewRows &&
-            a.d.nrows * ((int64_t)a.d.page_size * a.d.max_pages / 16 + 2) < (INT64_C(1) << 31);
+    p.by_tok = fast_div(p.tok);
+    p.few = most_tiles(p) <= kFewTiles && a.d.nreq <= kFewTiles &&
+            kFewTiles * ((int64_t)a.d.page_size * a.d.max_pages / 16 + 8) < (INT64_C(1) << 31);
     p.sms = sm_count();
     if (a.d.dtype == SSD_DTYPE_F32)
         return attn_launch_f32(p, mr, workspace, stream);
     const bool sized = a.d.page_size % 16 == 0 && (D == 64 || D == 128 || D == 256);
     return sized ? attn_launch_bf16(p, mr, workspace, stream) : attn_launch_bf16_any(p, mr, workspace, stream);
-}
-
-ssd_status_t attn_read_device_error(uint32_t *code)
-{
-    uint32_t b = 0, f = 0;
-    if (attn_bf16_any_error(&b) != cudaSuccess || attn_f32_error(&f) != cudaSuccess)
-        return SSD_ERR_CUDA;
-    *code = b ? b : f;
-    return SSD_OK;
 }
 
 }  // namespace ssd

@@ -199,50 +199,115 @@ struct Found {
 struct Shares {
     long long total, per;   // units of a key-value head, and of a share
     long long ntiles;
+    bool chunks;            // a share is at most `per` units of one tile, whose next one begins with the next share
 };
 
-// For at most kFewRows rows, one per request: each warp sums all rows' units (four
-// rows a lane) and finds its own share's beginning, without a barrier.
+// For at most kFewTiles tiles: each warp sums all tiles' units (four tiles a lane)
+// and finds its own share's beginning, without a barrier.  `list` (shared memory
+// of the warp, kFewTiles entries) is used when there is a start array.
 template <int UT, bool SOLO>
-__device__ __forceinline__ Shares locate_few(const AttnParams &p, int j, Cursor &cur)
+__device__ __forceinline__ Shares locate_few(const AttnParams &p, int j, Cursor &cur, int4 *list)
 {
-    const int lane = threadIdx.x & 31, n = (int)p.a.d.nrows;
-    int pos[4], units[4], sum = 0;
+    const int lane = threadIdx.x & 31;
+    int n = (int)p.a.d.nrows;
+    if (p.a.start) {   // first row, tokens, tile of the request and its rows left | request, of each tile
+        int s[4], e[4], cnt[4], mine = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        pos[i] = 4 * lane + i < n ? p.a.positions[4 * lane + i] : -1;
+        for (int i = 0; i < 4; ++i) {
+            s[i] = e[i] = 0;
+            if (4 * lane + i < (int)p.a.d.nreq)
+                request_rows(p, 4 * lane + i, s[i], e[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            mine += cnt[i] = div_fast(p.by_tok, e[i] - s[i] + p.tok - 1);
+        int at = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, at, o);
+            if (lane >= o)
+                at += u;
+        }
+        n = min(__shfl_sync(0xffffffffu, at, 31), kFewTiles);
+        at -= mine;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            for (int k = 0; k < cnt[i] && at < kFewTiles; ++k, ++at) {
+                const int row = s[i] + k * p.tok, nq = min(p.tok, e[i] - row);
+                list[at] = make_int4(row, nq | (4 * lane + i) << 8, k, e[i] - row - nq);
+            }
+        __syncwarp();
+    }
+    int pos[4], last[4], units[4], sum = 0, padded = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        pos[i] = last[i] = -1;
+        const int tile = 4 * lane + i;
+        if (tile < n) {
+            const int4 d = p.a.start ? list[tile] : make_int4(tile, 1, 0, 0);
+            pos[i] = last[i] = p.a.positions[d.x];
+            if ((d.y & 0xff) > 1)
+                last[i] = p.a.positions[d.x + (d.y & 0xff) - 1];
+        }
+    }
     Tile t{0, 0, 0, 1, 0, 0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        tile_extent<UT>(p, t, pos[i], pos[i]);
+        tile_extent<UT>(p, t, pos[i], last[i]);
         units[i] = 4 * lane + i < n ? t.units : 0;
         sum += units[i];
+        padded += (units[i] + kWarps - 1) / kWarps * kWarps;
     }
-    int inc = sum;
+    int inc = sum, incp = padded = min(padded, 1 << 20);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o)
+        const int u = __shfl_up_sync(0xffffffffu, inc, o), v = SOLO ? 0 : __shfl_up_sync(0xffffffffu, incp, o);
+        if (lane >= o) {
             inc += u;
+            incp += v;
+        }
     }
-    const int total = __shfl_sync(0xffffffffu, inc, 31);
+    int total = __shfl_sync(0xffffffffu, inc, 31);
+    // So little work that each CTA can have at most a unit per warp, of one tile
+    // (two tiles of a CTA would be one after the other): tiles begin with shares.
+    const int whole = SOLO ? 0 : __shfl_sync(0xffffffffu, incp, 31);
+    const bool chunks = !SOLO && whole <= p.of_head * kWarps;
+    if (chunks) {
+        total = whole;
+        sum = padded;
+        inc = incp;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            units[i] = (units[i] + kWarps - 1) / kWarps * kWarps;
+    }
     const int per = max(SOLO ? 1 : kWarps, (int)(((unsigned)total + p.of_head - 1) / (unsigned)p.of_head));
-    const Shares sh{total, per, n};
+    const Shares sh{total, per, n, chunks};
     const int u0 = (int)min((long long)j * per, (long long)total);   // (total: the share is empty)
     // the last lane that begins at or before u0, and the row of its four
     const int from = 31 - __clz(__ballot_sync(0xffffffffu, inc - sum <= u0));
-    int lin = inc - sum, row = 4 * lane, at = pos[0];
+    int lin = inc - sum, tile = 4 * lane, p0 = pos[0], p1 = last[0];
 #pragma unroll
     for (int i = 0; i < 3; ++i)
-        if (row == 4 * lane + i && units[i + 1] > 0 && u0 >= lin + units[i]) {
+        if (tile == 4 * lane + i && units[i + 1] > 0 && u0 >= lin + units[i]) {
             lin += units[i];
-            ++row;
-            at = pos[i + 1];
+            ++tile;
+            p0 = pos[i + 1];
+            p1 = last[i + 1];
         }
-    t.req = t.row = cur.tile = __shfl_sync(0xffffffffu, row, from);
-    at = __shfl_sync(0xffffffffu, at, from);
+    t.req = t.row = cur.tile = __shfl_sync(0xffffffffu, tile, from);
+    p0 = __shfl_sync(0xffffffffu, p0, from);
+    p1 = __shfl_sync(0xffffffffu, p1, from);
     cur.lin = __shfl_sync(0xffffffffu, lin, from);
-    tile_extent<UT>(p, t, at, at);
+    if (p.a.start) {
+        const int4 d = list[cur.tile];
+        t.row = d.x;
+        t.nq = d.y & 0xff;
+        t.req = d.y >> 8;
+        t.j = d.z;
+        t.rows_left = d.w;
+        __syncwarp();   // (the list's memory is the ring's)
+    }
+    tile_extent<UT>(p, t, p0, p1);
     cur.t = t;
     return sh;
 }
@@ -309,6 +374,7 @@ __device__ __forceinline__ Shares locate(const AttnParams &p, int *counts, long 
     Shares sh;
     sh.total = sum;
     sh.ntiles = ntiles;
+    sh.chunks = false;
     sh.per = max((long long)(SOLO ? 1 : kWarps), div_units(sum + p.of_head - 1, p.of_head));
     if (t0 < t1) {
         long long lin = before, tile = t0;
@@ -341,12 +407,17 @@ __device__ __forceinline__ Shares locate(const AttnParams &p, int *counts, long 
 
 // ---- the loader -------------------------------------------------------------
 
+// How a unit gets into the ring, always by 16-byte copies, each lane at a fixed
+// segment of every row.  ALIGNED: 16 aligned tokens never cross a page, so that one
+// offset serves 16 rows; else each row's offset comes from the lane that looked its
+// page up.
+
 // Streams a warp's units into its ring, K halves and V halves in turn.
-template <typename T, int DP, bool BULK, int UT>
+template <typename T, int DP, bool EX, bool ALIGNED, int UT>
 struct Loader {
     static constexpr int kSegMax = DP * (int)sizeof(T) / 16;
-    static constexpr int kSub = BULK ? 1 : UT / 16;
-    // 16-byte copies: a lane's segment is the same in each of its rows, which lie kRows apart
+    static constexpr int kSub = ALIGNED ? UT / 16 : 1;
+    // a lane's rows lie kRows apart
     static constexpr int kRows = 32 / kSegMax > 0 ? 32 / kSegMax : 1;    // rows per instruction
     static constexpr int kParts = kSegMax / 32 > 0 ? kSegMax / 32 : 1;   // instructions per row
     static constexpr int kStride = (kSegMax | 1) * 16;
@@ -354,18 +425,18 @@ struct Loader {
     Cursor c;
     int u, u_end;          // the unit within the tile (-1: none left); the share's units of the tile
     long long u1;          // end of the share
-    const char *kb, *vb;   // the key-value head in the caches (16-byte copies: at the lane's row and segment)
+    const char *kb, *vb;   // the key-value head in the caches (ALIGNED: at the lane's row and segment)
     const int32_t *table;  // the request's row
-    int page;              // table entry read ahead (bulk: of the lane's token, else of the lane's 16 tokens)
+    int page;              // table entry read ahead (of the lane's 16 tokens, or of its token)
     uint32_t mask;         // the unit's tokens that are to be read
-    // offsets in 16 bytes: of the first token of each 16; bulk: of the lane's token
+    // offsets in 16 bytes: of the first token of each 16, or of the lane's token
     uint64_t koff[kSub], voff[kSub];
 
     __device__ __forceinline__ void set_head(const AttnParams &p, int kvh, int lane)
     {
         kb = static_cast<const char *>(p.a.kc) + kvh * p.khead;
         vb = static_cast<const char *>(p.a.vc) + kvh * p.vhead;
-        if (!BULK) {
+        if (ALIGNED) {
             kb += (lane / kSegMax) * (long long)p.ktok * 16 + (lane % kSegMax) * 16;
             vb += (lane / kSegMax) * (long long)p.vtok * 16 + (lane % kSegMax) * 16;
         }
@@ -393,7 +464,7 @@ struct Loader {
     {
         page = -1;
         if (u >= 0) {
-            const int tok = (c.t.ub + u) * UT + (BULK ? lane % UT : kSub > 1 ? lane & 16 : 0);
+            const int tok = (c.t.ub + u) * UT + (ALIGNED ? (kSub > 1 ? lane & 16 : 0) : lane % UT);
             if (tok < c.t.end)   // (16 tokens are in the page of the first of them)
                 page = __ldg(table + div_fast(p.page, tok));
         }
@@ -408,14 +479,14 @@ struct Loader {
 #pragma unroll
         for (int b = 0; b < kSub; ++b) {
             // (an entry out of range masks its tokens: nothing is read at its offset)
-            const uint32_t pg = (uint32_t)max(!BULK && kSub > 1 ? __shfl_sync(0xffffffffu, page, 16 * b) : page, 0);
-            const int at = BULK ? tok : tok0 + 16 * b;
+            const uint32_t pg = (uint32_t)max(kSub > 1 ? __shfl_sync(0xffffffffu, page, 16 * b) : page, 0);
+            const int at = ALIGNED ? tok0 + 16 * b : tok;
             const uint32_t off = at - div_fast(p.page, at) * p.a.d.page_size;
             koff[b] = (uint64_t)pg * p.kpage + (uint64_t)off * p.ktok;
             voff[b] = (uint64_t)pg * p.vpage + (uint64_t)off * p.vtok;
         }
     }
-    // one half (UT tokens of K or V) into a ring slot, by 16-byte copies
+    // one half (UT tokens of K or V) into a ring slot; rows that are not read become zero
     __device__ __forceinline__ void copy(const AttnParams &p, const char *base, const uint64_t (&off)[kSub], uint32_t tok16,
                                          uint32_t slot, int lane)
     {
@@ -433,56 +504,45 @@ struct Loader {
                                          dst + (16 * b + i * kRows) * kStride + x * 512), "l"(s + x * 512) : "memory");
             }
         } else {
-#pragma unroll 1
-            for (int i = 0; i < UT / kRows; ++i) {
-                const int r = i * kRows;   // the instruction's first token
-                const char *s = base + ((kSub > 1 && r >= 16 ? off[kSub - 1] : off[0]) << 4) + (r % 16) * (long long)tok16 * 16;
-                const bool on = (mask >> (r + lane / kSegMax)) & 1;
+            const uint32_t mine = mask >> (lane / kSegMax);
 #pragma unroll
-                for (int x = 0; x < kParts; ++x)
-                    cp_async16(dst + r * kStride + x * 512, on ? s + x * 512 : static_cast<const char *>(p.a.q), on);
+            for (int b = 0; b < kSub; ++b) {
+                const char *s = base + (off[b] << 4);
+#pragma unroll
+                for (int i = 0; i < 16 / kRows; ++i, s += step) {
+                    const bool on = (mine >> (16 * b + i * kRows)) & 1;
+#pragma unroll
+                    for (int x = 0; x < kParts; ++x)
+                        cp_async16(dst + (16 * b + i * kRows) * kStride + x * 512,
+                                   on ? s + x * 512 : static_cast<const char *>(p.a.q), on);
+                }
             }
         }
     }
-    // ... by one bulk copy per token; `bar` completes when all are there.  Rows
-    // of V that are not read are zeroed (those of K only give scores that are
-    // masked).
-    __device__ __forceinline__ void copy_bulk(const AttnParams &p, const char *base, uint64_t off, char *slot, uint64_t *bar,
-                                              bool zero, int lane)
+    // ... of any page, a row's offset taken from its lane; the lanes of segments past
+    // the head's elements are idle
+    __device__ __forceinline__ void copy_any(const AttnParams &p, const char *base, uint64_t off, uint32_t slot, int lane)
     {
-        const int bytes = p.seg * 16;
-        char *dst = slot + (lane % UT) * p.stride;
-        const bool mine = lane < UT, on = mine && ((mask >> (lane % UT)) & 1);
-        if (zero && mask != kAll && mine && !on) {
-            for (int c = 0; c < p.seg; ++c)
-                *reinterpret_cast<uint4 *>(dst + c * 16) = make_uint4(0, 0, 0, 0);
-            ptx::fence_proxy_async_smem();   // (later bulk copies write the row)
+        const int r0 = lane / kSegMax, c = lane % kSegMax;
+        const uint32_t dst = slot + r0 * kStride + c * 16, mine = mask >> r0;
+        const char *src[UT / kRows];
+        // (sources first: the exchanges between lanes would stand between the copies)
+#pragma unroll
+        for (int i = 0; i < UT / kRows; ++i) {
+            const uint64_t from = __shfl_sync(0xffffffffu, off, r0 + i * kRows);
+            src[i] = base + (from << 4) + c * 16;
         }
-        if (lane == 0)
-            ptx::mbar_arrive_expect_tx(bar, (uint32_t)(__popc(mask) * bytes));
-        __syncwarp();
-        if (on)
-            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                             smem_addr(dst)), "l"(base + (off << 4)), "r"(bytes), "r"(smem_addr(bar))
-                         : "memory");
+#pragma unroll
+        for (int x = 0; x < kParts; ++x)
+            if (EX || c + 32 * x < p.seg) {
+#pragma unroll
+                for (int i = 0; i < UT / kRows; ++i) {
+                    const bool on = (mine >> (i * kRows)) & 1;
+                    cp_async16(dst + i * kRows * kStride + x * 512, on ? src[i] + x * 512 : static_cast<const char *>(p.a.q), on);
+                }
+            }
     }
 };
-
-// Set (to SSD_ERR_TIMEOUT) by a warp that gave up a wait for its copies.
-__device__ unsigned int g_attn_error;
-
-// A bounded wait for a bulk copy's barrier (about 2 s; after one that ran out,
-// the warp's next ones only poll).  A copy cannot fail to arrive in a healthy
-// context; if one did, the warp would go on with whatever its slot holds.
-__device__ __forceinline__ bool wait_bulk(uint64_t *bar, uint32_t parity, bool healthy)
-{
-#pragma unroll 1
-    for (int i = 0; i < (healthy ? 2000 : 1); ++i)
-        if (ptx::mbar_wait_for(bar, parity, 1000000))
-            return healthy;
-    atomicExch(&g_attn_error, (unsigned int)SSD_ERR_TIMEOUT);
-    return false;
-}
 
 // ---- the arithmetic: bf16 on mma.sync --------------------------------------
 
@@ -541,7 +601,7 @@ struct Mma {
     int lo[NM][2], hi[NM][2];   // positions a row sees
 
     __device__ __forceinline__ static int dim(const AttnParams &p) { return EX ? DP : p.a.d.headdim; }
-    __device__ __forceinline__ static int row_bytes(const AttnParams &p) { return EX ? ((DP / 8) | 1) * 16 : p.stride; }
+    static constexpr int kRowBytes = (DP / 8 | 1) * 16;   // of a ring slot: an odd number of segments, so that 8 rows' segments lie in different banks
 
     __device__ __forceinline__ void begin(const AttnParams &p, const Tile &t, int item, int lane)
     {
@@ -590,7 +650,7 @@ struct Mma {
     // [all0, all1): tokens that every row sees
     __device__ __forceinline__ void scores(const AttnParams &p, char *slot_ptr, uint32_t mask, int tok0, int all0, int all1, int lane)
     {
-        const int D = dim(p), stride = row_bytes(p);
+        const int D = dim(p), stride = kRowBytes;
         const uint32_t slot = smem_addr(slot_ptr);
 #pragma unroll
         for (int mt = 0; mt < NM; ++mt)
@@ -680,14 +740,34 @@ struct Mma {
         }
     }
 
-    // Tokens that some rows of the tile see and others do not are added row by
-    // row, to those that see them, and then left out of the product: there a
-    // weight 0 times an infinity or NaN of theirs would reach every row.
+    // whether the values of one of these tokens hold an infinity or NaN
+    __device__ __forceinline__ bool not_finite(const AttnParams &p, const char *slot_ptr, uint32_t tokens, int lane)
+    {
+        constexpr int kSegs = DP / 8, kAtOnce = 32 / kSegs;
+        const int c = lane % kSegs;
+        uint32_t bad = 0;
+        if (8 * c < dim(p)) {
+#pragma unroll 4
+            for (int r = lane / kSegs; r < kUnit; r += kAtOnce)
+                if ((tokens >> r) & 1) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(slot_ptr + r * kRowBytes + c * 16);
+                    // (an exponent of ones carries into the sign's place)
+                    bad |= ((v.x & 0x7f807f80u) + 0x00800080u) | ((v.y & 0x7f807f80u) + 0x00800080u) |
+                           ((v.z & 0x7f807f80u) + 0x00800080u) | ((v.w & 0x7f807f80u) + 0x00800080u);
+                }
+        }
+        return __any_sync(0xffffffffu, (bad & 0x80008000u) != 0);
+    }
+
+    // Tokens that some rows of the tile see and others do not, with values that are
+    // not finite, are added row by row, to those that see them, and then left out
+    // of the product: there a weight 0 times an infinity or NaN of theirs would
+    // reach every row.
     // (Unrolled over the tokens: a running token number would index the score
     // registers at run time and put them in local memory.)
     __device__ __forceinline__ void partial_tokens(const AttnParams &p, char *slot_ptr, uint32_t part, int tok0, int lane)
     {
-        const int stride = row_bytes(p);
+        const int stride = kRowBytes;
         const uint32_t slot = smem_addr(slot_ptr);
 #pragma unroll
         for (int tt = 0; tt < kUnit; ++tt) {
@@ -726,19 +806,18 @@ struct Mma {
             for (int c = lane; c < p.seg; c += 32)
                 *reinterpret_cast<uint4 *>(slot_ptr + tt * stride + c * 16) = make_uint4(0, 0, 0, 0);
         }
-        ptx::fence_proxy_async_smem();   // (later bulk copies write the rows)
         __syncwarp();
     }
 
     __device__ __forceinline__ void values(const AttnParams &p, char *slot_ptr, uint32_t mask, int tok0, int all0, int all1, int lane)
     {
-        const int D = dim(p), stride = row_bytes(p);
+        const int D = dim(p), stride = kRowBytes;
         if (tok0 < all0 || tok0 + kUnit > all1) {
             // bit tt: every row sees token tok0 + tt
             const int a0 = min(max(all0 - tok0, 0), kUnit), a1 = min(max(all1 - tok0, 0), kUnit);
             const uint32_t all = a1 > a0 ? (0xffffffffu >> (32 - a1)) & (0xffffffffu << a0) : 0u;
             const uint32_t part = mask & ~all;
-            if (part)
+            if (part && not_finite(p, slot_ptr, part, lane))
                 partial_tokens(p, slot_ptr, part, tok0, lane);
         }
         // lanes 0-7, 8-15: tokens 0-7, 8-15 of the first 16 bytes; 16-31: of the second
@@ -880,7 +959,7 @@ struct Simt {
     static constexpr bool kQSmem = false;
 
     __device__ __forceinline__ static int dim(const AttnParams &p) { return EX ? DP : p.a.d.headdim; }
-    __device__ __forceinline__ static int row_bytes(const AttnParams &p) { return EX ? ((DP / 4) | 1) * 16 : p.stride; }
+    static constexpr int kRowBytes = (DP / 4 | 1) * 16;   // of a ring slot: an odd number of segments, so that 8 rows' segments lie in different banks
 
     __device__ __forceinline__ void begin(const AttnParams &p, const Tile &t, int item, int lane)
     {
@@ -916,8 +995,8 @@ struct Simt {
     {
         constexpr int kHalf = kUnit / 2, NC = MR > 4 ? 1 : 2;   // NC: sums per row and token
         const int part = lane / kHalf, tt = lane % kUnit, D = dim(p);
-        const ulonglong2 *k0 = reinterpret_cast<const ulonglong2 *>(slot + (lane % kHalf) * row_bytes(p));
-        const ulonglong2 *k1 = reinterpret_cast<const ulonglong2 *>(slot + (lane % kHalf + kHalf) * row_bytes(p));
+        const ulonglong2 *k0 = reinterpret_cast<const ulonglong2 *>(slot + (lane % kHalf) * kRowBytes);
+        const ulonglong2 *k1 = reinterpret_cast<const ulonglong2 *>(slot + (lane % kHalf + kHalf) * kRowBytes);
         f32x2 acc[MR][2][NC];
 #pragma unroll
         for (int r = 0; r < MR; ++r)
@@ -981,7 +1060,7 @@ struct Simt {
     __device__ __forceinline__ void add_values(const AttnParams &p, const char *slot, int tok0, int lane)
     {
         constexpr int kTok = kUnit / kGroups;   // tokens of a half warp, or of the warp
-        const int grp = kGroups == 2 ? lane >> 4 : 0, el = 4 * (kGroups == 2 ? lane & 15 : lane), stride = row_bytes(p);
+        const int grp = kGroups == 2 ? lane >> 4 : 0, el = 4 * (kGroups == 2 ? lane & 15 : lane), stride = kRowBytes;
         const char *v0 = slot + grp * kTok * stride + 4 * el;
         const float *w0 = ps + grp * kTok;
 #pragma unroll RAGGED ? 1 : 2
@@ -1118,27 +1197,27 @@ __device__ __forceinline__ void store2(__nv_bfloat16 *p, float x, float y) { *re
 
 // shared memory: the warps' rings, their query rows (and fp32 weights), two
 // join buffers (in the query rows' place where those are bf16) -- all of whole
-// 16-byte segments -- then maxima, sums, barriers and slot masks.  NH: halves in
+// 16-byte segments -- then maxima, sums and slot masks.  NH: halves in
 // a warp's ring.
 template <typename M, int NH, bool SOLO>
 struct Layout {
     static constexpr int kQuery = kWarps * M::kQBytes;
-    static constexpr int kSmall = kWarps * NH * 8 + (kWarps * M::MR * 2 + M::MR * 2 + kWarps * NH) * 4;
-    static __host__ __device__ int join_stride(int D) { return D + 8; }
-    static __host__ __device__ int ring_bytes(int stride) { return kWarps * NH * M::kUnit * stride; }
-    static __host__ __device__ int join_bytes(int D) { return SOLO ? 0 : 2 * M::MR * join_stride(D) * 4; }
-    static __host__ __device__ int middle_bytes(int D)
+    static constexpr int kSmall = (kWarps * M::MR * 2 + M::MR * 2 + kWarps * NH) * 4;
+    static constexpr __host__ __device__ int join_stride(int D) { return D + 8; }
+    static constexpr int kRing = kWarps * NH * M::kUnit * M::kRowBytes;
+    static constexpr __host__ __device__ int join_bytes(int D) { return SOLO ? 0 : 2 * M::MR * join_stride(D) * 4; }
+    static constexpr __host__ __device__ int middle_bytes(int D)
     {
         return M::kQSmem ? (kQuery > join_bytes(D) ? kQuery : join_bytes(D)) : kQuery + join_bytes(D);
     }
-    static __host__ __device__ int total(int D, int stride) { return ring_bytes(stride) + middle_bytes(D) + kSmall; }
+    static constexpr __host__ __device__ int total(int D) { return kRing + middle_bytes(D) + kSmall; }
 };
 
 // SOLO: shares of warps, for many tiles: a warp goes through whole tiles without
 // a barrier, and a tile is cut into a few parts at most.  Else shares of CTAs,
 // for few: a tile is then cut into many parts, and joining a CTA's warps first
 // leaves a quarter of them to the second launch.
-template <typename M, int NH, bool SOLO, bool BULK, int MB>
+template <typename M, int NH, bool SOLO, bool ALIGNED, int MB>
 __global__ void __launch_bounds__(kThreads, MB) ssd_paged_attn_kernel(const __grid_constant__ AttnParams p)
 {
     using T = typename M::T;
@@ -1147,7 +1226,8 @@ __global__ void __launch_bounds__(kThreads, MB) ssd_paged_attn_kernel(const __gr
     extern __shared__ __align__(16) char smem[];
     __shared__ Found found[kWarps];
     __shared__ long long tmp[kWarps];
-    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, D = M::dim(p), stride = M::row_bytes(p);
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, D = M::dim(p);
+    constexpr int stride = M::kRowBytes;
     constexpr int kOwn = SOLO ? kWarps : 1;   // shares of a CTA at a time
     const int first_share = SOLO ? blockIdx.x * kWarps + w : blockIdx.x;
     // The parameters' cache lines cost some hundred cycles each when first
@@ -1159,13 +1239,12 @@ __global__ void __launch_bounds__(kThreads, MB) ssd_paged_attn_kernel(const __gr
             x ^= reinterpret_cast<const uint32_t *>(&p)[i];
         asm volatile("" ::"r"(x));
     }
-    const int half_bytes = UT * stride;
+    constexpr int half_bytes = UT * stride;
     char *ring = smem + (size_t)w * NH * half_bytes;        // [NH][UT][stride]
-    char *middle = smem + L::ring_bytes(stride);
+    char *middle = smem + L::kRing;
     char *qs = middle + w * M::kQBytes;
     float *join = reinterpret_cast<float *>(middle + (M::kQSmem ? 0 : L::kQuery));   // (16-byte accesses up to here)
-    uint64_t *bars = reinterpret_cast<uint64_t *>(middle + L::middle_bytes(D)) + w * NH;
-    float *ml = reinterpret_cast<float *>(bars - w * NH + kWarps * NH);   // [kWarps][MR][2]
+    float *ml = reinterpret_cast<float *>(middle + L::middle_bytes(D));   // [kWarps][MR][2]
     float *joint = ml + kWarps * M::MR * 2;                               // [MR] maxima, [MR] sums
     uint32_t *masks = reinterpret_cast<uint32_t *>(joint + M::MR * 2) + w * NH;
     const int ds = L::join_stride(D);
@@ -1177,13 +1256,14 @@ __global__ void __launch_bounds__(kThreads, MB) ssd_paged_attn_kernel(const __gr
     Shares sh;
     Cursor cur;
     const bool few = p.few;
+    const int padding = p.a.start ? p.a.start[p.a.d.nreq] : 0;   // first row of it
     if (few)
-        sh = locate_few<UT, SOLO>(p, p.of_head == 1 ? 0 : div_fast(p.by_items, first_share), cur);
+        sh = locate_few<UT, SOLO>(p, p.of_head == 1 ? 0 : div_fast(p.by_items, first_share), cur, reinterpret_cast<int4 *>(ring));
     else
         sh = locate<UT, SOLO>(p, reinterpret_cast<int *>(smem), tmp, found);
     // padding rows see nothing
     if (p.a.start) {
-        const long long r0 = min((long long)max(p.a.start[p.a.d.nreq], 0), (long long)p.a.d.nrows);
+        const long long r0 = min((long long)max(padding, 0), (long long)p.a.d.nrows);
         for (long long i = r0 * p.a.d.nheads + blockIdx.x; i < p.a.d.nrows * p.a.d.nheads; i += gridDim.x) {
             const long long row = i / p.a.d.nheads, h = i - row * p.a.d.nheads;
             T *out = static_cast<T *>(p.a.out) + row * p.a.d.o_stride[0] + h * p.a.d.o_stride[1];
@@ -1204,26 +1284,19 @@ __global__ void __launch_bounds__(kThreads, MB) ssd_paged_attn_kernel(const __gr
             for (int c = p.seg; c * 16 < stride; ++c)
                 *reinterpret_cast<uint4 *>(ring + (size_t)i * stride + c * 16) = make_uint4(0, 0, 0, 0);
     }
-    if (BULK) {
-        if (lane < NH)
-            ptx::mbar_init(bars + lane, 1);
-        ptx::fence_mbar_init();
-        ptx::fence_proxy_async_smem();
-    }
     __syncwarp();
 
+    const int req0 = few ? cur.t.req : 0;   // (of more shares than one each, the first begins with the first tile)
     // Half h (K of unit h / 2, V when odd) goes to slot h % NH; at step h the half
     // h + NH - 1 is loaded: with an even ring V of a unit while K of one is used,
     // with an odd one K while K.  Every step is one group of asynchronous copies,
     // empty past the share's end.
     constexpr int step = SOLO ? 1 : kWarps;
     int head = 0, tail = 0;   // slots of the next half to load, to use
-    uint32_t parity = 0;
-    bool healthy = true;
     // (one share each, but for more heads than there are warps or CTAs)
     for (int share = first_share; share < p.nshares; share += gridDim.x * kOwn) {
     const int j = div_fast(p.by_items, share), item = share - j * p.items;
-    const long long u0 = p.of_head == 1 ? 0 : j * sh.per, u1 = min(u0 + sh.per, sh.total);
+    const long long u0 = p.of_head == 1 ? 0 : j * sh.per;
     if (SOLO && lane == 0)
         p.desc[share] = make_int4(-1, 0, 0, 0);
     if (u0 >= sh.total)   // (empty)
@@ -1232,12 +1305,13 @@ __global__ void __launch_bounds__(kThreads, MB) ssd_paged_attn_kernel(const __gr
     const int h0 = kvh * p.group + hb * p.gh, nh = min(p.gh, p.group - hb * p.gh);
 
     if (!few || share != first_share) {   // (a further share begins where its head does)
-        const Found f = few ? Found{0, 0, 0, 0} : found[SOLO ? w : 0];
+        const Found f = few ? Found{req0, 0, 0, 0} : found[SOLO ? w : 0];
         set_tile<UT>(p, cur.t, f.req, f.j);
         cur.tile = f.tile;
         cur.lin = f.lin;
     }
-    Loader<T, M::kDim, BULK, UT> ld;
+    const long long u1 = min(u0 + sh.per, sh.chunks ? cur.lin + cur.t.units : sh.total);
+    Loader<T, M::kDim, M::kExact, ALIGNED, UT> ld;
     ld.c = cur;
     ld.u1 = u1;
     ld.set_head(p, kvh, lane);
@@ -1251,28 +1325,26 @@ __global__ void __launch_bounds__(kThreads, MB) ssd_paged_attn_kernel(const __gr
             ld.offsets(p, lane);
             if (lane == 0)
                 masks[head] = ld.mask;
-            if constexpr (!BULK)
+            if constexpr (ALIGNED)
                 ld.copy(p, ld.kb, ld.koff, p.ktok, smem_addr(slot), lane);
             else
-                ld.copy_bulk(p, ld.kb, ld.koff[0], slot, bars + head, false, lane);
+                ld.copy_any(p, ld.kb, ld.koff[0], smem_addr(slot), lane);
             head = head + 1 == NH ? 0 : head + 1;
         }
-        if (!BULK)
-            cp_commit();
+        cp_commit();
     };
     auto load_v = [&]() {
         if (ld.u >= 0) {
             char *slot = ring + head * half_bytes;
-            if constexpr (!BULK)
+            if constexpr (ALIGNED)
                 ld.copy(p, ld.vb, ld.voff, p.vtok, smem_addr(slot), lane);
             else
-                ld.copy_bulk(p, ld.vb, ld.voff[0], slot, bars + head, true, lane);
+                ld.copy_any(p, ld.vb, ld.voff[0], smem_addr(slot), lane);
             ld.skip(p, step);
             ld.fetch_page(p, lane);
             head = head + 1 == NH ? 0 : head + 1;
         }
-        if (!BULK)
-            cp_commit();
+        cp_commit();
     };
     M math;
     math.qs = reinterpret_cast<decltype(math.qs)>(qs);
@@ -1304,10 +1376,7 @@ __global__ void __launch_bounds__(kThreads, MB) ssd_paged_attn_kernel(const __gr
         const int skip = SOLO ? 0 : (w - (int)((cur.lin + u - u0) % kWarps) + kWarps) % kWarps;
         for (int x = u + skip; x < ue; x += step) {
             const int tok0 = (cur.t.ub + x) * UT;
-            if constexpr (BULK)
-                healthy = wait_bulk(bars + tail, parity, healthy);
-            else
-                cp_wait<NH - 2>();
+            cp_wait<NH - 2>();
             __syncwarp();
             const uint32_t mask = masks[tail];
             if (NH % 2 == 0)
@@ -1315,24 +1384,15 @@ __global__ void __launch_bounds__(kThreads, MB) ssd_paged_attn_kernel(const __gr
             else
                 load_k();
             math.scores(p, ring + tail * half_bytes, mask, tok0, all0, all1, lane);
-            if (++tail == NH) {
-                tail = 0;
-                parity ^= 1;
-            }
-            if constexpr (BULK)
-                healthy = wait_bulk(bars + tail, parity, healthy);
-            else
-                cp_wait<NH - 2>();
+            tail = tail + 1 == NH ? 0 : tail + 1;
+            cp_wait<NH - 2>();
             __syncwarp();
             if (NH % 2 == 0)
                 load_k();
             else
                 load_v();
             math.values(p, ring + tail * half_bytes, mask, tok0, all0, all1, lane);
-            if (++tail == NH) {
-                tail = 0;
-                parity ^= 1;
-            }
+            tail = tail + 1 == NH ? 0 : tail + 1;
         }
         const bool whole = u == 0 && ue == cur.t.units;
         const int slot = u > 0 ? 0 : 1;   // a tile begun in an earlier share, or in this one
@@ -1412,8 +1472,7 @@ __global__ void __launch_bounds__(kThreads, MB) ssd_paged_attn_kernel(const __gr
         advance<UT>(p, cur);
         begin();
     }
-    if (!BULK)
-        cp_wait<0>();
+    cp_wait<0>();
     __syncwarp();
     }
 }
@@ -1526,6 +1585,9 @@ __device__ __forceinline__ int desc_rows(const AttnParams &p, const int4 &d)
 }
 
 constexpr int kJoinWarps = 8;
+// Shares of a block of the join (where they are warps'): several only for tiles of a
+// few rows, which leave the block's other warps idle.
+template <int MR> constexpr int kJoinShares = MR >= 8 ? 1 : 4;
 
 // SOLO: few parts; a warp per row, a block per CTA of the first launch.  Else many
 // parts: a block per tile and row.
@@ -1538,23 +1600,23 @@ __global__ void __launch_bounds__(32 * kJoinWarps) ssd_paged_attn_join_kernel(co
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (SOLO) {
-        int4 d[kWarps];
+        int4 d[kJoinShares<MR>];
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) {
-            const int i = blockIdx.x * kWarps + k;
+        for (int k = 0; k < kJoinShares<MR>; ++k) {
+            const int i = blockIdx.x * kJoinShares<MR> + k;
             d[k] = i < p.ndesc ? p.desc[i] : make_int4(-1, 0, 0, 0);
         }
         int at = w;   // rows of all four, dealt to the warps; those of many parts are left to all of them
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) {
+        for (int k = 0; k < kJoinShares<MR>; ++k) {
             const int rows = d[k].w > 16 ? 0 : desc_rows(p, d[k]);
             for (; at < rows; at += kJoinWarps)
                 join_row<T, MR, 1>(p, d[k], at, 0, lane, sm, so);
             at -= rows;
         }
 #pragma unroll 1
-        for (int k = 0; k < kWarps; ++k) {
-            const int4 t = k == 0 ? d[0] : k == 1 ? d[1] : k == 2 ? d[2] : d[3];
+        for (int k = 0; k < kJoinShares<MR>; ++k) {
+            const int4 t = k == 0 ? d[0] : k == 1 ? d[1 % kJoinShares<MR>] : k == 2 ? d[2 % kJoinShares<MR>] : d[3 % kJoinShares<MR>];
             const int rows = t.w > 16 ? desc_rows(p, t) : 0;
             for (int r = 0; r < rows; ++r) {
                 join_row<T, MR, kJoinWarps>(p, t, r, w, lane, sm, so);
@@ -1572,13 +1634,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) ssd_paged_attn_join_kernel(co
 
 constexpr int kSmemMost = (227 << 10) - 1024;   // dynamic, beside the kernel's few static bytes
 
-template <typename M, int NH, bool SOLO, bool BULK, int MB>
+template <typename M, int NH, bool SOLO, bool ALIGNED, int MB>
 cudaError_t launch(AttnParams &p, void *workspace, cudaStream_t stream)
 {
     using T = typename M::T;
+    static_assert(Layout<M, NH, SOLO>::total(M::kDim) <= kSmemMost);
     const int D = p.a.d.headdim;
-    const int smem = std::max(Layout<M, NH, SOLO>::total(D, p.stride), p.a.start ? (int)(p.a.d.nreq + 1) * 4 : 0);
-    auto kernel = ssd_paged_attn_kernel<M, NH, SOLO, BULK, MB>;
+    const int smem = std::max(Layout<M, NH, SOLO>::total(D), p.a.start ? (int)(p.a.d.nreq + 1) * 4 : 0);
+    auto kernel = ssd_paged_attn_kernel<M, NH, SOLO, ALIGNED, MB>;
     static std::atomic<uint64_t> done{0};
     static std::atomic<int> regs{0};   // (the same for every device)
     cudaError_t e = allow_smem(kernel, kSmemMost, done);
@@ -1615,7 +1678,7 @@ cudaError_t launch(AttnParams &p, void *workspace, cudaStream_t stream)
     if ((e = cudaLaunchKernelEx(&cfg, kernel, p)) != cudaSuccess)
         return e;
     note_launches(1);
-    cfg.gridDim = SOLO ? dim3((p.ndesc + kWarps - 1) / kWarps) : dim3(p.ndesc, p.tok * p.gh);
+    cfg.gridDim = SOLO ? dim3((p.ndesc + kJoinShares<M::MR> - 1) / kJoinShares<M::MR>) : dim3(p.ndesc, p.tok * p.gh);
     cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&cfg, ssd_paged_attn_join_kernel<T, M::MR, SOLO>, p);
@@ -1626,20 +1689,10 @@ cudaError_t launch(AttnParams &p, void *workspace, cudaStream_t stream)
 
 // NH, NHS: halves in the ring with shares of CTAs, of warps; MB: CTAs per SM that the
 // registers must leave room for with shares of warps
-template <typename M, int NH, int NHS, int MB, bool BULK>
+template <typename M, int NH, int NHS, int MB, bool ALIGNED>
 cudaError_t launch_shares(AttnParams &p, void *ws, cudaStream_t st)
 {
-    return solo_shares(p) ? launch<M, NHS, true, BULK, MB>(p, ws, st) : launch<M, NH, false, BULK, 1>(p, ws, st);
-}
-
-cudaError_t take_error(uint32_t *code)
-{
-    unsigned int v = 0, zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(&v, g_attn_error, sizeof(v));
-    if (e == cudaSuccess && v != 0)
-        e = cudaMemcpyToSymbol(g_attn_error, &zero, sizeof(zero));
-    *code = v;
-    return e;
+    return solo_shares(p) ? launch<M, NHS, true, ALIGNED, MB>(p, ws, st) : launch<M, NH, false, ALIGNED, 1>(p, ws, st);
 }
 
 }  // namespace

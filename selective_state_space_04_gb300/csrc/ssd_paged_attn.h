@@ -24,8 +24,8 @@ struct AttnParams {
     int ndesc;          // entries of it
     int of_head;        // shares of a key-value head (and head block)
     int nshares;        // of_head * items
-    int few;            // at most kFewRows rows, one per request, whose units fit 32 bits
-    FastDiv by_items;
+    int few;            // at most kFewTiles tiles and requests, whose units fit 32 bits
+    FastDiv by_items, by_tok;
     int group;          // query heads per key-value head
     int gh;             // query heads of a tile (group, or a part of it when it is larger than MR)
     int nhb;            // head blocks per key-value head
@@ -34,13 +34,12 @@ struct AttnParams {
     int seg;            // 16-byte segments per row of K or V
     uint32_t kpage, ktok, vpage, vtok;   // strides in 16 bytes
     long long khead, vhead;              // in bytes
-    int stride;         // bytes from row to row of a ring slot (an odd number of segments)
     float f;            // |scale| log2(e), or 1 for scale 0
     int sign;           // of scale
     int sms;            // the device's SMs
 };
 
-constexpr int kFewRows = 128;
+constexpr int kFewTiles = 128;
 
 inline FastDiv fast_div(int d)
 {
@@ -74,8 +73,5 @@ constexpr int kMaxCtas = 1024;   // the workspace is sized for at most this many
 cudaError_t attn_launch_bf16(AttnParams &p, int mr, void *workspace, cudaStream_t stream);
 cudaError_t attn_launch_bf16_any(AttnParams &p, int mr, void *workspace, cudaStream_t stream);
 cudaError_t attn_launch_f32(AttnParams &p, int mr, void *workspace, cudaStream_t stream);
-// reads and clears the error words of the kernels that wait for bulk copies
-cudaError_t attn_bf16_any_error(uint32_t *code);
-cudaError_t attn_f32_error(uint32_t *code);
 
 }  // namespace ssd

@@ -9,10 +9,10 @@ cudaError_t launch_rows(AttnParams &p, void *ws, cudaStream_t st)
 {
     const int D = p.a.d.headdim;
     if (D <= 64)
-        return launch_shares<Simt<MR, 64, false>, 2, 2, 2, true>(p, ws, st);
+        return launch_shares<Simt<MR, 64, false>, 2, 2, 2, false>(p, ws, st);
     if (D <= 128)
-        return launch_shares<Simt<MR, 128, false>, MR == 8 ? 2 : 3, 2, 2, true>(p, ws, st);
-    return launch_shares<Simt<MR, 256, false>, 2, 2, 1, true>(p, ws, st);
+        return launch_shares<Simt<MR, 128, false>, MR == 8 ? 2 : 3, MR == 8 ? 2 : 3, 2, false>(p, ws, st);
+    return launch_shares<Simt<MR, 256, false>, MR == 8 ? 2 : 3, MR == 8 ? 2 : 3, 1, false>(p, ws, st);
 }
 
 }  // namespace
@@ -26,7 +26,5 @@ cudaError_t attn_launch_f32(AttnParams &p, int mr, void *ws, cudaStream_t st)
     default: return launch_rows<8>(p, ws, st);
     }
 }
-
-cudaError_t attn_f32_error(uint32_t *code) { return take_error(code); }
 
 }  // namespace ssd
