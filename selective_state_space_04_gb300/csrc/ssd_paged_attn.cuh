@@ -7,22 +7,26 @@
 // the requests' lengths, the same shares for every key-value head.  Neighbouring
 // warps (or CTAs) take the same share of neighbouring heads, so that a token's
 // heads, which lie side by side in a token-major cache, are read at about the
-// same time.  The CTAs that fit the GPU at once stay for the whole launch.  A warp streams its units through a ring of
-// shared-memory slots of its own, K and V halves in turn, and keeps a running
-// maximum, sum and output rows in registers: no barrier stands between loads and
-// arithmetic, and loads run ahead across tile boundaries.
+// same time.  The CTAs that fit the GPU at once stay for the whole launch.  A warp
+// streams its units through a ring of shared-memory slots of its own, K and V
+// halves in turn, and keeps a running maximum, sum and output rows in registers:
+// no barrier stands between loads and arithmetic, and loads run ahead across tile
+// boundaries.
 //
 // Shares belong to warps, or to CTAs, whose warps then take units in turn and
 // are joined in shared memory at the end of a tile (many tiles, or few: see
-// kernel).  A tile that lies in one share is finished there; one that is cut
+// solo_shares).  A tile that lies in one share is finished there; one that is cut
 // leaves partial results (maximum, sum, unnormalised rows), which a second
 // launch joins in the order of their shares.
 //
-// Two ways into the ring: 16-byte asynchronous copies, each lane at a fixed
-// segment of every row, where sizes are known at compile time and 16 aligned
-// tokens never cross a page; else one bulk copy per token and half, which takes
-// any row length and any page (at most one row per about 9 cycles and SM, which
-// bounds rows of 128 bytes at 4.1 TB/s, rows of 256 at the memory's rate).
+// What bounds it.  Up to 16 rows per tile: the cache's bytes, each read once
+// (bf16 heads of 128, 8 of them, 128 requests of 1..4096 tokens, 1.08 GB: 173 us,
+// 6.2 TB/s; 128 requests of 500..12000 with 4 new tokens each: 505 us, 6.5 TB/s).
+// Little work: a chain of dependent steps -- finding the share, table entry, keys,
+// values, join -- of 7 to 10 us (one request of 1000 tokens: 7.8 us).  More rows:
+// the products and the softmax beside them, on two warps per scheduler, which is
+// what the output rows' registers leave (64 requests of 100..8000, 20 rows: 200 us,
+// 5.3 TB/s; whole prompts of 8192 tokens: 3.0 ms, 0.18 PFLOP/s).
 //
 // The running form: with s2 = scale log2(e) q.k, m = max s2 so far,
 // p = 2^(s2 - m), l = sum p, o = sum p v; when m grows by d, l and o are
@@ -32,7 +36,8 @@
 // tokens; output: 16 rows x 8 elements over 16 tokens).  A score tile's
 // accumulator registers are, as they stand, the second product's A operand.
 // The weights p enter it as two bf16 terms, so that they carry 16 bits: one
-// bf16 term would add an error as large as the output's own rounding.
+// bf16 term would add an error as large as the output's own rounding, and saves
+// little (32 requests of 100..8000 tokens, 32 rows: 50 us instead of 52).
 // fp32: fp32 FMA (see Simt below).
 #pragma once
 
@@ -203,7 +208,8 @@ struct Shares {
 };
 
 // For at most kFewTiles tiles: each warp sums all tiles' units (four tiles a lane)
-// and finds its own share's beginning, without a barrier.  `list` (shared memory
+// and finds its own share's beginning, without a barrier (one request of 1000
+// tokens: 7.9 us instead of 8.6 by way of `locate`).  `list` (shared memory
 // of the warp, kFewTiles entries) is used when there is a start array.
 template <int UT, bool SOLO>
 __device__ __forceinline__ Shares locate_few(const AttnParams &p, int j, Cursor &cur, int4 *list)
@@ -270,6 +276,7 @@ __device__ __forceinline__ Shares locate_few(const AttnParams &p, int j, Cursor 
     int total = __shfl_sync(0xffffffffu, inc, 31);
     // So little work that each CTA can have at most a unit per warp, of one tile
     // (two tiles of a CTA would be one after the other): tiles begin with shares.
+    // 17 requests of two units or three: 7.3 us; four units to a CTA, across tiles: 13.8.
     const int whole = SOLO ? 0 : __shfl_sync(0xffffffffu, incp, 31);
     const bool chunks = !SOLO && whole <= p.of_head * kWarps;
     if (chunks) {
@@ -410,7 +417,12 @@ __device__ __forceinline__ Shares locate(const AttnParams &p, int *counts, long 
 // How a unit gets into the ring, always by 16-byte copies, each lane at a fixed
 // segment of every row.  ALIGNED: 16 aligned tokens never cross a page, so that one
 // offset serves 16 rows; else each row's offset comes from the lane that looked its
-// page up.
+// page up (in ALIGNED's place: 128 requests of 1..4096 tokens, heads of 128, 175 us
+// instead of 172; one of 1000, 8.1 instead of 7.8; heads of 64 no difference).  One
+// bulk copy per row was slower for bf16 (a row per some 9 cycles and SM: heads of
+// 64, 64 requests of 100..8000, 184 us instead of 99) and fp32 heads of 64 (198
+// requests of 1..3971: 345 instead of 267), though not for fp32 heads of 128 with
+// one query head each (157 instead of 169).
 
 // Streams a warp's units into its ring, K halves and V halves in turn.
 template <typename T, int DP, bool EX, bool ALIGNED, int UT>
@@ -601,7 +613,8 @@ struct Mma {
     int lo[NM][2], hi[NM][2];   // positions a row sees
 
     __device__ __forceinline__ static int dim(const AttnParams &p) { return EX ? DP : p.a.d.headdim; }
-    static constexpr int kRowBytes = (DP / 8 | 1) * 16;   // of a ring slot: an odd number of segments, so that 8 rows' segments lie in different banks
+    // of a ring slot: an odd number of segments, so that 8 rows' segments lie in different banks
+    static constexpr int kRowBytes = (DP / 8 | 1) * 16;
 
     __device__ __forceinline__ void begin(const AttnParams &p, const Tile &t, int item, int lane)
     {
@@ -959,7 +972,8 @@ struct Simt {
     static constexpr bool kQSmem = false;
 
     __device__ __forceinline__ static int dim(const AttnParams &p) { return EX ? DP : p.a.d.headdim; }
-    static constexpr int kRowBytes = (DP / 4 | 1) * 16;   // of a ring slot: an odd number of segments, so that 8 rows' segments lie in different banks
+    // of a ring slot: an odd number of segments, so that 8 rows' segments lie in different banks
+    static constexpr int kRowBytes = (DP / 4 | 1) * 16;
 
     __device__ __forceinline__ void begin(const AttnParams &p, const Tile &t, int item, int lane)
     {
@@ -1463,7 +1477,8 @@ __global__ void __launch_bounds__(kThreads, MB) ssd_paged_attn_kernel(const __gr
         }
         // where the parts of a cut tile are: this share and the head's next ones
         const long long at = SOLO ? share : (long long)cur.tile * p.items + item;
-        if ((SOLO ? !whole && slot == 1 && lane == 0 : slot == 1 && tid == 0) && at < p.ndesc)   // (a start array that descends has more tiles)
+        // (a start array that descends has more tiles than there are entries)
+        if ((SOLO ? !whole && slot == 1 && lane == 0 : slot == 1 && tid == 0) && at < p.ndesc)
             p.desc[at] = make_int4(whole ? -1 : cur.t.row, cur.t.nq | item << 8, (int)share,
                                    (int)div_units(cur.lin + cur.t.units - 1 - u0, sh.per) + 1);
         if (cur.lin + ue >= u1)
@@ -1586,7 +1601,9 @@ __device__ __forceinline__ int desc_rows(const AttnParams &p, const int4 &d)
 
 constexpr int kJoinWarps = 8;
 // Shares of a block of the join (where they are warps'): several only for tiles of a
-// few rows, which leave the block's other warps idle.
+// few rows, which leave the block's other warps idle (27 requests of 5 rows, window
+// 665: 29 us with one share per block, 46 with four; fp32 tiles of one row, 576
+// tiles: 51.5 with one, 50.1 with four).
 template <int MR> constexpr int kJoinShares = MR >= 8 ? 1 : 4;
 
 // SOLO: few parts; a warp per row, a block per CTA of the first launch.  Else many
@@ -1688,7 +1705,9 @@ cudaError_t launch(AttnParams &p, void *workspace, cudaStream_t stream)
 }
 
 // NH, NHS: halves in the ring with shares of CTAs, of warps; MB: CTAs per SM that the
-// registers must leave room for with shares of warps
+// registers must leave room for with shares of warps.  Several CTAs per SM count for
+// more than deep rings: heads of 128 with rings of 3 halves 181 us, of 2 172 (128
+// requests of 1..4096 tokens); fp32 180 and 176 (32 requests of 100..8000).
 template <typename M, int NH, int NHS, int MB, bool ALIGNED>
 cudaError_t launch_shares(AttnParams &p, void *ws, cudaStream_t st)
 {

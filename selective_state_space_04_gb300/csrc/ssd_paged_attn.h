@@ -60,7 +60,9 @@ inline long long most_tiles(const AttnParams &p)
 
 // Shares of warps for at least two tiles (times key-value heads) per SM: below
 // that a tile would be cut into more than four parts of warps, the join of
-// which costs more than the CTAs' own joins.
+// which costs more than the CTAs' own joins.  Measured with shares of warps, of
+// CTAs (8 key heads of 128, bf16): 128 tiles of 100..8000 tokens 55, 51 us; 256:
+// 92.5, 91.5; 384: 131.4, 132.7; 400 tiles of 10..500: 19.7, 26.0.
 inline bool solo_shares(const AttnParams &p) { return most_tiles(p) * p.items >= 2 * p.sms; }
 
 constexpr int kWarps = 4;        // per CTA

@@ -1,4 +1,6 @@
 // ssd_paged_attn_bf16_any.cu -- paged attention: bf16, any page and head size.
+// Heads of 64 and 128 keep their compile-time size (64 requests of 100..8000
+// tokens, pages of 24: heads of 64 99 us, of 128 175; heads of 80 146 us).
 #include "ssd_paged_attn.cuh"
 
 namespace ssd {

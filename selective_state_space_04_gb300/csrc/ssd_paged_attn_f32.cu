@@ -1,4 +1,6 @@
-// ssd_paged_attn_f32.cu -- paged attention: fp32.
+// ssd_paged_attn_f32.cu -- paged attention: fp32.  Bound by the cache's bytes up to
+// 4 rows (32 requests of 100..8000 tokens, 8 key heads of 128, 1.06 GB: 169 us for one
+// row, 176 for four), by the products for 8 (217 us).
 #include "ssd_paged_attn.cuh"
 
 namespace ssd {
@@ -11,7 +13,7 @@ cudaError_t launch_rows(AttnParams &p, void *ws, cudaStream_t st)
     if (D <= 64)
         return launch_shares<Simt<MR, 64, false>, 2, 2, 2, false>(p, ws, st);
     if (D <= 128)
-        return launch_shares<Simt<MR, 128, false>, MR == 8 ? 2 : 3, MR == 8 ? 2 : 3, 2, false>(p, ws, st);
+        return launch_shares<Simt<MR, 128, false>, 2, 2, 2, false>(p, ws, st);
     return launch_shares<Simt<MR, 256, false>, MR == 8 ? 2 : 3, MR == 8 ? 2 : 3, 1, false>(p, ws, st);
 }
 
