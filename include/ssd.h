@@ -586,7 +586,7 @@ typedef struct ssd_attn_dims {
     uint32_t reserved;   /* must be 0 */
     /* strides in elements, D contiguous; multiples of 16 bytes (table_stride: any) */
     int64_t q_stride[2], o_stride[2];     /* row, head */
-    int64_t kc_stride[3], vc_stride[3];   /* page, token, head */
+    int64_t kc_stride[3], vc_stride[3];   /* page, token, head; the first two below 2^32 x 16 bytes (else SSD_ERR_UNSUPPORTED) */
     int64_t table_stride;                 /* request */
 } ssd_attn_dims_t;
 
