@@ -25,7 +25,7 @@ long long rows_wanted(const ssd_attn_dims_t &d)
 // bf16: 32 rows where there are more than 16, so that the cache is read once for
 // them (64 requests of 100..8000 tokens, 5 new ones each, groups of 4: 197 us; in
 // tiles of 16 rows 319; groups of 16: 265 and 383.  Groups of 32 with one new token
-// have few tiles and lose: 52 and 49).  Heads above 128 leave registers for 16 only.
+// have few tiles and gain nothing: 49 either way).  Heads above 128 leave registers for 16 only.
 // fp32: no more rows than there are, each costs its share of the products (one row:
 // 172 us; as one of eight: 211).
 int tile_rows(const ssd_attn_dims_t &d)

@@ -37,7 +37,7 @@
 // accumulator registers are, as they stand, the second product's A operand.
 // The weights p enter it as two bf16 terms, so that they carry 16 bits: one
 // bf16 term would add an error as large as the output's own rounding, and saves
-// little (32 requests of 100..8000 tokens, 32 rows: 50 us instead of 52).
+// little (32 requests of 100..8000 tokens, 32 rows: 2 of 52 us).
 // fp32: fp32 FMA (see Simt below).
 #pragma once
 
@@ -1531,21 +1531,23 @@ __global__ void __launch_bounds__(kThreads, MB) ssd_paged_attn_kernel(const __gr
 // elements, each warp in the running form, so that the parts' maxima and rows
 // are loaded together, four at a time; then the warps through shared memory
 // (sm, so: of the NW warps).
-template <typename T, int MR, int NW>
-__device__ __forceinline__ void join_row(const AttnParams &p, const int4 &d, int r, int w, int lane, float (*sm)[2], float (*so)[256])
+template <typename T, int MR, int NV, int NW>
+__device__ __forceinline__ void join_row(const AttnParams &p, const int4 &d, int r, int w, int lane, float (*sm)[2], float (*so)[NV * 128])
 {
     const int row = d.x, item = d.y >> 8, n = d.w, D = p.a.d.headdim;
     const int kvh = p.nhb == 1 ? item : item / p.nhb, hb = item - kvh * p.nhb, nh = min(p.gh, p.group - hb * p.gh);
-    float mm = -INFINITY, ll = 0.f, o[2][4] = {};
+    float mm = -INFINITY, ll = 0.f, o[NV][4] = {};
     // part i lies in the head's i-th share from d.z on: slot 1 of the first, slot 0 of the others
     for (int i = w; i < n; i += 4 * NW) {
         float pm[4], pl[4];
-        float4 v[4][2];
+        float4 v[4][NV];
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
             pm[b] = -INFINITY;
             pl[b] = 0.f;
-            v[b][0] = v[b][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int x = 0; x < NV; ++x)
+                v[b][x] = make_float4(0.f, 0.f, 0.f, 0.f);
             const int part = i + NW * b;
             if (part < n) {
                 const size_t at = (((size_t)d.z + (size_t)part * p.items) * 2 + (part == 0 ? 1 : 0)) * MR + r;
@@ -1553,7 +1555,7 @@ __device__ __forceinline__ void join_row(const AttnParams &p, const int4 &d, int
                 pm[b] = t.y == 0.f ? -INFINITY : t.x;   // (a part that saw nothing)
                 pl[b] = t.y;
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
+                for (int x = 0; x < NV; ++x)
                     if (4 * lane + 128 * x < D)
                         v[b][x] = *reinterpret_cast<const float4 *>(p.part_o + at * D + 4 * lane + 128 * x);
             }
@@ -1563,7 +1565,7 @@ __device__ __forceinline__ void join_row(const AttnParams &p, const int4 &d, int
         mm = mn;
         ll *= keep;
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int x = 0; x < NV; ++x)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 o[x][e] *= keep;
@@ -1572,7 +1574,7 @@ __device__ __forceinline__ void join_row(const AttnParams &p, const int4 &d, int
             const float f = exp2_fast(pm[b] - base);
             ll += pl[b] * f;
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
+            for (int x = 0; x < NV; ++x) {
                 o[x][0] += f * v[b][x].x;
                 o[x][1] += f * v[b][x].y;
                 o[x][2] += f * v[b][x].z;
@@ -1583,7 +1585,7 @@ __device__ __forceinline__ void join_row(const AttnParams &p, const int4 &d, int
     float base = mm == -INFINITY ? 0.f : mm;
     if (NW > 1) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int x = 0; x < NV; ++x)
             *reinterpret_cast<float4 *>(&so[w][4 * lane + 128 * x]) = make_float4(o[x][0], o[x][1], o[x][2], o[x][3]);
         if (lane == 0) {
             sm[w][0] = mm;
@@ -1599,7 +1601,7 @@ __device__ __forceinline__ void join_row(const AttnParams &p, const int4 &d, int
         base = top == -INFINITY ? 0.f : top;
         ll = 0.f;
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int x = 0; x < NV; ++x)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 o[x][e] = 0.f;
@@ -1608,7 +1610,7 @@ __device__ __forceinline__ void join_row(const AttnParams &p, const int4 &d, int
             const float f = exp2_fast(sm[i][0] - base);
             ll += sm[i][1] * f;
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
+            for (int x = 0; x < NV; ++x) {
                 const float4 v = *reinterpret_cast<const float4 *>(&so[i][4 * lane + 128 * x]);
                 o[x][0] += f * v.x;
                 o[x][1] += f * v.y;
@@ -1621,7 +1623,7 @@ __device__ __forceinline__ void join_row(const AttnParams &p, const int4 &d, int
     const int j = (d.y & 0xff) == 1 ? 0 : r / nh, h = kvh * p.group + hb * p.gh + (r - j * nh);
     T *out = static_cast<T *>(p.a.out) + (long long)(row + j) * p.a.d.o_stride[0] + (long long)h * p.a.d.o_stride[1];
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+    for (int x = 0; x < NV; ++x)
         if (4 * lane + 128 * x < D)
             store4(out + 4 * lane + 128 * x, make_float4(o[x][0] * inv, o[x][1] * inv, o[x][2] * inv, o[x][3] * inv));
     if (p.a.lse && lane == 0)
@@ -1634,20 +1636,21 @@ __device__ __forceinline__ int desc_rows(const AttnParams &p, const int4 &d)
     return d.x < 0 ? 0 : (d.y & 0xff) * min(p.gh, p.group - hb * p.gh);
 }
 
-constexpr int kJoinWarps = 8;
 // Shares of a block of the join (where they are warps'): several only for tiles of a
 // few rows, which leave the block's other warps idle (27 requests of 5 rows, window
-// 665: 29 us with one share per block, 46 with four; fp32 tiles of one row, 576
+// 665: 28 us with one share per block, 46 with four; fp32 tiles of one row, 576
 // tiles: 51.5 with one, 50.1 with four).
 template <int MR> constexpr int kJoinShares = MR >= 8 ? 1 : 4;
 
-// SOLO: few parts; a warp per row, a block per CTA of the first launch.  Else many
-// parts: a block per tile and row.
-template <typename T, int MR, bool SOLO>
+// NV: float4 of a row per lane.  SOLO: few parts, a warp per row.  Else many parts: a
+// block per tile and row.
+constexpr int kJoinWarps = 8;   // of a block
+template <typename T, int MR, int NV, bool SOLO>
 __global__ void __launch_bounds__(32 * kJoinWarps) ssd_paged_attn_join_kernel(const __grid_constant__ AttnParams p)
 {
-    __shared__ float sm[kJoinWarps][2];
-    __shared__ __align__(16) float so[kJoinWarps][256];
+    constexpr int NW = kJoinWarps;
+    __shared__ float sm[NW][2];
+    __shared__ __align__(16) float so[NW][NV * 128];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -1662,8 +1665,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) ssd_paged_attn_join_kernel(co
 #pragma unroll
         for (int k = 0; k < kJoinShares<MR>; ++k) {
             const int rows = d[k].w > 16 ? 0 : desc_rows(p, d[k]);
-            for (; at < rows; at += kJoinWarps)
-                join_row<T, MR, 1>(p, d[k], at, 0, lane, sm, so);
+            for (; at < rows; at += NW)
+                join_row<T, MR, NV, 1>(p, d[k], at, 0, lane, sm, so);
             at -= rows;
         }
 #pragma unroll 1
@@ -1671,14 +1674,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) ssd_paged_attn_join_kernel(co
             const int4 t = k == 0 ? d[0] : k == 1 ? d[1 % kJoinShares<MR>] : k == 2 ? d[2 % kJoinShares<MR>] : d[3 % kJoinShares<MR>];
             const int rows = t.w > 16 ? desc_rows(p, t) : 0;
             for (int r = 0; r < rows; ++r) {
-                join_row<T, MR, kJoinWarps>(p, t, r, w, lane, sm, so);
+                join_row<T, MR, NV, NW>(p, t, r, w, lane, sm, so);
                 __syncthreads();   // (the next row's sums go where these are)
             }
         }
     } else {
         const int4 d = p.desc[blockIdx.x];
         if ((int)blockIdx.y < desc_rows(p, d))
-            join_row<T, MR, kJoinWarps>(p, d, blockIdx.y, w, lane, sm, so);
+            join_row<T, MR, NV, NW>(p, d, blockIdx.y, w, lane, sm, so);
     }
 }
 
@@ -1733,7 +1736,7 @@ cudaError_t launch(AttnParams &p, void *workspace, cudaStream_t stream)
     cfg.gridDim = SOLO ? dim3((p.ndesc + kJoinShares<M::MR> - 1) / kJoinShares<M::MR>) : dim3(p.ndesc, p.tok * p.gh);
     cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, ssd_paged_attn_join_kernel<T, M::MR, SOLO>, p);
+    e = cudaLaunchKernelEx(&cfg, ssd_paged_attn_join_kernel<T, M::MR, (M::kDim + 127) / 128, SOLO>, p);
     if (e == cudaSuccess)
         note_launches(1);
     return e;
