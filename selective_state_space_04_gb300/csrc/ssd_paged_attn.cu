@@ -73,6 +73,7 @@ cudaError_t attn_launch(const AttnArgs &a, void *workspace, cudaStream_t stream)
     p.page = fast_div(a.d.page_size);
     p.by_items = fast_div(p.items);
     p.by_tok = fast_div(p.tok);
+    p.most = (int)most_tiles(p);
     p.few = most_tiles(p) <= kFewTiles && a.d.nreq <= kFewTiles &&
             kFewTiles * ((int64_t)a.d.page_size * a.d.max_pages / 16 + 8) < (INT64_C(1) << 31);
     p.sms = sm_count();

@@ -21,11 +21,11 @@
 //
 // What bounds it.  Up to 16 rows per tile: the cache's bytes, each read once
 // (bf16 heads of 128, 8 of them, 128 requests of 1..4096 tokens, 1.08 GB: 173 us,
-// 6.2 TB/s; 128 requests of 500..12000 with 4 new tokens each: 505 us, 6.5 TB/s).
+// 6.2 TB/s; 128 requests of 500..12000 with 4 new tokens each: 498 us, 6.6 TB/s).
 // Little work: a chain of dependent steps -- finding the share, table entry, keys,
-// values, join -- of 7 to 10 us (one request of 1000 tokens: 7.8 us).  More rows:
+// values, join -- of 7 to 10 us (one request of 1000 tokens: 8 us).  More rows:
 // the products and the softmax beside them, on two warps per scheduler, which is
-// what the output rows' registers leave (64 requests of 100..8000, 20 rows: 197 us,
+// what the output rows' registers leave (64 requests of 100..8000, 20 rows: 196 us,
 // 5.4 TB/s; a whole prompt of 8192 tokens, 32 heads of 128: 2.8 ms, 0.20 PFLOP/s).
 //
 // The running form: with s2 = scale log2(e) q.k, m = max s2 so far,
@@ -340,12 +340,12 @@ __device__ __forceinline__ Shares locate(const AttnParams &p, int *counts, long 
         for (int r = r0; r < r1; ++r) {
             int s, e;
             request_rows(p, r, s, e);
-            counts[r] = (int)at;
+            counts[r] = (int)min(at, (long long)p.most);   // (a start array that descends could have more)
             at += (e - s + p.tok - 1) / p.tok;
         }
+        ntiles = min(all, (long long)p.most);
         if (tid == 0)
-            counts[nreq] = (int)all;
-        ntiles = all;
+            counts[nreq] = (int)ntiles;
         __syncthreads();
     }
     const long long run = (ntiles + kThreads - 1) / kThreads, t0 = min((long long)tid * run, ntiles), t1 = min(t0 + run, ntiles);
@@ -599,7 +599,7 @@ struct Mma {
     using T = __nv_bfloat16;
     static constexpr int MR = 16 * NM, kDim = DP, kUnit = 16 * NT;
     static constexpr bool kExact = EX;
-    // Query rows stay in registers, but for 64 KB of output rows per warp and
+    // Query rows stay in registers, but for 16 KB of output rows per warp and
     // more (256 of a lane's registers are not enough for both): then in shared
     // memory, read anew for each unit.
     static constexpr bool kQSmem = NM * DP >= 256;

@@ -30,6 +30,7 @@ struct AttnParams {
     int gh;             // query heads of a tile (group, or a part of it when it is larger than MR)
     int nhb;            // head blocks per key-value head
     int tok;            // most new tokens of a tile
+    int most;           // tiles that the sizes allow at most
     int items;          // nkv * nhb: tiles of the same rows
     int seg;            // 16-byte segments per row of K or V
     uint32_t kpage, ktok, vpage, vtok;   // strides in 16 bytes
