@@ -230,6 +230,22 @@ def test_large_scores(ssd, dtype):
     assert (np.abs(lse.double().cpu().numpy() - rlse) <= rel + 2.0 ** -20 * np.abs(rlse)).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("up", [True, False])
+@pytest.mark.parametrize("D,new", [(64, 1), (128, 5), (80, 5)])
+def test_scores_that_climb_or_fall(ssd, dtype, up, D, new):
+    # from 0 to 20 (or back) along 700 tokens: within a unit by less than the maximum may lag behind, over all by more
+    c = make(31, [700, 260], [new, new], 4, 1, D, 24, dtype)
+    c["q"] *= 0.05
+    c["q"][:, :, 0] = 4.0
+    for r, n in enumerate((700, 260)):
+        t = np.arange(n)
+        page = torch.from_numpy(c["table"][r].numpy()[t // 24].astype(np.int64))
+        climb = torch.from_numpy(5.0 * (t if up else 700 - t) / 700).to(dtype)
+        c["kc"][page, torch.from_numpy(t % 24), :, 0] = climb[:, None]
+    check(*run(ssd, c, scale=1.0), c, scale=1.0)
+
+
 def test_infinite_and_nan_values_reach_only_rows_that_see_them(ssd):
     # the last token's value is infinite: only the last of three rows sees it
     c = make(20, [50], [3], 4, 2, 64, 16, BF)
