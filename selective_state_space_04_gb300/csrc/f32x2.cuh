@@ -1,5 +1,5 @@
 // f32x2.cuh -- two fp32 lanes in one 64-bit register pair, and the packed
-// multiply and FMA of sm_100 and later (each lane rounded as fmaf / __fmul_rn,
+// add, multiply and FMA of sm_100 and later (each lane rounded as fmaf / __fmul_rn,
 // so a packed step gives the bits of the two scalar ones).
 #pragma once
 
@@ -30,6 +30,13 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c)
 {
     f32x2 d;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+// elementwise a + b
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b)
+{
+    f32x2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
 // elementwise a * b

@@ -18,7 +18,7 @@ struct AttnParams {
     AttnArgs a;
     FastDiv page;
     float *part_o;      // [shares][2][MR][D] partial rows
-    float *part_ml;     // [shares][2][MR][2] their maxima (base 2) and sums
+    float *part_ml;     // [shares][2][MR][2] their maxima (of the scores before `f`) and sums
     int4 *desc;         // the cut tiles: first row, tokens | item << 8, first share, parts; x -1: none.  Shares of
                         // warps: [shares], of the tile that starts in a share; shares of CTAs: [most tiles x items]
     int ndesc;          // entries of it
