@@ -484,7 +484,7 @@ struct Loader {
         if (u >= 0) {
             const int tok = (c.t.ub + u) * UT + (ALIGNED ? (kSub > 1 ? lane & 16 : 0) : lane % UT);
             if (tok < c.t.end)   // (16 tokens are in the page of the first of them)
-                page = __ldg(table + div_fast(p.page, tok));
+                page = table[div_fast(p.page, tok)];   // (not through the read-only path: the launch before may write it)
         }
     }
     __device__ __forceinline__ void offsets(const AttnParams &p, int lane)
