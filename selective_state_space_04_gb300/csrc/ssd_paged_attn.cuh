@@ -92,16 +92,26 @@ struct Tile {
     int first, end, ub, units;
 };
 
+// Positions are any int32, and the last one seen may be 2^31 - 2: neither may
+// overflow.  The end of what the row at `pos` sees, and its first position:
+__device__ __forceinline__ int seen_end(const AttnParams &p, int pos)
+{
+    return pos < 0 ? 0 : min(pos, p.a.d.max_pages * p.a.d.page_size - 1) + 1;
+}
+__device__ __forceinline__ int seen_first(const AttnParams &p, int pos)
+{
+    return p.a.d.window > 0 && pos >= p.a.d.window ? pos - p.a.d.window + 1 : 0;
+}
+
 // the extent from the positions of the first and the last row
 template <int UT>
 __device__ __forceinline__ void tile_extent(const AttnParams &p, Tile &t, int p0, int p1)
 {
-    const int limit = p.a.d.max_pages * p.a.d.page_size;
-    t.end = p1 < 0 ? 0 : min(p1, limit - 1) + 1;
-    t.first = p.a.d.window > 0 ? max(0, p0 - p.a.d.window + 1) : 0;
-    t.first = min(t.first, t.end);
+    t.end = seen_end(p, p1);
+    t.first = min(seen_first(p, p0), t.end);
     t.ub = t.first / UT;
-    t.units = max(1, (t.end + UT - 1) / UT - t.ub);   // (a tile that sees nothing still writes its rows)
+    const int units = (int)(((uint32_t)t.end + UT - 1) / UT);
+    t.units = max(1, units - t.ub);   // (a tile that sees nothing still writes its rows)
 }
 
 // rows [s, e) of request r, clamped to the rows there are
@@ -340,14 +350,14 @@ __device__ __forceinline__ Shares locate(const AttnParams &p, int *counts, long 
         for (int r = r0; r < r1; ++r) {
             int s, e;
             request_rows(p, r, s, e);
-            n += (e - s + p.tok - 1) / p.tok;
+            n += ((uint32_t)(e - s) + p.tok - 1) / p.tok;
         }
         long long at = block_exclusive(n, &all, tmp);
         for (int r = r0; r < r1; ++r) {
             int s, e;
             request_rows(p, r, s, e);
             counts[r] = (int)min(at, (long long)p.most);   // (a start array that descends could have more)
-            at += (e - s + p.tok - 1) / p.tok;
+            at += ((uint32_t)(e - s) + p.tok - 1) / p.tok;
         }
         ntiles = min(all, (long long)p.most);
         if (tid == 0)
@@ -634,7 +644,6 @@ struct Mma {
     {
         const int kvh = p.nhb == 1 ? item : item / p.nhb, hb = item - kvh * p.nhb, D = dim(p);
         const int h0 = hb * p.gh, nh = min(p.gh, p.group - h0), rows = t.nq * nh;
-        const int limit = p.a.d.max_pages * p.a.d.page_size;
         const uint32_t keep = p.sign == 0 ? 0u : 0xffffffffu, flip = p.sign < 0 ? 0x80008000u : 0u;
 #pragma unroll
         for (int mt = 0; mt < NM; ++mt)
@@ -642,8 +651,8 @@ struct Mma {
             for (int x = 0; x < 2; ++x) {
                 const int r = mt * 16 + x * 8 + (lane >> 2), rr = min(r, rows - 1), j = t.nq == 1 ? 0 : rr / nh, g = rr - j * nh;
                 const int pos = p.a.positions[t.row + j];
-                hi[mt][x] = pos < 0 ? 0 : min(pos, limit - 1) + 1;
-                lo[mt][x] = p.a.d.window > 0 ? max(0, pos - p.a.d.window + 1) : 0;
+                hi[mt][x] = seen_end(p, pos);
+                lo[mt][x] = seen_first(p, pos);
                 m[mt][x] = -INFINITY;
                 l[mt][x] = 0.f;
                 const T *src = static_cast<const T *>(p.a.q) + (long long)(t.row + j) * p.a.d.q_stride[0] +
@@ -717,7 +726,7 @@ struct Mma {
             }
         }
         constexpr uint32_t kAll = NT == 1 ? 0xffffu : 0xffffffffu;
-        if (mask != kAll || tok0 < all0 || tok0 + kUnit > all1) {
+        if (mask != kAll || tok0 < all0 || tok0 > all1 - kUnit) {
 #pragma unroll
             for (int n = 0; n < 2 * NT; ++n)
 #pragma unroll
@@ -863,7 +872,7 @@ struct Mma {
     __device__ __forceinline__ void values(const AttnParams &p, char *slot_ptr, uint32_t mask, int tok0, int all0, int all1, int lane)
     {
         const int D = dim(p), stride = kRowBytes;
-        if (tok0 < all0 || tok0 + kUnit > all1) {
+        if (tok0 < all0 || tok0 > all1 - kUnit) {
             // bit tt: every row sees token tok0 + tt
             const int a0 = min(max(all0 - tok0, 0), kUnit), a1 = min(max(all1 - tok0, 0), kUnit);
             const uint32_t all = a1 > a0 ? (0xffffffffu >> (32 - a1)) & (0xffffffffu << a0) : 0u;
@@ -1023,13 +1032,12 @@ struct Simt {
     {
         const int kvh = p.nhb == 1 ? item : item / p.nhb, hb = item - kvh * p.nhb, D = dim(p);
         const int h0 = hb * p.gh, nh = min(p.gh, p.group - h0), rows = t.nq * nh;
-        const int limit = p.a.d.max_pages * p.a.d.page_size;
 #pragma unroll
         for (int r = 0; r < MR; ++r) {
             const int rr = min(r, rows - 1), j = t.nq == 1 ? 0 : rr / nh, g = rr - j * nh;
             const int pos = p.a.positions[t.row + j];
-            hi[r] = pos < 0 ? 0 : min(pos, limit - 1) + 1;
-            lo[r] = p.a.d.window > 0 ? max(0, pos - p.a.d.window + 1) : 0;
+            hi[r] = seen_end(p, pos);
+            lo[r] = seen_first(p, pos);
             m[r] = -INFINITY;
             l[r] = 0.f;
             const float *src = static_cast<const float *>(p.a.q) + (long long)(t.row + j) * p.a.d.q_stride[0] +
@@ -1076,7 +1084,7 @@ struct Simt {
             }
         }
         constexpr uint32_t kAll = kUnit == 16 ? 0xffffu : 0xffffffffu;
-        const bool masked = mask != kAll || tok0 < all0 || tok0 + kUnit > all1;
+        const bool masked = mask != kAll || tok0 < all0 || tok0 > all1 - kUnit;
         float sc[MR];
         bool past = false;
 #pragma unroll
@@ -1162,7 +1170,7 @@ struct Simt {
     }
     __device__ __forceinline__ void values(const AttnParams &p, char *slot, uint32_t mask, int tok0, int all0, int all1, int lane)
     {
-        if (tok0 < all0 || tok0 + kUnit > all1)
+        if (tok0 < all0 || tok0 > all1 - kUnit)
             add_values<true>(p, slot, tok0, lane);
         else
             add_values<false>(p, slot, tok0, lane);
@@ -1423,10 +1431,8 @@ __global__ void __launch_bounds__(kThreads, MB) ssd_paged_attn_kernel(const __gr
     // tokens that every row of the tile sees: from the last row's first to the first row's last
     int all0, all1;
     auto begin = [&]() {
-        const int limit = p.a.d.max_pages * p.a.d.page_size;
-        const int p0 = p.a.positions[cur.t.row], p1 = p.a.positions[cur.t.row + cur.t.nq - 1];
-        all1 = p0 < 0 ? 0 : min(p0, limit - 1) + 1;
-        all0 = p.a.d.window > 0 ? max(0, p1 - p.a.d.window + 1) : 0;
+        all1 = seen_end(p, p.a.positions[cur.t.row]);
+        all0 = seen_first(p, p.a.positions[cur.t.row + cur.t.nq - 1]);
         math.begin(p, cur.t, item, lane);
     };
     begin();   // (its loads are on their way beside the first table entry's)
