@@ -529,9 +529,11 @@ typedef struct ssd_qk_dims {
  *   n = x / sqrt(mean(x^2) + eps) * weight
  *   (a, b) -> (a cos - b sin, b cos + a sin) for each rotated pair of n
  * with cos and sin [max_pos, R/2] fp32 taken at the token's position; computed
- * in fp32 and rounded once.  Inputs q [ntokens, Hq, D], k [ntokens, Hk, D],
- * q_weight and k_weight [D] fp32 (NULL: ones), positions [ntokens].  Outputs
- * q_out, k_out (k_out may be NULL when there is a cache).
+ * in fp32 and rounded once.  A row of zeros stays zero, with eps 0 too (its
+ * gradient is zero then, and it has no part in the weights').  Inputs q
+ * [ntokens, Hq, D], k [ntokens, Hk, D], q_weight and k_weight [D] fp32 (NULL:
+ * ones), positions [ntokens].  Outputs q_out, k_out (k_out may be NULL when
+ * there is a cache).
  * With k_cache (then v, v_cache and slots are required too): token t's keys
  * and its v [ntokens, Hk, D], unchanged, are also written to slot slots[t] of
  * the caches; a slot outside 0 .. npages * page_size - 1 is not written.
