@@ -540,7 +540,9 @@ typedef struct ssd_qk_dims {
  * A token whose position is outside 0 .. max_pos - 1 is padding: its q_out and
  * k_out are zero and nothing of it goes to the cache.
  * q_out may be q, and k_out k, with equal strides (in place); outputs overlap
- * no other input.  Two tokens of a call must not have the same slot.
+ * no other input.  The caches' rows are distinct memory, and the two caches may
+ * be views of one buffer but share no bytes.  Two tokens of a call must not have
+ * the same slot.
  */
 ssd_status_t ssd_qk_norm_rope_fwd(const void *q, const void *k, const void *v,
                                   const float *q_weight, const float *k_weight,

@@ -371,6 +371,94 @@ bool overlaps(const Strided &a, const Strided &b)
     return !(delta >= wa && delta + wb <= a.s0);
 }
 
+// Rows of `width` bytes at every combination of places on three axes.
+struct Rows {
+    const void *p;
+    int64_t width;
+    int64_t count[3], stride[3];   // strides >= 0, in bytes
+};
+
+struct StepAxis {
+    int64_t stride, lo, hi;   // steps d with lo <= d <= hi
+};
+
+int64_t div_down(int64_t a, int64_t b) { return a / b - (a % b < 0); }   // b > 0
+
+// Whether steps d exist, some of them not 0 unless `moved`, for which
+// lo < sum of d * stride < hi.  Axes by falling strides: where each is longer than
+// all after it together, two or three d per axis are in question.  `budget`: how
+// many places to look at before taking it that there are such steps.
+bool steps_between(const StepAxis *x, int n, int64_t lo, int64_t hi, bool moved, int &budget)
+{
+    if (--budget < 0)
+        return true;
+    if (n == 0)
+        return moved && lo < 0 && hi > 0;
+    int64_t least = 0, most = 0;   // what the axes after this one add
+    for (int i = 1; i < n; ++i) {
+        least += x[i].lo * x[i].stride;
+        most += x[i].hi * x[i].stride;
+    }
+    const int64_t s = x[0].stride, from = std::max(x[0].lo, div_down(lo - most, s) + 1),
+                  to = std::min(x[0].hi, -div_down(least - hi, s) - 1);
+    for (int64_t d = from; d <= to; ++d)
+        if (steps_between(x + 1, n - 1, lo - d * s, hi - d * s, moved || d != 0, budget))
+            return true;
+    return false;
+}
+
+constexpr int kViewBudget = 4096;
+
+// whether two sets of rows share bytes
+bool overlaps(const Rows &a, const Rows &b)
+{
+    StepAxis x[6];
+    int n = 0;
+    bool used[3] = {};
+    if (!a.p || !b.p)
+        return false;
+    for (int i = 0; i < 3; ++i)
+        if (a.count[i] <= 0 || b.count[i] <= 0)
+            return false;
+    for (int i = 0; i < 3; ++i) {
+        if (a.count[i] <= 1 || a.stride[i] == 0)
+            continue;
+        StepAxis &t = x[n++] = {a.stride[i], 0, a.count[i] - 1};
+        for (int j = 0; j < 3; ++j)
+            if (!used[j] && b.count[j] > 1 && b.stride[j] == a.stride[i]) {
+                used[j] = true;
+                t.lo = 1 - b.count[j];
+                break;
+            }
+    }
+    for (int j = 0; j < 3; ++j)
+        if (!used[j] && b.count[j] > 1 && b.stride[j] != 0)
+            x[n++] = {b.stride[j], 1 - b.count[j], 0};
+    std::sort(x, x + n, [](const StepAxis &u, const StepAxis &v) { return u.stride > v.stride; });
+    const int64_t delta = (int64_t)((uintptr_t)b.p - (uintptr_t)a.p);
+    int budget = kViewBudget;
+    return steps_between(x, n, delta - a.width, delta + b.width, true, budget);
+}
+
+// whether the rows are all distinct memory
+bool distinct_rows(const Rows &a)
+{
+    StepAxis x[3];
+    int n = 0;
+    for (int i = 0; i < 3; ++i) {
+        if (a.count[i] <= 0)
+            return true;
+        if (a.count[i] > 1) {
+            if (a.stride[i] == 0)
+                return false;
+            x[n++] = {a.stride[i], 1 - a.count[i], a.count[i] - 1};
+        }
+    }
+    std::sort(x, x + n, [](const StepAxis &u, const StepAxis &v) { return u.stride > v.stride; });
+    int budget = kViewBudget;
+    return !a.p || !steps_between(x, n, -a.width, a.width, false, budget);
+}
+
 bool same_view(const Strided &a, const Strided &b)
 {
     return a.p == b.p && a.n0 == b.n0 && a.n1 == b.n1 && a.s0 == b.s0 && a.s1 == b.s1;
@@ -1501,6 +1589,14 @@ ssd_status_t ssd_qk_norm_rope_fwd(const void *q, const void *k, const void *v, c
     for (const auto &f : flat)
         if (overlaps(f.p, f.bytes, k_cache, kcb) || overlaps(f.p, f.bytes, v_cache, vcb))
             return SSD_ERR_ALIASING;
+    if (cache) {
+        const auto rows = [&](const void *p, const int64_t *s) {
+            return Rows{p, w, {dims->npages, dims->page_size, Hk}, {s[0] * es, s[1] * es, s[2] * es}};
+        };
+        const Rows kr = rows(k_cache, dims->kc_stride), vr = rows(v_cache, dims->vc_stride);
+        if (overlaps(kr, vr) || !distinct_rows(kr) || !distinct_rows(vr))
+            return SSD_ERR_ALIASING;
+    }
     if (T == 0)
         return SSD_OK;
     QkArgs qa{};
