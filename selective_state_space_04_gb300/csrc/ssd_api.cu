@@ -355,22 +355,6 @@ struct Strided {
     int64_t extent() const { return n0 > 0 && n1 > 0 ? (n0 - 1) * s0 + (n1 - 1) * s1 + width : 0; }
 };
 
-// whether two strided operands share bytes.  Views of one fused buffer (equal
-// row strides, each row's heads within the stride) are told apart exactly;
-// otherwise overlapping extents count as overlap.
-bool overlaps(const Strided &a, const Strided &b)
-{
-    if (!overlaps(a.p, a.extent(), b.p, b.extent()))
-        return false;
-    const int64_t wa = (a.n1 - 1) * a.s1 + a.width, wb = (b.n1 - 1) * b.s1 + b.width;
-    if (a.s0 != b.s0 || a.s0 <= 0 || wa > a.s0 || wb > a.s0)
-        return true;
-    int64_t delta = (int64_t)((uintptr_t)b.p - (uintptr_t)a.p) % a.s0;
-    if (delta < 0)
-        delta += a.s0;
-    return !(delta >= wa && delta + wb <= a.s0);
-}
-
 // Rows of `width` bytes at every combination of places on three axes.
 struct Rows {
     const void *p;
@@ -459,19 +443,13 @@ bool distinct_rows(const Rows &a)
     return !a.p || !steps_between(x, n, -a.width, a.width, false, budget);
 }
 
+Rows rows_of(const Strided &a) { return {a.p, a.width, {a.n0, a.n1, 1}, {a.s0, a.s1, 0}}; }
+bool overlaps(const Strided &a, const Strided &b) { return overlaps(rows_of(a), rows_of(b)); }
+bool distinct_rows(const Strided &a) { return distinct_rows(rows_of(a)); }
+
 bool same_view(const Strided &a, const Strided &b)
 {
     return a.p == b.p && a.n0 == b.n0 && a.n1 == b.n1 && a.s0 == b.s0 && a.s1 == b.s1;
-}
-
-// whether an output's [D] rows are all distinct memory
-bool distinct_rows(const Strided &a)
-{
-    if (!a.p || a.n0 <= 0)
-        return true;
-    const bool row_major = (a.n1 == 1 || a.s1 >= a.width) && (a.n0 == 1 || a.s0 >= (a.n1 - 1) * a.s1 + a.width);
-    const bool head_major = (a.n0 == 1 || a.s0 >= a.width) && (a.n1 == 1 || a.s1 >= (a.n0 - 1) * a.s0 + a.width);
-    return row_major || head_major;
 }
 
 bool aligned(const void *p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }

@@ -58,3 +58,61 @@ def test_caches_of_one_buffer(layout, dtype):
     want[0, slots // 8, slots % 8], want[1, slots // 8, slots % 8] = ko, v
     assert torch.equal(kc, want[0]) and torch.equal(vc, want[1])
     assert int((buf != 5).sum()) == int((want != 5).sum())
+
+
+def scratch(ssd, ptrs, **kw):
+    """The backward with a workspace that is one byte short: found after the checks of the views, before any CUDA call."""
+    n = ctypes.c_uint64(0)
+    assert ssd.lib().ssd_qk_norm_rope_bwd_workspace_size(qk_dims(ssd, **kw), ctypes.byref(n)) == 0 and n.value > 0
+    return bwd(ssd, ptrs, ws=(at(20), n.value - 1), **kw)
+
+
+@pytest.mark.parametrize("ptrs,kw,status", [
+    # gradients into a fused [token, head, q/k/v, 64] gradient: rows of one between rows of the other
+    (dict(dq=at(9), dk=at(9) + W), dict(nheads_q=2, dq_stride=(384, 192), dk_stride=(384, 192)), SCRATCH),
+    # ... and over the incoming gradients, views of another such buffer
+    (dict(dq_out=at(9), dk_out=at(9) + W, dq=at(9), dk=at(9) + W),
+     dict(nheads_q=2, qo_stride=(384, 192), ko_stride=(384, 192), dq_stride=(384, 192), dk_stride=(384, 192)), SCRATCH),
+    # heads outermost, tokens of one buffer in turn
+    (dict(dq=at(9), dk=at(9) + W), dict(nheads_q=2, dq_stride=(128, 2048), dk_stride=(128, 2048)), SCRATCH),
+    # rows of different strides in one buffer: every second place of 64, then places of the other
+    (dict(dq=at(9), dk=at(9) + W), dict(nheads_q=2, dq_stride=(384, 128), dk_stride=(512, 128)), SCRATCH),
+    (dict(dq=at(9), dk=at(9) + 4 * W), dict(nheads_q=2, dq_stride=(384, 128), dk_stride=(512, 128)), ALIASING),
+    (dict(dq=at(9), dk=at(9) + W // 2), dict(nheads_q=2, dq_stride=(384, 192), dk_stride=(384, 192)), ALIASING),
+    (dict(dq=at(9), dk=at(9) + 2 * 384 * 2), dict(nheads_q=2, dq_stride=(384, 192), dk_stride=(384, 192)), ALIASING),
+    (dict(dk=at(1) + W), dict(k_stride=(256, 128), dk_stride=(256, 128)), SCRATCH),
+    (dict(dk=at(1) + W), dict(k_stride=(256, 64), dk_stride=(256, 64)), ALIASING),
+    (dict(), dict(dq_stride=(64, 64)), ALIASING),
+    (dict(), dict(dq_stride=(64, 1024)), SCRATCH),
+])
+def test_gradients_of_fused_buffers(ssd, ptrs, kw, status):
+    assert scratch(ssd, ptrs, **kw) == status
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("order", ["thcd", "tchd", "htcd", "cthd", "chtd", "hctd"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_in_place_in_a_fused_projection(order, dtype):
+    # q, k, v of one buffer: tokens t, heads h and the three c in any order
+    from selective_state_space_04_gb300 import build
+    build.build()
+    from selective_state_space_04_gb300 import ssd
+    T, H, D = 37, 4, 64
+    size = dict(t=T, h=H, c=3, d=D)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    buf, grad = (torch.randn([size[x] for x in order], device="cuda", generator=g).to(dtype) for _ in range(2))
+    perm = [order.index(x) for x in "cthd"]
+    q, k, v = buf.permute(perm)
+    dq, dk, dv = grad.permute(perm)
+    cos, sin = ssd.rope_table(64, D)
+    tab = (torch.ones(D, device="cuda"), None, cos, sin, torch.arange(T, dtype=torch.int32, device="cuda"))
+    c = lambda x: x.clone(memory_format=torch.contiguous_format)  # noqa: E731
+    v0, dv0 = c(v), c(dv)
+    want = ssd.qk_norm_rope_bwd(c(q), c(k), *tab, c(dq), c(dk))
+    got = ssd.qk_norm_rope_bwd(q, k, *tab, dq, dk, dq=dq, dk=dk)
+    qo, ko = ssd.qk_norm_rope_fwd(c(q), c(k), *tab)
+    ssd.qk_norm_rope_fwd(q, k, *tab, q_out=q, k_out=k)
+    torch.cuda.synchronize()
+    assert torch.equal(dq, want["dq"]) and torch.equal(dk, want["dk"]) and torch.equal(dv, dv0)
+    assert all(torch.equal(got[n], want[n]) for n in ("dq_weight", "dk_weight"))
+    assert torch.equal(q, qo) and torch.equal(k, ko) and torch.equal(v, v0)
