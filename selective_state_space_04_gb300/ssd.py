@@ -500,7 +500,15 @@ def _addr(t):
 
 
 def _stream_ptr(device, stream):
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    """The stream's handle.  The library works on the thread's current device, so that has to be the tensors', and the
+    stream's: checked on every call."""
+    if device.index != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on {device}, which is not the current device")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    if stream.device_index != device.index:
+        raise ValueError(f"the tensors are on {device}, the stream is not")
+    return stream.cuda_stream
 
 
 def _layout(t):
@@ -551,11 +559,11 @@ def _cache_args(device, dtype, k_cache, v_cache, heads, D):
             raise ValueError(f"{name} must be a {dtype} tensor on {device} with a contiguous last axis")
 
 
-def _workspace(workspace):
+def _workspace(workspace, device):
     if workspace is None:
         return None, 0
-    if not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -592,10 +600,11 @@ def paged_plan(lens, new_lens, block_table, free_ring, ring_pos, *, page_size, m
         _vectors(dev, (("ring_pos", ring_pos, 2), ("out ring_pos", o["ring_pos"], 2), ("slots", o["slots"], max_tokens)),
                  torch.int64)
         d = _remember(key, SsdPlanDims(R, max_tokens, free_ring.shape[0], page_size, block_table.shape[1], 0, 0))
+    st = _stream_ptr(dev, stream)
     _check(_lib.ssd_paged_plan(lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), free_ring.data_ptr(),
                                ring_pos.data_ptr(), o["lens"].data_ptr(), o["granted"].data_ptr(), o["start"].data_ptr(),
                                o["positions"].data_ptr(), o["token_req"].data_ptr(), o["slots"].data_ptr(),
-                               o["ring_pos"].data_ptr(), o["counts"].data_ptr(), d, _stream_ptr(dev, stream)),
+                               o["ring_pos"].data_ptr(), o["counts"].data_ptr(), d, st),
            "ssd_paged_plan")
     return out
 
@@ -659,13 +668,14 @@ def qk_norm_rope_fwd(q, k, q_weight, k_weight, cos, sin, positions, *, eps=1e-6,
         elif k_out is None and not return_k:
             raise ValueError("return_k=False takes a cache to write the keys to")
         _remember(key, d)
+    st = _stream_ptr(dev, stream)
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
     if k_out is None and return_k:
         k_out = torch.empty(k.shape, dtype=q.dtype, device=dev)
     _check(_lib.ssd_qk_norm_rope_fwd(q.data_ptr(), k.data_ptr(), _addr(v), _addr(q_weight), _addr(k_weight), cos.data_ptr(),
                                      sin.data_ptr(), positions.data_ptr(), q_out.data_ptr(), _addr(k_out), _addr(k_cache),
-                                     _addr(v_cache), _addr(slots), d, _stream_ptr(dev, stream)), "ssd_qk_norm_rope_fwd")
+                                     _addr(v_cache), _addr(slots), d, st), "ssd_qk_norm_rope_fwd")
     return q_out, k_out
 
 
@@ -685,16 +695,17 @@ def qk_norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, positions, dq_out, dk_o
         d.dq_stride = (q.shape[1] * D, D) if dq is None else dq.stride()[:2]
         d.dk_stride = (k.shape[1] * D, D) if dk is None else dk.stride()[:2]
         _remember(key, d)
+    st = _stream_ptr(dev, stream)
     if dq is None:
         dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
     if dk is None:
         dk = torch.empty(k.shape, dtype=q.dtype, device=dev)
     dqw, dkw = torch.empty(D, dtype=torch.float32, device=dev), torch.empty(D, dtype=torch.float32, device=dev)
-    ws, nws = _workspace(workspace)
+    ws, nws = _workspace(workspace, dev)
     _check(_lib.ssd_qk_norm_rope_bwd(q.data_ptr(), k.data_ptr(), _addr(q_weight), _addr(k_weight), cos.data_ptr(),
                                      sin.data_ptr(), positions.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(),
-                                     dq.data_ptr(), dk.data_ptr(), dqw.data_ptr(), dkw.data_ptr(), ws, nws, d,
-                                     _stream_ptr(dev, stream)), "ssd_qk_norm_rope_bwd")
+                                     dq.data_ptr(), dk.data_ptr(), dqw.data_ptr(), dkw.data_ptr(), ws, nws, d, st),
+           "ssd_qk_norm_rope_bwd")
     return dict(dq=dq, dk=dk, dq_weight=dqw, dk_weight=dkw)
 
 
@@ -746,14 +757,15 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, positions, start=None, *, s
         _vectors(dev, (("positions", positions, n), ("start", start, block_table.shape[0] + 1)), torch.int32)
         d.o_stride = (H * D, D) if out is None else out.stride()[:2]
         _remember(key, d)
+    st = _stream_ptr(dev, stream)
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=dev)
     if lse is None and return_lse:
         lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
-    ws, nws = _workspace(workspace)
+    ws, nws = _workspace(workspace, dev)
     _check(_lib.ssd_paged_attn_fwd(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-                                   positions.data_ptr(), _addr(start), out.data_ptr(), _addr(lse), ws, nws, d,
-                                   _stream_ptr(dev, stream)), "ssd_paged_attn_fwd")
+                                   positions.data_ptr(), _addr(start), out.data_ptr(), _addr(lse), ws, nws, d, st),
+           "ssd_paged_attn_fwd")
     return out, lse
 
 
