@@ -447,7 +447,10 @@ ssd_status_t ssd_scan_bwd(const void *x, const float *dt_raw, const float *dt_bi
  *
  * Arrays are DEVICE pointers of the current device, caller-owned.  Data
  * pointers are 16-byte aligned; positions, slots and the start array have
- * their type's alignment.  Calls enqueue on `stream` only, never synchronise,
+ * their type's alignment.  Queries, keys, values, their outputs and gradients,
+ * and the two caches among themselves, may be views that interleave in one
+ * buffer; an output that shares bytes with another operand is SSD_ERR_ALIASING,
+ * but for the in-place forms named below.  Calls enqueue on `stream` only, never synchronise,
  * may be captured into a CUDA graph, and return an ssd_status_t; nothing is
  * enqueued on an argument error.
  */
@@ -605,7 +608,9 @@ typedef struct ssd_attn_dims {
  * [nreq+1], ascending, as ssd_paged_plan writes it: request r has the rows
  * start[r] .. start[r+1] - 1, their positions ascending; rows from
  * start[nreq] on are padding.  nreq <= SSD_ATTN_MAX_REQUESTS then.
- * A row that sees nothing (position -1, padding) has out 0 and lse -inf.
+ * A row that sees nothing (a negative position, padding) has out 0 and lse
+ * -inf.  Infinities and NaN among the values that a row sees give what the sum
+ * gives.  However large finite scores are, weights come from their differences.
  * Positions past max_pages * page_size, and pages whose table entry is outside
  * 0 .. npages - 1, are not seen; table entries past a request's positions are not
  * read into the result, and neither are cache contents that a row does not

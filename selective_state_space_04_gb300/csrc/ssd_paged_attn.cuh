@@ -21,12 +21,12 @@
 //
 // What bounds it.  Up to 16 rows per tile: the cache's bytes, each read once
 // (bf16 heads of 128, 8 of them, 128 requests of 1..4096 tokens, 1.08 GB: 173 us,
-// 6.2 TB/s; 128 requests of 500..12000 with 4 new tokens each: 498 us, 6.6 TB/s).
+// 6.2 TB/s; 128 requests of 500..12000 with 4 new tokens each: 505 us, 6.5 TB/s).
 // Little work: a chain of dependent steps -- finding the share, table entry, keys,
 // values, join -- of 7 to 10 us (one request of 1000 tokens: 8 us).  More rows:
 // the products and the softmax beside them, on two warps per scheduler, which is
-// what the output rows' registers leave (64 requests of 100..8000, 20 rows: 196 us,
-// 5.4 TB/s; a whole prompt of 8192 tokens, 32 heads of 128: 2.8 ms, 0.20 PFLOP/s).
+// what the output rows' registers leave (64 requests of 100..8000, 20 rows: 195 us,
+// 5.5 TB/s; a whole prompt of 8192 tokens, 32 heads of 128: 2.73 ms, 0.20 PFLOP/s).
 //
 // The running form: with s = q.k (its sign that of the scaled score), f =
 // |scale| log2(e), m = max s so far, p = 2^(f (s - m)), l = sum p, o = sum p v;

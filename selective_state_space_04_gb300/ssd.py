@@ -491,6 +491,7 @@ def ssd_scan_bwd(x, dt_raw, dt_bias, A_log, B, C, D, init_state, dy, d_final=Non
 
 
 # ---- the attention layers of hybrid stacks: a step's plan, queries and keys, attention over the paged cache ----
+# Tensors, stream and workspace of a call are of the thread's current device (else ValueError).
 
 _DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
 
