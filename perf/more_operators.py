@@ -256,7 +256,7 @@ def _run_step(s):
     window = s["ring"][at[:, None], t % K].float()
     window = torch.where((t >= 0)[:, :, None], window, 0.0)
     window[:, K - 1] = s["xbc"].float()
-    conv = (window * s["cw"].t()).sum(1) + s["cb"]
+    conv = (window * s["cw"].flip(1).t()).sum(1) + s["cb"]   # (tap j multiplies the input j steps back)
     conv = conv / (1.0 + torch.exp(-conv))
     x = conv[:, :H * P].view(-1, H, P)
     B = conv[:, H * P:H * P + G * N].view(-1, G, 1, N).expand(-1, G, H // G, N).reshape(-1, H, 1, N)
@@ -407,9 +407,9 @@ def _exact_step(c, seed):
     for i, (slot, t) in enumerate(zip(s["slots"].tolist(), s["positions"].tolist())):
         if slot < 0:
             continue
-        u = cb + cw[:, K - 1] * xbc[i]
+        u = cb + cw[:, 0] * xbc[i]
         for back in range(1, min(K - 1, t) + 1):
-            u = u + cw[:, K - 1 - back] * ring[slot, (t - back) % K]
+            u = u + cw[:, back] * ring[slot, (t - back) % K]
         u = u * torch.sigmoid(u)
         x, B, C = u[:H * P].view(H, P), u[H * P:H * P + G * N].view(G, N)[head_group], u[H * P + G * N:].view(G, N)[head_group]
         dt = torch.logaddexp(s["dt"][i].double() + dt_bias, torch.zeros((), dtype=torch.float64, device="cuda"))
