@@ -630,6 +630,167 @@ ssd_status_t ssd_paged_attn_fwd(const void *q, const void *k_cache, const void *
                                 void *stream);
 ssd_status_t ssd_paged_attn_workspace_size(const ssd_attn_dims_t *dims, uint64_t *bytes);
 
+/*
+ * ---------------------------------------------------------------------------
+ * One layer's step around the scan: the norm in front with the residual's
+ * addition, products of 8-bit integers for the two projections, the gated norm
+ * into 8 bits, and the convolution and scan for single tokens.
+ *
+ * Rows are [rows, dim] with a stride between rows (elements; dim contiguous).
+ * An 8-bit row is a row of whole numbers q, -127 .. 127, with one fp32 scale:
+ * it stands for q * scale, scale = max|v| / 127 and q = v / scale rounded to
+ * nearest even.  A row of zeros has scale 0 (so has one whose scale would be
+ * below 2^-126); a row that holds an infinity or NaN has q 0 and scale NaN, so
+ * that whatever is computed from it is NaN.
+ *
+ * Pointers and errors as for the attention-layer entry points: DEVICE arrays of
+ * the current device, 16-byte aligned where nothing else is said; calls enqueue
+ * on `stream` only, never synchronise, may be captured into a CUDA graph;
+ * nothing is enqueued on an argument error.
+ */
+
+typedef struct ssd_norm_dims {
+    int64_t rows;            /* >= 0, below 2^31 */
+    int32_t dim;             /* D: a multiple of 8, 8 .. 16384 */
+    int32_t dtype;           /* ssd_dtype_t of x, out (and y, z; dout) */
+    int32_t residual_dtype;  /* ssd_dtype_t of residual and residual_out (h, dresidual and dx): dtype or SSD_DTYPE_F32 */
+    uint32_t flags;          /* must be 0 */
+    float eps;               /* >= 0 */
+    uint32_t reserved;       /* must be 0 */
+    /* row strides in elements, multiples of 16 bytes (q_stride: of 8) */
+    int64_t x_stride;        /* x; y; in the backward dout */
+    int64_t z_stride;        /* z */
+    int64_t residual_stride; /* residual; in the backward dresidual */
+    int64_t out_stride;      /* out; in the backward dx */
+    int64_t ro_stride;       /* residual_out; in the backward h */
+    int64_t q_stride;        /* q */
+} ssd_norm_dims_t;
+
+/*
+ * ssd_add_rmsnorm_fwd -- the residual's addition and RMSNorm, per row:
+ *   h = x + residual,   v = h / sqrt(mean(h^2) + eps) * weight
+ * computed in fp32 from the sum before it is rounded.  Outputs, each rounded
+ * once: residual_out = h (residual_dtype), out = v (dtype), or v as an 8-bit row
+ * in q [rows, D] and q_scale [rows].  Exactly one of out and q is given, q_scale
+ * with q.  residual NULL: h = x, and residual_out has to be NULL too; with a
+ * residual, residual_out may be NULL.  weight [D] fp32.  A row of zeros stays
+ * zero, with eps 0 too.  The mean square is an fp32 sum.
+ * residual_out may be residual with equal strides, and out may be x (in place);
+ * nothing else may overlap.
+ */
+ssd_status_t ssd_add_rmsnorm_fwd(const void *x, const void *residual, const float *weight,
+                                 void *out, int8_t *q, float *q_scale, void *residual_out,
+                                 const ssd_norm_dims_t *dims, void *stream);
+
+/*
+ * ssd_add_rmsnorm_bwd -- the gradients of ssd_add_rmsnorm_fwd (out in dtype).
+ * h is what the forward wrote as residual_out (without a residual: x), dout =
+ * dL/dout, dresidual = dL/dresidual_out (NULL: none).  With
+ * r = 1 / sqrt(mean(h^2) + eps) and g = dout weight:
+ *   dx = r (g - h r^2 mean(g h)) + dresidual   (of x and of residual alike)
+ *   dweight = sum over rows of dout h r        (fp32, a fixed order)
+ * h, dresidual and dx are in residual_dtype, dout in dtype.  dweight [D] fp32
+ * (NULL: not written).  A row of zeros with eps 0 has r = 0.  dx may be
+ * dresidual, or dout where the types are the same (equal strides, in place);
+ * outputs overlap nothing else.  `workspace` as for ssd_qk_norm_rope_bwd, with
+ * ssd_add_rmsnorm_bwd_workspace_size's bytes.
+ */
+ssd_status_t ssd_add_rmsnorm_bwd(const void *h, const float *weight, const void *dout,
+                                 const void *dresidual, void *dx, float *dweight,
+                                 void *workspace, uint64_t workspace_bytes,
+                                 const ssd_norm_dims_t *dims, void *stream);
+ssd_status_t ssd_add_rmsnorm_bwd_workspace_size(const ssd_norm_dims_t *dims, uint64_t *bytes);
+
+/*
+ * ssd_gated_rmsnorm_q8_fwd -- ssd_gated_rmsnorm_fwd with an 8-bit result:
+ *   v = y / sqrt(mean(y^2) + eps) * weight * SiLU(z)
+ * as an 8-bit row in q [rows, D] and q_scale [rows].  y and z [rows, D] in
+ * dtype, weight [D] fp32.  Outputs overlap nothing.
+ */
+ssd_status_t ssd_gated_rmsnorm_q8_fwd(const void *y, const void *z, const float *weight,
+                                      int8_t *q, float *q_scale, const ssd_norm_dims_t *dims,
+                                      void *stream);
+
+/* Weights of ssd_q8_matmul are kept in the order that it reads them: tiles of
+ * 128 output channels; in a tile, for each 16 inner elements, the 128 channels'
+ * 16 bytes side by side (byte ((tile * K64 * 4 + k / 16) * 128 + n % 128) * 16 +
+ * k % 16 with tile = n / 128 and K64 = ceil(K / 64)); zeros beyond N and K. */
+#define SSD_Q8_PACKED_BYTES(N, K) ((((int64_t)(N) + 127) / 128 * 128) * (((int64_t)(K) + 63) / 64 * 64))
+
+typedef struct ssd_q8_dims {
+    int64_t M;           /* tokens, >= 0, below 2^31 */
+    int32_t N;           /* output channels, 1 .. 2^24 */
+    int32_t K;           /* inner elements, 1 .. 65536 */
+    int32_t out_dtype;   /* ssd_dtype_t of y */
+    uint32_t flags;      /* must be 0 */
+    int64_t a_stride;    /* row strides in elements, any >= K (y: >= N); ssd_q8_pack_weight: the weight's */
+    int64_t y_stride;
+} ssd_q8_dims_t;
+
+/* ssd_q8_pack_weight -- w [N, K] (rows a_stride apart) into `packed`, SSD_Q8_PACKED_BYTES(N, K)
+ * bytes.  M, out_dtype and y_stride are not looked at.  w may have any alignment. */
+ssd_status_t ssd_q8_pack_weight(const int8_t *w, int8_t *packed, const ssd_q8_dims_t *dims, void *stream);
+
+/*
+ * ssd_q8_matmul -- products of 8-bit integers:
+ *   y[t, n] = (sum_k a[t, k] w[n, k]) * a_scale[t] * w_scale[n]
+ * a [M, K] int8 (all values -128 .. 127), w packed, a_scale [M], w_scale [N] fp32,
+ * y [M, N] in out_dtype.  The sum is exact whatever its order, so a row's result
+ * does not depend on the other rows or on how the work was split; it is
+ * rounded to fp32, multiplied by a_scale, then by w_scale, and rounded to
+ * out_dtype.  a and y have any alignment of their types, the scales 4 bytes.
+ * y overlaps nothing.  `workspace` as for ssd_qk_norm_rope_bwd, with
+ * ssd_q8_matmul_workspace_size's bytes (0 for few tokens).
+ */
+ssd_status_t ssd_q8_matmul(const int8_t *a, const float *a_scale, const int8_t *packed,
+                           const float *w_scale, void *y, void *workspace,
+                           uint64_t workspace_bytes, const ssd_q8_dims_t *dims, void *stream);
+ssd_status_t ssd_q8_matmul_workspace_size(const ssd_q8_dims_t *dims, uint64_t *bytes);
+
+typedef struct ssd_step_dims {
+    int64_t rows;        /* tokens of the step, >= 0; rows * nheads below 2^31 */
+    int64_t nslots;      /* sequences that conv_ring and states hold, >= 0 */
+    int32_t nheads;      /* H >= 1 */
+    int32_t headdim;     /* P >= 1 */
+    int32_t dstate;      /* N: a multiple of 4, 4 .. 512 */
+    int32_t ngroups;     /* G >= 1, H % G == 0 */
+    int32_t kernel_size; /* K: 2 .. 4 */
+    int32_t dtype;       /* ssd_dtype_t of xbc, conv_ring and y */
+    int32_t dt_dtype;    /* ssd_dtype_t of dt_raw: dtype or SSD_DTYPE_F32 */
+    uint32_t flags;      /* must be 0 */
+    /* row strides in elements, any */
+    int64_t xbc_stride;  /* >= C = H P + 2 G N */
+    int64_t dt_stride;   /* >= H */
+    int64_t y_stride;    /* >= H P */
+} ssd_step_dims_t;
+
+/*
+ * ssd_conv_scan_step -- ssd_conv_scan_fwd for one token of each of several
+ * sequences, their states in a pool.
+ *
+ * Row i is the token at position t = positions[i] of the sequence in slot s =
+ * slots[i].  conv_ring [nslots, K, C] holds each sequence's last K inputs, that
+ * of position p in entry p mod K.  With the K-1 inputs before it (zeros before
+ * position 0) and its own xbc[i]:
+ *   u = SiLU(bias + sum_j weight[:, j] input(t - j)),   x | B | C = u
+ *   h = exp(dt A) h + dt B x^T,   y[i] = C^T h + D x
+ * with dt = softplus(dt_raw[i] + dt_bias), A = -exp(A_log) and h = states[s]
+ * [H, P, N] fp32, updated in place; xbc[i] goes into the ring's entry t mod K.  At
+ * position 0 a sequence begins: neither the ring nor the state of the slot is
+ * read.  x, B and C are kept in fp32 between the convolution and the scan.
+ * A row with a slot outside 0 .. nslots - 1 or a negative position is padding: its
+ * y is zero and nothing is written for it.  Two rows must not have the same slot.
+ * xbc [rows, C], dt_raw [rows, H], y [rows, H P]; weight [C, K], bias [C] (NULL:
+ * none), dt_bias, A_log, D [H] fp32; slots and positions [rows] int32.  xbc, dt_raw
+ * and y have any alignment of their types, the [H] arrays, bias, slots and
+ * positions 4 bytes.  Outputs overlap nothing.
+ */
+ssd_status_t ssd_conv_scan_step(const void *xbc, void *conv_ring, const float *weight,
+                                const float *bias, const void *dt_raw, const float *dt_bias,
+                                const float *A_log, const float *D, float *states,
+                                const int32_t *slots, const int32_t *positions, void *y,
+                                const ssd_step_dims_t *dims, void *stream);
+
 /* Which path SSD_PATH_AUTO resolves to for these dims on the current device
  * (SSD_PATH_SEQUENTIAL, SSD_PATH_CHUNKED or SSD_PATH_DECODE), or
  * -(ssd_status_t) if the dims are

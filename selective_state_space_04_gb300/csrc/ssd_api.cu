@@ -546,6 +546,75 @@ ssd_status_t check_attn_dims(const ssd_attn_dims_t *d)
     return SSD_OK;
 }
 
+// ---- rows [n, width] of the entry points around the scan
+
+// rows `stride` elements of es bytes apart
+Strided row_view(const void *p, int64_t n, int64_t stride, int64_t width, int64_t es)
+{
+    return {p, n, 1, n > 1 ? stride * es : 0, 0, width};
+}
+
+// a row stride: `least` or more (outputs, whose rows are distinct) or 0 or more, a
+// multiple of `unit` bytes, the extent within bounds
+ssd_status_t row_stride_ok(int64_t n, int64_t stride, int64_t least, int64_t es, int64_t unit)
+{
+    int64_t t;
+    if (n <= 1)
+        return SSD_OK;
+    if (stride < least || !mul_ok(stride, es, &t) || !mul_ok(t, n, &t) || t > (INT64_C(1) << 46))
+        return SSD_ERR_INVALID_DIMS;
+    return stride * es % unit == 0 ? SSD_OK : SSD_ERR_MISALIGNED;
+}
+
+Strided flat(const void *p, int64_t bytes) { return {p, bytes > 0 ? 1 : 0, 1, 0, 0, bytes}; }
+
+// SSD_ERR_ALIASING if one of the outputs shares bytes with an input (but for the
+// pairs named in `in_place`, as {output, input}, where they are the same rows) or with
+// another output
+template <int NO, int NI, int NP>
+ssd_status_t check_aliasing(const Strided (&outs)[NO], const Strided (&ins)[NI], const int (&in_place)[NP][2])
+{
+    for (int o = 0; o < NO; ++o) {
+        for (int i = 0; i < NI; ++i) {
+            bool may = false;
+            for (int k = 0; k < NP; ++k)
+                may = may || (in_place[k][0] == o && in_place[k][1] == i);
+            if (overlaps(outs[o], ins[i]) && !(may && same_view(outs[o], ins[i]) && outs[o].width == ins[i].width))
+                return SSD_ERR_ALIASING;
+        }
+        for (int o2 = o + 1; o2 < NO; ++o2)
+            if (overlaps(outs[o], outs[o2]))
+                return SSD_ERR_ALIASING;
+    }
+    return SSD_OK;
+}
+
+ssd_status_t check_norm_dims(const ssd_norm_dims_t *d)
+{
+    if (!d)
+        return SSD_ERR_NULL_PTR;
+    if (d->rows < 0 || d->rows >= (INT64_C(1) << 31) || d->dim < 1 || d->flags != 0 || d->reserved != 0 || !(d->eps >= 0.f))
+        return SSD_ERR_INVALID_DIMS;
+    if ((d->dtype != SSD_DTYPE_F32 && d->dtype != SSD_DTYPE_BF16) ||
+        (d->residual_dtype != d->dtype && d->residual_dtype != SSD_DTYPE_F32))
+        return SSD_ERR_UNSUPPORTED_DTYPE;
+    return d->dim % 8 != 0 || d->dim > 16384 ? SSD_ERR_UNSUPPORTED : SSD_OK;
+}
+
+int64_t workspace_extent(const void *workspace, uint64_t bytes)
+{
+    return workspace ? (int64_t)std::min<uint64_t>(bytes, (uint64_t)1 << 60) : 0;
+}
+
+ssd_status_t check_q8_dims(const ssd_q8_dims_t *d)
+{
+    if (!d)
+        return SSD_ERR_NULL_PTR;
+    if (d->M < 0 || d->M >= (INT64_C(1) << 31) || d->N < 1 || d->N > (1 << 24) || d->K < 1 || d->flags != 0)
+        return SSD_ERR_INVALID_DIMS;
+    return d->K > 65536 ? SSD_ERR_UNSUPPORTED : SSD_OK;
+}
+
 // Runs `launch` with the caller's workspace, or with one from the library pool.
 template <typename F>
 ssd_status_t with_workspace(void *workspace, uint64_t have, size_t need, cudaStream_t st, F launch)
@@ -1746,6 +1815,226 @@ ssd_status_t ssd_paged_attn_fwd(const void *q, const void *k_cache, const void *
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return with_workspace(workspace, workspace_bytes, attn_workspace_bytes(*dims), st,
                           [&](void *ws) { return attn_launch(aa, ws, st); });
+}
+
+ssd_status_t ssd_add_rmsnorm_fwd(const void *x, const void *residual, const float *weight, void *out, int8_t *q,
+                                 float *q_scale, void *residual_out, const ssd_norm_dims_t *dims, void *stream)
+{
+    SSD_NVTX_RANGE("ssd_add_rmsnorm_fwd");
+    const ssd_status_t s = check_norm_dims(dims);
+    if (s != SSD_OK)
+        return s;
+    const int64_t n = dims->rows, D = dims->dim, es = (int64_t)elem_size(dims->dtype), rs = (int64_t)elem_size(dims->residual_dtype);
+    if ((out != nullptr) == (q != nullptr) && n > 0)
+        return out ? SSD_ERR_INVALID_DIMS : SSD_ERR_NULL_PTR;
+    if (n > 0 && (!x || !weight || (q && !q_scale) || (residual_out && !residual)))
+        return SSD_ERR_NULL_PTR;
+    const struct { bool used; int64_t stride, least, es, unit; } st[] = {
+        {true, dims->x_stride, 0, es, 16}, {residual != nullptr, dims->residual_stride, 0, rs, 16},
+        {out != nullptr, dims->out_stride, D, es, 16}, {residual_out != nullptr, dims->ro_stride, D, rs, 16},
+        {q != nullptr, dims->q_stride, D, 1, 8}};
+    for (const auto &t : st) {
+        const ssd_status_t why = t.used ? row_stride_ok(n, t.stride, t.least, t.es, t.unit) : SSD_OK;
+        if (why != SSD_OK)
+            return why;
+    }
+    const void *ptrs[] = {x, residual, weight, out, residual_out};
+    for (const void *p : ptrs)
+        if (!aligned16(p))
+            return SSD_ERR_MISALIGNED;
+    if (!aligned(q, 8) || !aligned(q_scale, 4))
+        return SSD_ERR_MISALIGNED;
+    const Strided ins[] = {row_view(x, n, dims->x_stride, D * es, es), row_view(residual, n, dims->residual_stride, D * rs, rs),
+                           flat(weight, D * 4)};
+    const Strided outs[] = {row_view(out, n, dims->out_stride, D * es, es), row_view(residual_out, n, dims->ro_stride, D * rs, rs),
+                            row_view(q, n, dims->q_stride, D, 1), flat(q ? q_scale : nullptr, n * 4)};
+    const int in_place[][2] = {{0, 0}, {1, 1}};
+    const ssd_status_t why = check_aliasing(outs, ins, in_place);
+    if (why != SSD_OK)
+        return why;
+    NormArgs a = {x, residual, nullptr, weight, out, q, q_scale, residual_out, *dims};
+    return norm_launch(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
+ssd_status_t ssd_gated_rmsnorm_q8_fwd(const void *y, const void *z, const float *weight, int8_t *q, float *q_scale,
+                                      const ssd_norm_dims_t *dims, void *stream)
+{
+    SSD_NVTX_RANGE("ssd_gated_rmsnorm_q8_fwd");
+    const ssd_status_t s = check_norm_dims(dims);
+    if (s != SSD_OK)
+        return s;
+    const int64_t n = dims->rows, D = dims->dim, es = (int64_t)elem_size(dims->dtype);
+    if (n > 0 && (!y || !z || !weight || !q || !q_scale))
+        return SSD_ERR_NULL_PTR;
+    const ssd_status_t sy = row_stride_ok(n, dims->x_stride, 0, es, 16), sz = row_stride_ok(n, dims->z_stride, 0, es, 16),
+                       sq = row_stride_ok(n, dims->q_stride, D, 1, 8);
+    if (sy != SSD_OK || sz != SSD_OK || sq != SSD_OK)
+        return sy != SSD_OK ? sy : sz != SSD_OK ? sz : sq;
+    if (!aligned16(y) || !aligned16(z) || !aligned16(weight) || !aligned(q, 8) || !aligned(q_scale, 4))
+        return SSD_ERR_MISALIGNED;
+    const Strided ins[] = {row_view(y, n, dims->x_stride, D * es, es), row_view(z, n, dims->z_stride, D * es, es), flat(weight, D * 4)};
+    const Strided outs[] = {row_view(q, n, dims->q_stride, D, 1), flat(q_scale, n * 4)};
+    const int in_place[][2] = {{-1, -1}};
+    const ssd_status_t why = check_aliasing(outs, ins, in_place);
+    if (why != SSD_OK)
+        return why;
+    NormArgs a = {y, nullptr, z, weight, nullptr, q, q_scale, nullptr, *dims};
+    return norm_launch(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
+ssd_status_t ssd_add_rmsnorm_bwd_workspace_size(const ssd_norm_dims_t *dims, uint64_t *bytes)
+{
+    const ssd_status_t s = check_norm_dims(dims);
+    if (s != SSD_OK)
+        return s;
+    if (!bytes)
+        return SSD_ERR_NULL_PTR;
+    *bytes = norm_bwd_workspace_bytes(*dims);
+    return SSD_OK;
+}
+
+ssd_status_t ssd_add_rmsnorm_bwd(const void *h, const float *weight, const void *dout, const void *dresidual, void *dx,
+                                 float *dweight, void *workspace, uint64_t workspace_bytes, const ssd_norm_dims_t *dims,
+                                 void *stream)
+{
+    SSD_NVTX_RANGE("ssd_add_rmsnorm_bwd");
+    const ssd_status_t s = check_norm_dims(dims);
+    if (s != SSD_OK)
+        return s;
+    const int64_t n = dims->rows, D = dims->dim, es = (int64_t)elem_size(dims->dtype), rs = (int64_t)elem_size(dims->residual_dtype);
+    if (n > 0 && (!h || !weight || !dout || !dx))
+        return SSD_ERR_NULL_PTR;
+    const struct { bool used; int64_t stride, least, es; } st[] = {
+        {true, dims->ro_stride, 0, rs}, {true, dims->x_stride, 0, es}, {dresidual != nullptr, dims->residual_stride, 0, rs},
+        {true, dims->out_stride, D, rs}};
+    for (const auto &t : st) {
+        const ssd_status_t why = t.used ? row_stride_ok(n, t.stride, t.least, t.es, 16) : SSD_OK;
+        if (why != SSD_OK)
+            return why;
+    }
+    const void *ptrs[] = {h, weight, dout, dresidual, dx, dweight, workspace};
+    for (const void *p : ptrs)
+        if (!aligned16(p))
+            return SSD_ERR_MISALIGNED;
+    const Strided ins[] = {row_view(h, n, dims->ro_stride, D * rs, rs), row_view(dout, n, dims->x_stride, D * es, es),
+                           row_view(dresidual, n, dims->residual_stride, D * rs, rs), flat(weight, D * 4)};
+    const Strided outs[] = {row_view(dx, n, dims->out_stride, D * rs, rs), flat(dweight, D * 4),
+                            flat(workspace, workspace_extent(workspace, workspace_bytes))};
+    const int in_place[][2] = {{0, 2}, {0, 1}};
+    const ssd_status_t why = check_aliasing(outs, ins, in_place);
+    if (why != SSD_OK)
+        return why;
+    NormBwdArgs a = {h, dout, dresidual, weight, dx, dweight, *dims};
+    const size_t need = n > 0 && dweight ? norm_bwd_workspace_bytes(*dims) : 0;
+    cudaStream_t st_ = static_cast<cudaStream_t>(stream);
+    return with_workspace(workspace, workspace_bytes, need, st_, [&](void *ws) { return norm_bwd_launch(a, ws, st_); });
+}
+
+ssd_status_t ssd_q8_pack_weight(const int8_t *w, int8_t *packed, const ssd_q8_dims_t *dims, void *stream)
+{
+    SSD_NVTX_RANGE("ssd_q8_pack_weight");
+    const ssd_status_t s = check_q8_dims(dims);
+    if (s != SSD_OK)
+        return s;
+    if (!w || !packed)
+        return SSD_ERR_NULL_PTR;
+    const ssd_status_t why = row_stride_ok(dims->N, dims->a_stride, dims->K, 1, 1);
+    if (why != SSD_OK)
+        return why;
+    if (!aligned16(packed))
+        return SSD_ERR_MISALIGNED;
+    if (overlaps(row_view(w, dims->N, dims->a_stride, dims->K, 1), flat(packed, SSD_Q8_PACKED_BYTES(dims->N, dims->K))))
+        return SSD_ERR_ALIASING;
+    return q8_pack_launch(w, packed, *dims, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
+ssd_status_t ssd_q8_matmul_workspace_size(const ssd_q8_dims_t *dims, uint64_t *bytes)
+{
+    const ssd_status_t s = check_q8_dims(dims);
+    if (s != SSD_OK)
+        return s;
+    if (!bytes)
+        return SSD_ERR_NULL_PTR;
+    *bytes = q8_workspace_bytes(*dims);
+    return SSD_OK;
+}
+
+ssd_status_t ssd_q8_matmul(const int8_t *a, const float *a_scale, const int8_t *packed, const float *w_scale, void *y,
+                           void *workspace, uint64_t workspace_bytes, const ssd_q8_dims_t *dims, void *stream)
+{
+    SSD_NVTX_RANGE("ssd_q8_matmul");
+    const ssd_status_t s = check_q8_dims(dims);
+    if (s != SSD_OK)
+        return s;
+    if (dims->out_dtype != SSD_DTYPE_F32 && dims->out_dtype != SSD_DTYPE_BF16)
+        return SSD_ERR_UNSUPPORTED_DTYPE;
+    const int64_t M = dims->M, N = dims->N, K = dims->K, es = (int64_t)elem_size(dims->out_dtype);
+    if (M > 0 && (!a || !a_scale || !packed || !w_scale || !y))
+        return SSD_ERR_NULL_PTR;
+    const ssd_status_t sa = row_stride_ok(M, dims->a_stride, 0, 1, 1), sy = row_stride_ok(M, dims->y_stride, N, es, 1);
+    if (sa != SSD_OK || sy != SSD_OK)
+        return sa != SSD_OK ? sa : sy;
+    if (!aligned16(packed) || !aligned16(workspace) || !aligned(y, es) || !aligned(a_scale, 4) || !aligned(w_scale, 4))
+        return SSD_ERR_MISALIGNED;
+    const Strided ins[] = {row_view(a, M, dims->a_stride, K, 1), flat(a_scale, M * 4), flat(packed, SSD_Q8_PACKED_BYTES(N, K)),
+                           flat(w_scale, N * 4)};
+    const Strided outs[] = {row_view(y, M, dims->y_stride, N * es, es), flat(workspace, workspace_extent(workspace, workspace_bytes))};
+    const int in_place[][2] = {{-1, -1}};
+    const ssd_status_t why = check_aliasing(outs, ins, in_place);
+    if (why != SSD_OK)
+        return why;
+    if (M == 0)
+        return SSD_OK;
+    const Q8Args qa = {a, packed, a_scale, w_scale, y, *dims};
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return with_workspace(workspace, workspace_bytes, q8_workspace_bytes(*dims), st, [&](void *ws) { return q8_launch(qa, ws, st); });
+}
+
+ssd_status_t ssd_conv_scan_step(const void *xbc, void *conv_ring, const float *weight, const float *bias, const void *dt_raw,
+                                const float *dt_bias, const float *A_log, const float *D, float *states, const int32_t *slots,
+                                const int32_t *positions, void *y, const ssd_step_dims_t *dims, void *stream)
+{
+    SSD_NVTX_RANGE("ssd_conv_scan_step");
+    if (!dims)
+        return SSD_ERR_NULL_PTR;
+    const int64_t n = dims->rows, H = dims->nheads, P = dims->headdim, N = dims->dstate, G = dims->ngroups, K = dims->kernel_size;
+    if (n < 0 || dims->nslots < 0 || dims->nslots >= (INT64_C(1) << 31) || H < 1 || P < 1 || N < 1 || G < 1 || K < 1 || H % G != 0 ||
+        dims->flags != 0)
+        return SSD_ERR_INVALID_DIMS;
+    if ((dims->dtype != SSD_DTYPE_F32 && dims->dtype != SSD_DTYPE_BF16) ||
+        (dims->dt_dtype != dims->dtype && dims->dt_dtype != SSD_DTYPE_F32))
+        return SSD_ERR_UNSUPPORTED_DTYPE;
+    if (N % 4 != 0 || N > 512 || K < 2 || K > 4 || P > 2048 || H > (1 << 20) || n >= (INT64_C(1) << 31) || n * H >= (INT64_C(1) << 31))
+        return SSD_ERR_UNSUPPORTED;
+    const int64_t es = (int64_t)elem_size(dims->dtype), ds = (int64_t)elem_size(dims->dt_dtype), C = H * P + 2 * G * N;
+    int64_t ringb, stateb;
+    if (C >= (INT64_C(1) << 30) || !mul_ok(dims->nslots, K * C * es, &ringb) || !mul_ok(dims->nslots, H * P * N * 4, &stateb) ||
+        stateb > (INT64_C(1) << 46))
+        return SSD_ERR_INVALID_DIMS;
+    if (n > 0 && (!xbc || !weight || !dt_raw || !dt_bias || !A_log || !D || !slots || !positions || !y ||
+                  (dims->nslots > 0 && (!conv_ring || !states))))
+        return SSD_ERR_NULL_PTR;
+    const ssd_status_t sx = row_stride_ok(n, dims->xbc_stride, 0, es, 1), sd = row_stride_ok(n, dims->dt_stride, 0, ds, 1),
+                       sy = row_stride_ok(n, dims->y_stride, H * P, es, 1);
+    if (sx != SSD_OK || sd != SSD_OK || sy != SSD_OK)
+        return sx != SSD_OK ? sx : sd != SSD_OK ? sd : sy;
+    if (!aligned16(conv_ring) || !aligned16(weight) || !aligned16(states) || !aligned(xbc, es) || !aligned(dt_raw, ds) ||
+        !aligned(y, es))
+        return SSD_ERR_MISALIGNED;
+    const void *words[] = {bias, dt_bias, A_log, D, slots, positions};
+    for (const void *p : words)
+        if (!aligned(p, 4))
+            return SSD_ERR_MISALIGNED;
+    const Strided ins[] = {row_view(xbc, n, dims->xbc_stride, C * es, es), flat(weight, C * K * 4), flat(bias, C * 4),
+                           row_view(dt_raw, n, dims->dt_stride, H * ds, ds), flat(dt_bias, H * 4), flat(A_log, H * 4),
+                           flat(D, H * 4), flat(slots, n * 4), flat(positions, n * 4)};
+    const Strided outs[] = {row_view(y, n, dims->y_stride, H * P * es, es), flat(conv_ring, ringb), flat(states, stateb)};
+    const int in_place[][2] = {{-1, -1}};
+    const ssd_status_t why = check_aliasing(outs, ins, in_place);
+    if (why != SSD_OK)
+        return why;
+    const StepArgs a = {xbc, dt_raw, conv_ring, y, weight, bias, dt_bias, A_log, D, states, slots, positions, *dims};
+    return step_launch(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
 }  // extern "C"

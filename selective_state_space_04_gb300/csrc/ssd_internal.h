@@ -254,6 +254,50 @@ struct AttnArgs {
 size_t attn_workspace_bytes(const ssd_attn_dims_t &d);
 cudaError_t attn_launch(const AttnArgs &a, void *workspace, cudaStream_t stream);
 
+// ---- one layer's step around the scan, after validation.  Device pointers.
+// ssd_norm.cu: RMSNorm with the residual's addition or a gate, 8-bit rows, and its gradients
+struct NormArgs {
+    const void *x, *residual, *z;               // [rows, D]; residual and z may be null
+    const float *weight;
+    void *out;                                  // or null: then q and q_scale
+    int8_t *q;
+    float *q_scale;
+    void *residual_out;                         // or null
+    ssd_norm_dims_t d;
+};
+cudaError_t norm_launch(const NormArgs &a, cudaStream_t stream);
+struct NormBwdArgs {
+    const void *h, *dout, *dres;                // dres may be null
+    const float *weight;
+    void *dx;
+    float *dweight;                             // or null
+    ssd_norm_dims_t d;
+};
+size_t norm_bwd_workspace_bytes(const ssd_norm_dims_t &d);
+cudaError_t norm_bwd_launch(const NormBwdArgs &a, void *workspace, cudaStream_t stream);
+
+// ssd_q8.cu: products of 8-bit integers
+struct Q8Args {
+    const int8_t *a, *packed;
+    const float *a_scale, *w_scale;
+    void *y;
+    ssd_q8_dims_t d;
+};
+cudaError_t q8_pack_launch(const int8_t *w, int8_t *packed, const ssd_q8_dims_t &d, cudaStream_t stream);
+size_t q8_workspace_bytes(const ssd_q8_dims_t &d);
+cudaError_t q8_launch(const Q8Args &a, void *workspace, cudaStream_t stream);
+
+// ssd_step.cu: conv1d + SiLU and the scan for single tokens on a pool of states
+struct StepArgs {
+    const void *xbc, *dt_raw;
+    void *ring, *y;
+    const float *weight, *bias, *dt_bias, *A_log, *D;
+    float *states;
+    const int32_t *slots, *positions;
+    ssd_step_dims_t d;
+};
+cudaError_t step_launch(const StepArgs &a, cudaStream_t stream);
+
 // launch accounting
 void note_launches(int n);
 // SMs of the current device (152 when the driver cannot say)

@@ -74,6 +74,27 @@ class SsdAttnDims(ctypes.Structure):
                 ("kc_stride", ctypes.c_int64 * 3), ("vc_stride", ctypes.c_int64 * 3), ("table_stride", ctypes.c_int64)]
 
 
+class SsdNormDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("residual_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32), ("eps", ctypes.c_float),
+                ("reserved", ctypes.c_uint32), ("x_stride", ctypes.c_int64), ("z_stride", ctypes.c_int64),
+                ("residual_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64), ("ro_stride", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64)]
+
+
+class SsdQ8Dims(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("flags", ctypes.c_uint32), ("a_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64)]
+
+
+class SsdStepDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("nslots", ctypes.c_int64), ("nheads", ctypes.c_int32),
+                ("headdim", ctypes.c_int32), ("dstate", ctypes.c_int32), ("ngroups", ctypes.c_int32),
+                ("kernel_size", ctypes.c_int32), ("dtype", ctypes.c_int32), ("dt_dtype", ctypes.c_int32),
+                ("flags", ctypes.c_uint32), ("xbc_stride", ctypes.c_int64), ("dt_stride", ctypes.c_int64),
+                ("y_stride", ctypes.c_int64)]
+
+
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise ImportError(f"libssd is not built ({path} missing); run "
@@ -127,6 +148,22 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.ssd_paged_attn_fwd.argtypes = [vp] * 9 + [ctypes.c_uint64, ctypes.POINTER(SsdAttnDims), vp]
     lib.ssd_paged_attn_workspace_size.restype = ctypes.c_int
     lib.ssd_paged_attn_workspace_size.argtypes = [ctypes.POINTER(SsdAttnDims), ctypes.POINTER(ctypes.c_uint64)]
+    lib.ssd_add_rmsnorm_fwd.restype = ctypes.c_int
+    lib.ssd_add_rmsnorm_fwd.argtypes = [vp] * 7 + [ctypes.POINTER(SsdNormDims), vp]
+    lib.ssd_gated_rmsnorm_q8_fwd.restype = ctypes.c_int
+    lib.ssd_gated_rmsnorm_q8_fwd.argtypes = [vp] * 5 + [ctypes.POINTER(SsdNormDims), vp]
+    lib.ssd_add_rmsnorm_bwd.restype = ctypes.c_int
+    lib.ssd_add_rmsnorm_bwd.argtypes = [vp] * 7 + [ctypes.c_uint64, ctypes.POINTER(SsdNormDims), vp]
+    lib.ssd_add_rmsnorm_bwd_workspace_size.restype = ctypes.c_int
+    lib.ssd_add_rmsnorm_bwd_workspace_size.argtypes = [ctypes.POINTER(SsdNormDims), ctypes.POINTER(ctypes.c_uint64)]
+    lib.ssd_q8_pack_weight.restype = ctypes.c_int
+    lib.ssd_q8_pack_weight.argtypes = [vp] * 2 + [ctypes.POINTER(SsdQ8Dims), vp]
+    lib.ssd_q8_matmul.restype = ctypes.c_int
+    lib.ssd_q8_matmul.argtypes = [vp] * 6 + [ctypes.c_uint64, ctypes.POINTER(SsdQ8Dims), vp]
+    lib.ssd_q8_matmul_workspace_size.restype = ctypes.c_int
+    lib.ssd_q8_matmul_workspace_size.argtypes = [ctypes.POINTER(SsdQ8Dims), ctypes.POINTER(ctypes.c_uint64)]
+    lib.ssd_conv_scan_step.restype = ctypes.c_int
+    lib.ssd_conv_scan_step.argtypes = [vp] * 12 + [ctypes.POINTER(SsdStepDims), vp]
     return lib
 
 
@@ -776,3 +813,263 @@ def paged_attn_workspace_size(q, k_cache, v_cache, block_table) -> int:
     n = ctypes.c_uint64(0)
     _check(_lib.ssd_paged_attn_workspace_size(ctypes.byref(d), ctypes.byref(n)), "ssd_paged_attn_workspace_size")
     return int(n.value)
+
+
+# ---- one layer's step around the scan: residual norm, 8-bit products, conv and scan for single tokens ----
+# Devices, streams and workspaces as for the attention layers' calls.
+
+def _matrix(device, named):
+    """[n, width] tensors with a contiguous last axis (``named``: (name, tensor or None, dtype, shape))."""
+    for name, t, dtype, shape in named:
+        if t is None:
+            continue
+        if t.dtype != dtype or t.device != device or t.shape != shape:
+            raise ValueError(f"{name} must be a {tuple(shape)} {dtype} tensor on {device}")
+        if shape[1] != 1 and t.stride(1) != 1:
+            raise ValueError(f"{name} must have a contiguous last axis")
+
+
+def _contiguous(device, named):
+    """Contiguous tensors (``named``: (name, tensor or None, dtype, shape))."""
+    for name, t, dtype, shape in named:
+        if t is None:
+            continue
+        if t.dtype != dtype or t.device != device or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {tuple(shape)} {dtype} tensor on {device}")
+
+
+def _norm_dims(x, name, weight, residual_dtype, eps):
+    if x.dim() != 2 or not x.is_cuda:
+        raise ValueError(f"{name} must be a [rows, D] CUDA tensor")
+    if x.dtype not in _DTYPES or residual_dtype not in _DTYPES:
+        raise SsdError(9, f"{name} and the residual must be bf16 or fp32")
+    n, D = x.shape
+    _matrix(x.device, ((name, x, x.dtype, x.shape),))
+    _vectors(x.device, (("weight", weight, D),), torch.float32)
+    return SsdNormDims(n, D, _DTYPES[x.dtype], _DTYPES[residual_dtype], 0, eps, 0, x.stride(0), 0, 0, D, D, D)
+
+
+def _add_rmsnorm(what, x, weight, residual, eps, out, q, scale, residual_out, return_residual, stream):
+    dev = x.device
+    key = (what, *map(_layout, (x, weight, residual, out, q, scale, residual_out)), eps, return_residual)
+    d = _known.get(key)
+    if d is None:
+        d = _norm_dims(x, "x", weight, x.dtype if residual is None else residual.dtype, eps)
+        if residual is None and residual_out is not None:
+            raise ValueError("residual_out without a residual")
+        for name, t, dtype in (("residual", residual, residual.dtype if residual is not None else None), ("out", out, x.dtype),
+                               ("q", q, torch.int8), ("residual_out", residual_out, residual.dtype if residual is not None else None)):
+            _matrix(dev, ((name, t, dtype, x.shape),))
+        _vectors(dev, (("scale", scale, x.shape[0]),), torch.float32)
+        for field, t in (("residual_stride", residual), ("out_stride", out), ("ro_stride", residual_out), ("q_stride", q)):
+            if t is not None:
+                setattr(d, field, t.stride(0))
+        _remember(key, d)
+    st = _stream_ptr(dev, stream)
+    if what is add_rmsnorm_fwd:
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    else:
+        if q is None:
+            q = torch.empty(x.shape, dtype=torch.int8, device=dev)
+        if scale is None:
+            scale = torch.empty(x.shape[0], dtype=torch.float32, device=dev)
+    if residual is not None and residual_out is None and return_residual:
+        residual_out = torch.empty(x.shape, dtype=residual.dtype, device=dev)
+    _check(_lib.ssd_add_rmsnorm_fwd(x.data_ptr(), _addr(residual), weight.data_ptr(), _addr(out), _addr(q), _addr(scale),
+                                    _addr(residual_out), d, st), "ssd_add_rmsnorm_fwd")
+    return out, q, scale, residual_out
+
+
+def add_rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, out=None, residual_out=None, return_residual=True, stream=None):
+    """``h = x + residual`` and ``out = h / sqrt(mean(h^2) + eps) * weight`` per row (``ssd_add_rmsnorm_fwd``).
+    Returns ``(out, residual_out)``.
+
+    ``x [rows, D]`` in bf16 or fp32, ``residual`` in x's dtype or fp32 (None: h is x and nothing is returned for it),
+    ``weight [D]`` fp32; rows may have any stride of whole 16 bytes.  ``residual_out`` (h, in the residual's dtype) may
+    be ``residual`` and ``out`` may be ``x``; ``return_residual=False`` leaves h out (None)."""
+    out, _, _, residual_out = _add_rmsnorm(add_rmsnorm_fwd, x, weight, residual, eps, out, None, None, residual_out, return_residual, stream)
+    return out, residual_out
+
+
+def add_rmsnorm_q8_fwd(x, weight, residual=None, *, eps=1e-6, q=None, scale=None, residual_out=None, return_residual=True,
+                       stream=None):
+    """:func:`add_rmsnorm_fwd` with an 8-bit result: ``q [rows, D]`` int8 and ``scale [rows]`` fp32, standing for
+    ``q * scale[:, None]``.  Returns ``(q, scale, residual_out)``."""
+    _, q, scale, residual_out = _add_rmsnorm(add_rmsnorm_q8_fwd, x, weight, residual, eps, None, q, scale, residual_out, return_residual,
+                                             stream)
+    return q, scale, residual_out
+
+
+def gated_rmsnorm_q8_fwd(y, z, weight, eps=1e-6, *, q=None, scale=None, stream=None):
+    """``RMSNorm(y) * weight * SiLU(z)`` per row (:func:`gated_rmsnorm_fwd`) with an 8-bit result, as
+    :func:`add_rmsnorm_q8_fwd` gives it (``ssd_gated_rmsnorm_q8_fwd``).  ``y, z [rows, D]``.  Returns ``(q, scale)``."""
+    dev = y.device
+    key = (gated_rmsnorm_q8_fwd, *map(_layout, (y, z, weight, q, scale)), eps)
+    d = _known.get(key)
+    if d is None:
+        d = _norm_dims(y, "y", weight, y.dtype, eps)
+        _matrix(dev, (("z", z, y.dtype, y.shape), ("q", q, torch.int8, y.shape)))
+        _vectors(dev, (("scale", scale, y.shape[0]),), torch.float32)
+        d.z_stride = z.stride(0)
+        d.q_stride = y.shape[1] if q is None else q.stride(0)
+        _remember(key, d)
+    st = _stream_ptr(dev, stream)
+    if q is None:
+        q = torch.empty(y.shape, dtype=torch.int8, device=dev)
+    if scale is None:
+        scale = torch.empty(y.shape[0], dtype=torch.float32, device=dev)
+    _check(_lib.ssd_gated_rmsnorm_q8_fwd(y.data_ptr(), z.data_ptr(), weight.data_ptr(), q.data_ptr(), scale.data_ptr(), d, st),
+           "ssd_gated_rmsnorm_q8_fwd")
+    return q, scale
+
+
+def add_rmsnorm_bwd(h, weight, dout, dresidual=None, *, eps=1e-6, dx=None, dweight=None, workspace=None, stream=None):
+    """Gradients of :func:`add_rmsnorm_fwd` (``ssd_add_rmsnorm_bwd``).  ``h`` is its ``residual_out`` (without a residual:
+    x), ``dout`` and ``dresidual`` the gradients of its outputs.  Returns ``(dx, dweight)``: the gradient of x and of the
+    residual alike, in h's dtype, and that of the weight in fp32.  ``dx`` may be ``dresidual``, or ``dout`` where that
+    is in h's dtype."""
+    dev = h.device
+    key = (add_rmsnorm_bwd, *map(_layout, (h, weight, dout, dresidual, dx, dweight)), eps)
+    d = _known.get(key)
+    if d is None:
+        d = _norm_dims(dout, "dout", weight, h.dtype, eps)
+        _matrix(dev, (("h", h, h.dtype, dout.shape), ("dout", dout, dout.dtype, dout.shape), ("dresidual", dresidual, h.dtype, dout.shape),
+                      ("dx", dx, h.dtype, dout.shape)))
+        _vectors(dev, (("dweight", dweight, h.shape[1]),), torch.float32)
+        d.ro_stride = h.stride(0)
+        for field, t in (("residual_stride", dresidual), ("out_stride", dx)):
+            if t is not None:
+                setattr(d, field, t.stride(0))
+        _remember(key, d)
+    st = _stream_ptr(dev, stream)
+    if dx is None:
+        dx = torch.empty(h.shape, dtype=h.dtype, device=dev)
+    if dweight is None:
+        dweight = torch.empty(h.shape[1], dtype=torch.float32, device=dev)
+    ws, nws = _workspace(workspace, dev)
+    _check(_lib.ssd_add_rmsnorm_bwd(h.data_ptr(), weight.data_ptr(), dout.data_ptr(), _addr(dresidual), dx.data_ptr(), dweight.data_ptr(),
+                                    ws, nws, d, st), "ssd_add_rmsnorm_bwd")
+    return dx, dweight
+
+
+def add_rmsnorm_bwd_workspace_size(h, dout) -> int:
+    """Bytes of scratch ``add_rmsnorm_bwd`` needs for such tensors on the current device."""
+    d = SsdNormDims(h.shape[0], h.shape[1], _DTYPES[dout.dtype], _DTYPES[h.dtype])
+    n = ctypes.c_uint64(0)
+    _check(_lib.ssd_add_rmsnorm_bwd_workspace_size(ctypes.byref(d), ctypes.byref(n)), "ssd_add_rmsnorm_bwd_workspace_size")
+    return int(n.value)
+
+
+def q8_pack_weight(w, *, packed=None, stream=None):
+    """``w [N, K]`` int8 in the order in which :func:`q8_matmul` reads it (``ssd_q8_pack_weight``): once per weight."""
+    if w.dim() != 2 or not w.is_cuda:
+        raise ValueError("w must be a [N, K] CUDA tensor")
+    N, K = w.shape
+    _matrix(w.device, (("w", w, torch.int8, w.shape),))
+    size = -(-N // 128) * 128 * (-(-K // 64) * 64)
+    _vectors(w.device, (("packed", packed, size),), torch.int8)
+    st = _stream_ptr(w.device, stream)
+    if packed is None:
+        packed = torch.empty(size, dtype=torch.int8, device=w.device)
+    _check(_lib.ssd_q8_pack_weight(w.data_ptr(), packed.data_ptr(), SsdQ8Dims(0, N, K, 0, 0, w.stride(0), N), st), "ssd_q8_pack_weight")
+    return packed
+
+
+def _q8_dims(a, N, dtype):
+    if a.dim() != 2 or not a.is_cuda:
+        raise ValueError("a must be a [tokens, K] CUDA tensor")
+    if dtype not in _DTYPES:
+        raise SsdError(9, "the result must be bf16 or fp32")
+    _matrix(a.device, (("a", a, torch.int8, a.shape),))
+    return SsdQ8Dims(a.shape[0], N, a.shape[1], _DTYPES[dtype], 0, a.stride(0), N)
+
+
+def q8_matmul(a, a_scale, packed, w_scale, *, dtype=torch.bfloat16, out=None, workspace=None, stream=None):
+    """Products of 8-bit integers with a scale per token and per output channel (``ssd_q8_matmul``):
+    ``(a @ w.T) * a_scale[:, None] * w_scale`` with the sums exact.  Returns ``[tokens, N]`` in ``dtype`` (bf16 or fp32; that
+    of ``out``, if given).
+
+    ``a [tokens, K]`` int8 (any row stride) and ``a_scale [tokens]`` as the norms give them; ``packed`` from
+    :func:`q8_pack_weight`, ``w_scale [N]`` fp32."""
+    dev = a.device
+    if out is not None:
+        dtype = out.dtype
+    key = (q8_matmul, *map(_layout, (a, a_scale, packed, w_scale, out)), dtype)
+    d = _known.get(key)
+    if d is None:
+        N = w_scale.shape[0]
+        d = _q8_dims(a, N, dtype)
+        _vectors(dev, (("a_scale", a_scale, a.shape[0]), ("w_scale", w_scale, N)), torch.float32)
+        _vectors(dev, (("packed", packed, -(-N // 128) * 128 * (-(-a.shape[1] // 64) * 64)),), torch.int8)
+        _matrix(dev, (("out", out, dtype, (a.shape[0], N)),))
+        if out is not None:
+            d.y_stride = out.stride(0)
+        _remember(key, d)
+    st = _stream_ptr(dev, stream)
+    if out is None:
+        out = torch.empty((a.shape[0], w_scale.shape[0]), dtype=dtype, device=dev)
+    ws, nws = _workspace(workspace, dev)
+    _check(_lib.ssd_q8_matmul(a.data_ptr(), a_scale.data_ptr(), packed.data_ptr(), w_scale.data_ptr(), out.data_ptr(), ws, nws, d, st),
+           "ssd_q8_matmul")
+    return out
+
+
+def q8_matmul_workspace_size(a, N) -> int:
+    """Bytes of scratch ``q8_matmul`` needs for such tokens and N output channels on the current device."""
+    n = ctypes.c_uint64(0)
+    _check(_lib.ssd_q8_matmul_workspace_size(ctypes.byref(_q8_dims(a, N, torch.float32)), ctypes.byref(n)), "ssd_q8_matmul_workspace_size")
+    return int(n.value)
+
+
+def conv_scan_step(xbc, conv_ring, weight, bias, dt_raw, dt_bias, A_log, D, states, slots, positions, *, ngroups, y=None,
+                   stream=None):
+    """The causal conv1d + SiLU and the scan (:func:`conv_scan_fwd`) for one token of each of several sequences, on a
+    pool of their states (``ssd_conv_scan_step``).  Returns ``y [rows, H, P]``.
+
+    Row i is the token at ``positions[i]`` of the sequence in ``slots[i]`` (both int32); a slot outside the pool or a
+    negative position makes it padding (y zero, nothing else written).  ``conv_ring [nslots, K, C]`` (xbc's dtype; the input
+    of position p in entry p mod K, see :func:`conv_ring_store`) and ``states [nslots, H, P, N]`` fp32 are updated in place;
+    at position 0 neither is read.  ``xbc [rows, C]`` and ``dt_raw [rows, H]`` (xbc's dtype or fp32) may be views of one
+    projection; ``weight [C, K]``, ``bias [C]`` or None, ``dt_bias, A_log, D [H]`` fp32."""
+    dev = xbc.device
+    key = (conv_scan_step, *map(_layout, (xbc, conv_ring, weight, bias, dt_raw, dt_bias, A_log, D, states, slots, positions, y)), ngroups)
+    d = _known.get(key)
+    if d is None:
+        if xbc.dim() != 2 or not xbc.is_cuda:
+            raise ValueError("xbc must be a [rows, C] CUDA tensor")
+        if xbc.dtype not in _DTYPES or dt_raw.dtype not in _DTYPES:
+            raise SsdError(9, "xbc and dt_raw must be bf16 or fp32")
+        if states.dim() != 4 or weight.dim() != 2:
+            raise ValueError("states must be [nslots, H, P, N] and weight [C, K]")
+        n, C = xbc.shape
+        S, H, P, N = states.shape
+        K = weight.shape[1]
+        if C != H * P + 2 * ngroups * N:
+            raise ValueError(f"xbc must have H P + 2 G N = {H * P + 2 * ngroups * N} channels")
+        _matrix(dev, (("xbc", xbc, xbc.dtype, (n, C)), ("dt_raw", dt_raw, dt_raw.dtype, (n, H))))
+        _contiguous(dev, (("conv_ring", conv_ring, xbc.dtype, (S, K, C)), ("weight", weight, torch.float32, (C, K)),
+                          ("states", states, torch.float32, (S, H, P, N))))
+        _vectors(dev, (("bias", bias, C), ("dt_bias", dt_bias, H), ("A_log", A_log, H), ("D", D, H)), torch.float32)
+        _vectors(dev, (("slots", slots, n), ("positions", positions, n)), torch.int32)
+        if y is not None and (y.dtype != xbc.dtype or y.device != dev or y.shape != (n, H, P) or
+                              (P > 1 and y.stride(2) != 1) or (H > 1 and y.stride(1) != P)):
+            raise ValueError(f"y must be a {(n, H, P)} {xbc.dtype} tensor on {dev} with contiguous rows")
+        d = _remember(key, SsdStepDims(n, S, H, P, N, ngroups, K, _DTYPES[xbc.dtype], _DTYPES[dt_raw.dtype], 0, xbc.stride(0),
+                                       dt_raw.stride(0), H * P if y is None else y.stride(0)))
+    st = _stream_ptr(dev, stream)
+    if y is None:
+        y = torch.empty((xbc.shape[0], *states.shape[1:3]), dtype=xbc.dtype, device=dev)
+    _check(_lib.ssd_conv_scan_step(xbc.data_ptr(), conv_ring.data_ptr(), weight.data_ptr(), _addr(bias), dt_raw.data_ptr(),
+                                   dt_bias.data_ptr(), A_log.data_ptr(), D.data_ptr(), states.data_ptr(), slots.data_ptr(),
+                                   positions.data_ptr(), y.data_ptr(), d, st), "ssd_conv_scan_step")
+    return y
+
+
+def conv_ring_store(conv_ring, conv_state, slots, lengths):
+    """Puts a prompt's carried inputs where :func:`conv_scan_step` looks for them: ``conv_state [B, K-1, C]`` as
+    :func:`conv1d_silu_fwd` or :func:`conv_scan_fwd` returns it, of sequences that now hold ``lengths [B]`` tokens, into the
+    entries of ``slots [B]`` in ``conv_ring [nslots, K, C]`` (slots and lengths int64 tensors)."""
+    K = conv_ring.shape[1]
+    at = lengths[:, None] - (K - 1) + torch.arange(K - 1, device=lengths.device)
+    conv_ring[slots[:, None], at % K] = conv_state
