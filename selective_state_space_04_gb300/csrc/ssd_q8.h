@@ -1,0 +1,60 @@
+// ssd_q8.h -- what the kernels of the 8-bit product share.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "ssd_internal.h"
+
+namespace ssd {
+
+struct Q8Params {
+    const int8_t *a, *w;          // [M, K] rows sa apart; packed
+    const float *as, *ws;
+    void *y;                      // [M, N] rows sy apart
+    long long M, sa, sy;
+    int N, K, k64, tiles;         // k64: slabs of 64 inner elements; tiles of 128 channels
+    int vec;                      // a's rows are 16-byte aligned
+};
+
+cudaError_t q8_mid_launch(const Q8Params &p, bool f32, cudaStream_t st);
+
+#ifdef __CUDACC__
+// Offset of 16-byte piece c of row r in a tile of 128-byte rows with the 128-byte swizzle.
+__device__ __forceinline__ uint32_t sw128(uint32_t r, uint32_t c) { return r * 128u + ((c ^ (r & 7u)) << 4); }
+
+// 16 8-bit integers to fp16, exactly: b + 128 below the bits of 1024 (spacing 1 there)
+// is 1024 + 128 + b; 1152 is taken off again.
+__device__ __forceinline__ void widen16(const uint4 &u, uint32_t *f)
+{
+    const uint32_t v[4] = {u.x ^ 0x80808080u, u.y ^ 0x80808080u, u.z ^ 0x80808080u, u.w ^ 0x80808080u};
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = __byte_perm(v[i], 0x64646464u, 0x4140), hi = __byte_perm(v[i], 0x64646464u, 0x4342);
+        const __half2 a = __hsub2(*reinterpret_cast<const __half2 *>(&lo), off), b = __hsub2(*reinterpret_cast<const __half2 *>(&hi), off);
+        f[2 * i] = *reinterpret_cast<const uint32_t *>(&a);
+        f[2 * i + 1] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+}
+
+// a[t, k .. k + 15], zeros beyond M and K
+__device__ __forceinline__ uint4 load16(const Q8Params &p, long long t, int k)
+{
+    if (t >= p.M || k >= p.K)
+        return make_uint4(0u, 0u, 0u, 0u);
+    const int8_t *src = p.a + t * p.sa + k;
+    if (p.vec && k + 16 <= p.K)
+        return __ldg(reinterpret_cast<const uint4 *>(src));
+    uint32_t v[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+        if (k + e < p.K)
+            v[e / 4] |= (uint32_t)(uint8_t)src[e] << (8 * (e % 4));
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+#endif
+
+}  // namespace ssd

@@ -1,0 +1,375 @@
+// ssd_q8_mid.cu -- the 8-bit product for up to a few hundred tokens, on tcgen05.
+//
+// One CTA: 128 output channels x up to 128 tokens x a range of K, in slabs of 64 inner
+// elements.  sm_103a's tensor cores take 8-bit integers slowly, so both operands are widened to
+// fp16, which holds -128 .. 127 exactly, and the products are added in fp32: exactly, as
+// long as a partial sum stays below 2^24, which 1024 products of at most 2^14 do.
+// So every 1024 inner elements have an accumulator of their own, as far as TMEM goes;
+// beyond that the accumulators are drained into 32-bit integers in shared memory.
+//
+// A slab's weights (8 KB, contiguous) come by bulk copy; four warps widen them, a
+// thread per channel, and put them into TMEM as the MMA's A operand, which keeps them
+// out of shared memory's bandwidth: at the memory's rate the weights alone would take
+// 6.8 TB/s into shared memory, as much out, and twice that again each way as fp16.
+// Four more warps widen the tokens into swizzled shared memory, the B operand.
+//
+// K is split over a cluster of CTAs where there are few tiles; each CTA ends with the
+// sums of its range, they are exchanged through distributed shared memory, every CTA
+// adding and storing its part of the tokens.  Sums are integers: any order is exact.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "ptx.cuh"
+#include "ssd_internal.h"
+#include "ssd_q8.h"
+
+namespace ssd {
+
+using namespace ptx;
+
+static __device__ unsigned int g_q8_mid_error;
+
+namespace {
+
+constexpr int kThreads = 320;   // warps 0-3: weights and results, 4-7: tokens, 8: copies, 9: MMA
+constexpr int kStages = 4;      // slabs in TMEM (A) and shared memory (B)
+constexpr int kSlabBytes = 128 * 64;
+constexpr int kChunkSlabs = 16;   // slabs of one accumulator: 1024 inner elements
+constexpr uint64_t kTimeoutNs = 2000000000ull;
+
+template <int MT> struct Shape {
+    // Weight slabs on their way.  With them a CTA takes more than a third of an SM's shared memory: a
+    // third CTA on an SM would wait for tensor memory, and the CTAs of two clusters that wait
+    // for each other's that way would wait for ever.
+    static constexpr int kW = MT == 128 ? 5 : 8;
+    static constexpr int kB = MT * 128;                   // a slab of tokens as fp16
+    static constexpr int kOffB = 0;                       // (1024-byte aligned)
+    static constexpr int kOffW = kStages * kB;
+    static constexpr int kRings = kOffW + kW * kSlabBytes;
+    static constexpr int kSums = 128 * MT * 4;            // drained sums, [token][channel]
+    static constexpr int kAccs = 128 / MT;                // accumulators, 128 columns of TMEM
+    static constexpr int kRound = kAccs * kChunkSlabs;    // slabs between drains
+    static_assert(kRings > 78 * 1024, "three CTAs would fit");
+    static_assert(kRings >= (MT + 7 * 8) * 128 * 4, "the exchange takes the rings' place");
+};
+constexpr int kColA = 128, kCols = 256;   // TMEM: accumulators, then the weights' stages
+
+enum { BAR_WFULL = 0, BAR_WEMPTY = 8, BAR_FULL = 16, BAR_EMPTY = BAR_FULL + kStages, BAR_ACC = BAR_EMPTY + kStages, BAR_DRAINED, kBars };
+
+__device__ bool wait_bar(uint64_t *bar, uint32_t parity)
+{
+    if (mbar_wait_for(bar, parity, 1000000u))
+        return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < kTimeoutNs)
+        if (mbar_wait_for(bar, parity, 1000000u))
+            return true;
+    atomicCAS(&g_q8_mid_error, 0u, (unsigned)SSD_ERR_TIMEOUT);
+    return false;
+}
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity)
+{
+    return __all_sync(0xffffffffu, wait_bar(bar, parity));
+}
+__device__ __forceinline__ void warp_arrive(uint64_t *bar)
+{
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+        mbar_arrive(bar);
+}
+
+template <typename T> __device__ __forceinline__ T from_f32(float v);
+template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+template <int MT, typename T>
+__global__ void __launch_bounds__(kThreads, 2) ssd_q8_mid_kernel(const Q8Params p, int splits, int multi)
+{
+    using S = Shape<MT>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t bars[kBars];
+    __shared__ uint32_t holder;
+    __shared__ float token_scale[MT];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tile = blockIdx.x / splits, rank = blockIdx.x - tile * splits;
+    const long long t0 = (long long)blockIdx.y * MT;
+    // this CTA's slabs
+    const int first = (int)((long long)p.k64 * rank / splits), last = (int)((long long)p.k64 * (rank + 1) / splits);
+    const int slabs = last - first;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kW; ++i) {
+            mbar_init(&bars[BAR_WFULL + i], 1);
+            mbar_init(&bars[BAR_WEMPTY + i], 4);
+        }
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&bars[BAR_FULL + i], 8);
+            mbar_init(&bars[BAR_EMPTY + i], 1);
+        }
+        mbar_init(&bars[BAR_ACC], 1);
+        mbar_init(&bars[BAR_DRAINED], 4);
+        fence_mbar_init();
+    }
+    if (warp == 9) {
+        tmem_alloc(&holder, kCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = holder;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    bool ok = true;
+    for (int i = threadIdx.x; i < MT; i += kThreads)
+        token_scale[i] = t0 + i < p.M ? p.as[t0 + i] : 0.f;
+
+    const uint32_t quarter = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    int *sums = reinterpret_cast<int *>(smem + S::kRings) + 32 * (warp & 3) + lane;   // (with `multi`)
+    // warps 0-3: 8 tokens' sums of the accumulators in use, and of what was drained before
+    auto collect = [&](int c0, int accs, bool more, int (&v)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = more ? sums[(c0 + i) * 128] : 0;
+        for (int j = 0; j < accs; ++j) {
+            uint32_t u[8];
+            tmem_ld8(quarter + j * MT + c0, u);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] += __float2int_rn(__uint_as_float(u[i]));
+        }
+    };
+
+    if (warp < 4) {
+        const int row = threadIdx.x;
+        uint32_t round = 0;
+        for (int k = 0; k < slabs && ok; ++k) {
+            const int w = k % S::kW, s = k % kStages;
+            if (!(ok = warp_wait(&bars[BAR_WFULL + w], (k / S::kW) & 1)))
+                break;
+            uint32_t f[32];
+            const uint8_t *src = smem + S::kOffW + w * kSlabBytes + row * 16;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                widen16(*reinterpret_cast<const uint4 *>(src + c * 2048), &f[8 * c]);
+            warp_arrive(&bars[BAR_WEMPTY + w]);
+            if (k >= kStages && !(ok = warp_wait(&bars[BAR_EMPTY + s], (k / kStages - 1) & 1)))
+                break;
+            tc_fence_after();
+            tmem_st32(quarter + kColA + 32 * s, f);
+            tmem_wait_st();
+            tc_fence_before();
+            warp_arrive(&bars[BAR_FULL + s]);
+            if (k + 1 < slabs && (k + 1) % S::kRound == 0) {   // (only with `multi`)
+                if (!(ok = warp_wait(&bars[BAR_ACC], round & 1)))
+                    break;
+                tc_fence_after();
+                for (int c0 = 0; c0 < MT; c0 += 8) {
+                    int v[8];
+                    collect(c0, S::kAccs, round > 0, v);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        sums[(c0 + i) * 128] = v[i];
+                }
+                tc_fence_before();
+                warp_arrive(&bars[BAR_DRAINED]);
+                ++round;
+            }
+        }
+        if (ok && (ok = warp_wait(&bars[BAR_ACC], round & 1)))
+            tc_fence_after();
+    } else if (warp < 8) {
+        constexpr int kPer = MT / 32;     // 16-byte pieces of a slab per thread
+        constexpr int kAhead = 8 / kPer;  // slabs on their way in registers
+        const int tid = threadIdx.x - 128;
+        uint4 buf[kAhead][kPer];
+        auto fetch = [&](int k, uint4 (&u)[kPer]) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int id = i * 128 + tid;
+                u[i] = k < slabs ? load16(p, t0 + id / 4, (first + k) * 64 + (id % 4) * 16) : make_uint4(0u, 0u, 0u, 0u);
+            }
+        };
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            fetch(j, buf[j]);
+        for (int k0 = 0; k0 < slabs && ok; k0 += kAhead) {
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const int k = k0 + j, s = k % kStages;
+                if (k >= slabs || !ok)
+                    break;
+                if (k >= kStages && !(ok = warp_wait(&bars[BAR_EMPTY + s], (k / kStages - 1) & 1)))
+                    break;
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    const int id = i * 128 + tid;
+                    uint32_t f[8];
+                    widen16(buf[j][i], f);
+                    uint8_t *to = smem + S::kOffB + s * S::kB;
+                    *reinterpret_cast<uint4 *>(to + sw128(id / 4, 2 * (id % 4))) = make_uint4(f[0], f[1], f[2], f[3]);
+                    *reinterpret_cast<uint4 *>(to + sw128(id / 4, 2 * (id % 4) + 1)) = make_uint4(f[4], f[5], f[6], f[7]);
+                }
+                fetch(k + kAhead, buf[j]);
+                fence_proxy_async_smem();
+                warp_arrive(&bars[BAR_FULL + s]);
+            }
+        }
+    } else if (warp == 8) {
+        if (lane == 0) {
+            const int8_t *src = p.w + ((size_t)tile * p.k64 + first) * kSlabBytes;
+            int k = 0;
+            for (; k < slabs; ++k) {
+                const int w = k % S::kW;
+                if (k >= S::kW && !(ok = wait_bar(&bars[BAR_WEMPTY + w], (k / S::kW - 1) & 1)))
+                    break;
+                mbar_arrive_expect_tx(&bars[BAR_WFULL + w], kSlabBytes);
+                bulk_load(smem + S::kOffW + w * kSlabBytes, src + (size_t)k * kSlabBytes, kSlabBytes, &bars[BAR_WFULL + w]);
+            }
+            // no copy may be under way when shared memory is given up
+            for (int j = max(0, k - S::kW); j < k; ++j)
+                wait_bar(&bars[BAR_WFULL + j % S::kW], (j / S::kW) & 1);
+        }
+        __syncwarp();
+    } else {
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc_f16_f32(128, MT);
+            uint32_t round = 0;
+            for (int k = 0; k < slabs; ++k) {
+                const int s = k % kStages;
+                if (k > 0 && k % S::kRound == 0) {
+                    mma_commit(&bars[BAR_ACC]);
+                    if (!(ok = wait_bar(&bars[BAR_DRAINED], round & 1)))
+                        break;
+                    tc_fence_after();
+                    ++round;
+                }
+                if (!(ok = wait_bar(&bars[BAR_FULL + s], (k / kStages) & 1)))
+                    break;
+                tc_fence_after();
+                const uint32_t b = smem_u32(smem + S::kOffB + s * S::kB), acc = tmem + (k / kChunkSlabs) % S::kAccs * MT;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_ts(acc, tmem + kColA + 32 * s + 8 * kk, sdesc_sw128(b + 32 * kk, 16, 1024), idesc,
+                           k % kChunkSlabs > 0 || kk > 0);
+                mma_commit(&bars[BAR_EMPTY + s]);
+            }
+            mma_commit(&bars[BAR_ACC]);   // (every MMA issued so far)
+            wait_bar(&bars[BAR_ACC], round & 1);
+        }
+        __syncwarp();
+    }
+    const int accs = ((slabs - 1) % S::kRound) / kChunkSlabs + 1;
+    const bool more = multi && slabs > S::kRound;
+    T *y = static_cast<T *>(p.y) + t0 * p.sy + tile * 128;
+    const int left = (int)min((long long)MT, p.M - t0);   // tokens
+    const int n = threadIdx.x & 127;
+    const bool mine = tile * 128 + n < p.N;
+    const float ws = warp < 8 && mine ? p.ws[tile * 128 + n] : 0.f;
+    if (splits == 1) {
+        __syncthreads();   // (token_scale)
+        if (warp < 4 && ok)
+            for (int c0 = 0; c0 < left; c0 += 8) {
+                int v[8];
+                collect(c0, accs, more, v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (mine && c0 + i < left)
+                        y[(c0 + i) * p.sy + n] = from_f32<T>((float)v[i] * token_scale[c0 + i] * ws);
+            }
+    } else {
+        // CTA q of the cluster adds up and stores the tokens q * cols ...: the others put their sums of
+        // these into its shared memory, where the rings were; they are done with in this CTA
+        // (the last wait above was for every MMA) and, after the barrier, in the whole cluster.
+        const int cols = ((MT + splits - 1) / splits + 7) / 8 * 8;
+        cluster_sync();
+        if (warp < 4 && ok)
+            for (int c0 = 0; c0 < left; c0 += 8) {
+                int v[8];
+                collect(c0, accs, more, v);
+                const int owner = c0 / cols;
+                const uint32_t to = cluster_addr(smem_u32(smem) + 4u * ((rank * cols + c0 - owner * cols) * 128 + n), owner);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    cluster_st(to + 512u * i, v[i]);
+            }
+        cluster_sync();
+        const int *parts = reinterpret_cast<const int *>(smem) + n;
+        const int c1 = min(cols, left - rank * cols);
+        if (warp < 8 && mine)
+            for (int c = threadIdx.x >> 7; c < c1; c += 2) {
+                int v = 0;
+#pragma unroll 4
+                for (int q = 0; q < splits; ++q)
+                    v += parts[(q * cols + c) * 128];
+                y[(rank * cols + c) * p.sy + n] = from_f32<T>((float)v * token_scale[rank * cols + c] * ws);
+            }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kCols);
+    }
+}
+
+template <int MT, typename T>
+cudaError_t launch_t(const Q8Params &p, int splits, cudaStream_t st)
+{
+    using S = Shape<MT>;
+    const int most = (p.k64 + splits - 1) / splits;
+    const int multi = most > S::kRound;
+    const int smem = S::kRings + (multi ? S::kSums : 0) + 1024;
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(ssd_q8_mid_kernel<MT, T>, S::kRings + S::kSums + 1024, done);
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = splits;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.tiles * splits, (unsigned)((p.M + MT - 1) / MT));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, ssd_q8_mid_kernel<MT, T>, p, splits, multi);
+    if (e == cudaSuccess)
+        note_launches(1);
+    return e;
+}
+
+}  // namespace
+
+cudaError_t q8_mid_launch(const Q8Params &p, bool f32, cudaStream_t st)
+{
+    const int mt = p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
+    const long long tiles = (long long)p.tiles * ((p.M + mt - 1) / mt);
+    // ranges of K: as many as let every CTA run at once, two on an SM, and none below 2 slabs
+    const int splits = (int)std::max<long long>(1, std::min<long long>({8, 2 * sm_count() / tiles, p.k64 / 2}));
+    if (mt == 32)
+        return f32 ? launch_t<32, float>(p, splits, st) : launch_t<32, __nv_bfloat16>(p, splits, st);
+    if (mt == 64)
+        return f32 ? launch_t<64, float>(p, splits, st) : launch_t<64, __nv_bfloat16>(p, splits, st);
+    return f32 ? launch_t<128, float>(p, splits, st) : launch_t<128, __nv_bfloat16>(p, splits, st);
+}
+
+ssd_status_t q8_mid_read_device_error(uint32_t *code)
+{
+    unsigned int v = 0, zero = 0;
+    if (cudaMemcpyFromSymbol(&v, g_q8_mid_error, sizeof(v)) != cudaSuccess ||
+        cudaMemcpyToSymbol(g_q8_mid_error, &zero, sizeof(zero)) != cudaSuccess)
+        return SSD_ERR_CUDA;
+    *code = v;
+    return SSD_OK;
+}
+
+}  // namespace ssd
