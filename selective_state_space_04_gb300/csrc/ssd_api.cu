@@ -1001,7 +1001,7 @@ ssd_status_t ssd_get_device_error(void *stream, uint32_t *code)
     if (s2 == SSD_OK)
         s2 = complex_tc_read_device_error(&cplx);
     if (s2 == SSD_OK)
-        s2 = q8_mid_read_device_error(&q8);
+        s2 = q8_read_device_error(&q8);
     if (s2 != SSD_OK)
         return s2;
     if (*code == 0)

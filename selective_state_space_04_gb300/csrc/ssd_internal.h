@@ -286,7 +286,7 @@ struct Q8Args {
 cudaError_t q8_pack_launch(const int8_t *w, int8_t *packed, const ssd_q8_dims_t &d, cudaStream_t stream);
 size_t q8_workspace_bytes(const ssd_q8_dims_t &d);
 cudaError_t q8_launch(const Q8Args &a, void *workspace, cudaStream_t stream);
-ssd_status_t q8_mid_read_device_error(uint32_t *code);
+ssd_status_t q8_read_device_error(uint32_t *code);
 
 // ssd_step.cu: conv1d + SiLU and the scan for single tokens on a pool of states
 struct StepArgs {

@@ -46,13 +46,13 @@ cudaError_t q8_pack_launch(const int8_t *w, int8_t *packed, const ssd_q8_dims_t 
     return e;
 }
 
-size_t q8_workspace_bytes(const ssd_q8_dims_t &) { return 0; }
+namespace {
 
-cudaError_t q8_launch(const Q8Args &a, void *, cudaStream_t st)
+// from here on widening both operands first pays
+constexpr long long kMany = 257;
+
+Q8Params params(const Q8Args &a)
 {
-    SSD_NVTX_RANGE("q8_launch");
-    if (a.d.M == 0)
-        return cudaSuccess;
     Q8Params p;
     p.a = a.a;
     p.w = a.packed;
@@ -67,7 +67,33 @@ cudaError_t q8_launch(const Q8Args &a, void *, cudaStream_t st)
     p.k64 = (p.K + 63) / 64;
     p.tiles = (p.N + 127) / 128;
     p.vec = ((uintptr_t)p.a & 15) == 0 && (p.sa % 16 == 0 || p.M == 1);
-    return q8_mid_launch(p, a.d.out_dtype == SSD_DTYPE_F32, st);
+    return p;
+}
+
+}  // namespace
+
+size_t q8_workspace_bytes(const ssd_q8_dims_t &d)
+{
+    return d.M >= kMany ? q8_many_workspace_bytes(params(Q8Args{nullptr, nullptr, nullptr, nullptr, nullptr, d})) : 0;
+}
+
+cudaError_t q8_launch(const Q8Args &a, void *workspace, cudaStream_t st)
+{
+    SSD_NVTX_RANGE("q8_launch");
+    const Q8Params p = params(a);
+    const bool f32 = a.d.out_dtype == SSD_DTYPE_F32;
+    return p.M >= kMany ? q8_many_launch(p, f32, workspace, st) : q8_mid_launch(p, f32, st);
+}
+
+ssd_status_t q8_read_device_error(uint32_t *code)
+{
+    uint32_t many = 0;
+    ssd_status_t s = q8_mid_read_device_error(code);
+    if (s == SSD_OK)
+        s = q8_many_read_device_error(&many);
+    if (*code == 0)
+        *code = many;
+    return s;
 }
 
 }  // namespace ssd

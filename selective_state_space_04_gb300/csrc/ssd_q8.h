@@ -19,7 +19,13 @@ struct Q8Params {
     int vec;                      // a's rows are 16-byte aligned
 };
 
+// many tokens (workspace: 16-byte aligned)
+size_t q8_many_workspace_bytes(const Q8Params &p);
+cudaError_t q8_many_launch(const Q8Params &p, bool f32, void *workspace, cudaStream_t st);
+// up to a few hundred tokens
 cudaError_t q8_mid_launch(const Q8Params &p, bool f32, cudaStream_t st);
+ssd_status_t q8_many_read_device_error(uint32_t *code);
+ssd_status_t q8_mid_read_device_error(uint32_t *code);
 
 #ifdef __CUDACC__
 // Offset of 16-byte piece c of row r in a tile of 128-byte rows with the 128-byte swizzle.

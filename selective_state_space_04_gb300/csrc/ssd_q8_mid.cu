@@ -58,14 +58,18 @@ constexpr int kColA = 128, kCols = 256;   // TMEM: accumulators, then the weight
 
 enum { BAR_WFULL = 0, BAR_WEMPTY = 8, BAR_FULL = 16, BAR_EMPTY = BAR_FULL + kStages, BAR_ACC = BAR_EMPTY + kStages, BAR_DRAINED, kBars };
 
+// bounded wait; false after kTimeoutNs
 __device__ bool wait_bar(uint64_t *bar, uint32_t parity)
 {
-    if (mbar_wait_for(bar, parity, 1000000u))
-        return true;
-    const uint64_t t0 = globaltimer_ns();
-    while (globaltimer_ns() - t0 < kTimeoutNs)
-        if (mbar_wait_for(bar, parity, 1000000u))
+    for (int i = 0; i < 64; ++i)
+        if (mbar_test(bar, parity))
             return true;
+    const uint64_t t0 = globaltimer_ns();
+    do {
+        for (int i = 0; i < 64; ++i)
+            if (mbar_test(bar, parity))
+                return true;
+    } while (globaltimer_ns() - t0 < kTimeoutNs);
     atomicCAS(&g_q8_mid_error, 0u, (unsigned)SSD_ERR_TIMEOUT);
     return false;
 }
