@@ -66,7 +66,7 @@ Q8Params params(const Q8Args &a)
     p.K = a.d.K;
     p.k64 = (p.K + 63) / 64;
     p.tiles = (p.N + 127) / 128;
-    p.vec = ((uintptr_t)p.a & 15) == 0 && (p.sa % 16 == 0 || p.M == 1);
+    p.vec = ((uintptr_t)p.a & 7) == 0 && (p.sa % 8 == 0 || p.M == 1);
     return p;
 }
 
@@ -74,7 +74,8 @@ Q8Params params(const Q8Args &a)
 
 size_t q8_workspace_bytes(const ssd_q8_dims_t &d)
 {
-    return d.M >= kMany ? q8_many_workspace_bytes(params(Q8Args{nullptr, nullptr, nullptr, nullptr, nullptr, d})) : 0;
+    const Q8Params p = params(Q8Args{nullptr, nullptr, nullptr, nullptr, nullptr, d});
+    return d.M >= kMany ? q8_many_workspace_bytes(p) : q8_mid_workspace_bytes(p);
 }
 
 cudaError_t q8_launch(const Q8Args &a, void *workspace, cudaStream_t st)
@@ -82,7 +83,7 @@ cudaError_t q8_launch(const Q8Args &a, void *workspace, cudaStream_t st)
     SSD_NVTX_RANGE("q8_launch");
     const Q8Params p = params(a);
     const bool f32 = a.d.out_dtype == SSD_DTYPE_F32;
-    return p.M >= kMany ? q8_many_launch(p, f32, workspace, st) : q8_mid_launch(p, f32, st);
+    return p.M >= kMany ? q8_many_launch(p, f32, workspace, st) : q8_mid_launch(p, f32, workspace, st);
 }
 
 ssd_status_t q8_read_device_error(uint32_t *code)

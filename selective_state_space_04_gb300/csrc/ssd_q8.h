@@ -16,14 +16,19 @@ struct Q8Params {
     void *y;                      // [M, N] rows sy apart
     long long M, sa, sy;
     int N, K, k64, tiles;         // k64: slabs of 64 inner elements; tiles of 128 channels
-    int vec;                      // a's rows are 16-byte aligned
+    int vec;                      // a's rows are 8-byte aligned
 };
 
 // many tokens (workspace: 16-byte aligned)
 size_t q8_many_workspace_bytes(const Q8Params &p);
 cudaError_t q8_many_launch(const Q8Params &p, bool f32, void *workspace, cudaStream_t st);
 // up to a few hundred tokens
-cudaError_t q8_mid_launch(const Q8Params &p, bool f32, cudaStream_t st);
+size_t q8_mid_workspace_bytes(const Q8Params &p);
+cudaError_t q8_mid_launch(const Q8Params &p, bool f32, void *workspace, cudaStream_t st);
+// fp16 images of 128 rows x 64 elements, swizzled, from the first `wslabs` slabs of the weights (to
+// wi) and all the tokens' (to ai)
+constexpr int kQ8Image = 128 * 128;   // bytes
+cudaError_t q8_widen_launch(const Q8Params &p, uint8_t *wi, uint8_t *ai, long long wslabs, cudaStream_t st);
 ssd_status_t q8_many_read_device_error(uint32_t *code);
 ssd_status_t q8_mid_read_device_error(uint32_t *code);
 
@@ -31,35 +36,38 @@ ssd_status_t q8_mid_read_device_error(uint32_t *code);
 // Offset of 16-byte piece c of row r in a tile of 128-byte rows with the 128-byte swizzle.
 __device__ __forceinline__ uint32_t sw128(uint32_t r, uint32_t c) { return r * 128u + ((c ^ (r & 7u)) << 4); }
 
-// 16 8-bit integers to fp16, exactly: b + 128 below the bits of 1024 (spacing 1 there)
+// 4 8-bit integers to fp16, exactly: b + 128 below the bits of 1024 (spacing 1 there)
 // is 1024 + 128 + b; 1152 is taken off again.
+__device__ __forceinline__ void widen4(uint32_t u, uint32_t *f)
+{
+    const uint32_t v = u ^ 0x80808080u, lo = __byte_perm(v, 0x64646464u, 0x4140), hi = __byte_perm(v, 0x64646464u, 0x4342);
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));
+    const __half2 a = __hsub2(*reinterpret_cast<const __half2 *>(&lo), off), b = __hsub2(*reinterpret_cast<const __half2 *>(&hi), off);
+    f[0] = *reinterpret_cast<const uint32_t *>(&a);
+    f[1] = *reinterpret_cast<const uint32_t *>(&b);
+}
 __device__ __forceinline__ void widen16(const uint4 &u, uint32_t *f)
 {
-    const uint32_t v[4] = {u.x ^ 0x80808080u, u.y ^ 0x80808080u, u.z ^ 0x80808080u, u.w ^ 0x80808080u};
-    const __half2 off = __half2half2(__ushort_as_half(0x6480));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = __byte_perm(v[i], 0x64646464u, 0x4140), hi = __byte_perm(v[i], 0x64646464u, 0x4342);
-        const __half2 a = __hsub2(*reinterpret_cast<const __half2 *>(&lo), off), b = __hsub2(*reinterpret_cast<const __half2 *>(&hi), off);
-        f[2 * i] = *reinterpret_cast<const uint32_t *>(&a);
-        f[2 * i + 1] = *reinterpret_cast<const uint32_t *>(&b);
-    }
+    widen4(u.x, f);
+    widen4(u.y, f + 2);
+    widen4(u.z, f + 4);
+    widen4(u.w, f + 6);
 }
 
-// a[t, k .. k + 15], zeros beyond M and K
-__device__ __forceinline__ uint4 load16(const Q8Params &p, long long t, int k)
+// a[t, k .. k + 7], zeros beyond M and K
+__device__ __forceinline__ uint2 load8(const Q8Params &p, long long t, int k)
 {
     if (t >= p.M || k >= p.K)
-        return make_uint4(0u, 0u, 0u, 0u);
+        return make_uint2(0u, 0u);
     const int8_t *src = p.a + t * p.sa + k;
-    if (p.vec && k + 16 <= p.K)
-        return __ldg(reinterpret_cast<const uint4 *>(src));
-    uint32_t v[4] = {0u, 0u, 0u, 0u};
+    if (p.vec && k + 8 <= p.K)
+        return __ldg(reinterpret_cast<const uint2 *>(src));
+    uint32_t v[2] = {0u, 0u};
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
+    for (int e = 0; e < 8; ++e)
         if (k + e < p.K)
             v[e / 4] |= (uint32_t)(uint8_t)src[e] << (8 * (e % 4));
-    return make_uint4(v[0], v[1], v[2], v[3]);
+    return make_uint2(v[0], v[1]);
 }
 #endif
 

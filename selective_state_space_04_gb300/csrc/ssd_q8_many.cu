@@ -28,7 +28,7 @@ static __device__ unsigned int g_q8_many_error;
 
 namespace {
 
-constexpr int kImage = 128 * 128;   // bytes of 128 rows x 64 fp16
+constexpr int kImage = kQ8Image;
 constexpr int kStages = 6;
 constexpr int kStageBytes = 2 * kImage;
 constexpr int kChunkSlabs = 16;
@@ -60,42 +60,38 @@ template <typename T> __device__ __forceinline__ T from_f32(float v);
 template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// 16 elements (16-byte piece c16 of a slab) of row r into an image
-__device__ __forceinline__ void put16(uint8_t *image, int r, int c16, const uint4 &u)
-{
-    uint32_t f[8];
-    widen16(u, f);
-    *reinterpret_cast<uint4 *>(image + sw128(r, 2 * c16)) = make_uint4(f[0], f[1], f[2], f[3]);
-    *reinterpret_cast<uint4 *>(image + sw128(r, 2 * c16 + 1)) = make_uint4(f[4], f[5], f[6], f[7]);
-}
-
 // Widens the weights' slabs (the first `wslabs`: tile by tile, slab by slab; none on later
-// panels) and the panel's tokens'.  One block per image: 4 lanes a row, so that a
-// warp's stores are whole 128-byte rows.
+// panels and for the tokens alone) and the panel's tokens'.  One block per image, 8 lanes a row
+// with 8 elements each, so that a warp's stores are whole 128-byte rows (16
+// elements a lane, two stores with a gap between: 23 us for 4096 tokens and 10576 x 2560
+// weights).
 __global__ void __launch_bounds__(256) ssd_q8_widen_kernel(const Q8Params p, uint8_t *wi, uint8_t *ai, long long wslabs, long long slabs)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int c = threadIdx.x & 3, r0 = threadIdx.x >> 2;
+    const int c = threadIdx.x & 7, r0 = threadIdx.x >> 3;
     for (long long i = blockIdx.x; i < slabs; i += gridDim.x) {
+        uint2 u[4];
+        uint8_t *image;
         if (i < wslabs) {
-            uint4 u[2];
+            image = wi + i * kImage;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                u[h] = __ldg(reinterpret_cast<const uint4 *>(p.w + i * 8192 + c * 2048 + (r0 + 64 * h) * 16));
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                put16(wi + i * kImage, r0 + 64 * h, c, u[h]);
+            for (int h = 0; h < 4; ++h)
+                u[h] = __ldg(reinterpret_cast<const uint2 *>(p.w + i * 8192 + (c >> 1) * 2048 + (r0 + 32 * h) * 16 + (c & 1) * 8));
         } else {
             const long long j = i - wslabs, t0 = j / p.k64 * 128;
-            const int k0 = (int)(j % p.k64) * 64 + c * 16;
-            uint4 u[2];
+            const int k0 = (int)(j % p.k64) * 64 + c * 8;
+            image = ai + j * kImage;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                u[h] = load16(p, t0 + r0 + 64 * h, k0);
+            for (int h = 0; h < 4; ++h)
+                u[h] = load8(p, t0 + r0 + 32 * h, k0);
+        }
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                put16(ai + j * kImage, r0 + 64 * h, c, u[h]);
+        for (int h = 0; h < 4; ++h) {
+            uint32_t f[4];
+            widen4(u[h].x, f);
+            widen4(u[h].y, f + 2);
+            *reinterpret_cast<uint4 *>(image + sw128(r0 + 32 * h, c)) = make_uint4(f[0], f[1], f[2], f[3]);
         }
     }
 }
@@ -267,6 +263,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
 }
 
+cudaLaunchConfig_t after(cudaLaunchAttribute (&pdl)[1], cudaStream_t st)
+{
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = st;
+    cfg.attrs = pdl;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
 template <typename T>
 cudaError_t many_t(const Q8Params &p, uint8_t *ws, cudaStream_t st)
 {
@@ -275,12 +282,7 @@ cudaError_t many_t(const Q8Params &p, uint8_t *ws, cudaStream_t st)
     if (e != cudaSuccess)
         return e;
     cudaLaunchAttribute pdl[1];
-    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    pdl[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.stream = st;
-    cfg.attrs = pdl;
-    cfg.numAttrs = 1;
+    cudaLaunchConfig_t cfg = after(pdl, st);
     const long long wslabs = (long long)p.tiles * p.k64;
     uint8_t *ai = ws + wslabs * kImage;
     for (long long m0 = 0; m0 < p.M; m0 += kPanel) {
@@ -290,14 +292,9 @@ cudaError_t many_t(const Q8Params &p, uint8_t *ws, cudaStream_t st)
         q.as = p.as + m0;
         q.y = static_cast<T *>(p.y) + m0 * p.sy;
         const int ttiles = (int)((q.M + 127) / 128), cp = (p.tiles + 1) / 2, tp = (ttiles + 1) / 2;
-        const long long now = m0 == 0 ? wslabs : 0, slabs = now + (long long)ttiles * p.k64;
-        cfg.gridDim = dim3((unsigned)std::min<long long>(slabs, 1 << 16));
-        cfg.blockDim = dim3(256);
-        cfg.dynamicSmemBytes = 0;
-        e = cudaLaunchKernelEx(&cfg, ssd_q8_widen_kernel, q, ws, ai, now, slabs);
+        e = q8_widen_launch(q, ws, ai, m0 == 0 ? wslabs : 0, st);
         if (e != cudaSuccess)
             return e;
-        note_launches(1);
         cfg.gridDim = dim3(2 * (unsigned)std::min(cp * tp, sm_count() / 2));
         cfg.blockDim = dim3(kThreads);
         cfg.dynamicSmemBytes = kSmem;
@@ -310,6 +307,19 @@ cudaError_t many_t(const Q8Params &p, uint8_t *ws, cudaStream_t st)
 }
 
 }  // namespace
+
+cudaError_t q8_widen_launch(const Q8Params &p, uint8_t *wi, uint8_t *ai, long long wslabs, cudaStream_t st)
+{
+    const long long slabs = wslabs + (p.M + 127) / 128 * p.k64;
+    cudaLaunchAttribute pdl[1];
+    cudaLaunchConfig_t cfg = after(pdl, st);
+    cfg.gridDim = dim3((unsigned)std::min<long long>(slabs, 1 << 16));
+    cfg.blockDim = dim3(256);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, ssd_q8_widen_kernel, p, wi, ai, wslabs, slabs);
+    if (e == cudaSuccess)
+        note_launches(1);
+    return e;
+}
 
 size_t q8_many_workspace_bytes(const Q8Params &p)
 {

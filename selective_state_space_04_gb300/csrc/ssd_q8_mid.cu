@@ -7,11 +7,14 @@
 // So every 1024 inner elements have an accumulator of their own, as far as TMEM goes;
 // beyond that the accumulators are drained into 32-bit integers in shared memory.
 //
-// A slab's weights (8 KB, contiguous) come by bulk copy; four warps widen them, a
-// thread per channel, and put them into TMEM as the MMA's A operand, which keeps them
-// out of shared memory's bandwidth: at the memory's rate the weights alone would take
-// 6.8 TB/s into shared memory, as much out, and twice that again each way as fp16.
-// Four more warps widen the tokens into swizzled shared memory, the B operand.
+// A slab's weights (8 KB, contiguous) come by bulk copy; two groups of four warps take the
+// slabs in turn, widen them, a thread per channel, and put them into TMEM as the MMA's A
+// operand, which keeps them out of shared memory's bandwidth: at the memory's rate the
+// weights alone would take 6.8 TB/s into shared memory, as much out, and twice that again
+// each way as fp16.  The tokens, the B operand, are widened by a small launch in
+// front, into the images that the copies bring (ssd_q8_many.cu): widened in here, the
+// fence between ordinary stores and the MMA waits for every load under way as well,
+// which cost a memory latency a slab (128 tokens: 23.7 us).
 //
 // K is split over a cluster of CTAs where there are few tiles; each CTA ends with the
 // sums of its range, they are exchanged through distributed shared memory, every CTA
@@ -33,17 +36,21 @@ static __device__ unsigned int g_q8_mid_error;
 
 namespace {
 
-constexpr int kThreads = 320;   // warps 0-3: weights and results, 4-7: tokens, 8: copies, 9: MMA
+constexpr int kThreads = 320;   // warps 0-7: weights and results, 8: copies, 9: MMA
 constexpr int kStages = 4;      // slabs in TMEM (A) and shared memory (B)
 constexpr int kSlabBytes = 128 * 64;
 constexpr int kChunkSlabs = 16;   // slabs of one accumulator: 1024 inner elements
+constexpr int kImage = kQ8Image;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
 template <int MT> struct Shape {
     // Weight slabs on their way.  With them a CTA takes more than a third of an SM's shared memory: a
     // third CTA on an SM would wait for tensor memory, and the CTAs of two clusters that wait
     // for each other's that way would wait for ever.
-    static constexpr int kW = MT == 128 ? 5 : 8;
+    // Even, as kStages is: a place in either ring then always has the same group of warps, which has
+    // seen each of its phases (a wait for a phase whose predecessor is not done with passes).
+    static constexpr int kW = MT == 128 ? 4 : 8;
+    static_assert(kW % 2 == 0 && kStages % 2 == 0, "two groups take the slabs in turn");
     static constexpr int kB = MT * 128;                   // a slab of tokens as fp16
     static constexpr int kOffB = 0;                       // (1024-byte aligned)
     static constexpr int kOffW = kStages * kB;
@@ -56,7 +63,7 @@ template <int MT> struct Shape {
 };
 constexpr int kColA = 128, kCols = 256;   // TMEM: accumulators, then the weights' stages
 
-enum { BAR_WFULL = 0, BAR_WEMPTY = 8, BAR_FULL = 16, BAR_EMPTY = BAR_FULL + kStages, BAR_ACC = BAR_EMPTY + kStages, BAR_DRAINED, kBars };
+enum { BAR_WFULL = 0, BAR_WEMPTY = 8, BAR_A = 16, BAR_B = BAR_A + kStages, BAR_EMPTY = BAR_B + kStages, BAR_ACC = BAR_EMPTY + kStages, BAR_DRAINED, kBars };
 
 // bounded wait; false after kTimeoutNs
 __device__ bool wait_bar(uint64_t *bar, uint32_t parity)
@@ -89,7 +96,7 @@ template <> __device__ __forceinline__ float from_f32<float>(float v) { return v
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
 template <int MT, typename T>
-__global__ void __launch_bounds__(kThreads, 2) ssd_q8_mid_kernel(const Q8Params p, int splits, int multi)
+__global__ void __launch_bounds__(kThreads, 2) ssd_q8_mid_kernel(const Q8Params p, const uint8_t *images, int splits, int multi)
 {
     using S = Shape<MT>;
     extern __shared__ uint8_t smem_raw[];
@@ -110,11 +117,12 @@ __global__ void __launch_bounds__(kThreads, 2) ssd_q8_mid_kernel(const Q8Params 
             mbar_init(&bars[BAR_WEMPTY + i], 4);
         }
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&bars[BAR_FULL + i], 8);
+            mbar_init(&bars[BAR_A + i], 4);
+            mbar_init(&bars[BAR_B + i], 1);
             mbar_init(&bars[BAR_EMPTY + i], 1);
         }
         mbar_init(&bars[BAR_ACC], 1);
-        mbar_init(&bars[BAR_DRAINED], 4);
+        mbar_init(&bars[BAR_DRAINED], 8);
         fence_mbar_init();
     }
     if (warp == 9) {
@@ -125,15 +133,15 @@ __global__ void __launch_bounds__(kThreads, 2) ssd_q8_mid_kernel(const Q8Params 
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = holder;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // The launch in front of this one writes the tokens' images, and has waited for all before it before
+    // it let this one begin: weights and scales may be read at once, the images after the wait.
     bool ok = true;
     for (int i = threadIdx.x; i < MT; i += kThreads)
         token_scale[i] = t0 + i < p.M ? p.as[t0 + i] : 0.f;
 
     const uint32_t quarter = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
     int *sums = reinterpret_cast<int *>(smem + S::kRings) + 32 * (warp & 3) + lane;   // (with `multi`)
-    // warps 0-3: 8 tokens' sums of the accumulators in use, and of what was drained before
+    // warps 0-7: 8 tokens' sums of the accumulators in use, and of what was drained before
     auto collect = [&](int c0, int accs, bool more, int (&v)[8]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -148,95 +156,78 @@ __global__ void __launch_bounds__(kThreads, 2) ssd_q8_mid_kernel(const Q8Params 
         }
     };
 
-    if (warp < 4) {
-        const int row = threadIdx.x;
-        uint32_t round = 0;
-        for (int k = 0; k < slabs && ok; ++k) {
-            const int w = k % S::kW, s = k % kStages;
-            if (!(ok = warp_wait(&bars[BAR_WFULL + w], (k / S::kW) & 1)))
-                break;
-            uint32_t f[32];
-            const uint8_t *src = smem + S::kOffW + w * kSlabBytes + row * 16;
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                widen16(*reinterpret_cast<const uint4 *>(src + c * 2048), &f[8 * c]);
-            warp_arrive(&bars[BAR_WEMPTY + w]);
-            if (k >= kStages && !(ok = warp_wait(&bars[BAR_EMPTY + s], (k / kStages - 1) & 1)))
-                break;
-            tc_fence_after();
-            tmem_st32(quarter + kColA + 32 * s, f);
-            tmem_wait_st();
-            tc_fence_before();
-            warp_arrive(&bars[BAR_FULL + s]);
-            if (k + 1 < slabs && (k + 1) % S::kRound == 0) {   // (only with `multi`)
-                if (!(ok = warp_wait(&bars[BAR_ACC], round & 1)))
+    if (warp < 8) {
+        const int row = 32 * (warp & 3) + lane, group = warp >> 2;
+        for (int round = 0, k = group; ok; ++round) {
+            const int end = min(slabs, (round + 1) * S::kRound);
+            for (; k < end; k += 2) {
+                const int w = k % S::kW, s = k % kStages;
+                if (!(ok = warp_wait(&bars[BAR_WFULL + w], (k / S::kW) & 1)))
                     break;
-                tc_fence_after();
-                for (int c0 = 0; c0 < MT; c0 += 8) {
-                    int v[8];
-                    collect(c0, S::kAccs, round > 0, v);
+                uint32_t f[32];
+                const uint8_t *src = smem + S::kOffW + w * kSlabBytes + row * 16;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        sums[(c0 + i) * 128] = v[i];
-                }
-                tc_fence_before();
-                warp_arrive(&bars[BAR_DRAINED]);
-                ++round;
-            }
-        }
-        if (ok && (ok = warp_wait(&bars[BAR_ACC], round & 1)))
-            tc_fence_after();
-    } else if (warp < 8) {
-        constexpr int kPer = MT / 32;     // 16-byte pieces of a slab per thread
-        constexpr int kAhead = 8 / kPer;  // slabs on their way in registers
-        const int tid = threadIdx.x - 128;
-        uint4 buf[kAhead][kPer];
-        auto fetch = [&](int k, uint4 (&u)[kPer]) {
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int id = i * 128 + tid;
-                u[i] = k < slabs ? load16(p, t0 + id / 4, (first + k) * 64 + (id % 4) * 16) : make_uint4(0u, 0u, 0u, 0u);
-            }
-        };
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-            fetch(j, buf[j]);
-        for (int k0 = 0; k0 < slabs && ok; k0 += kAhead) {
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-                const int k = k0 + j, s = k % kStages;
-                if (k >= slabs || !ok)
-                    break;
+                for (int c = 0; c < 4; ++c)
+                    widen16(*reinterpret_cast<const uint4 *>(src + c * 2048), &f[8 * c]);
+                warp_arrive(&bars[BAR_WEMPTY + w]);
                 if (k >= kStages && !(ok = warp_wait(&bars[BAR_EMPTY + s], (k / kStages - 1) & 1)))
                     break;
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) {
-                    const int id = i * 128 + tid;
-                    uint32_t f[8];
-                    widen16(buf[j][i], f);
-                    uint8_t *to = smem + S::kOffB + s * S::kB;
-                    *reinterpret_cast<uint4 *>(to + sw128(id / 4, 2 * (id % 4))) = make_uint4(f[0], f[1], f[2], f[3]);
-                    *reinterpret_cast<uint4 *>(to + sw128(id / 4, 2 * (id % 4) + 1)) = make_uint4(f[4], f[5], f[6], f[7]);
-                }
-                fetch(k + kAhead, buf[j]);
-                fence_proxy_async_smem();
-                warp_arrive(&bars[BAR_FULL + s]);
+                tc_fence_after();
+                tmem_st32(quarter + kColA + 32 * s, f);
+                tmem_wait_st();
+                tc_fence_before();
+                warp_arrive(&bars[BAR_A + s]);
             }
+            if (!ok || !(ok = warp_wait(&bars[BAR_ACC], round & 1)))
+                break;
+            tc_fence_after();
+            if (end == slabs)
+                break;
+            for (int c0 = 8 * group; c0 < MT; c0 += 16) {   // (only with `multi`)
+                int v[8];
+                collect(c0, S::kAccs, round > 0, v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    sums[(c0 + i) * 128] = v[i];
+            }
+            tc_fence_before();
+            warp_arrive(&bars[BAR_DRAINED]);
         }
     } else if (warp == 8) {
         if (lane == 0) {
             const int8_t *src = p.w + ((size_t)tile * p.k64 + first) * kSlabBytes;
-            int k = 0;
-            for (; k < slabs; ++k) {
+            const uint8_t *tokens = images + ((size_t)(t0 / 128) * p.k64 + first) * kImage;
+            auto weights = [&](int k) {
                 const int w = k % S::kW;
                 if (k >= S::kW && !(ok = wait_bar(&bars[BAR_WEMPTY + w], (k / S::kW - 1) & 1)))
-                    break;
+                    return;
                 mbar_arrive_expect_tx(&bars[BAR_WFULL + w], kSlabBytes);
                 bulk_load(smem + S::kOffW + w * kSlabBytes, src + (size_t)k * kSlabBytes, kSlabBytes, &bars[BAR_WFULL + w]);
+            };
+            int kw = 0, k = 0;
+            for (; kw < min(slabs, S::kW); ++kw)
+                weights(kw);
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            for (; k < slabs; ++k) {
+                const int s = k % kStages;
+                if (k >= kStages && !(ok = wait_bar(&bars[BAR_EMPTY + s], (k / kStages - 1) & 1)))
+                    break;
+                mbar_arrive_expect_tx(&bars[BAR_B + s], S::kB);
+                bulk_load(smem + S::kOffB + s * S::kB, tokens + (size_t)k * kImage, S::kB, &bars[BAR_B + s]);
+                if (kw < slabs) {
+                    weights(kw);
+                    if (!ok) {
+                        ++k;
+                        break;
+                    }
+                    ++kw;
+                }
             }
             // no copy may be under way when shared memory is given up
-            for (int j = max(0, k - S::kW); j < k; ++j)
+            for (int j = max(0, kw - S::kW); j < kw; ++j)
                 wait_bar(&bars[BAR_WFULL + j % S::kW], (j / S::kW) & 1);
+            for (int j = max(0, k - kStages); j < k; ++j)
+                wait_bar(&bars[BAR_B + j % kStages], (j / kStages) & 1);
         }
         __syncwarp();
     } else {
@@ -252,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 2) ssd_q8_mid_kernel(const Q8Params 
                     tc_fence_after();
                     ++round;
                 }
-                if (!(ok = wait_bar(&bars[BAR_FULL + s], (k / kStages) & 1)))
+                if (!(ok = wait_bar(&bars[BAR_A + s], (k / kStages) & 1)) || !(ok = wait_bar(&bars[BAR_B + s], (k / kStages) & 1)))
                     break;
                 tc_fence_after();
                 const uint32_t b = smem_u32(smem + S::kOffB + s * S::kB), acc = tmem + (k / kChunkSlabs) % S::kAccs * MT;
@@ -267,6 +258,9 @@ __global__ void __launch_bounds__(kThreads, 2) ssd_q8_mid_kernel(const Q8Params 
         }
         __syncwarp();
     }
+    // (whoever is launched after this one waits for its end before it touches anything)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int accs = ((slabs - 1) % S::kRound) / kChunkSlabs + 1;
     const bool more = multi && slabs > S::kRound;
     T *y = static_cast<T *>(p.y) + t0 * p.sy + tile * 128;
@@ -276,8 +270,8 @@ __global__ void __launch_bounds__(kThreads, 2) ssd_q8_mid_kernel(const Q8Params 
     const float ws = warp < 8 && mine ? p.ws[tile * 128 + n] : 0.f;
     if (splits == 1) {
         __syncthreads();   // (token_scale)
-        if (warp < 4 && ok)
-            for (int c0 = 0; c0 < left; c0 += 8) {
+        if (warp < 8 && ok)
+            for (int c0 = 8 * (warp >> 2); c0 < left; c0 += 16) {
                 int v[8];
                 collect(c0, accs, more, v);
 #pragma unroll
@@ -291,8 +285,8 @@ __global__ void __launch_bounds__(kThreads, 2) ssd_q8_mid_kernel(const Q8Params 
         // (the last wait above was for every MMA) and, after the barrier, in the whole cluster.
         const int cols = ((MT + splits - 1) / splits + 7) / 8 * 8;
         cluster_sync();
-        if (warp < 4 && ok)
-            for (int c0 = 0; c0 < left; c0 += 8) {
+        if (warp < 8 && ok)
+            for (int c0 = 8 * (warp >> 2); c0 < left; c0 += 16) {
                 int v[8];
                 collect(c0, accs, more, v);
                 const int owner = c0 / cols;
@@ -322,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 2) ssd_q8_mid_kernel(const Q8Params 
 }
 
 template <int MT, typename T>
-cudaError_t launch_t(const Q8Params &p, int splits, cudaStream_t st)
+cudaError_t launch_t(const Q8Params &p, const uint8_t *images, int splits, cudaStream_t st)
 {
     using S = Shape<MT>;
     const int most = (p.k64 + splits - 1) / splits;
@@ -345,7 +339,7 @@ cudaError_t launch_t(const Q8Params &p, int splits, cudaStream_t st)
     cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, ssd_q8_mid_kernel<MT, T>, p, splits, multi);
+    e = cudaLaunchKernelEx(&cfg, ssd_q8_mid_kernel<MT, T>, p, images, splits, multi);
     if (e == cudaSuccess)
         note_launches(1);
     return e;
@@ -353,17 +347,25 @@ cudaError_t launch_t(const Q8Params &p, int splits, cudaStream_t st)
 
 }  // namespace
 
-cudaError_t q8_mid_launch(const Q8Params &p, bool f32, cudaStream_t st)
+size_t q8_mid_workspace_bytes(const Q8Params &p) { return (size_t)((p.M + 127) / 128) * p.k64 * kImage; }
+
+cudaError_t q8_mid_launch(const Q8Params &p, bool f32, void *workspace, cudaStream_t st)
 {
     const int mt = p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
     const long long tiles = (long long)p.tiles * ((p.M + mt - 1) / mt);
-    // ranges of K: as many as let every CTA run at once, two on an SM, and none below 2 slabs
-    const int splits = (int)std::max<long long>(1, std::min<long long>({8, 2 * sm_count() / tiles, p.k64 / 2}));
+    // Ranges of K: as many as let every CTA run at once, two on an SM, and none below 2 slabs; and
+    // where that is not many, as many as spare a CTA the draining.
+    const long long spare = std::min(8, (p.k64 + 128 / mt * kChunkSlabs - 1) / (128 / mt * kChunkSlabs));
+    const int splits = (int)std::max(spare, std::min<long long>({8, 2 * sm_count() / tiles, p.k64 / 2}));
+    uint8_t *images = static_cast<uint8_t *>(workspace);
+    const cudaError_t e = q8_widen_launch(p, nullptr, images, 0, st);
+    if (e != cudaSuccess)
+        return e;
     if (mt == 32)
-        return f32 ? launch_t<32, float>(p, splits, st) : launch_t<32, __nv_bfloat16>(p, splits, st);
+        return f32 ? launch_t<32, float>(p, images, splits, st) : launch_t<32, __nv_bfloat16>(p, images, splits, st);
     if (mt == 64)
-        return f32 ? launch_t<64, float>(p, splits, st) : launch_t<64, __nv_bfloat16>(p, splits, st);
-    return f32 ? launch_t<128, float>(p, splits, st) : launch_t<128, __nv_bfloat16>(p, splits, st);
+        return f32 ? launch_t<64, float>(p, images, splits, st) : launch_t<64, __nv_bfloat16>(p, images, splits, st);
+    return f32 ? launch_t<128, float>(p, images, splits, st) : launch_t<128, __nv_bfloat16>(p, images, splits, st);
 }
 
 ssd_status_t q8_mid_read_device_error(uint32_t *code)
