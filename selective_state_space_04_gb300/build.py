@@ -21,7 +21,7 @@ LIB_PATH = os.path.join(BUILD_DIR, "libssd.so")
 SOURCES = ["ssd_api.cu", "ssd_seq.cu", "ssd_chunk.cu", "ssd_decode.cu", "ssd_trap.cu", "ssd_neighbors.cu", "ssd_bwd.cu", "ssd_bwd_chunk.cu", "ssd_bwd_tc.cu", "ssd_complex.cu", "ssd_complex_tc.cu",
            "ssd_paged_plan.cu", "ssd_qk_rope.cu", "ssd_paged_attn.cu",
            "ssd_paged_attn_bf16.cu", "ssd_paged_attn_bf16_any.cu", "ssd_paged_attn_f32.cu",
-           "ssd_norm.cu", "ssd_step.cu", "ssd_q8.cu", "ssd_q8_mid.cu", "ssd_q8_many.cu"]
+           "ssd_norm.cu", "ssd_step.cu", "ssd_q8.cu", "ssd_q8_few.cu", "ssd_q8_mid.cu", "ssd_q8_many.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

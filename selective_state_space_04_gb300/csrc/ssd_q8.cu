@@ -48,8 +48,8 @@ cudaError_t q8_pack_launch(const int8_t *w, int8_t *packed, const ssd_q8_dims_t 
 
 namespace {
 
-// from here on widening both operands first pays
-constexpr long long kMany = 257;
+constexpr long long kFew = 32;     // up to here the weights go through registers and mma.sync
+constexpr long long kMany = 257;   // from here on widening both operands first pays
 
 Q8Params params(const Q8Args &a)
 {
@@ -75,7 +75,7 @@ Q8Params params(const Q8Args &a)
 size_t q8_workspace_bytes(const ssd_q8_dims_t &d)
 {
     const Q8Params p = params(Q8Args{nullptr, nullptr, nullptr, nullptr, nullptr, d});
-    return d.M >= kMany ? q8_many_workspace_bytes(p) : q8_mid_workspace_bytes(p);
+    return d.M >= kMany ? q8_many_workspace_bytes(p) : d.M > kFew ? q8_mid_workspace_bytes(p) : 0;
 }
 
 cudaError_t q8_launch(const Q8Args &a, void *workspace, cudaStream_t st)
@@ -83,6 +83,8 @@ cudaError_t q8_launch(const Q8Args &a, void *workspace, cudaStream_t st)
     SSD_NVTX_RANGE("q8_launch");
     const Q8Params p = params(a);
     const bool f32 = a.d.out_dtype == SSD_DTYPE_F32;
+    if (p.M <= kFew)
+        return q8_few_launch(p, f32, st);
     return p.M >= kMany ? q8_many_launch(p, f32, workspace, st) : q8_mid_launch(p, f32, workspace, st);
 }
 

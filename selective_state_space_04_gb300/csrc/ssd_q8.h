@@ -19,6 +19,8 @@ struct Q8Params {
     int vec;                      // a's rows are 8-byte aligned
 };
 
+// up to 16 tokens
+cudaError_t q8_few_launch(const Q8Params &p, bool f32, cudaStream_t st);
 // many tokens (workspace: 16-byte aligned)
 size_t q8_many_workspace_bytes(const Q8Params &p);
 cudaError_t q8_many_launch(const Q8Params &p, bool f32, void *workspace, cudaStream_t st);
@@ -54,7 +56,25 @@ __device__ __forceinline__ void widen16(const uint4 &u, uint32_t *f)
     widen4(u.w, f + 6);
 }
 
-// a[t, k .. k + 7], zeros beyond M and K
+// a[t, k .. k + 15], zeros beyond M and K
+__device__ __forceinline__ uint4 load16(const Q8Params &p, long long t, int k)
+{
+    if (t >= p.M || k >= p.K)
+        return make_uint4(0u, 0u, 0u, 0u);
+    const int8_t *src = p.a + t * p.sa + k;
+    if (p.vec && k + 16 <= p.K) {
+        const uint2 lo = __ldg(reinterpret_cast<const uint2 *>(src)), hi = __ldg(reinterpret_cast<const uint2 *>(src) + 1);
+        return make_uint4(lo.x, lo.y, hi.x, hi.y);
+    }
+    uint32_t v[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+        if (k + e < p.K)
+            v[e / 4] |= (uint32_t)(uint8_t)src[e] << (8 * (e % 4));
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// a[t, k .. k + 7], likewise
 __device__ __forceinline__ uint2 load8(const Q8Params &p, long long t, int k)
 {
     if (t >= p.M || k >= p.K)

@@ -220,7 +220,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 acc[j] = 0;
             for (int ch = 0; ch < chunks; ++ch, ++m) {
                 const uint32_t b = m & 1;
-                if (!(ok = __all_sync(0xffffffffu, wait_bar(&bars[BAR_ACC + b], (m / 2) & 1))))
+                if (lane == 0)   // (32 lanes that ask keep shared memory busy)
+                    ok = wait_bar(&bars[BAR_ACC + b], (m / 2) & 1);
+                if (!(ok = __shfl_sync(0xffffffffu, ok, 0)))
                     break;
                 tc_fence_after();
 #pragma unroll

@@ -65,12 +65,8 @@ constexpr int kColA = 128, kCols = 256;   // TMEM: accumulators, then the weight
 
 enum { BAR_WFULL = 0, BAR_WEMPTY = 8, BAR_A = 16, BAR_B = BAR_A + kStages, BAR_EMPTY = BAR_B + kStages, BAR_ACC = BAR_EMPTY + kStages, BAR_DRAINED, kBars };
 
-// bounded wait; false after kTimeoutNs
-__device__ bool wait_bar(uint64_t *bar, uint32_t parity)
+__device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity)
 {
-    for (int i = 0; i < 64; ++i)
-        if (mbar_test(bar, parity))
-            return true;
     const uint64_t t0 = globaltimer_ns();
     do {
         for (int i = 0; i < 64; ++i)
@@ -79,6 +75,11 @@ __device__ bool wait_bar(uint64_t *bar, uint32_t parity)
     } while (globaltimer_ns() - t0 < kTimeoutNs);
     atomicCAS(&g_q8_mid_error, 0u, (unsigned)SSD_ERR_TIMEOUT);
     return false;
+}
+// bounded wait; false after kTimeoutNs
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity)
+{
+    return mbar_test(bar, parity) || wait_long(bar, parity);
 }
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity)
 {
@@ -139,6 +140,9 @@ __global__ void __launch_bounds__(kThreads, 2) ssd_q8_mid_kernel(const Q8Params 
     for (int i = threadIdx.x; i < MT; i += kThreads)
         token_scale[i] = t0 + i < p.M ? p.as[t0 + i] : 0.f;
 
+    const int n = threadIdx.x & 127;   // (of warps 0-7: their channel)
+    const bool mine = tile * 128 + n < p.N;
+    const float ws = warp < 8 && mine ? p.ws[tile * 128 + n] : 0.f;
     const uint32_t quarter = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
     int *sums = reinterpret_cast<int *>(smem + S::kRings) + 32 * (warp & 3) + lane;   // (with `multi`)
     // warps 0-7: 8 tokens' sums of the accumulators in use, and of what was drained before
@@ -160,23 +164,30 @@ __global__ void __launch_bounds__(kThreads, 2) ssd_q8_mid_kernel(const Q8Params 
         const int row = 32 * (warp & 3) + lane, group = warp >> 2;
         for (int round = 0, k = group; ok; ++round) {
             const int end = min(slabs, (round + 1) * S::kRound);
-            for (; k < end; k += 2) {
-                const int w = k % S::kW, s = k % kStages;
-                if (!(ok = warp_wait(&bars[BAR_WFULL + w], (k / S::kW) & 1)))
-                    break;
-                uint32_t f[32];
-                const uint8_t *src = smem + S::kOffW + w * kSlabBytes + row * 16;
+            for (; k < end && ok; k += S::kW) {
+                const uint32_t wpar = (k / S::kW) & 1;
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    widen16(*reinterpret_cast<const uint4 *>(src + c * 2048), &f[8 * c]);
-                warp_arrive(&bars[BAR_WEMPTY + w]);
-                if (k >= kStages && !(ok = warp_wait(&bars[BAR_EMPTY + s], (k / kStages - 1) & 1)))
-                    break;
-                tc_fence_after();
-                tmem_st32(quarter + kColA + 32 * s, f);
-                tmem_wait_st();
-                tc_fence_before();
-                warp_arrive(&bars[BAR_A + s]);
+                for (int i = 0; i < S::kW; i += 2) {
+                    if (k + i >= end)
+                        break;
+                    const int w = i + group, s = w % kStages;
+                    const uint32_t spar = ((k + i) / kStages - 1) & 1;
+                    if (!(ok = warp_wait(&bars[BAR_WFULL + w], wpar)))
+                        break;
+                    uint32_t f[32];
+                    const uint8_t *src = smem + S::kOffW + w * kSlabBytes + row * 16;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        widen16(*reinterpret_cast<const uint4 *>(src + c * 2048), &f[8 * c]);
+                    warp_arrive(&bars[BAR_WEMPTY + w]);
+                    if (k + i >= kStages && !(ok = warp_wait(&bars[BAR_EMPTY + s], spar)))
+                        break;
+                    tc_fence_after();
+                    tmem_st32(quarter + kColA + 32 * s, f);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    warp_arrive(&bars[BAR_A + s]);
+                }
             }
             if (!ok || !(ok = warp_wait(&bars[BAR_ACC], round & 1)))
                 break;
@@ -233,9 +244,11 @@ __global__ void __launch_bounds__(kThreads, 2) ssd_q8_mid_kernel(const Q8Params 
     } else {
         if (lane == 0) {
             constexpr uint32_t idesc = idesc_f16_f32(128, MT);
-            uint32_t round = 0;
-            for (int k = 0; k < slabs; ++k) {
-                const int s = k % kStages;
+            const uint64_t b0 = sdesc_sw128(smem_u32(smem + S::kOffB), 16, 1024);
+            uint32_t round = 0, parity = 0;
+            // one thread issues all this, and its instructions are what a slab takes: stages and descriptors
+            // are constants, the rest is looked at every kStages slabs
+            for (int k = 0; k < slabs && ok; k += kStages, parity ^= 1) {
                 if (k > 0 && k % S::kRound == 0) {
                     mma_commit(&bars[BAR_ACC]);
                     if (!(ok = wait_bar(&bars[BAR_DRAINED], round & 1)))
@@ -243,15 +256,20 @@ __global__ void __launch_bounds__(kThreads, 2) ssd_q8_mid_kernel(const Q8Params 
                     tc_fence_after();
                     ++round;
                 }
-                if (!(ok = wait_bar(&bars[BAR_A + s], (k / kStages) & 1)) || !(ok = wait_bar(&bars[BAR_B + s], (k / kStages) & 1)))
-                    break;
-                tc_fence_after();
-                const uint32_t b = smem_u32(smem + S::kOffB + s * S::kB), acc = tmem + (k / kChunkSlabs) % S::kAccs * MT;
+                const uint32_t acc = tmem + (k / kChunkSlabs) % S::kAccs * MT;
+                const uint32_t more = k % kChunkSlabs > 0;
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_ts(acc, tmem + kColA + 32 * s + 8 * kk, sdesc_sw128(b + 32 * kk, 16, 1024), idesc,
-                           k % kChunkSlabs > 0 || kk > 0);
-                mma_commit(&bars[BAR_EMPTY + s]);
+                for (int s = 0; s < kStages; ++s) {
+                    if (k + s >= slabs)
+                        break;
+                    if (!(ok = wait_bar(&bars[BAR_A + s], parity) && wait_bar(&bars[BAR_B + s], parity)))
+                        break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)   // (descriptors count 16 bytes)
+                        mma_ts(acc, tmem + kColA + 32 * s + 8 * kk, b0 + (s * S::kB + 32 * kk) / 16, idesc, s + kk > 0 ? 1u : more);
+                    mma_commit(&bars[BAR_EMPTY + s]);
+                }
             }
             mma_commit(&bars[BAR_ACC]);   // (every MMA issued so far)
             wait_bar(&bars[BAR_ACC], round & 1);
@@ -265,9 +283,6 @@ __global__ void __launch_bounds__(kThreads, 2) ssd_q8_mid_kernel(const Q8Params 
     const bool more = multi && slabs > S::kRound;
     T *y = static_cast<T *>(p.y) + t0 * p.sy + tile * 128;
     const int left = (int)min((long long)MT, p.M - t0);   // tokens
-    const int n = threadIdx.x & 127;
-    const bool mine = tile * 128 + n < p.N;
-    const float ws = warp < 8 && mine ? p.ws[tile * 128 + n] : 0.f;
     if (splits == 1) {
         __syncthreads();   // (token_scale)
         if (warp < 8 && ok)
@@ -283,6 +298,8 @@ __global__ void __launch_bounds__(kThreads, 2) ssd_q8_mid_kernel(const Q8Params 
         // CTA q of the cluster adds up and stores the tokens q * cols ...: the others put their sums of
         // these into its shared memory, where the rings were; they are done with in this CTA
         // (the last wait above was for every MMA) and, after the barrier, in the whole cluster.
+        // The sums of 4 tokens lie side by side, [4 tokens][channel][token], so that both the
+        // stores to the other SMs and the loads are 16 bytes a lane.
         const int cols = ((MT + splits - 1) / splits + 7) / 8 * 8;
         cluster_sync();
         if (warp < 8 && ok)
@@ -290,21 +307,29 @@ __global__ void __launch_bounds__(kThreads, 2) ssd_q8_mid_kernel(const Q8Params 
                 int v[8];
                 collect(c0, accs, more, v);
                 const int owner = c0 / cols;
-                const uint32_t to = cluster_addr(smem_u32(smem) + 4u * ((rank * cols + c0 - owner * cols) * 128 + n), owner);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    cluster_st(to + 512u * i, v[i]);
+                const uint32_t to = cluster_addr(smem_u32(smem) + 16u * ((rank * cols + c0 - owner * cols) / 4 * 128 + n), owner);
+                cluster_st4(to, v[0], v[1], v[2], v[3]);
+                cluster_st4(to + 2048u, v[4], v[5], v[6], v[7]);
             }
         cluster_sync();
-        const int *parts = reinterpret_cast<const int *>(smem) + n;
         const int c1 = min(cols, left - rank * cols);
+        const int4 *parts = reinterpret_cast<const int4 *>(smem) + n;
         if (warp < 8 && mine)
-            for (int c = threadIdx.x >> 7; c < c1; c += 2) {
-                int v = 0;
-#pragma unroll 4
-                for (int q = 0; q < splits; ++q)
-                    v += parts[(q * cols + c) * 128];
-                y[(rank * cols + c) * p.sy + n] = from_f32<T>((float)v * token_scale[rank * cols + c] * ws);
+#pragma unroll 2
+            for (int c = 4 * (warp >> 2); c < c1; c += 8) {
+                int4 v = make_int4(0, 0, 0, 0);
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    if (q < splits) {
+                        const int4 u = parts[(q * cols + c) / 4 * 128];
+                        v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+                    }
+                const int w[4] = {v.x, v.y, v.z, v.w};
+                T *to = y + (rank * cols + c) * p.sy + n;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (c + i < c1)
+                        to[i * p.sy] = from_f32<T>((float)w[i] * token_scale[rank * cols + c + i] * ws);
             }
     }
     tc_fence_before();
