@@ -243,6 +243,15 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N)
     return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// One lane of a converged warp.  Where the whole warp walks a loop and only the issue itself is the elected
+// lane's, descriptors and counters stay in uniform registers, which the MMA takes them from.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // TMEM allocation: executed by one whole warp; the base address is written to
 // shared memory at `dst`.
 __device__ __forceinline__ void tmem_alloc(uint32_t *dst, uint32_t ncols)

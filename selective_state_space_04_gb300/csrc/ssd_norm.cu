@@ -116,6 +116,11 @@ __device__ __forceinline__ float inv_rms(float ss, int D, float eps)
     return m == 0.f ? 0.f : 1.f / sqrtf(m);
 }
 
+// v sigmoid(v) with the fast exponential and quotient (a few units of 2^-23; the IEEE quotient made the
+// gated norm arithmetic-bound: 34.8 us for 4096 rows of 5120).  Below about -88 the divisor
+// overflows and the result is 0, as it should be.
+__device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.f + __expf(-v)); }
+
 // VPT: vectors a thread holds.  kWarp: a row is one warp's, else one block's.
 template <typename T, typename R, int kMode, bool kQ8, int VPT, bool kWarp>
 __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kMaxThreads) ssd_norm_kernel(NormParams p)
@@ -175,7 +180,7 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kMaxThreads) ssd_norm
                 uz[a].get(f);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    w[a][e] *= f[e] / (1.f + __expf(-f[e]));
+                    w[a][e] *= silu(f[e]);
             }
         }
     }
@@ -250,8 +255,8 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kMaxThreads) ssd_norm
     }
 }
 
-template <typename K>
-cudaError_t launch_after(K *kernel, unsigned grid, unsigned threads, cudaStream_t st, const auto &...args)
+template <typename K, typename... A>
+cudaError_t launch_after(K *kernel, unsigned grid, unsigned threads, cudaStream_t st, const A &...args)
 {
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -311,21 +316,24 @@ struct NormBwdParams {
     float eps;
 };
 
-constexpr int kBwdWarpRows = 8;
+constexpr int kBwdWarpRows = 8, kBwdThreads = 512;
+constexpr int kBwdWarpDim = 512;   // rows up to here are one warp's, 2 vectors a lane at most
 
-// Blocks (warps where a row is one warp's) take rows blockIdx, blockIdx + grid, ...; the
-// weight's gradient is summed in registers over a block's rows and written as one
-// partial row per block, which a second launch adds in block order.
+// Blocks (warps where a row is one warp's) take rows blockIdx, blockIdx + grid, ..., the next row's
+// loads under way while one is summed and written; the weight's gradient is summed in registers over a
+// block's rows and written as one partial row per block, which a second launch adds in block order.
 template <typename T, typename R, bool kRes, int VPT, bool kWarp>
-__global__ void __launch_bounds__(kWarp ? 32 * kBwdWarpRows : kMaxThreads) ssd_norm_bwd_kernel(NormBwdParams p)
+__global__ void __launch_bounds__(kWarp ? 32 * kBwdWarpRows : kBwdThreads, kWarp || VPT > 1 || sizeof(R) > 2 ? 1 : 2) ssd_norm_bwd_kernel(NormBwdParams p)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    __shared__ float2 part[2][kMaxThreads / 32];
-    __shared__ float sums[kWarp ? kWarpRowDim : 1];
+    constexpr bool kAhead = VPT < 4;   // (more would not fit the registers)
+    __shared__ float2 part[2][kBwdThreads / 32];
+    __shared__ __align__(16) float sums[kWarp ? kBwdWarpRows * kBwdWarpDim : 4];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int tid = kWarp ? lane : threadIdx.x, group = kWarp ? 32 : blockDim.x;
     const int nv = p.D / 8;
+    const float dim = (float)p.D;
     float w[VPT][8], acc[VPT][8];
 #pragma unroll
     for (int a = 0; a < VPT; ++a) {
@@ -337,19 +345,37 @@ __global__ void __launch_bounds__(kWarp ? 32 * kBwdWarpRows : kMaxThreads) ssd_n
     }
     const long long first = kWarp ? (long long)blockIdx.x * kBwdWarpRows + warp : blockIdx.x;
     const long long step = kWarp ? (long long)gridDim.x * kBwdWarpRows : gridDim.x;
-    int turn = 0;
-    for (long long row = first; row < p.rows; row += step) {
-        Vec<R> uh[VPT], ur[VPT];
-        Vec<T> ud[VPT];
+    Vec<R> uh[VPT], ur[VPT], nh[VPT], nr[VPT];
+    Vec<T> ud[VPT], nd[VPT];
+    auto load = [&](long long row, Vec<R> (&h)[VPT], Vec<T> (&d)[VPT], Vec<R> (&r)[VPT]) {
+        if (row >= p.rows)
+            return;
 #pragma unroll
         for (int a = 0; a < VPT; ++a) {
             const int v = tid + a * group;
             if (v < nv) {
-                uh[a].load(p.h, row * p.hs + 8 * v);
-                ud[a].load(p.dout, row * p.ds + 8 * v);
+                h[a].load(p.h, row * p.hs + 8 * v);
+                d[a].load(p.dout, row * p.ds + 8 * v);
                 if (kRes)
-                    ur[a].load(p.dres, row * p.rs + 8 * v);
+                    r[a].load(p.dres, row * p.rs + 8 * v);
             }
+        }
+    };
+    if (kAhead)
+        load(first, nh, nd, nr);
+    int turn = 0;
+    for (long long row = first; row < p.rows; row += step) {
+        if (kAhead) {
+#pragma unroll
+            for (int a = 0; a < VPT; ++a) {
+                uh[a] = nh[a];
+                ud[a] = nd[a];
+                if (kRes)
+                    ur[a] = nr[a];
+            }
+            load(row + step, nh, nd, nr);
+        } else {
+            load(row, uh, ud, ur);
         }
         float ss = 0.f, c = 0.f;
 #pragma unroll
@@ -377,7 +403,7 @@ __global__ void __launch_bounds__(kWarp ? 32 * kBwdWarpRows : kMaxThreads) ssd_n
             turn ^= 1;
         }
         const float r = inv_rms(ss, p.D, p.eps);
-        const float k = r * r * c / (float)p.D;
+        const float k = r * r * c / dim;
 #pragma unroll
         for (int a = 0; a < VPT; ++a) {
             const int v = tid + a * group;
@@ -402,32 +428,23 @@ __global__ void __launch_bounds__(kWarp ? 32 * kBwdWarpRows : kMaxThreads) ssd_n
     if (!p.part)
         return;
     float *to = p.part + (size_t)blockIdx.x * p.D;
-    if (kWarp) {   // the block's warps, one after the other
-        for (int i = 0; i < kBwdWarpRows; ++i) {
-            if (warp == i) {
 #pragma unroll
-                for (int a = 0; a < VPT; ++a) {
-                    const int v = tid + a * group;
-                    if (v < nv)
+    for (int a = 0; a < VPT; ++a) {
+        const int v = tid + a * group;
+        if (v >= nv)
+            continue;
+        float4 *at = reinterpret_cast<float4 *>(kWarp ? sums + warp * kBwdWarpDim : to) + 2 * v;
+        at[0] = make_float4(acc[a][0], acc[a][1], acc[a][2], acc[a][3]);
+        at[1] = make_float4(acc[a][4], acc[a][5], acc[a][6], acc[a][7]);
+    }
+    if (kWarp) {   // the block's warps in order
+        __syncthreads();
+        for (int i = threadIdx.x; i < p.D; i += blockDim.x) {
+            float s = 0.f;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float s = acc[a][e] + (i > 0 ? sums[8 * v + e] : 0.f);
-                            sums[8 * v + e] = s;
-                        }
-                }
-            }
-            __syncthreads();
-        }
-        for (int i = threadIdx.x; i < p.D; i += blockDim.x)
-            to[i] = sums[i];
-    } else {
-#pragma unroll
-        for (int a = 0; a < VPT; ++a) {
-            const int v = tid + a * group;
-            if (v < nv) {
-                reinterpret_cast<float4 *>(to)[2 * v] = make_float4(acc[a][0], acc[a][1], acc[a][2], acc[a][3]);
-                reinterpret_cast<float4 *>(to)[2 * v + 1] = make_float4(acc[a][4], acc[a][5], acc[a][6], acc[a][7]);
-            }
+            for (int j = 0; j < kBwdWarpRows; ++j)
+                s += sums[j * kBwdWarpDim + i];
+            to[i] = s;
         }
     }
 }
@@ -453,37 +470,50 @@ __global__ void __launch_bounds__(1024) ssd_norm_dweight_kernel(const float *par
         dw[out] = t;
 }
 
+// vectors a thread holds, and threads of a row; of fp32 rows two, where one would be 512 threads: their
+// registers are what fits on an SM
+int bwd_threads(const ssd_norm_dims_t &d, int *vpt)
+{
+    const int nv = d.dim / 8;
+    *vpt = nv <= (d.residual_dtype == SSD_DTYPE_F32 ? kBwdThreads / 2 : kBwdThreads) ? 1 : nv <= 2 * kBwdThreads ? 2 : 4;
+    return ((nv + *vpt - 1) / *vpt + 31) / 32 * 32;
+}
+
+// Blocks: as many as run at once (1024 threads an SM, measured best: on 32768 rows of 2560 three blocks
+// of 320 take 111 us, two 125, four 134; where a row is a warp's, two blocks of 256 of them), but
+// eight rows each (per warp) where that fills the SMs: a block's partial sums cost as much as a row.
 int bwd_blocks(const ssd_norm_dims_t &d)
 {
-    if (d.dim <= kWarpRowDim)
-        return (int)std::min<int64_t>((d.rows + kBwdWarpRows - 1) / kBwdWarpRows, (int64_t)sm_count() * 4);
-    const int nv = d.dim / 8, vpt = nv <= 512 ? 1 : 2;
-    const int threads = ((nv + vpt - 1) / vpt + 31) / 32 * 32;
-    return (int)std::min<int64_t>(d.rows, (int64_t)sm_count() * std::max(1, 1536 / threads));
+    if (d.rows <= 0)
+        return 0;
+    int vpt;
+    const bool warp = d.dim <= kBwdWarpDim;
+    const int per_sm = warp ? 2 : std::max(1, 1024 / bwd_threads(d, &vpt));
+    const int64_t rows = warp ? (d.rows + kBwdWarpRows - 1) / kBwdWarpRows : d.rows;
+    return (int)std::min<int64_t>({rows, std::max<int64_t>(sm_count(), (rows + 7) / 8), (int64_t)sm_count() * per_sm});
 }
 
 template <typename T, typename R, bool kRes>
-cudaError_t bwd_launch_t(const NormBwdParams &p, int blocks, cudaStream_t st)
+cudaError_t bwd_launch_t(const NormBwdParams &p, const ssd_norm_dims_t &d, int blocks, cudaStream_t st)
 {
-    const int nv = p.D / 8;
-    if (p.D <= kWarpRowDim) {
-        if (nv <= 32)
+    if (p.D <= kBwdWarpDim) {
+        if (p.D <= 256)
             return launch_after(ssd_norm_bwd_kernel<T, R, kRes, 1, true>, blocks, 32 * kBwdWarpRows, st, p);
-        if (nv <= 64)
-            return launch_after(ssd_norm_bwd_kernel<T, R, kRes, 2, true>, blocks, 32 * kBwdWarpRows, st, p);
-        return launch_after(ssd_norm_bwd_kernel<T, R, kRes, 4, true>, blocks, 32 * kBwdWarpRows, st, p);
+        return launch_after(ssd_norm_bwd_kernel<T, R, kRes, 2, true>, blocks, 32 * kBwdWarpRows, st, p);
     }
-    const int vpt = nv <= 512 ? 1 : 2;
-    const unsigned threads = (unsigned)(((nv + vpt - 1) / vpt + 31) / 32 * 32);
+    int vpt;
+    const unsigned threads = bwd_threads(d, &vpt);
     if (vpt == 1)
         return launch_after(ssd_norm_bwd_kernel<T, R, kRes, 1, false>, blocks, threads, st, p);
-    return launch_after(ssd_norm_bwd_kernel<T, R, kRes, 2, false>, blocks, threads, st, p);
+    if (vpt == 2)
+        return launch_after(ssd_norm_bwd_kernel<T, R, kRes, 2, false>, blocks, threads, st, p);
+    return launch_after(ssd_norm_bwd_kernel<T, R, kRes, 4, false>, blocks, threads, st, p);
 }
 
 template <typename T, typename R>
-cudaError_t bwd_launch_types(const NormBwdParams &p, int blocks, cudaStream_t st)
+cudaError_t bwd_launch_types(const NormBwdParams &p, const ssd_norm_dims_t &d, int blocks, cudaStream_t st)
 {
-    return p.dres ? bwd_launch_t<T, R, true>(p, blocks, st) : bwd_launch_t<T, R, false>(p, blocks, st);
+    return p.dres ? bwd_launch_t<T, R, true>(p, d, blocks, st) : bwd_launch_t<T, R, false>(p, d, blocks, st);
 }
 
 }  // namespace
@@ -541,10 +571,10 @@ cudaError_t norm_bwd_launch(const NormBwdArgs &a, void *workspace, cudaStream_t 
     const int blocks = bwd_blocks(a.d);
     cudaError_t e;
     if (a.d.dtype == SSD_DTYPE_F32)
-        e = bwd_launch_types<float, float>(p, blocks, st);
+        e = bwd_launch_types<float, float>(p, a.d, blocks, st);
     else
-        e = a.d.residual_dtype == SSD_DTYPE_F32 ? bwd_launch_types<__nv_bfloat16, float>(p, blocks, st)
-                                                : bwd_launch_types<__nv_bfloat16, __nv_bfloat16>(p, blocks, st);
+        e = a.d.residual_dtype == SSD_DTYPE_F32 ? bwd_launch_types<__nv_bfloat16, float>(p, a.d, blocks, st)
+                                                : bwd_launch_types<__nv_bfloat16, __nv_bfloat16>(p, a.d, blocks, st);
     if (e != cudaSuccess || !a.dweight)
         return e;
     return launch_after(ssd_norm_dweight_kernel, (unsigned)((p.D + 31) / 32), 1024, st, (const float *)p.part, a.dweight, blocks, p.D);

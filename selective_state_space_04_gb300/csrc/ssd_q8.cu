@@ -67,6 +67,7 @@ Q8Params params(const Q8Args &a)
     p.k64 = (p.K + 63) / 64;
     p.tiles = (p.N + 127) / 128;
     p.vec = ((uintptr_t)p.a & 7) == 0 && (p.sa % 8 == 0 || p.M == 1);
+    p.yvec = ((uintptr_t)p.y & 15) == 0 && p.sy * (a.d.out_dtype == SSD_DTYPE_BF16 ? 2 : 4) % 16 == 0;
     return p;
 }
 

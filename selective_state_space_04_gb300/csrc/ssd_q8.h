@@ -17,6 +17,9 @@ struct Q8Params {
     long long M, sa, sy;
     int N, K, k64, tiles;         // k64: slabs of 64 inner elements; tiles of 128 channels
     int vec;                      // a's rows are 8-byte aligned
+    int yvec;                     // y's rows are 16-byte aligned
+    // rows of a slab of the tokens' images
+    __host__ __device__ long long padded() const { return (M + 127) / 128 * 128; }
 };
 
 // up to 16 tokens
@@ -28,7 +31,7 @@ cudaError_t q8_many_launch(const Q8Params &p, bool f32, void *workspace, cudaStr
 size_t q8_mid_workspace_bytes(const Q8Params &p);
 cudaError_t q8_mid_launch(const Q8Params &p, bool f32, void *workspace, cudaStream_t st);
 // fp16 images of 128 rows x 64 elements, swizzled, from the first `wslabs` slabs of the weights (to
-// wi) and all the tokens' (to ai)
+// wi, tile by tile) and all the tokens' (to ai, slab by slab, padded() rows each)
 constexpr int kQ8Image = 128 * 128;   // bytes
 cudaError_t q8_widen_launch(const Q8Params &p, uint8_t *wi, uint8_t *ai, long long wslabs, cudaStream_t st);
 ssd_status_t q8_many_read_device_error(uint32_t *code);

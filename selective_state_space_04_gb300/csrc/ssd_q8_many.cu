@@ -2,13 +2,15 @@
 //
 // Two launches.  The first widens both operands to fp16 (exactly: see ssd_q8_mid.cu) into
 // scratch, as the images of the tiles that the second reads: 128 rows x 64 inner
-// elements, 16 KB, swizzled, in the order of use, so that a tile is one contiguous copy.
+// elements, 16 KB, swizzled, in the order of use, so that a tile is one contiguous copy
+// (the tokens' slab by slab, all of them in a row, so that a tile may have any number of them).
 // It moves 3 bytes per element of the operands, a few percent of the product's time where
 // there are many tokens, and takes all work but copies out of the second.
 //
-// The second: pairs of CTAs (cta_group::2) on tiles of 256 channels x 256 tokens.  Each
-// CTA holds its 128 rows of the channels' and of the tokens' operand, so that a slab of 64
-// inner elements is 32 KB of copies per CTA for 512 clocks of MMA.  Accumulators take
+// The second: pairs of CTAs (cta_group::2) on tiles of 256 channels x up to 256 tokens.  Each
+// CTA holds its half of the channels' and of the tokens' operand, so that a slab of 64
+// inner elements is at most 32 KB of copies per CTA for 512 clocks of MMA.  That is what bounds it: 13 TB/s
+// from L2 over all SMs, which is what copies alone reach.  Accumulators take
 // 1024 inner elements each, as in ssd_q8_mid.cu, two of them in turn: while one is
 // filled, eight warps add the other to 32-bit integers in registers (128 per thread).
 #include <cuda_bf16.h>
@@ -40,12 +42,8 @@ constexpr long long kPanel = 32768;   // tokens widened at once: bounds the scra
 
 enum { BAR_FULL = 0, BAR_EMPTY = kStages, BAR_ACC = 2 * kStages, BAR_DRAINED = BAR_ACC + 2, kBars = BAR_DRAINED + 2 };
 
-// bounded wait; false after kTimeoutNs
-__device__ bool wait_bar(uint64_t *bar, uint32_t parity)
+__device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity)
 {
-    for (int i = 0; i < 64; ++i)
-        if (mbar_test(bar, parity))
-            return true;
     const uint64_t t0 = globaltimer_ns();
     do {
         for (int i = 0; i < 64; ++i)
@@ -55,6 +53,30 @@ __device__ bool wait_bar(uint64_t *bar, uint32_t parity)
     atomicCAS(&g_q8_many_error, 0u, (unsigned)SSD_ERR_TIMEOUT);
     return false;
 }
+// bounded wait; false after kTimeoutNs
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity)
+{
+    return mbar_test(bar, parity) || wait_long(bar, parity);
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity)
+{
+    return __all_sync(0xffffffffu, wait_bar(bar, parity));
+}
+
+// The ring's next place, and the parity of its present use.  (Single threads walk the ring, and their
+// instructions count: a division by the ring's size at each slab was a tenth of its time.)
+struct Place {
+    uint32_t s = 0, parity = 0;
+    // the next
+    __device__ __forceinline__ void next()
+    {
+        if (++s == kStages) {
+            s = 0;
+            parity ^= 1;
+        }
+    }
+};
 
 template <typename T> __device__ __forceinline__ T from_f32(float v);
 template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
@@ -79,9 +101,9 @@ __global__ void __launch_bounds__(256) ssd_q8_widen_kernel(const Q8Params p, uin
             for (int h = 0; h < 4; ++h)
                 u[h] = __ldg(reinterpret_cast<const uint2 *>(p.w + i * 8192 + (c >> 1) * 2048 + (r0 + 32 * h) * 16 + (c & 1) * 8));
         } else {
-            const long long j = i - wslabs, t0 = j / p.k64 * 128;
-            const int k0 = (int)(j % p.k64) * 64 + c * 8;
-            image = ai + j * kImage;
+            const long long j = i - wslabs, t0 = j / p.k64 * 128, k = j % p.k64;
+            const int k0 = (int)k * 64 + c * 8;
+            image = ai + (k * p.padded() + t0) * 128;
 #pragma unroll
             for (int h = 0; h < 4; ++h)
                 u[h] = load8(p, t0 + r0 + 32 * h, k0);
@@ -96,6 +118,28 @@ __global__ void __launch_bounds__(256) ssd_q8_widen_kernel(const Q8Params p, uin
     }
 }
 
+// Lane l of 8 holds (as pairs, lower half first) its column of an 8 x 8 matrix of 16-bit values; it gets row l.
+__device__ __forceinline__ uint4 transpose8(const uint32_t (&v)[4], int lane)
+{
+    // rows 4 .. 7 against rows 0 .. 3 of the lane 4 on
+    uint32_t a[4], b[4];
+    const bool h4 = lane & 4, h2 = lane & 2, h1 = lane & 1;
+    uint32_t s0 = __shfl_xor_sync(0xffffffffu, h4 ? v[0] : v[2], 4), s1 = __shfl_xor_sync(0xffffffffu, h4 ? v[1] : v[3], 4);
+    // a[0..1]: rows (0,1),(2,3) (+4 if h4) of the lower lane of the pair, a[2..3]: of the upper
+    a[0] = h4 ? s0 : v[0], a[1] = h4 ? s1 : v[1], a[2] = h4 ? v[2] : s0, a[3] = h4 ? v[3] : s1;
+    s0 = __shfl_xor_sync(0xffffffffu, h2 ? a[0] : a[1], 2), s1 = __shfl_xor_sync(0xffffffffu, h2 ? a[2] : a[3], 2);
+    // b[c]: the row pair of this lane's row, of columns c0 = lane & 1, c0 + 2, c0 + 4, c0 + 6
+    b[0] = h2 ? s0 : a[0], b[1] = h2 ? a[1] : s0, b[2] = h2 ? s1 : a[2], b[3] = h2 ? a[3] : s1;
+    uint32_t r[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const uint32_t o = __shfl_xor_sync(0xffffffffu, b[c], 1);
+        // columns 2 c and 2 c + 1: of an even lane, its own and the other's lower halves
+        r[c] = h1 ? __byte_perm(o, b[c], 0x7632) : __byte_perm(b[c], o, 0x5410);
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
 // tile index -> (channel pair, token pair): 8 token pairs wide, channel pairs within
 __device__ __forceinline__ void tile_at(int i, int cp, int tp, int &c, int &t)
 {
@@ -106,7 +150,7 @@ __device__ __forceinline__ void tile_at(int i, int cp, int tp, int &c, int &t)
 
 template <typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    ssd_q8_many_kernel(const Q8Params p, const uint8_t *wi, const uint8_t *ai, int cp, int tp, int ttiles)
+    ssd_q8_many_kernel(const Q8Params p, const uint8_t *wi, const uint8_t *ai, int tn, int cp, int tp)
 {
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint64_t bars[kBars];
@@ -143,20 +187,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     if (warp == 8) {
         if (lane == 0) {
+            const size_t slab = (size_t)p.padded() * 128;
             uint32_t n = 0;   // slabs so far
+            Place at;
             bool ok = true;
             for (int i = me; i < items && ok; i += pairs) {
                 int c, t;
                 tile_at(i, cp, tp, c, t);
                 const uint8_t *w = wi + (size_t)min(2 * c + (int)rank, p.tiles - 1) * p.k64 * kImage;
-                const uint8_t *a = ai + (size_t)min(2 * t + (int)rank, ttiles - 1) * p.k64 * kImage;
-                for (int k = 0; k < p.k64; ++k, ++n) {
-                    const uint32_t s = n % kStages;
-                    if (n >= kStages && !(ok = wait_bar(&bars[BAR_EMPTY + s], (n / kStages - 1) & 1)))
+                // (rows past the tokens', in the last tile, are another slab's or the scratch's end)
+                const uint8_t *a = ai + ((size_t)t * tn + rank * (tn / 2)) * 128;
+                for (int k = 0; k < p.k64; ++k, ++n, at.next()) {
+                    const uint32_t s = at.s;
+                    if (n >= kStages && !(ok = wait_bar(&bars[BAR_EMPTY + s], at.parity ^ 1)))
                         break;
-                    mbar_arrive_expect_tx(&bars[BAR_FULL + s], kStageBytes);
+                    mbar_arrive_expect_tx(&bars[BAR_FULL + s], kImage + tn * 64);
                     bulk_load(smem + s * kStageBytes, w + (size_t)k * kImage, kImage, &bars[BAR_FULL + s]);
-                    bulk_load(smem + s * kStageBytes + kImage, a + (size_t)k * kImage, kImage, &bars[BAR_FULL + s]);
+                    bulk_load(smem + s * kStageBytes + kImage, a + (size_t)k * slab, tn * 64, &bars[BAR_FULL + s]);
                 }
             }
             // no copy may be under way when shared memory is given up (each stage's last phase)
@@ -165,55 +212,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else if (warp == 9) {
-        if (lane == 0 && rank == 0) {
-            constexpr uint32_t idesc = idesc_f16_f32(256, 256);
-            uint32_t n = 0, m = 0;   // slabs, accumulators so far
+        if (rank == 0) {
+            const bool issue = elect_one();
+            const uint32_t idesc = idesc_f16_f32(256, tn);
+            const uint64_t a0 = sdesc_sw128(smem_u32(smem), 16, 1024);   // (descriptors count 16 bytes)
+            uint32_t m = 0;   // accumulators so far
+            Place at;
             bool ok = true;
             for (int i = me; i < items && ok; i += pairs)
                 for (int ch = 0; ch < chunks && ok; ++ch, ++m) {
-                    const uint32_t b = m & 1;
-                    if (m >= 2 && !(ok = wait_bar(&bars[BAR_DRAINED + b], (m / 2 - 1) & 1)))
+                    const uint32_t b = m & 1, acc = tmem + 256 * b;
+                    if (m >= 2 && !(ok = warp_wait(&bars[BAR_DRAINED + b], (m / 2 - 1) & 1)))
                         break;
                     tc_fence_after();
-                    const int end = min(p.k64, (ch + 1) * kChunkSlabs);
-                    for (int k = ch * kChunkSlabs; k < end; ++k, ++n) {
-                        const uint32_t s = n % kStages;
-                        if (!(ok = wait_bar(&bars[BAR_FULL + s], (n / kStages) & 1)))
+                    const int n = min(kChunkSlabs, p.k64 - ch * kChunkSlabs);
+                    for (int k = 0; k < n; ++k, at.next()) {
+                        if (!(ok = warp_wait(&bars[BAR_FULL + at.s], at.parity)))
                             break;
                         tc_fence_after();
-                        const uint32_t at = smem_u32(smem + s * kStageBytes);
+                        const uint64_t d = a0 + at.s * (kStageBytes / 16);
+                        if (issue) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma2_ss(tmem + 256 * b, sdesc_sw128(at + 32 * kk, 16, 1024), sdesc_sw128(at + kImage + 32 * kk, 16, 1024), idesc,
-                                    k > ch * kChunkSlabs || kk > 0);
-                        mma2_commit(&bars[BAR_EMPTY + s]);
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma2_ss(acc, d + 2 * kk, d + kImage / 16 + 2 * kk, idesc, kk > 0 ? 1u : (uint32_t)(k > 0));
+                            mma2_commit(&bars[BAR_EMPTY + at.s]);
+                        }
+                        __syncwarp();
                     }
-                    mma2_commit(&bars[BAR_ACC + b]);
+                    if (issue)
+                        mma2_commit(&bars[BAR_ACC + b]);
+                    __syncwarp();
                 }
             // no MMA may be in flight when the pair gives its memories up: each accumulator's last
             for (uint32_t j = m > 2 ? m - 2 : 0; j < m; ++j)
                 wait_bar(&bars[BAR_ACC + (j & 1)], (j / 2) & 1);
         } else if (lane == 0) {
             // this CTA's copies, told to the leader
-            uint32_t n = 0;
+            Place at;
             bool ok = true;
             for (int i = me; i < items && ok; i += pairs)
-                for (int k = 0; k < p.k64 && ok; ++k, ++n) {
-                    if ((ok = wait_bar(&bars[BAR_FULL + n % kStages], (n / kStages) & 1)))
-                        mbar_arrive_at(&bars[BAR_FULL + n % kStages], 0);
-                }
+                for (int k = 0; k < p.k64 && ok; ++k, at.next())
+                    if ((ok = wait_bar(&bars[BAR_FULL + at.s], at.parity)))
+                        mbar_arrive_at(&bars[BAR_FULL + at.s], 0);
         }
         __syncwarp();
     } else {
         const int q = warp & 3, half = warp >> 2;
-        const uint32_t from = tmem + (static_cast<uint32_t>(32 * q) << 16) + 128 * half;
+        const uint32_t from = tmem + (static_cast<uint32_t>(32 * q) << 16) + tn / 2 * half;
         uint32_t m = 0;
         bool ok = true;
         for (int i = me; i < items && ok; i += pairs) {
             int c, t;
             tile_at(i, cp, tp, c, t);
             const int channel = (2 * c + (int)rank) * 128 + 32 * q + lane;
-            const long long t0 = 256ll * t + 128 * half;
+            const long long t0 = (long long)tn * t + tn / 2 * half;
             int acc[128];
 #pragma unroll
             for (int j = 0; j < 128; ++j)
@@ -227,6 +279,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tc_fence_after();
 #pragma unroll
                 for (int j = 0; j < 128; j += 16) {
+                    if (j >= tn / 2)
+                        break;
                     uint32_t v[16];
                     tmem_ld16(from + 256 * b + j, v);
                     tmem_wait_ld();
@@ -243,17 +297,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 break;
             const bool mine = channel < p.N;
             const float ws = mine ? p.ws[channel] : 0.f;
-            T *y = static_cast<T *>(p.y) + t0 * p.sy + channel;
-            const int left = (int)max(0ll, min(128ll, p.M - t0));
+            const int left = (int)max(0ll, min((long long)(tn / 2), p.M - t0));
+            // whole 16-byte pieces of the result's rows, where they are that and all channels are there
+            const int ch0 = channel - lane;
+            if (sizeof(T) == 2 && p.yvec && ch0 + 32 <= p.N) {
+                // 8 tokens of 8 lanes' channels are transposed among the lanes: lane l gets token l's
+                T *y = static_cast<T *>(p.y) + (t0 + (lane & 7)) * p.sy + ch0 + (lane & 24);
 #pragma unroll
-            for (int j = 0; j < 128; j += 32) {
-                const float as = j + lane < left ? p.as[t0 + j + lane] : 0.f;
+                for (int j = 0; j < 128; j += 8) {
+                    if (j >= left)
+                        break;
+                    const float as = j + (lane & 7) < left ? p.as[t0 + j + (lane & 7)] : 0.f;
+                    float f[8];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const float f = __shfl_sync(0xffffffffu, as, e);
-                    if (mine && j + e < left)
-                        y[(j + e) * p.sy] = from_f32<T>((float)acc[j + e] * f * ws);
+                    for (int e = 0; e < 8; ++e)
+                        f[e] = (float)acc[j + e] * __shfl_sync(0xffffffffu, as, e, 8) * ws;
+                    uint32_t v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        v[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
+                    const uint4 u = transpose8(v, lane);
+                    if (j + (lane & 7) < left)
+                        __stcs(reinterpret_cast<uint4 *>(y + j * p.sy), u);
                 }
+            } else {
+                T *y = static_cast<T *>(p.y) + t0 * p.sy + channel;
+#pragma unroll
+                for (int j = 0; j < 128; ++j)
+                    if (mine && j < left)
+                        y[j * p.sy] = from_f32<T>((float)acc[j] * p.as[t0 + j] * ws);
             }
         }
     }
@@ -293,14 +365,27 @@ cudaError_t many_t(const Q8Params &p, uint8_t *ws, cudaStream_t st)
         q.a = p.a + m0 * p.sa;
         q.as = p.as + m0;
         q.y = static_cast<T *>(p.y) + m0 * p.sy;
-        const int ttiles = (int)((q.M + 127) / 128), cp = (p.tiles + 1) / 2, tp = (ttiles + 1) / 2;
+        const int cp = (p.tiles + 1) / 2, pairs = sm_count() / 2;
+        // Tokens of a tile: the pairs take tiles in waves, and a slab's time goes by its bytes, 16 KB of
+        // weights and 64 a token.  (160 tiles of 256 tokens are 3 waves of 76, the third almost
+        // empty; 220 of 192 are 3 shorter ones: 4096 tokens of 2560 x 5120 99 -> 87 us.)
+        int tn = 256;
+        long long best = INT64_MAX;
+        for (int n = 256; n >= 64; n -= 32) {
+            const long long cost = ((q.M + n - 1) / n * cp + pairs - 1) / pairs * (256 + n);
+            if (cost < best) {
+                best = cost;
+                tn = n;
+            }
+        }
+        const int tp = (int)((q.M + tn - 1) / tn);
         e = q8_widen_launch(q, ws, ai, m0 == 0 ? wslabs : 0, st);
         if (e != cudaSuccess)
             return e;
-        cfg.gridDim = dim3(2 * (unsigned)std::min(cp * tp, sm_count() / 2));
+        cfg.gridDim = dim3(2 * (unsigned)std::min<long long>((long long)cp * tp, pairs));
         cfg.blockDim = dim3(kThreads);
         cfg.dynamicSmemBytes = kSmem;
-        e = cudaLaunchKernelEx(&cfg, ssd_q8_many_kernel<T>, q, (const uint8_t *)ws, (const uint8_t *)ai, cp, tp, ttiles);
+        e = cudaLaunchKernelEx(&cfg, ssd_q8_many_kernel<T>, q, (const uint8_t *)ws, (const uint8_t *)ai, tn, cp, tp);
         if (e != cudaSuccess)
             return e;
         note_launches(1);
@@ -325,7 +410,8 @@ cudaError_t q8_widen_launch(const Q8Params &p, uint8_t *wi, uint8_t *ai, long lo
 
 size_t q8_many_workspace_bytes(const Q8Params &p)
 {
-    return ((size_t)p.tiles + (size_t)((std::min(kPanel, p.M) + 127) / 128)) * p.k64 * kImage;
+    // (the last tile's copies end up to 256 rows behind the tokens')
+    return ((size_t)p.tiles + (size_t)((std::min(kPanel, p.M) + 127) / 128)) * p.k64 * kImage + 256 * 128;
 }
 
 cudaError_t q8_many_launch(const Q8Params &p, bool f32, void *workspace, cudaStream_t st)

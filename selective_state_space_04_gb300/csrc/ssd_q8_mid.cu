@@ -40,7 +40,6 @@ constexpr int kThreads = 320;   // warps 0-7: weights and results, 8: copies, 9:
 constexpr int kStages = 4;      // slabs in TMEM (A) and shared memory (B)
 constexpr int kSlabBytes = 128 * 64;
 constexpr int kChunkSlabs = 16;   // slabs of one accumulator: 1024 inner elements
-constexpr int kImage = kQ8Image;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
 template <int MT> struct Shape {
@@ -207,7 +206,8 @@ __global__ void __launch_bounds__(kThreads, 2) ssd_q8_mid_kernel(const Q8Params 
     } else if (warp == 8) {
         if (lane == 0) {
             const int8_t *src = p.w + ((size_t)tile * p.k64 + first) * kSlabBytes;
-            const uint8_t *tokens = images + ((size_t)(t0 / 128) * p.k64 + first) * kImage;
+            const size_t slab = (size_t)p.padded() * 128;
+            const uint8_t *tokens = images + first * slab + t0 * 128;
             auto weights = [&](int k) {
                 const int w = k % S::kW;
                 if (k >= S::kW && !(ok = wait_bar(&bars[BAR_WEMPTY + w], (k / S::kW - 1) & 1)))
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 2) ssd_q8_mid_kernel(const Q8Params 
                 if (k >= kStages && !(ok = wait_bar(&bars[BAR_EMPTY + s], (k / kStages - 1) & 1)))
                     break;
                 mbar_arrive_expect_tx(&bars[BAR_B + s], S::kB);
-                bulk_load(smem + S::kOffB + s * S::kB, tokens + (size_t)k * kImage, S::kB, &bars[BAR_B + s]);
+                bulk_load(smem + S::kOffB + s * S::kB, tokens + k * slab, S::kB, &bars[BAR_B + s]);
                 if (kw < slabs) {
                     weights(kw);
                     if (!ok) {
@@ -242,16 +242,19 @@ __global__ void __launch_bounds__(kThreads, 2) ssd_q8_mid_kernel(const Q8Params 
         }
         __syncwarp();
     } else {
-        if (lane == 0) {
+        {
+            const bool issue = elect_one();
             constexpr uint32_t idesc = idesc_f16_f32(128, MT);
             const uint64_t b0 = sdesc_sw128(smem_u32(smem + S::kOffB), 16, 1024);
             uint32_t round = 0, parity = 0;
-            // one thread issues all this, and its instructions are what a slab takes: stages and descriptors
+            // one warp walks this, and its instructions are what a slab takes at least: stages and descriptors
             // are constants, the rest is looked at every kStages slabs
             for (int k = 0; k < slabs && ok; k += kStages, parity ^= 1) {
                 if (k > 0 && k % S::kRound == 0) {
-                    mma_commit(&bars[BAR_ACC]);
-                    if (!(ok = wait_bar(&bars[BAR_DRAINED], round & 1)))
+                    if (issue)
+                        mma_commit(&bars[BAR_ACC]);
+                    __syncwarp();
+                    if (!(ok = warp_wait(&bars[BAR_DRAINED], round & 1)))
                         break;
                     tc_fence_after();
                     ++round;
@@ -262,17 +265,22 @@ __global__ void __launch_bounds__(kThreads, 2) ssd_q8_mid_kernel(const Q8Params 
                 for (int s = 0; s < kStages; ++s) {
                     if (k + s >= slabs)
                         break;
-                    if (!(ok = wait_bar(&bars[BAR_A + s], parity) && wait_bar(&bars[BAR_B + s], parity)))
+                    if (!(ok = warp_wait(&bars[BAR_A + s], parity) && warp_wait(&bars[BAR_B + s], parity)))
                         break;
                     tc_fence_after();
+                    if (issue) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)   // (descriptors count 16 bytes)
-                        mma_ts(acc, tmem + kColA + 32 * s + 8 * kk, b0 + (s * S::kB + 32 * kk) / 16, idesc, s + kk > 0 ? 1u : more);
-                    mma_commit(&bars[BAR_EMPTY + s]);
+                        for (int kk = 0; kk < 4; ++kk)   // (descriptors count 16 bytes)
+                            mma_ts(acc, tmem + kColA + 32 * s + 8 * kk, b0 + (s * S::kB + 32 * kk) / 16, idesc, s + kk > 0 ? 1u : more);
+                        mma_commit(&bars[BAR_EMPTY + s]);
+                    }
+                    __syncwarp();
                 }
             }
-            mma_commit(&bars[BAR_ACC]);   // (every MMA issued so far)
-            wait_bar(&bars[BAR_ACC], round & 1);
+            if (issue)
+                mma_commit(&bars[BAR_ACC]);   // (every MMA issued so far)
+            __syncwarp();
+            warp_wait(&bars[BAR_ACC], round & 1);
         }
         __syncwarp();
     }
@@ -372,7 +380,7 @@ cudaError_t launch_t(const Q8Params &p, const uint8_t *images, int splits, cudaS
 
 }  // namespace
 
-size_t q8_mid_workspace_bytes(const Q8Params &p) { return (size_t)((p.M + 127) / 128) * p.k64 * kImage; }
+size_t q8_mid_workspace_bytes(const Q8Params &p) { return (size_t)p.padded() * p.k64 * 128; }
 
 cudaError_t q8_mid_launch(const Q8Params &p, bool f32, void *workspace, cudaStream_t st)
 {

@@ -44,7 +44,7 @@ def check(ssd, a, w, dtype, **kw):
 SIZES = [  # M, N, K
     (1, 1, 1), (1, 128, 64), (1, 300, 2560), (2, 129, 65), (7, 127, 63), (8, 1000, 129), (16, 256, 1024), (17, 384, 1040), (31, 200, 2048),
     (33, 640, 777), (64, 130, 4100), (65, 512, 512), (77, 333, 1001), (100, 64, 8192), (128, 1056, 640), (129, 257, 320), (200, 900, 1536),
-    (255, 128, 192), (256, 256, 256), (257, 513, 1025), (500, 300, 2100), (1000, 700, 500), (1025, 257, 1100), (2048, 512, 768), (3000, 130, 130),
+    (255, 128, 192), (256, 256, 256), (257, 513, 1025), (500, 300, 2100), (1000, 700, 500), (1025, 257, 1100), (2048, 512, 768), (3000, 130, 130), (288, 20000, 70), (416, 9000, 100), (33000, 40, 64),
 ]
 
 
