@@ -48,8 +48,12 @@ cudaError_t q8_pack_launch(const int8_t *w, int8_t *packed, const ssd_q8_dims_t 
 
 namespace {
 
-constexpr long long kFew = 32;     // up to here the weights go through registers and mma.sync
-constexpr long long kMany = 257;   // from here on widening both operands first pays
+// Up to here the weights go through registers and mma.sync (8 and 16 tokens of 10576 x 2560: 9.3 and 15.9 us, with
+// ssd_q8_mid.cu 12.1 and 12.2).
+constexpr long long kFew = 8;
+// From here on both operands are widened first (256, 384 and 512 tokens of 10576 x 2560: 30.2, 37.5 and 53 us
+// without; 288, 384 and 512 tokens 36.3, 37.2 and 39.2 us with).
+constexpr long long kMany = 257;
 
 Q8Params params(const Q8Args &a)
 {

@@ -22,12 +22,12 @@ struct Q8Params {
     __host__ __device__ long long padded() const { return (M + 127) / 128 * 128; }
 };
 
-// up to 16 tokens
+// up to 8 tokens
 cudaError_t q8_few_launch(const Q8Params &p, bool f32, cudaStream_t st);
 // many tokens (workspace: 16-byte aligned)
 size_t q8_many_workspace_bytes(const Q8Params &p);
 cudaError_t q8_many_launch(const Q8Params &p, bool f32, void *workspace, cudaStream_t st);
-// up to a few hundred tokens
+// up to 256 tokens (workspace: 16-byte aligned)
 size_t q8_mid_workspace_bytes(const Q8Params &p);
 cudaError_t q8_mid_launch(const Q8Params &p, bool f32, void *workspace, cudaStream_t st);
 // fp16 images of 128 rows x 64 elements, swizzled, from the first `wslabs` slabs of the weights (to

@@ -1,12 +1,12 @@
 // ssd_q8_few.cu -- the 8-bit product for a handful of tokens, bound by the weights' bytes.
 //
-// One CTA: 16 output channels x up to 32 tokens; its warps take the slabs of 64 inner elements in
+// One CTA: 16 output channels x up to 8 tokens; its warps take the slabs of 64 inner elements in
 // turn and add up their sums at the end.  So there are N / 16 CTAs, several on every SM, without
 // an exchange between them (tiles of 128 channels with K split over a cluster: 14.4 us for 8
 // tokens of 10576 x 2560, in two uneven waves).  Operands go from memory into registers, 16 bytes
 // a lane and row, some slabs at a time, and from there into mma.sync m16n8k32 on 8-bit
-// integers.  sm_103a runs it at 270 products a clock and SM (fp16: 1020), which is enough for 8
-// tokens at the memory's rate (190); widening for the fp16 form took 60 instructions a slab and warp
+// integers.  sm_103a runs it at 270 products a clock and SM (fp16: 1020), 190 are 8 tokens at the
+// memory's rate; widening for the fp16 form took 60 instructions a slab and warp
 // and more time than the weights' bytes (10.8 us; with rings of asynchronous copies 13.5).
 // A lane's 16 consecutive elements of a row are two k-steps' fragments when both operands
 // are read in the same order, so neither is shuffled.
@@ -20,8 +20,8 @@ namespace ssd {
 namespace {
 
 constexpr int kMaxWarps = 16;
-// slabs whose loads a warp issues before it uses the first
-template <int NT> constexpr int kBatch = NT == 4 ? 3 : 5;
+constexpr int kBatch = 5;         // slabs whose loads a warp issues before it uses the first
+constexpr int kTokens = 8;
 
 template <typename T> __device__ __forceinline__ T from_f32(float v);
 template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
@@ -34,11 +34,10 @@ __device__ __forceinline__ void mma16832(int (&c)[4], uint32_t a0, uint32_t a1, 
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// NT: groups of 8 tokens
-template <int NT, typename T>
+template <typename T>
 __global__ void __launch_bounds__(kMaxWarps * 32, 1) ssd_q8_few_kernel(const Q8Params p)
 {
-    constexpr int MT = 8 * NT, B = kBatch<NT>;
+    constexpr int B = kBatch;
     extern __shared__ __align__(16) int part[];   // [warp][token][channel]
     const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int tile = blockIdx.x >> 3, ch0 = (blockIdx.x & 7) * 16;
@@ -47,9 +46,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) ssd_q8_few_kernel(const Q8P
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    int sum[NT][4] = {};
+    int sum[4] = {};
     for (int s = warp; s < p.k64; s += warps * B) {
-        uint4 u[B][2], v[B][NT];
+        uint4 u[B][2], v[B];
 #pragma unroll
         for (int i = 0; i < B; ++i) {
             const int k = s + warps * i;
@@ -61,22 +60,16 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) ssd_q8_few_kernel(const Q8P
         }
 #pragma unroll
         for (int i = 0; i < B; ++i)
+            v[i] = load16(p, g, (s + warps * i) * 64 + 16 * t);
 #pragma unroll
-            for (int q = 0; q < NT; ++q)
-                v[i][q] = load16(p, 8 * q + g, (s + warps * i) * 64 + 16 * t);
-#pragma unroll
-        for (int i = 0; i < B; ++i)
-#pragma unroll
-            for (int q = 0; q < NT; ++q) {
-                mma16832(sum[q], u[i][0].x, u[i][1].x, u[i][0].y, u[i][1].y, v[i][q].x, v[i][q].y);
-                mma16832(sum[q], u[i][0].z, u[i][1].z, u[i][0].w, u[i][1].w, v[i][q].z, v[i][q].w);
-            }
+        for (int i = 0; i < B; ++i) {
+            mma16832(sum, u[i][0].x, u[i][1].x, u[i][0].y, u[i][1].y, v[i].x, v[i].y);
+            mma16832(sum, u[i][0].z, u[i][1].z, u[i][0].w, u[i][1].w, v[i].z, v[i].w);
+        }
     }
 #pragma unroll
-    for (int q = 0; q < NT; ++q)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)   // token 8 q + 2 t + (e & 1), channel g + 8 (e >> 1)
-            part[warp * MT * 16 + (8 * q + 2 * t + (e & 1)) * 16 + g + 8 * (e >> 1)] = sum[q][e];
+    for (int e = 0; e < 4; ++e)   // token 2 t + (e & 1), channel g + 8 (e >> 1)
+        part[warp * kTokens * 16 + (2 * t + (e & 1)) * 16 + g + 8 * (e >> 1)] = sum[e];
     __syncthreads();
     for (int i = threadIdx.x; i < (int)p.M * 16; i += blockDim.x) {
         const int tok = i >> 4, channel = tile * 128 + ch0 + (i & 15);
@@ -84,12 +77,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) ssd_q8_few_kernel(const Q8P
             continue;
         int v = 0;
         for (int q = 0; q < warps; ++q)
-            v += part[q * MT * 16 + i];
+            v += part[q * kTokens * 16 + i];
         static_cast<T *>(p.y)[tok * p.sy + channel] = from_f32<T>((float)v * p.as[tok] * p.ws[channel]);
     }
 }
 
-template <int NT, typename T>
+template <typename T>
 cudaError_t launch_t(const Q8Params &p, cudaStream_t st)
 {
     // warps per CTA: as many as let all CTAs run at once with about 20 warps on every SM
@@ -100,27 +93,21 @@ cudaError_t launch_t(const Q8Params &p, cudaStream_t st)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(items);
     cfg.blockDim = dim3(warps * 32);
-    cfg.dynamicSmemBytes = (size_t)warps * 8 * NT * 16 * 4;
+    cfg.dynamicSmemBytes = (size_t)warps * kTokens * 16 * 4;
     cfg.stream = st;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, ssd_q8_few_kernel<NT, T>, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, ssd_q8_few_kernel<T>, p);
     if (e == cudaSuccess)
         note_launches(1);
     return e;
-}
-
-template <typename T>
-cudaError_t launch_nt(const Q8Params &p, cudaStream_t st)
-{
-    return p.M <= 8 ? launch_t<1, T>(p, st) : p.M <= 16 ? launch_t<2, T>(p, st) : launch_t<4, T>(p, st);
 }
 
 }  // namespace
 
 cudaError_t q8_few_launch(const Q8Params &p, bool f32, cudaStream_t st)
 {
-    return f32 ? launch_nt<float>(p, st) : launch_nt<__nv_bfloat16>(p, st);
+    return f32 ? launch_t<float>(p, st) : launch_t<__nv_bfloat16>(p, st);
 }
 
 }  // namespace ssd

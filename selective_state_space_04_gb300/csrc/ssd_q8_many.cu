@@ -186,30 +186,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (warp == 8) {
-        if (lane == 0) {
-            const size_t slab = (size_t)p.padded() * 128;
-            uint32_t n = 0;   // slabs so far
-            Place at;
-            bool ok = true;
-            for (int i = me; i < items && ok; i += pairs) {
-                int c, t;
-                tile_at(i, cp, tp, c, t);
-                const uint8_t *w = wi + (size_t)min(2 * c + (int)rank, p.tiles - 1) * p.k64 * kImage;
-                // (rows past the tokens', in the last tile, are another slab's or the scratch's end)
-                const uint8_t *a = ai + ((size_t)t * tn + rank * (tn / 2)) * 128;
-                for (int k = 0; k < p.k64; ++k, ++n, at.next()) {
-                    const uint32_t s = at.s;
-                    if (n >= kStages && !(ok = wait_bar(&bars[BAR_EMPTY + s], at.parity ^ 1)))
-                        break;
-                    mbar_arrive_expect_tx(&bars[BAR_FULL + s], kImage + tn * 64);
-                    bulk_load(smem + s * kStageBytes, w + (size_t)k * kImage, kImage, &bars[BAR_FULL + s]);
-                    bulk_load(smem + s * kStageBytes + kImage, a + (size_t)k * slab, tn * 64, &bars[BAR_FULL + s]);
+        const bool issue = elect_one();
+        const size_t slab = (size_t)p.padded() * 128;
+        uint32_t n = 0;   // slabs so far
+        Place at;
+        bool ok = true;
+        for (int i = me; i < items && ok; i += pairs) {
+            int c, t;
+            tile_at(i, cp, tp, c, t);
+            const uint8_t *w = wi + (size_t)min(2 * c + (int)rank, p.tiles - 1) * p.k64 * kImage;
+            // (rows past the tokens', in the last tile, are another slab's or the scratch's end)
+            const uint8_t *a = ai + ((size_t)t * tn + rank * (tn / 2)) * 128;
+            for (int k = 0; k < p.k64; ++k, ++n, at.next(), w += kImage, a += slab) {
+                if (n >= kStages && !(ok = warp_wait(&bars[BAR_EMPTY + at.s], at.parity ^ 1)))
+                    break;
+                if (issue) {
+                    mbar_arrive_expect_tx(&bars[BAR_FULL + at.s], kImage + tn * 64);
+                    bulk_load(smem + at.s * kStageBytes, w, kImage, &bars[BAR_FULL + at.s]);
+                    bulk_load(smem + at.s * kStageBytes + kImage, a, tn * 64, &bars[BAR_FULL + at.s]);
                 }
+                __syncwarp();
             }
-            // no copy may be under way when shared memory is given up (each stage's last phase)
-            for (uint32_t j = n > kStages ? n - kStages : 0; j < n; ++j)
-                wait_bar(&bars[BAR_FULL + j % kStages], (j / kStages) & 1);
         }
+        // no copy may be under way when shared memory is given up (each stage's last phase)
+        for (uint32_t j = n > kStages ? n - kStages : 0; j < n; ++j)
+            wait_bar(&bars[BAR_FULL + j % kStages], (j / kStages) & 1);
         __syncwarp();
     } else if (warp == 9) {
         if (rank == 0) {

@@ -22,7 +22,7 @@ namespace ssd {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kRowsPerWarp = 8;   // state rows of one warp in flight together, as in ssd_decode.cu
+constexpr int kLoads = 8;   // 16-byte loads of a lane (for NV = 1) in flight together, as in ssd_decode.cu
 
 struct StepParams {
     const void *xbc, *dt_raw;
@@ -54,14 +54,16 @@ __device__ __forceinline__ float convolved(const T *in, const T *ring, const flo
     return u / (1.f + expf(-u));
 }
 
-// NV: float4 chunks of a state row per lane (N <= 128 NV)
-template <typename T, typename TD, int NV, int K>
-__global__ void __launch_bounds__(kWarps * 32) ssd_step_kernel(StepParams p)
+// A state row is 4 LPR NV elements at most: LPR lanes with NV pieces of 4 each, 32 / LPR rows side by side in
+// a warp (NV > 1 with whole warps only).
+template <typename T, typename TD, int LPR, int NV, int K>
+__global__ void __launch_bounds__(kWarps * 32, NV == 1 ? 8 : 1) ssd_step_kernel(StepParams p)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ float conv[];   // x [P], B [N], C [N]
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kSide = 32 / LPR, kPass = kLoads * kSide;   // rows of a warp at once
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / LPR, col = 4 * (lane % LPR);
     const int H = p.H, P = p.P, N = p.N, C = p.C;
     const long long i = blockIdx.x / H;
     const int h = (int)(blockIdx.x - i * H), per = H / p.G, g = h / per;
@@ -73,19 +75,18 @@ __global__ void __launch_bounds__(kWarps * 32) ssd_step_kernel(StepParams p)
             y[c] = from_f32<T>(0.f);
         return;
     }
-    float *state = p.states + ((size_t)slot * H + h) * P * N;
-    float4 hv[kRowsPerWarp][NV];
+    float *state = p.states + ((size_t)slot * H + h) * P * N + (size_t)sub * N + col;
+    float4 hv[kLoads][NV];
     auto load = [&](int p0) {
 #pragma unroll
-        for (int r = 0; r < kRowsPerWarp; ++r)
+        for (int r = 0; r < kLoads; ++r)
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int n = 4 * lane + 128 * k;
-                hv[r][k] = t > 0 && p0 + r < P && n < N ? __ldcs(reinterpret_cast<const float4 *>(state + (size_t)(p0 + r) * N + n))
-                                                       : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
+            for (int k = 0; k < NV; ++k)
+                hv[r][k] = t > 0 && p0 + r * kSide + sub < P && col + 128 * k < N
+                               ? __ldcs(reinterpret_cast<const float4 *>(state + (size_t)(p0 + r * kSide) * N + 128 * k))
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
     };
-    load(warp * kRowsPerWarp);
+    load(warp * kPass);
 
     const T *in = static_cast<const T *>(p.xbc) + i * p.xs;
     T *ring = static_cast<T *>(p.ring) + (size_t)slot * K * C;
@@ -108,16 +109,16 @@ __global__ void __launch_bounds__(kWarps * 32) ssd_step_kernel(StepParams p)
     for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int n = 4 * lane + 128 * k + e;
+            const int n = col + 128 * k + e;
             bv[k][e] = n < N ? conv[P + n] : 0.f;
             cv[k][e] = n < N ? conv[P + N + n] : 0.f;
         }
-    for (int p0 = warp * kRowsPerWarp; p0 < P; p0 += kWarps * kRowsPerWarp) {
-        if (p0 != warp * kRowsPerWarp)
+    for (int p0 = warp * kPass; p0 < P; p0 += kWarps * kPass) {
+        if (p0 != warp * kPass)
             load(p0);
 #pragma unroll
-        for (int r = 0; r < kRowsPerWarp; ++r) {
-            const int pr = p0 + r;
+        for (int r = 0; r < kLoads; ++r) {
+            const int pr = p0 + r * kSide + sub;
             const float x = pr < P ? conv[pr] : 0.f, dtx = dt * x;
             float acc = 0.f;
 #pragma unroll
@@ -131,20 +132,19 @@ __global__ void __launch_bounds__(kWarps * 32) ssd_step_kernel(StepParams p)
                 acc = fmaf(cv[k][1], v.y, acc);
                 acc = fmaf(cv[k][2], v.z, acc);
                 acc = fmaf(cv[k][3], v.w, acc);
-                const int n = 4 * lane + 128 * k;
-                if (pr < P && n < N)
-                    __stcs(reinterpret_cast<float4 *>(state + (size_t)pr * N + n), v);
+                if (pr < P && col + 128 * k < N)
+                    __stcs(reinterpret_cast<float4 *>(state + (size_t)(p0 + r * kSide) * N + 128 * k), v);
             }
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
+            for (int o = LPR / 2; o > 0; o >>= 1)
                 acc += __shfl_xor_sync(0xffffffffu, acc, o);
-            if (lane == 0 && pr < P)
+            if (col == 0 && pr < P)
                 y[pr] = from_f32<T>(fmaf(Dh, x, acc));
         }
     }
 }
 
-template <typename T, typename TD, int NV, int K>
+template <typename T, typename TD, int LPR, int NV, int K>
 cudaError_t launch_k(const StepParams &p, unsigned grid, cudaStream_t st)
 {
     cudaLaunchAttribute pdl[1];
@@ -157,19 +157,25 @@ cudaError_t launch_k(const StepParams &p, unsigned grid, cudaStream_t st)
     cfg.stream = st;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, ssd_step_kernel<T, TD, NV, K>, p);
+    return cudaLaunchKernelEx(&cfg, ssd_step_kernel<T, TD, LPR, NV, K>, p);
 }
 
-template <typename T, typename TD, int NV>
-cudaError_t launch_nv(const StepParams &p, unsigned grid, cudaStream_t st)
+template <typename T, typename TD, int LPR, int NV>
+cudaError_t launch_row(const StepParams &p, unsigned grid, cudaStream_t st)
 {
-    return p.K == 2 ? launch_k<T, TD, NV, 2>(p, grid, st) : p.K == 3 ? launch_k<T, TD, NV, 3>(p, grid, st) : launch_k<T, TD, NV, 4>(p, grid, st);
+    return p.K == 2   ? launch_k<T, TD, LPR, NV, 2>(p, grid, st)
+           : p.K == 3 ? launch_k<T, TD, LPR, NV, 3>(p, grid, st)
+                      : launch_k<T, TD, LPR, NV, 4>(p, grid, st);
 }
 
 template <typename T, typename TD>
 cudaError_t launch_t(const StepParams &p, unsigned grid, cudaStream_t st)
 {
-    return p.N <= 128 ? launch_nv<T, TD, 1>(p, grid, st) : p.N <= 256 ? launch_nv<T, TD, 2>(p, grid, st) : launch_nv<T, TD, 4>(p, grid, st);
+    if (p.N <= 32)
+        return p.N <= 16 ? launch_row<T, TD, 4, 1>(p, grid, st) : launch_row<T, TD, 8, 1>(p, grid, st);
+    if (p.N <= 128)
+        return p.N <= 64 ? launch_row<T, TD, 16, 1>(p, grid, st) : launch_row<T, TD, 32, 1>(p, grid, st);
+    return p.N <= 256 ? launch_row<T, TD, 32, 2>(p, grid, st) : launch_row<T, TD, 32, 4>(p, grid, st);
 }
 
 }  // namespace
