@@ -430,7 +430,9 @@ cudaError_t q8_mid_launch(const Q8Params &p, bool f32, void *workspace, cudaStre
     auto waves = [](long long n, long long at_once) { return (n + at_once - 1) / at_once; };
     long long best = waves(tiles, sms) * (p.k64 * 47 / 2 + 150 + mt * 37 / 10 + (p.k64 - 1) / (2 * round) * 100);
     int splits = 0;   // (alone)
-    for (int n = 1; n <= 8 && 2 * n <= std::max(2, p.k64); ++n) {
+    for (int n : {1, 2, 3, 4, 6, 8}) {   // (five and seven place worse still)
+        if (n > 1 && 2 * n > p.k64)
+            break;
         const long long slabs = (p.k64 + n - 1) / n;
         const bool apart = tiles * n <= sms || slabs > round;   // (drained sums take the second CTA's place)
         const long long at_once = apart ? sms : n > 4 ? 2 * sms * 7 / 8 : n > 2 ? 2 * sms * 15 / 16 : 2 * sms;
