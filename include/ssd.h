@@ -657,7 +657,7 @@ typedef struct ssd_norm_dims {
     uint32_t flags;          /* must be 0 */
     float eps;               /* >= 0 */
     uint32_t reserved;       /* must be 0 */
-    /* row strides in elements, multiples of 16 bytes (q_stride: of 8) */
+    /* row strides in elements, multiples of 16 bytes (q_stride: of 8; z_stride: any) */
     int64_t x_stride;        /* x; y; in the backward dout */
     int64_t z_stride;        /* z */
     int64_t residual_stride; /* residual; in the backward dresidual */
@@ -705,7 +705,8 @@ ssd_status_t ssd_add_rmsnorm_bwd_workspace_size(const ssd_norm_dims_t *dims, uin
  * ssd_gated_rmsnorm_q8_fwd -- ssd_gated_rmsnorm_fwd with an 8-bit result:
  *   v = y / sqrt(mean(y^2) + eps) * weight * SiLU(z)
  * as an 8-bit row in q [rows, D] and q_scale [rows].  y and z [rows, D] in
- * dtype, weight [D] fp32.  Outputs overlap nothing.
+ * dtype, weight [D] fp32.  z may have any alignment of its type (a slice of the
+ * projection's rows).  Outputs overlap nothing.
  */
 ssd_status_t ssd_gated_rmsnorm_q8_fwd(const void *y, const void *z, const float *weight,
                                       int8_t *q, float *q_scale, const ssd_norm_dims_t *dims,

@@ -1868,11 +1868,11 @@ ssd_status_t ssd_gated_rmsnorm_q8_fwd(const void *y, const void *z, const float 
     const int64_t n = dims->rows, D = dims->dim, es = (int64_t)elem_size(dims->dtype);
     if (n > 0 && (!y || !z || !weight || !q || !q_scale))
         return SSD_ERR_NULL_PTR;
-    const ssd_status_t sy = row_stride_ok(n, dims->x_stride, 0, es, 16), sz = row_stride_ok(n, dims->z_stride, 0, es, 16),
+    const ssd_status_t sy = row_stride_ok(n, dims->x_stride, 0, es, 16), sz = row_stride_ok(n, dims->z_stride, 0, es, 1),
                        sq = row_stride_ok(n, dims->q_stride, D, 1, 8);
     if (sy != SSD_OK || sz != SSD_OK || sq != SSD_OK)
         return sy != SSD_OK ? sy : sz != SSD_OK ? sz : sq;
-    if (!aligned16(y) || !aligned16(z) || !aligned16(weight) || !aligned(q, 8) || !aligned(q_scale, 4))
+    if (!aligned16(y) || !aligned(z, es) || !aligned16(weight) || !aligned(q, 8) || !aligned(q_scale, 4))
         return SSD_ERR_MISALIGNED;
     const Strided ins[] = {row_view(y, n, dims->x_stride, D * es, es), row_view(z, n, dims->z_stride, D * es, es), flat(weight, D * 4)};
     const Strided outs[] = {row_view(q, n, dims->q_stride, D, 1), flat(q_scale, n * 4)};

@@ -15,6 +15,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <cstring>
 
 #include "ssd_internal.h"
 
@@ -38,6 +39,7 @@ struct NormParams {
     long long xs, rs, zs, os, ros, qst;   // row strides, elements
     int D;
     float eps;
+    bool zvec;                       // z's rows are 16-byte aligned
 };
 
 // 8 consecutive elements as they lie in memory
@@ -49,6 +51,16 @@ template <typename T> struct Vec {
 #pragma unroll
         for (int i = 0; i < (int)sizeof(T) / 2; ++i)
             u[i] = __ldcs(s + i);
+    }
+    // the same from any alignment of T's
+    __device__ __forceinline__ void load_any(const void *p, long long at)
+    {
+        const T *s = static_cast<const T *>(p) + at;
+        T v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = s[i];
+        memcpy(u, v, sizeof(u));
     }
     __device__ __forceinline__ void store(void *p, long long at) const
     {
@@ -146,8 +158,12 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kMaxThreads) ssd_norm
                 ux[a].load(p.x, row * p.xs + 8 * v);
                 if (kMode == kResidual)
                     ur[a].load(p.res, row * p.rs + 8 * v);
-                if (kMode == kGate)
-                    uz[a].load(p.z, row * p.zs + 8 * v);
+                if (kMode == kGate) {
+                    if (p.zvec)
+                        uz[a].load(p.z, row * p.zs + 8 * v);
+                    else
+                        uz[a].load_any(p.z, row * p.zs + 8 * v);
+                }
             }
         }
 #pragma unroll
@@ -541,6 +557,7 @@ cudaError_t norm_launch(const NormArgs &a, cudaStream_t st)
     p.qst = a.d.q_stride;
     p.D = a.d.dim;
     p.eps = a.d.eps;
+    p.zvec = ((uintptr_t)a.z & 15) == 0 && (p.rows == 1 || p.zs * (a.d.dtype == SSD_DTYPE_F32 ? 4 : 2) % 16 == 0);
     if (a.d.dtype == SSD_DTYPE_F32)
         return norm_launch_types<float, float>(a, p, st);
     return a.d.residual_dtype == SSD_DTYPE_F32 ? norm_launch_types<__nv_bfloat16, float>(a, p, st)

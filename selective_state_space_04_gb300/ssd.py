@@ -903,7 +903,8 @@ def add_rmsnorm_q8_fwd(x, weight, residual=None, *, eps=1e-6, q=None, scale=None
 
 def gated_rmsnorm_q8_fwd(y, z, weight, eps=1e-6, *, q=None, scale=None, stream=None):
     """``RMSNorm(y) * weight * SiLU(z)`` per row (:func:`gated_rmsnorm_fwd`) with an 8-bit result, as
-    :func:`add_rmsnorm_q8_fwd` gives it (``ssd_gated_rmsnorm_q8_fwd``).  ``y, z [rows, D]``.  Returns ``(q, scale)``."""
+    :func:`add_rmsnorm_q8_fwd` gives it (``ssd_gated_rmsnorm_q8_fwd``).  ``y, z [rows, D]``, z at any row stride (a slice of the projection).  Returns
+    ``(q, scale)``."""
     dev = y.device
     key = (gated_rmsnorm_q8_fwd, *map(_layout, (y, z, weight, q, scale)), eps)
     d = _known.get(key)

@@ -83,6 +83,17 @@ def test_gated(ssd, D, dtype):
     check_q8(q, scale, ref, GATE)
 
 
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("D", [64, 1000, 2560, 8192])
+def test_gate_as_a_slice_of_the_projection(ssd, D, dtype):
+    """z at an odd offset, its rows an odd stride apart."""
+    n = 11
+    y, w, proj = normal(45, n, D, dtype=dtype), weight(46, D), normal(47, n, D + 13, dtype=dtype)
+    q, scale = ssd.gated_rmsnorm_q8_fwd(y, proj[:, 5:5 + D], w, EPS)
+    rq, rscale = ssd.gated_rmsnorm_q8_fwd(y, proj[:, 5:5 + D].contiguous(), w, EPS)
+    assert torch.equal(q, rq) and torch.equal(scale, rscale)
+
+
 @pytest.mark.parametrize("dtype,rdtype,with_res", [(BF, BF, True), (BF, F, True), (BF, BF, False), (F, F, True), (F, F, False)])
 @pytest.mark.parametrize("n,D", [(1, 8), (37, 264), (700, 1000), (5, 1032), (1500, 2560), (65, 4104), (3, 16384), (9000, 64)])
 def test_gradients(ssd, n, D, dtype, rdtype, with_res):

@@ -88,7 +88,8 @@ def test_norm_forward_pointers(ssd, ptrs, q8, status):
 
 
 @pytest.mark.parametrize("ptrs,status", [
-    *[({n: None}, NULL) for n in GATED], *[({n: at(i) + 2}, MISALIGNED) for i, n in enumerate(GATED)],
+    *[({n: None}, NULL) for n in GATED], *[({n: at(i) + 2}, MISALIGNED) for i, n in enumerate(GATED) if n != "z"],
+    (dict(z=at(1) + 1), MISALIGNED),
     (dict(q=at(0)), ALIASING), (dict(q=at(1) + 64), ALIASING), (dict(q_scale=at(2)), ALIASING), (dict(q_scale=at(3)), ALIASING)])
 def test_gated_pointers(ssd, ptrs, status):
     assert gated(ssd, ptrs) == status
