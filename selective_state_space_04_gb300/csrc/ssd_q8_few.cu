@@ -4,10 +4,12 @@
 // turn and add up their sums at the end.  So there are N / 16 CTAs, several on every SM, without
 // an exchange between them (tiles of 128 channels with K split over a cluster: 14.4 us for 8
 // tokens of 10576 x 2560, in two uneven waves).  Operands go from memory into registers, 16 bytes
-// a lane and row, some slabs at a time, and from there into mma.sync m16n8k32 on 8-bit
-// integers.  sm_103a runs it at 270 products a clock and SM (fp16: 1020), 190 are 8 tokens at the
+// a lane and row, some slabs at a time, and from there into mma.sync m16n8k32 on 8-bit integers,
+// or for one token into dp4a.  sm_103a runs it at 270 products a clock and SM (fp16: 1020), 190 are 8 tokens at the
 // memory's rate; widening for the fp16 form took 60 instructions a slab and warp
-// and more time than the weights' bytes (10.8 us; with rings of asynchronous copies 13.5).
+// and more time than the weights' bytes (10.8 us; with rings of asynchronous copies 13.5).  dp4a has the same
+// rate, but no 8 columns to fill: one token takes an eighth of the products (8.4 -> 7.6 us; two already
+// take 10.2, 8.8 with mma.sync).
 // A lane's 16 consecutive elements of a row are two k-steps' fragments when both operands
 // are read in the same order, so neither is shuffled.
 #include <cuda_bf16.h>
@@ -21,7 +23,6 @@ namespace {
 
 constexpr int kMaxWarps = 16;
 constexpr int kBatch = 5;         // slabs whose loads a warp issues before it uses the first
-constexpr int kTokens = 8;
 
 template <typename T> __device__ __forceinline__ T from_f32(float v);
 template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
@@ -34,19 +35,28 @@ __device__ __forceinline__ void mma16832(int (&c)[4], uint32_t a0, uint32_t a1, 
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <typename T>
+// TOK: tokens at most; 8 with mma.sync, 1 with dp4a
+template <int TOK, typename T>
 __global__ void __launch_bounds__(kMaxWarps * 32, 1) ssd_q8_few_kernel(const Q8Params p)
 {
+    constexpr bool kMma = TOK == 8;
     constexpr int B = kBatch;
     extern __shared__ __align__(16) int part[];   // [warp][token][channel]
     const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int tile = blockIdx.x >> 3, ch0 = (blockIdx.x & 7) * 16;
     // this lane's bytes of a slab's rows g and g + 8 (128 bytes on)
     const int8_t *w = p.w + (size_t)tile * p.k64 * 8192 + t * 2048 + (ch0 + g) * 16;
+    // While the launch in front ends: the first weights into L2 (whoever wrote them, it is where they are).
+    if (g == 0)
+        for (int i = 0; i < B; ++i)
+            if (warp + warps * i < p.k64) {
+                const int8_t *line = w + (size_t)(warp + warps * i) * 8192;
+                asm volatile("prefetch.global.L2 [%0];\n\tprefetch.global.L2 [%0 + 128];" ::"l"(line));
+            }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    int sum[4] = {};
+    int sum[kMma ? 4 : 2] = {};   // (dp4a: rows g and g + 8, this lane's elements)
     for (int s = warp; s < p.k64; s += warps * B) {
         uint4 u[B][2], v[B];
 #pragma unroll
@@ -60,16 +70,37 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) ssd_q8_few_kernel(const Q8P
         }
 #pragma unroll
         for (int i = 0; i < B; ++i)
-            v[i] = load16(p, g, (s + warps * i) * 64 + 16 * t);
+            v[i] = load16(p, kMma ? g : 0, (s + warps * i) * 64 + 16 * t);
 #pragma unroll
         for (int i = 0; i < B; ++i) {
-            mma16832(sum, u[i][0].x, u[i][1].x, u[i][0].y, u[i][1].y, v[i].x, v[i].y);
-            mma16832(sum, u[i][0].z, u[i][1].z, u[i][0].w, u[i][1].w, v[i].z, v[i].w);
+            if constexpr (kMma) {
+                mma16832(sum, u[i][0].x, u[i][1].x, u[i][0].y, u[i][1].y, v[i].x, v[i].y);
+                mma16832(sum, u[i][0].z, u[i][1].z, u[i][0].w, u[i][1].w, v[i].z, v[i].w);
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    int &c = sum[h];
+                    c = __dp4a((int)u[i][h].x, (int)v[i].x, c);
+                    c = __dp4a((int)u[i][h].y, (int)v[i].y, c);
+                    c = __dp4a((int)u[i][h].z, (int)v[i].z, c);
+                    c = __dp4a((int)u[i][h].w, (int)v[i].w, c);
+                }
+            }
         }
     }
+    if constexpr (kMma) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)   // token 2 t + (e & 1), channel g + 8 (e >> 1)
-        part[warp * kTokens * 16 + (2 * t + (e & 1)) * 16 + g + 8 * (e >> 1)] = sum[e];
+        for (int e = 0; e < 4; ++e)   // token 2 t + (e & 1), channel g + 8 (e >> 1)
+            part[warp * TOK * 16 + (2 * t + (e & 1)) * 16 + g + 8 * (e >> 1)] = sum[e];
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
+            sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
+            if (t == 0)
+                part[warp * 16 + g + 8 * h] = sum[h];
+        }
+    }
     __syncthreads();
     for (int i = threadIdx.x; i < (int)p.M * 16; i += blockDim.x) {
         const int tok = i >> 4, channel = tile * 128 + ch0 + (i & 15);
@@ -77,12 +108,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) ssd_q8_few_kernel(const Q8P
             continue;
         int v = 0;
         for (int q = 0; q < warps; ++q)
-            v += part[q * kTokens * 16 + i];
+            v += part[q * TOK * 16 + i];
         static_cast<T *>(p.y)[tok * p.sy + channel] = from_f32<T>((float)v * p.as[tok] * p.ws[channel]);
     }
 }
 
-template <typename T>
+template <int TOK, typename T>
 cudaError_t launch_t(const Q8Params &p, cudaStream_t st)
 {
     // warps per CTA: as many as let all CTAs run at once with about 20 warps on every SM
@@ -93,11 +124,11 @@ cudaError_t launch_t(const Q8Params &p, cudaStream_t st)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(items);
     cfg.blockDim = dim3(warps * 32);
-    cfg.dynamicSmemBytes = (size_t)warps * kTokens * 16 * 4;
+    cfg.dynamicSmemBytes = (size_t)warps * TOK * 16 * 4;
     cfg.stream = st;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, ssd_q8_few_kernel<T>, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, ssd_q8_few_kernel<TOK, T>, p);
     if (e == cudaSuccess)
         note_launches(1);
     return e;
@@ -107,7 +138,9 @@ cudaError_t launch_t(const Q8Params &p, cudaStream_t st)
 
 cudaError_t q8_few_launch(const Q8Params &p, bool f32, cudaStream_t st)
 {
-    return f32 ? launch_t<float>(p, st) : launch_t<__nv_bfloat16>(p, st);
+    if (p.M == 1)
+        return f32 ? launch_t<1, float>(p, st) : launch_t<1, __nv_bfloat16>(p, st);
+    return f32 ? launch_t<8, float>(p, st) : launch_t<8, __nv_bfloat16>(p, st);
 }
 
 }  // namespace ssd
