@@ -674,7 +674,8 @@ typedef struct ssd_norm_dims {
  * in q [rows, D] and q_scale [rows].  Exactly one of out and q is given, q_scale
  * with q.  residual NULL: h = x, and residual_out has to be NULL too; with a
  * residual, residual_out may be NULL.  weight [D] fp32.  A row of zeros stays
- * zero, with eps 0 too.  The mean square is an fp32 sum.
+ * zero, with eps 0 too.  The mean square is an fp32 sum: where it overflows (values
+ * near 2^64), the row is normalised to zeros.
  * residual_out may be residual with equal strides, and out may be x (in place);
  * nothing else may overlap.
  */
