@@ -48,11 +48,11 @@ cudaError_t q8_pack_launch(const int8_t *w, int8_t *packed, const ssd_q8_dims_t 
 
 namespace {
 
-// Up to here the weights go through registers and mma.sync (8 and 16 tokens of 10576 x 2560: 9.3 and 15.9 us, with
-// ssd_q8_mid.cu 12.1 and 12.2).
+// Up to here the weights go through registers and mma.sync (8 tokens of 10576 x 2560: 8.4 us, with ssd_q8_mid.cu
+// 12.1; 16 tokens 15.9 in an earlier form of two such passes, with ssd_q8_mid.cu 12.1).
 constexpr long long kFew = 8;
 // From here on both operands are widened first (256, 384 and 512 tokens of 10576 x 2560: 30.2, 37.5 and 53 us
-// without; 288, 384 and 512 tokens 36.3, 37.2 and 39.2 us with).
+// without; 288, 384 and 512 tokens 36.3, 37.0 and 39 to 43 us with).
 constexpr long long kMany = 257;
 
 Q8Params params(const Q8Args &a)

@@ -9,8 +9,9 @@
 //
 // The second: pairs of CTAs (cta_group::2) on tiles of 256 channels x up to 256 tokens.  Each
 // CTA holds its half of the channels' and of the tokens' operand, so that a slab of 64
-// inner elements is at most 32 KB of copies per CTA for 512 clocks of MMA.  That is what bounds it: 13 TB/s
-// from L2 over all SMs, which is what copies alone reach.  Accumulators take
+// inner elements is at most 32 KB of copies per CTA for 512 clocks of MMA.  The tensor pipe is busy 83% of the
+// time at 8192 tokens of 10576 x 2560 (both launches 254 to 260 us, 1.75 to 1.71 PFLOP/s; repeated without a pause the
+// power limit holds the clock near 1.78 GHz and it is 282 us), 71% at 4096 of 2560 x 5120.  Accumulators take
 // 1024 inner elements each, as in ssd_q8_mid.cu, two of them in turn: while one is
 // filled, eight warps add the other to 32-bit integers in registers (128 per thread).
 #include <cuda_bf16.h>
@@ -369,7 +370,7 @@ cudaError_t many_t(const Q8Params &p, uint8_t *ws, cudaStream_t st)
         const int cp = (p.tiles + 1) / 2, pairs = sm_count() / 2;
         // Tokens of a tile: the pairs take tiles in waves, and a slab's time goes by its bytes, 16 KB of
         // weights and 64 a token.  (160 tiles of 256 tokens are 3 waves of 76, the third almost
-        // empty; 220 of 192 are 3 shorter ones: 4096 tokens of 2560 x 5120 99 -> 87 us.)
+        // empty; 220 of 192 are 3 shorter ones: 4096 tokens of 2560 x 5120 95 -> 80 us.)
         int tn = 256;
         long long best = INT64_MAX;
         for (int n = 256; n >= 64; n -= 32) {
