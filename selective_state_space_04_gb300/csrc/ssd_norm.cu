@@ -10,6 +10,9 @@
 //   q = rint(t * 127 / max|t|),   scale = r max|t| / 127.
 // The maximum is taken over the bit patterns of |t|, in which an infinity or NaN
 // is above every finite number and is not lost as it is by fmaxf.
+//
+// Bound by memory: 32768 rows of 2560 with a residual, bf16, take 95 us (104% of a plain copy's rate), their
+// gradients 111 (89%).  The gated form reaches 60% (4096 rows of 5120: 25.6 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -49,7 +49,7 @@ cudaError_t q8_pack_launch(const int8_t *w, int8_t *packed, const ssd_q8_dims_t 
 namespace {
 
 // Up to here the weights go through registers and mma.sync (8 tokens of 10576 x 2560: 8.4 us, with ssd_q8_mid.cu
-// 12.1; 16 tokens 15.9 in an earlier form of two such passes, with ssd_q8_mid.cu 12.1).
+// 12.1; 16 tokens 15.9, when they went through registers too, and 12.1).
 constexpr long long kFew = 8;
 // From here on both operands are widened first (256, 384 and 512 tokens of 10576 x 2560: 30.2, 37.5 and 53 us
 // without; 288, 384 and 512 tokens 36.3, 37.0 and 39 to 43 us with).

@@ -9,7 +9,8 @@
 // memory's rate; widening for the fp16 form took 60 instructions a slab and warp
 // and more time than the weights' bytes (10.8 us; with rings of asynchronous copies 13.5).  dp4a has the same
 // rate, but no 8 columns to fill: one token takes an eighth of the products (8.4 -> 7.6 us; two already
-// take 10.2, 8.8 with mma.sync).
+// take 10.2, 8.8 with mma.sync).  With the prefetch below 1 and 8 tokens of 10576 x 2560 take 6.8 and 8.4 us, 59 and 48%
+// of the rate of a plain copy, of 16384 x 8192 28.2 and 32.4 us, 70 and 61%.
 // A lane's 16 consecutive elements of a row are two k-steps' fragments when both operands
 // are read in the same order, so neither is shuffled.
 #include <cuda_bf16.h>
