@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(kWarp ? 32 * kBwdWarpRows : kBwdThreads, kWarp
             turn ^= 1;
         }
         const float r = inv_rms(ss, p.D, p.eps);
-        const float k = r * r * c / dim;
+        const float k = r * c / dim;   // (h r is of the order of 1; r r would be infinite where rows are tiny and eps is 0)
 #pragma unroll
         for (int a = 0; a < VPT; ++a) {
             const int v = tid + a * group;
@@ -447,9 +447,9 @@ __global__ void __launch_bounds__(kWarp ? 32 * kBwdWarpRows : kBwdThreads, kWarp
                 ur[a].get(f);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float dx = r * (d[e] * w[a][e] - h[e] * k);
+                const float n = h[e] * r, dx = r * (d[e] * w[a][e] - n * k);
                 o[e] = kRes ? dx + f[e] : dx;
-                acc[a][e] = fmaf(d[e], h[e] * r, acc[a][e]);
+                acc[a][e] = fmaf(d[e], n, acc[a][e]);
             }
             Vec<R> u;
             u.set(o);
