@@ -639,9 +639,11 @@ ssd_status_t ssd_paged_attn_workspace_size(const ssd_attn_dims_t *dims, uint64_t
  * Rows are [rows, dim] with a stride between rows (elements; dim contiguous).
  * An 8-bit row is a row of whole numbers q, -127 .. 127, with one fp32 scale:
  * it stands for q * scale, scale = max|v| / 127 and q = v / scale rounded to
- * nearest even.  A row of zeros has scale 0 (so has one whose scale would be
- * below 2^-126); a row that holds an infinity or NaN has q 0 and scale NaN, so
- * that whatever is computed from it is NaN.
+ * nearest even.  A row of zeros has scale 0, and a row that holds an infinity or
+ * NaN has q 0 and scale NaN, so that whatever is computed from it is NaN.  The
+ * ends of the range: v is r times t = h * weight (* SiLU(z)), r one factor a row, and
+ * t is formed in fp32.  A row whose largest |t|, or whose scale, is below 2^-126
+ * has scale 0; one where t leaves fp32's range is taken to hold an infinity.
  *
  * Pointers and errors as for the attention-layer entry points: DEVICE arrays of
  * the current device, 16-byte aligned where nothing else is said; calls enqueue
@@ -675,7 +677,8 @@ typedef struct ssd_norm_dims {
  * with q.  residual NULL: h = x, and residual_out has to be NULL too; with a
  * residual, residual_out may be NULL.  weight [D] fp32.  A row of zeros stays
  * zero, with eps 0 too.  The mean square is an fp32 sum: where it overflows (values
- * near 2^64), the row is normalised to zeros.
+ * near 2^64), the row is normalised to zeros.  With eps 0, values below about
+ * 2^-63 have squares that lose bits, and a row of values below 2^-75 counts as zeros.
  * residual_out may be residual with equal strides, and out may be x (in place);
  * nothing else may overlap.
  */

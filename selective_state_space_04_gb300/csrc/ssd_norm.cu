@@ -133,7 +133,7 @@ __device__ __forceinline__ float inv_rms(float ss, int D, float eps)
 
 // v sigmoid(v) from the approximate exponential and reciprocal (a few units of 2^-23 and |v| of 2^-24;
 // five instructions: this and the rounding below took the gated norm of 4096 rows of 5120 from 28.2 us to 25.6).  Below
-// about -88 the exponential is infinite and the result 0, as it should be.
+// about -87.3, where the reciprocal is under 2^-126, the result is 0 (at most 2^-119 off).
 __device__ __forceinline__ float silu(float v)
 {
     float e, r;
@@ -242,11 +242,18 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : kMaxThreads) ssd_norm
     if (kQ8) {
         const float m = __uint_as_float(most);
         float scale = r * m / 127.f, by = 127.f / m;
-        if (!(scale <= 3.4028235e38f) || !(m <= 3.4028235e38f)) {   // an infinity or NaN in the row
+        if (!(scale <= 3.4028235e38f) || !(m <= 3.4028235e38f)) {   // an infinity or NaN in the row, or a product past fp32
             scale = __uint_as_float(0x7fffffffu);
             by = 0.f;
-        } else if (scale < kTiny || m < 127.f * kTiny) {
+        } else if (scale < kTiny || m < kTiny) {   // (products below 2^-126 have lost bits)
             scale = by = 0.f;
+        } else if (m < 127.f * kTiny) {   // the quotient would leave the range: both by 2^32
+            by = 127.f / (m * 4294967296.f);
+#pragma unroll
+            for (int a = 0; a < VPT; ++a)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    h[a][e] *= 4294967296.f;
         }
         if (tid == 0)
             p.qs[row] = scale;
