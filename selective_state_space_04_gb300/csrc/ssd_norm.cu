@@ -110,9 +110,10 @@ template <typename T> struct Vec {
     }
 };
 
+// (not through the read-only path: the launch before may write the weights while this one lives)
 __device__ __forceinline__ void load_w(const float *w, int v, float (&f)[8])
 {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(w) + 2 * v), b = __ldg(reinterpret_cast<const float4 *>(w) + 2 * v + 1);
+    const float4 a = reinterpret_cast<const float4 *>(w)[2 * v], b = reinterpret_cast<const float4 *>(w)[2 * v + 1];
     f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
 }
 

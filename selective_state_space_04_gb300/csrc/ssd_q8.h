@@ -59,14 +59,15 @@ __device__ __forceinline__ void widen16(const uint4 &u, uint32_t *f)
     widen4(u.w, f + 6);
 }
 
-// a[t, k .. k + 15], zeros beyond M and K
+// a[t, k .. k + 15], zeros beyond M and K.  (Not through the read-only path: the launch before may write the
+// tokens while this one lives.)
 __device__ __forceinline__ uint4 load16(const Q8Params &p, long long t, int k)
 {
     if (t >= p.M || k >= p.K)
         return make_uint4(0u, 0u, 0u, 0u);
     const int8_t *src = p.a + t * p.sa + k;
     if (p.vec && k + 16 <= p.K) {
-        const uint2 lo = __ldg(reinterpret_cast<const uint2 *>(src)), hi = __ldg(reinterpret_cast<const uint2 *>(src) + 1);
+        const uint2 lo = reinterpret_cast<const uint2 *>(src)[0], hi = reinterpret_cast<const uint2 *>(src)[1];
         return make_uint4(lo.x, lo.y, hi.x, hi.y);
     }
     uint32_t v[4] = {0u, 0u, 0u, 0u};
@@ -84,7 +85,7 @@ __device__ __forceinline__ uint2 load8(const Q8Params &p, long long t, int k)
         return make_uint2(0u, 0u);
     const int8_t *src = p.a + t * p.sa + k;
     if (p.vec && k + 8 <= p.K)
-        return __ldg(reinterpret_cast<const uint2 *>(src));
+        return *reinterpret_cast<const uint2 *>(src);
     uint32_t v[2] = {0u, 0u};
 #pragma unroll
     for (int e = 0; e < 8; ++e)

@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(256) ssd_q8_widen_kernel(const Q8Params p, uin
             image = wi + i * kImage;
 #pragma unroll
             for (int h = 0; h < 4; ++h)
-                u[h] = __ldg(reinterpret_cast<const uint2 *>(p.w + i * 8192 + (c >> 1) * 2048 + (r0 + 32 * h) * 16 + (c & 1) * 8));
+                u[h] = *reinterpret_cast<const uint2 *>(p.w + i * 8192 + (c >> 1) * 2048 + (r0 + 32 * h) * 16 + (c & 1) * 8);
         } else {
             const long long j = i - wslabs, t0 = j / p.k64 * 128, k = j % p.k64;
             const int k0 = (int)k * 64 + c * 8;
