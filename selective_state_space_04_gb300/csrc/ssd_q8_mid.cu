@@ -140,14 +140,15 @@ __global__ void __launch_bounds__(kThreads, kAlone ? 1 : 2) ssd_q8_mid_kernel(co
     tc_fence_after();
     const uint32_t tmem = holder;
     // The launch in front of this one writes the tokens' images, and has waited for all before it before
-    // it let this one begin: weights and scales may be read at once, the images after the wait.
+    // it let this one begin: weights and scales may be read at once, the images after the wait.  From L2, where
+    // the launches before that one have left them; what this SM's L1 holds is settled by the wait only.
     bool ok = true;
     for (int i = threadIdx.x; i < MT; i += kThreads)
-        token_scale[i] = t0 + i < p.M ? p.as[t0 + i] : 0.f;
+        token_scale[i] = t0 + i < p.M ? __ldcg(p.as + t0 + i) : 0.f;
 
     const int n = threadIdx.x & 127;   // (of warps 0-7: their channel)
     const bool mine = tile * 128 + n < p.N;
-    const float ws = warp < 8 && mine ? p.ws[tile * 128 + n] : 0.f;
+    const float ws = warp < 8 && mine ? __ldcg(p.ws + tile * 128 + n) : 0.f;
     const uint32_t quarter = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
     int *sums = reinterpret_cast<int *>(smem + S::kRings) + 32 * (warp & 3) + lane;   // (with `multi`, not alone)
     int kept[kAlone ? MT / 2 : 1] = {};                                               // (alone: every other 8 tokens)

@@ -20,6 +20,15 @@ def test_no_read_only_loads():
             assert word not in s, f"{word} in {os.path.basename(f)}"
 
 
+def test_scales_read_ahead_of_the_wait_come_from_l2():
+    """The product for 9 to 256 tokens reads its scales before it waits for the launch in front, when only L2 is sure to hold
+    what the launches before that one wrote: an ordinary load may find an older line in L1."""
+    with open(os.path.join(CSRC, "ssd_q8_mid.cu")) as f:
+        s = f.read()
+    assert s.count("__ldcg(p.as +") == 1 and s.count("__ldcg(p.ws +") == 1
+    assert "p.as[" not in s and "p.ws[" not in s
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("rows", [1, 8, 40, 300])
 def test_products_directly_behind_the_norm(rows):
