@@ -1067,10 +1067,30 @@ def conv_scan_step(xbc, conv_ring, weight, bias, dt_raw, dt_bias, A_log, D, stat
     return y
 
 
-def conv_ring_store(conv_ring, conv_state, slots, lengths):
+def conv_ring_store(conv_ring, conv_state, slots, lengths, *, stream=None):
     """Puts a prompt's carried inputs where :func:`conv_scan_step` looks for them: ``conv_state [B, K-1, C]`` as
     :func:`conv1d_silu_fwd` or :func:`conv_scan_fwd` returns it, of sequences that now hold ``lengths [B]`` tokens, into the
-    entries of ``slots [B]`` in ``conv_ring [nslots, K, C]`` (slots and lengths int64 tensors)."""
-    K = conv_ring.shape[1]
-    at = lengths[:, None] - (K - 1) + torch.arange(K - 1, device=lengths.device)
-    conv_ring[slots[:, None], at % K] = conv_state
+    entries of ``slots [B]`` in ``conv_ring [nslots, K, C]`` (slots and lengths int32 or int64).  As there, a slot outside
+    the pool or a negative length makes a row padding, and two rows must not have the same slot."""
+    dev = conv_ring.device
+    if conv_ring.dim() != 3 or conv_ring.shape[1] < 2 or conv_ring.dtype not in _DTYPES:
+        raise ValueError("conv_ring must be a [nslots, K, C] bf16 or fp32 tensor")
+    S, K, C = conv_ring.shape
+    for name, t in (("slots", slots), ("lengths", lengths)):
+        if t.dim() != 1 or t.shape != slots.shape or t.dtype not in (torch.int32, torch.int64) or t.device != dev:
+            raise ValueError(f"{name} must be a [B] int32 or int64 tensor on {dev}")
+    B = slots.shape[0]
+    if conv_state.shape != (B, K - 1, C) or conv_state.dtype != conv_ring.dtype or conv_state.device != dev:
+        raise ValueError(f"conv_state must be a {(B, K - 1, C)} {conv_ring.dtype} tensor on {dev}")
+    if conv_ring.is_cuda:
+        _stream_ptr(dev, stream)
+    if S == 0 or B == 0:
+        return
+    with torch.cuda.stream(stream):
+        slots, lengths = slots.long(), lengths.long()
+        real = (slots >= 0) & (slots < S) & (lengths >= 0)
+        # Padding stores what another row stores, in the same place; where all rows are padding, what is there.
+        row = torch.where(real, torch.arange(B, device=dev), real.byte().argmax())
+        to = slots[row].clamp(0, S - 1)[:, None]
+        at = (lengths[row][:, None] - (K - 1) + torch.arange(K - 1, device=dev)) % K
+        conv_ring[to, at] = torch.where(real.any(), conv_state[row], conv_ring[to, at])
