@@ -80,7 +80,8 @@ def make_weights(c: Config, seed: int = 0) -> dict:
 def quantized(w):
     """A weight as 8-bit integers with a scale per output channel, in the order that ssd.q8_matmul reads."""
     scale = w.abs().amax(1) / 127.0
-    return ssd.q8_pack_weight(torch.clamp(torch.round(w / scale[:, None]), -127, 127).to(torch.int8)), scale
+    rows = torch.where(scale > 0, scale, 1.0)[:, None]   # (a channel of zeros stays zeros, with scale 0)
+    return ssd.q8_pack_weight(torch.clamp(torch.round(w / rows), -127, 127).to(torch.int8)), scale
 
 
 def rms(x):
