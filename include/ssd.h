@@ -659,7 +659,8 @@ typedef struct ssd_norm_dims {
     uint32_t flags;          /* must be 0 */
     float eps;               /* >= 0 */
     uint32_t reserved;       /* must be 0 */
-    /* row strides in elements, multiples of 16 bytes (q_stride: of 8; z_stride: any) */
+    /* row strides in elements, multiples of 16 bytes (q_stride: of 8; z_stride: any); inputs 0 or more (rows may
+     * share bytes), outputs at least dim; not looked at where there is one row */
     int64_t x_stride;        /* x; y; in the backward dout */
     int64_t z_stride;        /* z */
     int64_t residual_stride; /* residual; in the backward dresidual */
@@ -728,7 +729,8 @@ typedef struct ssd_q8_dims {
     int32_t K;           /* inner elements, 1 .. 65536 */
     int32_t out_dtype;   /* ssd_dtype_t of y */
     uint32_t flags;      /* must be 0 */
-    int64_t a_stride;    /* row strides in elements, any >= K (y: >= N); ssd_q8_pack_weight: the weight's */
+    int64_t a_stride;    /* row strides in elements: a any from 0 up (rows may share bytes), y any >= N; */
+                         /* ssd_q8_pack_weight: the weight's, >= K */
     int64_t y_stride;
 } ssd_q8_dims_t;
 
@@ -745,7 +747,11 @@ ssd_status_t ssd_q8_pack_weight(const int8_t *w, int8_t *packed, const ssd_q8_di
  * rounded to fp32, multiplied by a_scale, then by w_scale, and rounded to
  * out_dtype.  a and y have any alignment of their types, the scales 4 bytes.
  * y overlaps nothing.  `workspace` as for ssd_qk_norm_rope_bwd, with
- * ssd_q8_matmul_workspace_size's bytes (0 for few tokens).
+ * ssd_q8_matmul_workspace_size's bytes:
+ *   M <= 8:    none
+ *   M <= 256:  128 ceil(M / 128) * 128 ceil(K / 64), the tokens in 16 bits
+ *   above:     16384 ceil(K / 64) (ceil(N / 128) + ceil(min(M, 32768) / 128)) + 32768, the weights
+ *              in 16 bits (about 2 N K bytes, whatever M is) and up to 32768 tokens at a time
  */
 ssd_status_t ssd_q8_matmul(const int8_t *a, const float *a_scale, const int8_t *packed,
                            const float *w_scale, void *y, void *workspace,
@@ -755,17 +761,17 @@ ssd_status_t ssd_q8_matmul_workspace_size(const ssd_q8_dims_t *dims, uint64_t *b
 typedef struct ssd_step_dims {
     int64_t rows;        /* tokens of the step, >= 0; rows * nheads below 2^31 */
     int64_t nslots;      /* sequences that conv_ring and states hold, >= 0 */
-    int32_t nheads;      /* H >= 1 */
-    int32_t headdim;     /* P >= 1 */
+    int32_t nheads;      /* H: 1 .. 2^20 */
+    int32_t headdim;     /* P: 1 .. 2048 */
     int32_t dstate;      /* N: a multiple of 4, 4 .. 512 */
-    int32_t ngroups;     /* G >= 1, H % G == 0 */
+    int32_t ngroups;     /* G >= 1, H % G == 0; C = H P + 2 G N below 2^30 */
     int32_t kernel_size; /* K: 2 .. 4 */
     int32_t dtype;       /* ssd_dtype_t of xbc, conv_ring and y */
     int32_t dt_dtype;    /* ssd_dtype_t of dt_raw: dtype or SSD_DTYPE_F32 */
     uint32_t flags;      /* must be 0 */
-    /* row strides in elements, any */
-    int64_t xbc_stride;  /* >= C = H P + 2 G N */
-    int64_t dt_stride;   /* >= H */
+    /* row strides in elements; inputs any from 0 up (rows may share bytes) */
+    int64_t xbc_stride;
+    int64_t dt_stride;
     int64_t y_stride;    /* >= H P */
 } ssd_step_dims_t;
 

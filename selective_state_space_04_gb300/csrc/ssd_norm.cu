@@ -12,7 +12,9 @@
 // is above every finite number and is not lost as it is by fmaxf.
 //
 // Bound by memory: 32768 rows of 2560 with a residual, bf16, take 95 us (104% of a plain copy's rate), their
-// gradients 111 (89%).  The gated form reaches 60% (4096 rows of 5120: 25.6 us).
+// gradients 111 (89%); 16384 such rows in fp32 96 us (103%) and 107 (92%).  Into 8 bits, 8192 rows of 2560 with an fp32
+// residual take 37.5 us (91%).  The gated form reaches 60% (4096 rows of 5120: 25.6 us; with z at an odd offset, read
+// element by element, 30.8).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -324,7 +326,7 @@ cudaError_t norm_launch_t(const NormParams &p, cudaStream_t st)
             return launch_after(ssd_norm_kernel<T, R, kMode, kQ8, 2, true>, grid, 32 * kWarpRows, st, p);
         return launch_after(ssd_norm_kernel<T, R, kMode, kQ8, 4, true>, grid, 32 * kWarpRows, st, p);
     }
-    const int vpt = nv <= 512 ? 1 : 2;
+    const int vpt = nv <= 512 ? 1 : 2;   // (one vector up to 1024 threads was not measured)
     const unsigned threads = (unsigned)(((nv + vpt - 1) / vpt + 31) / 32 * 32);
     if (vpt == 1)
         return launch_after(ssd_norm_kernel<T, R, kMode, kQ8, 1, false>, (unsigned)p.rows, threads, st, p);
@@ -510,7 +512,9 @@ __global__ void __launch_bounds__(1024) ssd_norm_dweight_kernel(const float *par
 }
 
 // vectors a thread holds, and threads of a row; of fp32 rows two, where one would be 512 threads: their
-// registers are what fits on an SM
+// registers are what fits on an SM.  Four vectors (rows above 8192) have no room for the next row's loads, and with
+// fp32 rows some registers go to local memory: 4096 rows of 16384 take 110 us in bf16 and 256 in fp32 (72 and 62% of a
+// plain copy's rate), 8192 rows of 8192 89 and 168 (88 and 94%).
 int bwd_threads(const ssd_norm_dims_t &d, int *vpt)
 {
     const int nv = d.dim / 8;
@@ -518,7 +522,7 @@ int bwd_threads(const ssd_norm_dims_t &d, int *vpt)
     return ((nv + *vpt - 1) / *vpt + 31) / 32 * 32;
 }
 
-// Blocks: as many as run at once (1024 threads an SM, measured best: on 32768 rows of 2560 three blocks
+// Blocks: as many as run at once (1024 threads an SM, measured best on the one width that was tried: on 32768 rows of 2560 three blocks
 // of 320 take 111 us, two 125, four 134; where a row is a warp's, two blocks of 256 of them), but
 // eight rows each (per warp) where that fills the SMs: a block's partial sums cost as much as a row.
 int bwd_blocks(const ssd_norm_dims_t &d)

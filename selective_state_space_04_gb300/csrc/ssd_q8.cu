@@ -49,10 +49,12 @@ cudaError_t q8_pack_launch(const int8_t *w, int8_t *packed, const ssd_q8_dims_t 
 namespace {
 
 // Up to here the weights go through registers and mma.sync (8 tokens of 10576 x 2560: 8.4 us, with ssd_q8_mid.cu
-// 12.1; 16 tokens 15.9, when they went through registers too, and 12.1).
+// 12.1; 16 tokens 15.9, when they went through registers too, and 12.1).  Measured on these weights: of
+// 16384 x 8192 8 tokens take 32.5 us here and 16 take 27.6 there, of 2560 x 5120 9.0 and 8.7.
 constexpr long long kFew = 8;
 // From here on both operands are widened first (256, 384 and 512 tokens of 10576 x 2560: 30.2, 37.5 and 53 us
-// without; 288, 384 and 512 tokens 36.3, 37.0 and 39 to 43 us with).
+// without; 288, 384 and 512 tokens 36.3, 37.0 and 39 to 43 us with).  Measured on these weights; what the widening
+// costs goes by N K: 256 tokens of 16384 x 8192 take 77.6 us without and 288 take 133 with, of 2560 x 5120 17.8 and 26.9.
 constexpr long long kMany = 257;
 
 Q8Params params(const Q8Args &a)

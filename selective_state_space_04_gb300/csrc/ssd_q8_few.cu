@@ -9,8 +9,10 @@
 // memory's rate; widening for the fp16 form took 60 instructions a slab and warp
 // and more time than the weights' bytes (10.8 us; with rings of asynchronous copies 13.5).  dp4a has the same
 // rate, but no 8 columns to fill: one token takes an eighth of the products (8.4 -> 7.6 us; two already
-// take 10.2, 8.8 with mma.sync).  With the prefetch below 1 and 8 tokens of 10576 x 2560 take 6.8 and 8.4 us, 59 and 48%
-// of the rate of a plain copy, of 16384 x 8192 28.2 and 32.4 us, 70 and 61%.
+// take 10.2, 8.8 with mma.sync).  With the prefetch below 1 and 8 tokens of 10576 x 2560 take 6.7 and 8.3 us, 60 and 48%
+// of the rate of a plain copy, of 16384 x 8192 28.0 and 32.5 us, 71 and 61%.  At that the products are under half of
+// what the tensor cores do; the start and end of each CTA, and the part wave above 12160 channels, are what is
+// known of the rest.
 // A lane's 16 consecutive elements of a row are two k-steps' fragments when both operands
 // are read in the same order, so neither is shuffled.
 #include <cuda_bf16.h>
@@ -117,7 +119,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) ssd_q8_few_kernel(const Q8P
 template <int TOK, typename T>
 cudaError_t launch_t(const Q8Params &p, cudaStream_t st)
 {
-    // warps per CTA: as many as let all CTAs run at once with about 20 warps on every SM
+    // Warps per CTA: as many as let all CTAs run at once with about 20 warps on every SM, as far as that goes: five
+    // CTAs of 4 warps are what the registers allow (91 to 93 a thread), 760 in all.  From 12161 channels on
+    // some start when others end (12160 and 12176 x 8192: 1 token 18.0 and 21.2 us, 8 tokens 22.0 and 28.0).
     const int items = (p.N + 15) / 16, warps = items <= 2 * sm_count() ? 16 : items <= 3 * sm_count() ? 8 : 4;
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

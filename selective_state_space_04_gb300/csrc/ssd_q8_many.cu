@@ -39,7 +39,7 @@ constexpr int kEpiWarps = 8;
 constexpr int kThreads = (kEpiWarps + 2) * 32;   // warps 0-7: results, 8: copies, 9: MMA (leader) or its relay
 constexpr int kSmem = kStages * kStageBytes + 1024;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
-constexpr long long kPanel = 32768;   // tokens widened at once: bounds the scratch
+constexpr long long kPanel = 32768;   // tokens widened at once: bounds their scratch (the weights' is 2 N K bytes)
 
 enum { BAR_FULL = 0, BAR_EMPTY = kStages, BAR_ACC = 2 * kStages, BAR_DRAINED = BAR_ACC + 2, kBars = BAR_DRAINED + 2 };
 

@@ -427,6 +427,8 @@ cudaError_t q8_mid_launch(const Q8Params &p, bool f32, void *workspace, cudaStre
     // for 16384 x 8192).  With K in ranges and the exchange between them: 25 a slab and 300 + 3 a token, and
     // where two share an SM 32 each and 400 + 4 a token (17.3, 11.9 and 60 us).  Clusters of more than two leave
     // some SMs' second place empty (of 304 places 291 to 296 are taken up to four, 266 to 290 up to eight).
+    // (235 ns are about 480 clocks; the MMAs of a slab and 128 tokens take 259, and two CTAs that share an SM 320 ns for
+    // two slabs.  What the others of a CTA alone go to was not isolated.)
     const long long sms = sm_count(), round = 128 / mt * kChunkSlabs;
     auto waves = [](long long n, long long at_once) { return (n + at_once - 1) / at_once; };
     long long best = waves(tiles, sms) * (p.k64 * 47 / 2 + 150 + mt * 37 / 10 + (p.k64 - 1) / (2 * round) * 100);
