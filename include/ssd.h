@@ -695,7 +695,9 @@ ssd_status_t ssd_add_rmsnorm_fwd(const void *x, const void *residual, const floa
  *   dx = r (g - h r^2 mean(g h)) + dresidual   (of x and of residual alike)
  *   dweight = sum over rows of dout h r        (fp32, a fixed order)
  * h, dresidual and dx are in residual_dtype, dout in dtype.  dweight [D] fp32
- * (NULL: not written).  A row of zeros with eps 0 has r = 0.  dx may be
+ * (NULL: not written).  A row of zeros with eps 0 has r = 0, and so has
+ * one whose mean square overflows (its dx is dresidual; NaN where the sum of g h
+ * overflows too, with values near 2^120).  dx may be
  * dresidual, or dout where the types are the same (equal strides, in place);
  * outputs overlap nothing else.  `workspace` as for ssd_qk_norm_rope_bwd, with
  * ssd_add_rmsnorm_bwd_workspace_size's bytes.
